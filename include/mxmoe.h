@@ -50,7 +50,8 @@ enum mx_status {
   MX_ERR_ALIGN = -3,     /* a pointer is not aligned as required */
   MX_ERR_WORKSPACE = -4, /* workspace missing or smaller than moe_mxfp4_workspace_size */
   MX_ERR_HIP = -5,       /* the HIP runtime reported an error while enqueueing */
-  MX_ERR_SCRATCH = -6    /* moe_mxfp4_forward_noalloc: the call needs more than its static scratch */
+  MX_ERR_SCRATCH = -6,   /* moe_mxfp4_forward_noalloc: the call needs more than its static scratch */
+  MX_ERR_ARG = -7        /* a scalar, a mode or a combination of optional arguments is not allowed */
 };
 
 /* Limits checked by every call. */
@@ -382,6 +383,159 @@ MX_API int moe_mxfp4_forward_persistent(const uint16_t* x, const float* router_l
                                         const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,
                                         const uint8_t* s_down, uint16_t* y, int64_t T, int64_t H, int64_t I,
                                         int64_t E, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Dense feed-forward operators around MXFP4 weights: the layers of a mixture-of-experts model
+ * that every token takes (its first, dense blocks and its shared experts), and the norms and
+ * residual around every block.  For decode steps (T = 1) as for prompts and training batches
+ * (T up to 2^24).  The weights are frozen; the backward calls give the gradients of the inputs,
+ * biases and norm weights, for training what lies below or beside them.
+ *
+ * For all of them:
+ *   - products are exact in fp32, sums, activations, norms and gradients are fp32, and every
+ *     output is rounded once (to nearest even) when it is stored.  Results do not depend on
+ *     timing: two calls on the same inputs give the same bits.
+ *   - "optional" pointers may be NULL.
+ *   - 1 <= T <= 2^24; a reduction length K (or H, I where they are one) is a multiple of 32
+ *     with 32 <= K <= 2^20; weight rows N (or 2I) <= 2^22, any number; no activation tensor
+ *     has more than 2^38 values.  MX_ERR_SHAPE otherwise.
+ *   - bf16 tensors are 16-byte aligned, weight codes 16, fp32 outputs 4; weight scales 8 where
+ *     the reduction length of a forward call is a multiple of 256 (else 1).
+ *   - `workspace` is scratch of at least the size that the call's *_workspace_size gives (0:
+ *     it may be NULL), 256-byte aligned; it needs no initialization, and calls that share one
+ *     must not overlap in time.  *_workspace_size returns 0 for sizes that the call rejects.
+ *   - Outputs must not overlap inputs or one another, except where stated.
+ */
+enum mx_act {
+  MX_ACT_NONE = 0,      /* z */
+  MX_ACT_RELU = 1,      /* max(z, 0); its slope at 0 is 0 */
+  MX_ACT_SILU = 2,      /* z / (1 + exp(-z)) */
+  MX_ACT_GELU = 3,      /* z/2 (1 + erf(z / sqrt 2)) */
+  MX_ACT_GELU_TANH = 4, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+  MX_ACT_SIGMOID = 5    /* 1 / (1 + exp(-z)) */
+};
+
+/*
+ * Dense MXFP4 linear layer with its epilogue:
+ *   z[t,n] = sum_k x[t,k] w[n,k] + bias[n],   y[t,n] = residual[t,n] + scale * act(z[t,n])
+ *   x bf16 [T, K]; w_codes uint8 [N, K/2], w_scales uint8 [N, K/32]
+ *   bias      optional, bf16 [N]
+ *   residual  optional, bf16 [T, N]; may be y itself
+ *   scale     finite;  act: an mx_act
+ *   y bf16 [T, N] (written);  z  optional, bf16 [T, N] (written): what the backward call takes
+ */
+MX_API size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N);
+MX_API int mx_linear_fused(const uint16_t* x, const uint8_t* w_codes, const uint8_t* w_scales, const uint16_t* bias,
+                           const uint16_t* residual, float scale, int act, uint16_t* y, uint16_t* z, int64_t T,
+                           int64_t K, int64_t N, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward, from dy [T, N] bf16:  dz = scale * dy * act'(z),
+ *   dx[t,k] = sum_n dz[t,n] w[n,k],  dbias[n] = sum_t dz[t,n]   (the residual's gradient is dy).
+ *   z      bf16 [T, N] as mx_linear_fused wrote it; not read for MX_ACT_NONE (may be NULL)
+ *   dx     optional, bf16 [T, K] (written);  dbias  optional, fp32 [N] (written); one is needed
+ *   w_codes, w_scales  as for mx_linear_fused; may be NULL without dx
+ * For dx, dz is rounded to bf16 where there is an activation (the matrix instructions take
+ * bf16): each product is off by at most 2^-8 of itself.  dbias sums the fp32 values.
+ */
+MX_API size_t mx_linear_fused_backward_workspace_size(int64_t T, int64_t K, int64_t N);
+MX_API int mx_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const uint8_t* w_codes,
+                                    const uint8_t* w_scales, float scale, int act, uint16_t* dx, float* dbias,
+                                    int64_t T, int64_t K, int64_t N, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * The gated half of a feed-forward block, both projections, the activation and the product:
+ *   g[t,n] = sum_k x[t,k] w[n,k] + bias[n],  u[t,n] = sum_k x[t,k] w[I+n,k] + bias[I+n],
+ *   h[t,n] = act(g[t,n]) * u[t,n]            n < I      (MX_ACT_SILU: SwiGLU)
+ *   x bf16 [T, H]; w_gate_up uint8 [2I, H/2], s_gate_up uint8 [2I, H/32]: rows [0, I) gate,
+ *   rows [I, 2I) up, the layout of one expert of moe_mxfp4_forward
+ *   bias  optional, bf16 [2I]
+ *   h bf16 [T, I] (written);  z  optional, bf16 [T, 2I] (written): g then u of each token
+ */
+MX_API size_t mx_gate_up_workspace_size(int64_t T, int64_t H, int64_t I);
+MX_API int mx_gate_up(const uint16_t* x, const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint16_t* bias,
+                      int act, uint16_t* h, uint16_t* z, int64_t T, int64_t H, int64_t I, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Its backward, from dh [T, I] bf16 and z [T, 2I] as mx_gate_up wrote it:
+ *   dz = [ dh * u * act'(g) | dh * act(g) ],  dx = dz W,  dbias[n] = sum_t dz[t,n]
+ *   dx  optional, bf16 [T, H] (written);  dbias  optional, fp32 [2I] (written); one is needed.
+ * dz is rounded to bf16 for dx, as in mx_linear_fused_backward.
+ */
+MX_API size_t mx_gate_up_backward_workspace_size(int64_t T, int64_t H, int64_t I);
+MX_API int mx_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t* w_gate_up,
+                               const uint8_t* s_gate_up, int act, uint16_t* dx, float* dbias, int64_t T, int64_t H,
+                               int64_t I, void* workspace, size_t workspace_bytes, void* stream);
+
+/* How mx_norm_residual's gate is laid out. */
+enum mx_gate_mode {
+  MX_GATE_NONE = 0,    /* no gate (1) */
+  MX_GATE_TOKEN = 1,   /* bf16 [T]: one value per token */
+  MX_GATE_CHANNEL = 2, /* bf16 [H]: one value per channel */
+  MX_GATE_FULL = 3     /* bf16 [T, H] */
+};
+#define MX_NORM_MAX_H 16384
+
+/*
+ * The norms after and before a block with the block's gate, residual scale and residual:
+ *   rms_norm(v)[i] = v[i] / sqrt(mean_j v[j]^2 + eps)            (squares and mean in fp32)
+ *   n  = rms_norm(b) * w_post   (b itself without w_post)
+ *   y  = x + scale * gate * n                                    (rounded to bf16)
+ *   xn = rms_norm(y) * w_pre                                     (of y as rounded)
+ *   x      bf16 [T, H], the residual stream before the block
+ *   b      optional, bf16 [T, H], the block's output (moe_mxfp4_forward's or mx_linear_fused's
+ *          y).  Without it the call is the norm before a block alone: xn = rms_norm(x) * w_pre,
+ *          and w_post, gate and y must be NULL
+ *   w_post optional, bf16 [H];  gate as gate_mode says (NULL exactly for MX_GATE_NONE)
+ *   w_pre  optional with b, bf16 [H];  xn bf16 [T, H] (written; given exactly with w_pre)
+ *   y      bf16 [T, H] (written; given exactly with b); may be x itself
+ *   scale finite, eps finite and > 0 (MX_ERR_ARG otherwise); 8 <= H <= MX_NORM_MAX_H, H % 8 == 0.
+ */
+MX_API int mx_norm_residual(const uint16_t* x, const uint16_t* b, const uint16_t* w_post, const uint16_t* gate,
+                            int gate_mode, float scale, const uint16_t* w_pre, float eps, uint16_t* y, uint16_t* xn,
+                            int64_t T, int64_t H, void* stream);
+
+/*
+ * Its backward, from the gradients of y and xn:
+ *   D = dy + (gradient of xn into y),  dx = D,  e = scale * D,  dgate = e * n,
+ *   dw_post = sum_t e * gate * rms_norm(b),  db = gradient of n into b applied to e * gate,
+ *   dw_pre = sum_t dxn * rms_norm(y)
+ *   dy   bf16 [T, H]; optional with w_pre (no gradient into y from beyond).  dxn bf16 [T, H],
+ *        given exactly with w_pre
+ *   y    bf16 [T, H], the forward's y (its x where there is no b); not read without w_pre
+ *   b, w_post, gate, gate_mode, scale, w_pre, eps  as in the forward
+ *   dx   bf16 [T, H] (written)
+ *   db   optional, bf16 [T, H] (written)
+ *   dgate optional: fp32 [T] for MX_GATE_TOKEN, fp32 [H] for MX_GATE_CHANNEL, bf16 [T, H] for
+ *        MX_GATE_FULL (written)
+ *   dw_post, dw_pre  optional, fp32 [H] (written)
+ */
+MX_API size_t mx_norm_residual_backward_workspace_size(int64_t T, int64_t H);
+MX_API int mx_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const uint16_t* y, const uint16_t* b,
+                                     const uint16_t* w_post, const uint16_t* gate, int gate_mode, float scale,
+                                     const uint16_t* w_pre, float eps, uint16_t* dx, uint16_t* db, void* dgate,
+                                     float* dw_post, float* dw_pre, int64_t T, int64_t H, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * A dense feed-forward block of a transformer, the path that runs the calls above together:
+ *   xn = rms_norm(x) * w_pre (x without w_pre);  h = mx_gate_up(xn);  b = h W_down^T + bias_down,
+ *   y  = x + scale * gate * rms_norm(b) * w_post
+ * With neither w_post nor gate, the residual and scale are applied in the down projection's
+ * epilogue (b is then never rounded).
+ *   x bf16 [T, H]; w_gate_up, s_gate_up, bias_gate_up, act as for mx_gate_up;
+ *   w_down uint8 [H, I/2], s_down uint8 [H, I/32], bias_down optional, bf16 [H];
+ *   w_pre, w_post, gate, gate_mode, scale, eps as for mx_norm_residual;  y bf16 [T, H] (written).
+ *   H % 32 == 0 and I % 32 == 0; with a norm or gate also H <= MX_NORM_MAX_H.
+ */
+MX_API size_t mx_ffn_block_workspace_size(int64_t T, int64_t H, int64_t I);
+MX_API int mx_ffn_block(const uint16_t* x, const uint16_t* w_pre, const uint8_t* w_gate_up, const uint8_t* s_gate_up,
+                        const uint16_t* bias_gate_up, int act, const uint8_t* w_down, const uint8_t* s_down,
+                        const uint16_t* bias_down, const uint16_t* w_post, const uint16_t* gate, int gate_mode,
+                        float scale, float eps, uint16_t* y, int64_t T, int64_t H, int64_t I, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /*
  * HBM reference kernels (measurement utilities, not steps of the layer).  "Zyphra

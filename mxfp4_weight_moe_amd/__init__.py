@@ -60,6 +60,28 @@ _lib.mxfp8_quantize.argtypes = [_P, _I64, _I64, _P, _P, _P]
 _lib.moe_mxfp4_forward_noalloc.argtypes = [_P, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _P]
 _lib.mx_hbm_read.argtypes = [_P, ctypes.c_size_t, _P, _P]
 _lib.mx_hbm_copy.argtypes = [_P, _P, ctypes.c_size_t, _P]
+_SZ = ctypes.c_size_t
+_F = ctypes.c_float
+_INT = ctypes.c_int
+_lib.mx_linear_fused.argtypes = [_P, _P, _P, _P, _P, _F, _INT, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
+_lib.mx_linear_fused_backward.argtypes = [_P, _P, _P, _P, _F, _INT, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
+_lib.mx_gate_up.argtypes = [_P, _P, _P, _P, _INT, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
+_lib.mx_gate_up_backward.argtypes = [_P, _P, _P, _P, _INT, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
+_lib.mx_norm_residual.argtypes = [_P, _P, _P, _P, _INT, _F, _P, _F, _P, _P, _I64, _I64, _P]
+_lib.mx_norm_residual_backward.argtypes = [_P, _P, _P, _P, _P, _P, _INT, _F, _P, _F, _P, _P, _P, _P, _P, _I64, _I64,
+                                           _P, _SZ, _P]
+_lib.mx_ffn_block.argtypes = [_P, _P, _P, _P, _P, _INT, _P, _P, _P, _P, _P, _INT, _F, _F, _P, _I64, _I64, _I64, _P,
+                              _SZ, _P]
+_FFN_SIZES = ("mx_linear_fused_workspace_size", "mx_linear_fused_backward_workspace_size",
+              "mx_gate_up_workspace_size", "mx_gate_up_backward_workspace_size", "mx_ffn_block_workspace_size",
+              "mx_norm_residual_backward_workspace_size")
+_FFN_CALLS = ("mx_linear_fused", "mx_linear_fused_backward", "mx_gate_up", "mx_gate_up_backward", "mx_norm_residual",
+              "mx_norm_residual_backward", "mx_ffn_block")
+for _n in _FFN_SIZES:
+    getattr(_lib, _n).restype = _SZ
+    getattr(_lib, _n).argtypes = [_I64] * (2 if "norm" in _n else 3)
+for _n in _FFN_CALLS:
+    getattr(_lib, _n).restype = ctypes.c_int
 for _n in ("mx_linear", "mxfp4_dequantize", "moe_route_topk", "moe_sort_by_expert", "moe_route_sort",
            "moe_gate_up_swiglu", "moe_down_combine", "moe_mxfp4_forward", "moe_mxfp4_forward_persistent",
            "moe_mxfp4_forward_shared", "moe_mxfp4_forward_a8", "mx_linear_a8", "mxfp8_quantize", "mx_hbm_read",
@@ -72,7 +94,7 @@ EXPORTED = ("mx_version", "mx_status_string", "mx_linear", "mxfp4_dequantize", "
             "moe_mxfp4_workspace_size", "moe_mxfp4_forward", "moe_mxfp4_forward_persistent",
             "moe_mxfp4_forward_shared", "moe_mxfp4_forward_a8", "mx_linear_a8", "mxfp8_quantize", "mx_hbm_read",
             "mx_hbm_copy", "moe_mxfp4_forward_noalloc", "moe_gate_up_swiglu_from_ids", "moe_expert_gemms_from_ids",
-            "moe_combine")
+            "moe_combine") + _FFN_CALLS + _FFN_SIZES
 MX_ERR_SCRATCH = -6
 MX_NOALLOC_SCRATCH_BYTES = 40 << 20
 
@@ -121,7 +143,7 @@ def _check(t: torch.Tensor, name: str, dtype, ndim=None, device=None):
 
 def _raise(status: int, call: str):
     if status != MX_OK:
-        if status == -2:
+        if status in (-2, -7):  # MX_ERR_SHAPE, MX_ERR_ARG
             raise ValueError(f"{call}: {status_string(status)}")
         raise MxError(status, call)
 
@@ -525,4 +547,278 @@ def moe_mxfp4_forward(x: torch.Tensor, router_logits: torch.Tensor, top_k: int, 
     _raise(st, name)
     if persistent and check and not torch.cuda.is_current_stream_capturing():
         raise_for_persistent_error(take_persistent_error(ws))
+    return out
+
+
+# ------------------------------------------------------------------ dense feed-forward operators
+
+_ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
+_GATE_NONE, _GATE_TOKEN, _GATE_CHANNEL, _GATE_FULL = 0, 1, 2, 3
+MX_NORM_MAX_H = 16384
+_BF16, _U8, _F32 = torch.bfloat16, torch.uint8, torch.float32
+
+
+def _act_code(act: str) -> int:
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {', '.join(_ACTS)}, got {act!r}")
+    return code
+
+
+def _tensor(t, name: str, dtype, shape, dev):
+    """_check with the whole shape at once."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
+        _check(t, name, dtype, None, dev)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _opt(t) -> int | None:
+    return None if t is None else t.data_ptr()
+
+
+def _scratch(nbytes: int, dev, ws):
+    """(tensor, pointer, bytes) of a call's workspace: the caller's, or a fresh one from the
+    allocator, which keeps it for this stream (and, under graph capture, for this graph)."""
+    if ws is not None:
+        _check(ws, "workspace", _U8, 1, dev)
+        return ws, ws.data_ptr(), ws.numel()
+    if nbytes == 0:
+        return None, None, 0
+    ws = torch.empty(nbytes, dtype=_U8, device=dev)
+    return ws, ws.data_ptr(), nbytes
+
+
+def _call(name: str, dev, *args):
+    """The C call `name` on dev's current stream, which is its last argument."""
+    stream = torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(_lib, name)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(_lib, name)(*args, stream)
+    if st != MX_OK:
+        _raise(st, name)
+
+
+def _bf16_rows(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dtype != _BF16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 2:
+        _check(t, name, _BF16, 2)
+    if t.numel() == 0:
+        raise ValueError(f"{name} is empty: {list(t.shape)}")
+    return t.shape
+
+
+def _weights(codes, scales, name: str, rows: int | None, K: int, dev) -> int:
+    rows = codes.shape[0] if rows is None and isinstance(codes, torch.Tensor) and codes.dim() else rows
+    if K % 32:
+        raise ValueError(f"the reduction length {K} must be a multiple of 32")
+    _tensor(codes, f"{name} codes", _U8, (rows, K // 2), dev)
+    _tensor(scales, f"{name} scales", _U8, (rows, K // 32), dev)
+    return rows
+
+
+def mx_linear_fused(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor, bias: torch.Tensor | None = None,
+                    residual: torch.Tensor | None = None, scale: float = 1.0, act: str = "none",
+                    save_z: bool = False, out: torch.Tensor | None = None, ws: torch.Tensor | None = None):
+    """y[T,N] = residual + scale * act(x W^T + bias), all in fp32, rounded once to bf16.
+    act: none, relu, silu, gelu, gelu_tanh or sigmoid.  out may be the residual itself.
+    save_z=True: (y, z), z = x W^T + bias in bf16 for mx_linear_fused_backward."""
+    T, K = _bf16_rows(x, "x")
+    dev = x.device
+    N = _weights(w_codes, w_scales, "weight", None, K, dev)
+    if bias is not None:
+        _tensor(bias, "bias", _BF16, (N,), dev)
+    if residual is not None:
+        _tensor(residual, "residual", _BF16, (T, N), dev)
+    code = _act_code(act)
+    if out is None:
+        out = torch.empty((T, N), dtype=_BF16, device=dev)
+    else:
+        _tensor(out, "out", _BF16, (T, N), dev)
+    z = torch.empty((T, N), dtype=_BF16, device=dev) if save_z else None
+    ws, wp, wn = _scratch(_lib.mx_linear_fused_workspace_size(T, K, N), dev, ws)
+    _call("mx_linear_fused", dev, x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), _opt(bias), _opt(residual),
+          scale, code, out.data_ptr(), _opt(z), T, K, N, wp, wn)
+    return (out, z) if save_z else out
+
+
+def mx_linear_fused_backward(dy: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                             z: torch.Tensor | None = None, scale: float = 1.0, act: str = "none",
+                             need_dx: bool = True, need_dbias: bool = True, ws: torch.Tensor | None = None):
+    """(dx bf16 [T,K], dbias fp32 [N]) of mx_linear_fused from dy and its saved z (not needed
+    for act "none"); None for what is not asked for.  The residual's gradient is dy."""
+    T, N = _bf16_rows(dy, "dy")
+    dev = dy.device
+    if not isinstance(w_codes, torch.Tensor) or w_codes.dim() != 2:
+        raise ValueError("w_codes must be a 2-d tensor")
+    K = w_codes.shape[1] * 2
+    _weights(w_codes, w_scales, "weight", N, K, dev)
+    code = _act_code(act)
+    if code and z is None:
+        raise ValueError(f"act {act!r} needs z, the pre-activations of the forward call")
+    if z is not None:
+        _tensor(z, "z", _BF16, (T, N), dev)
+    if not need_dx and not need_dbias:
+        raise ValueError("neither dx nor dbias is asked for")
+    dx = torch.empty((T, K), dtype=_BF16, device=dev) if need_dx else None
+    dbias = torch.empty(N, dtype=_F32, device=dev) if need_dbias else None
+    ws, wp, wn = _scratch(_lib.mx_linear_fused_backward_workspace_size(T, K, N), dev, ws)
+    _call("mx_linear_fused_backward", dev, dy.data_ptr(), _opt(z), w_codes.data_ptr(), w_scales.data_ptr(), scale, code,
+          _opt(dx), _opt(dbias), T, K, N, wp, wn)
+    return dx, dbias
+
+
+def mx_gate_up(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor, bias: torch.Tensor | None = None,
+               act: str = "silu", save_z: bool = False, out: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None):
+    """h[T,I] = act(x Wg^T + bg) * (x Wu^T + bu) with W_gate_up [2I, H/2] (gate rows, then up
+    rows), all in fp32, rounded once to bf16.  save_z=True: (h, z), z bf16 [T, 2I] the two
+    pre-activations for mx_gate_up_backward."""
+    T, H = _bf16_rows(x, "x")
+    dev = x.device
+    two_i = _weights(W_gate_up, S_gate_up, "W_gate_up", None, H, dev)
+    if two_i % 2:
+        raise ValueError("W_gate_up must have an even number of rows")
+    I = two_i // 2
+    if bias is not None:
+        _tensor(bias, "bias", _BF16, (two_i,), dev)
+    code = _act_code(act)
+    if out is None:
+        out = torch.empty((T, I), dtype=_BF16, device=dev)
+    else:
+        _tensor(out, "out", _BF16, (T, I), dev)
+    z = torch.empty((T, two_i), dtype=_BF16, device=dev) if save_z else None
+    ws, wp, wn = _scratch(_lib.mx_gate_up_workspace_size(T, H, I), dev, ws)
+    _call("mx_gate_up", dev, x.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), _opt(bias), code, out.data_ptr(),
+          _opt(z), T, H, I, wp, wn)
+    return (out, z) if save_z else out
+
+
+def mx_gate_up_backward(dh: torch.Tensor, z: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor,
+                        act: str = "silu", need_dx: bool = True, need_dbias: bool = True,
+                        ws: torch.Tensor | None = None):
+    """(dx bf16 [T,H], dbias fp32 [2I]) of mx_gate_up from dh and its saved z; None for what is
+    not asked for."""
+    T, I = _bf16_rows(dh, "dh")
+    dev = dh.device
+    if not isinstance(W_gate_up, torch.Tensor) or W_gate_up.dim() != 2:
+        raise ValueError("W_gate_up must be a 2-d tensor")
+    H = W_gate_up.shape[1] * 2
+    _weights(W_gate_up, S_gate_up, "W_gate_up", 2 * I, H, dev)
+    _tensor(z, "z", _BF16, (T, 2 * I), dev)
+    code = _act_code(act)
+    if not need_dx and not need_dbias:
+        raise ValueError("neither dx nor dbias is asked for")
+    dx = torch.empty((T, H), dtype=_BF16, device=dev) if need_dx else None
+    dbias = torch.empty(2 * I, dtype=_F32, device=dev) if need_dbias else None
+    ws, wp, wn = _scratch(_lib.mx_gate_up_backward_workspace_size(T, H, I), dev, ws)
+    _call("mx_gate_up_backward", dev, dh.data_ptr(), z.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), code,
+          _opt(dx), _opt(dbias), T, H, I, wp, wn)
+    return dx, dbias
+
+
+def _gate_mode(gate, T: int, H: int, dev) -> int:
+    if gate is None:
+        return _GATE_NONE
+    if not isinstance(gate, torch.Tensor) or tuple(gate.shape) not in ((T, 1), (H,), (T, H)):
+        raise ValueError(f"gate must be a tensor of shape [T, 1], [H] or [T, H] with T={T}, H={H}")
+    _check(gate, "gate", _BF16, None, dev)
+    return _GATE_CHANNEL if gate.dim() == 1 else _GATE_TOKEN if gate.shape[1] == 1 else _GATE_FULL
+
+
+def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                     gate: torch.Tensor | None = None, scale: float = 1.0, w_pre: torch.Tensor | None = None,
+                     eps: float = 1e-6, out: torch.Tensor | None = None):
+    """(y, xn): y = x + scale * gate * rms_norm(b) * w_post, the residual stream after a block
+    with output b, and xn = rms_norm(y) * w_pre, the next block's input; each norm where its
+    weight is given, xn None without w_pre.  gate: [T, 1] per token, [H] per channel or [T, H].
+    Without b: (x, rms_norm(x) * w_pre).  out, for y, may be x itself."""
+    T, H = _bf16_rows(x, "x")
+    dev = x.device
+    for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _tensor(t, n, _BF16, (H,), dev)
+    mode = _gate_mode(gate, T, H, dev)
+    if b is None:
+        if w_post is not None or gate is not None or out is not None or w_pre is None:
+            raise ValueError("without b the call takes w_pre alone")
+        y = None
+    else:
+        _tensor(b, "b", _BF16, (T, H), dev)
+        y = out
+        if y is None:
+            y = torch.empty((T, H), dtype=_BF16, device=dev)
+        else:
+            _tensor(y, "out", _BF16, (T, H), dev)
+    xn = torch.empty((T, H), dtype=_BF16, device=dev) if w_pre is not None else None
+    _call("mx_norm_residual", dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale, _opt(w_pre), eps,
+          _opt(y), _opt(xn), T, H)
+    return (x if y is None else y), xn
+
+
+def mx_norm_residual_backward(dy: torch.Tensor | None, dxn: torch.Tensor | None, y: torch.Tensor | None,
+                              b: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                              gate: torch.Tensor | None = None, scale: float = 1.0,
+                              w_pre: torch.Tensor | None = None, eps: float = 1e-6,
+                              ws: torch.Tensor | None = None) -> dict:
+    """All gradients of mx_norm_residual from those of y and xn: a dict of dx, db (bf16 [T, H]),
+    dgate (fp32 [T, 1] or [H], bf16 [T, H]), dw_post and dw_pre (fp32 [H]), None for what the
+    forward did not have.  y is the forward's y (its x without b); dy may be None with w_pre."""
+    first = dy if dy is not None else dxn
+    T, H = _bf16_rows(first, "dy" if dy is not None else "dxn")
+    dev = first.device
+    for t, n in ((dy, "dy"), (dxn, "dxn"), (y, "y"), (b, "b")):
+        if t is not None:
+            _tensor(t, n, _BF16, (T, H), dev)
+    for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _tensor(t, n, _BF16, (H,), dev)
+    mode = _gate_mode(gate, T, H, dev)
+    if (w_pre is None) != (dxn is None) or (w_pre is not None and y is None):
+        raise ValueError("w_pre, dxn and y go together")
+    if b is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need b")
+    dx = torch.empty((T, H), dtype=_BF16, device=dev)
+    db = torch.empty((T, H), dtype=_BF16, device=dev) if b is not None else None
+    dgate = None
+    if gate is not None:
+        dgate = torch.empty(tuple(gate.shape), dtype=_BF16 if mode == _GATE_FULL else _F32, device=dev)
+    dw_post = torch.empty(H, dtype=_F32, device=dev) if w_post is not None else None
+    dw_pre = torch.empty(H, dtype=_F32, device=dev) if w_pre is not None else None
+    ws, wp, wn = _scratch(_lib.mx_norm_residual_backward_workspace_size(T, H), dev, ws)
+    _call("mx_norm_residual_backward", dev, _opt(dy), _opt(dxn), _opt(y), _opt(b), _opt(w_post), _opt(gate), mode,
+          scale, _opt(w_pre), eps, dx.data_ptr(), _opt(db), _opt(dgate), _opt(dw_post), _opt(dw_pre), T, H, wp, wn)
+    return dict(dx=dx, db=db, dgate=dgate, dw_post=dw_post, dw_pre=dw_pre)
+
+
+def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor, W_down: torch.Tensor,
+                 S_down: torch.Tensor, w_pre: torch.Tensor | None = None, bias_gate_up: torch.Tensor | None = None,
+                 bias_down: torch.Tensor | None = None, act: str = "silu", w_post: torch.Tensor | None = None,
+                 gate: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
+                 out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """A dense feed-forward block of a transformer: y = x + scale * gate * rms_norm(b) * w_post
+    with b = mx_gate_up(rms_norm(x) * w_pre) W_down^T + bias_down; each norm where its weight is
+    given, gate as for mx_norm_residual."""
+    T, H = _bf16_rows(x, "x")
+    dev = x.device
+    two_i = _weights(W_gate_up, S_gate_up, "W_gate_up", None, H, dev)
+    if two_i % 2:
+        raise ValueError("W_gate_up must have an even number of rows")
+    I = two_i // 2
+    _weights(W_down, S_down, "W_down", H, I, dev)
+    for t, n, size in ((w_pre, "w_pre", H), (w_post, "w_post", H), (bias_gate_up, "bias_gate_up", two_i),
+                       (bias_down, "bias_down", H)):
+        if t is not None:
+            _tensor(t, n, _BF16, (size,), dev)
+    mode = _gate_mode(gate, T, H, dev)
+    code = _act_code(act)
+    if out is None:
+        out = torch.empty((T, H), dtype=_BF16, device=dev)
+    else:
+        _tensor(out, "out", _BF16, (T, H), dev)
+    ws, wp, wn = _scratch(_lib.mx_ffn_block_workspace_size(T, H, I), dev, ws)
+    _call("mx_ffn_block", dev, x.data_ptr(), _opt(w_pre), W_gate_up.data_ptr(), S_gate_up.data_ptr(),
+          _opt(bias_gate_up), code, W_down.data_ptr(), S_down.data_ptr(), _opt(bias_down), _opt(w_post), _opt(gate), mode,
+          scale, eps, out.data_ptr(), T, H, I, wp, wn)
     return out

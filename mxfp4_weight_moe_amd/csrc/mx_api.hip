@@ -136,6 +136,7 @@ const char* mx_status_string(int status) {
     case MX_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case MX_ERR_HIP: return "the HIP runtime reported an error while enqueueing";
     case MX_ERR_SCRATCH: return "the call needs more scratch than the library's static array holds";
+    case MX_ERR_ARG: return "a scalar, a mode or a combination of optional arguments is not allowed";
     default: return "unknown status";
   }
 }

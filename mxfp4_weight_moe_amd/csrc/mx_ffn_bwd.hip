@@ -1,0 +1,324 @@
+// Backward of the dense feed-forward operators (frozen MXFP4 weights):
+//   linear   dz = scale * dy * act'(z);  dx = dz W;  dbias = sum over tokens of dz
+//   gate_up  dz = [dh * u * act'(g) | dh * act(g)] with z = [g | u]; dx and dbias the same way
+// First launch: dz in bf16 (rounded here once, as the matrix instructions take bf16; the bias
+// sums use the unrounded fp32 values) and per-strip column sums; then the strips' sums; then
+// the product dz W in tiles (mx_tile.hpp).
+#include "mx_epilogue.hpp"
+#include "mx_tile.hpp"
+
+namespace mx {
+
+// ------------------------------------------------------------------ dz and the bias gradient
+
+// A workgroup takes 256 columns (32 threads of 8) and a strip of rows, 8 at a time.
+constexpr int DZ_COLS = 256;
+
+struct LinearSlope {
+  const uint16_t* dy;  // [T, N]
+  const uint16_t* z;   // [T, N] or null (act none)
+  int N, act;
+  float scale;
+  __device__ __forceinline__ int cols() const { return N; }
+  __device__ __forceinline__ void dz(int64_t t, int n, float (&v)[8], bool wide, int left) const {
+    load_bf16<8>(dy + (size_t)t * N + n, v, wide, left);
+    if (z) {
+      float zv[8];
+      load_bf16<8>(z + (size_t)t * N + n, zv, wide, left);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a, d;
+        act_value_slope(act, zv[i], a, d);
+        v[i] *= d;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= scale;
+  }
+};
+
+// dz (bf16 [T][ldz], zeros in columns N .. ldz) and, if parts is set, the fp32 column sums of
+// this strip in parts[strip][cols].
+template <class Slope>
+__global__ void __launch_bounds__(256) dz_kernel(Slope f, uint16_t* __restrict__ dz, int ldz, float* __restrict__ parts,
+                                                 int64_t T, int strip_rows) {
+  __shared__ float red[8][DZ_COLS];
+  const int N = f.cols();
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int n = blockIdx.x * DZ_COLS + cx * 8;
+  const int64_t t0 = (int64_t)blockIdx.y * strip_rows, t1 = min(t0 + strip_rows, T);
+  const bool wide = n + 8 <= N && (N & 7) == 0;
+  const int left = N - n;
+  float sum[8] = {};
+  if (n < (dz ? ldz : N)) {
+    for (int64_t t = t0 + ry; t < t1; t += 8) {
+      float v[8];
+      f.dz(t, n, v, wide, left);
+      if (dz) store_bf16<8>(dz + (size_t)t * ldz + n, v, true, 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += v[i];
+    }
+  }
+  if (!parts) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) red[ry][cx * 8 + i] = sum[i];
+  __syncthreads();
+  const int c = blockIdx.x * DZ_COLS + threadIdx.x;
+  if (c < N) {
+    float a = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) a += red[r][threadIdx.x];
+    parts[(size_t)blockIdx.y * N + c] = a;
+  }
+}
+
+// gate_up: 8 columns of both halves a thread.
+__global__ void __launch_bounds__(256) dz_gated_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ z,
+                                                       int I, int act, uint16_t* __restrict__ dz, int ldz,
+                                                       float* __restrict__ parts, int64_t T, int strip_rows) {
+  __shared__ float red[2][8][DZ_COLS];
+  const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
+  const int n = blockIdx.x * DZ_COLS + cx * 8;
+  const int64_t t0 = (int64_t)blockIdx.y * strip_rows, t1 = min(t0 + strip_rows, T);
+  const bool wide = n + 8 <= I && (I & 7) == 0;
+  const int left = I - n;
+  float sg[8] = {}, su[8] = {};
+  if (n < I) {
+    for (int64_t t = t0 + ry; t < t1; t += 8) {
+      float d[8], g[8], u[8];
+      load_bf16<8>(dh + (size_t)t * I + n, d, wide, left);
+      load_bf16<8>(z + (size_t)t * 2 * I + n, g, wide, left);
+      load_bf16<8>(z + (size_t)t * 2 * I + I + n, u, wide, left);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float a, sl;
+        act_value_slope(act, g[i], a, sl);
+        const float du = d[i] * a;
+        g[i] = d[i] * u[i] * sl;
+        u[i] = du;
+        sg[i] += g[i];
+        su[i] += du;
+      }
+      if (dz) {
+        store_bf16<8>(dz + (size_t)t * ldz + n, g, wide, left);
+        store_bf16<8>(dz + (size_t)t * ldz + I + n, u, wide, left);
+        if (n + 8 >= I)  // the padding columns of this row
+          for (int c = 2 * I; c < ldz; ++c) dz[(size_t)t * ldz + c] = 0;
+      }
+    }
+  }
+  if (!parts) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    red[0][ry][cx * 8 + i] = sg[i];
+    red[1][ry][cx * 8 + i] = su[i];
+  }
+  __syncthreads();
+  const int c = blockIdx.x * DZ_COLS + threadIdx.x;
+  if (c < I) {
+    float a = 0.f, b = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      a += red[0][r][threadIdx.x];
+      b += red[1][r][threadIdx.x];
+    }
+    parts[(size_t)blockIdx.y * 2 * I + c] = a;
+    parts[(size_t)blockIdx.y * 2 * I + I + c] = b;
+  }
+}
+
+// out[k][c] = sum over strips, in a fixed order, of parts[strip][k][c] for the k whose out is
+// set: a workgroup takes 64 columns of one k, its 4 waves a quarter of the strips each.
+struct StripOut {
+  float* p[3];
+};
+
+__global__ void __launch_bounds__(256) strip_sum_kernel(const float* __restrict__ parts, StripOut out, int strips,
+                                                        int cols, int arrays) {
+  __shared__ float red[4][64];
+  const int k = blockIdx.y;
+  if (!out.p[k]) return;
+  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  float a = 0.f;
+  if (c < cols)
+    for (int i = strips * q / 4; i < strips * (q + 1) / 4; ++i) a += parts[((size_t)i * arrays + k) * cols + c];
+  red[q][threadIdx.x & 63] = a;
+  __syncthreads();
+  if (q == 0 && c < cols)
+    out.p[k][c] = red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x];
+}
+
+int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float* const* out, hipStream_t stream) {
+  StripOut o{};
+  for (int k = 0; k < arrays; ++k) o.p[k] = out[k];
+  hipLaunchKernelGGL(strip_sum_kernel, dim3((cols + 63) / 64, arrays), dim3(256), 0, stream, parts, o, strips, cols,
+                     arrays);
+  return hip_status(hipGetLastError());
+}
+
+// ------------------------------------------------------------------ dx = alpha * dz W
+
+template <int MT, int WM, int WN>
+__global__ void __launch_bounds__(WM * WN * 64, 2)
+    backward_kernel(const uint16_t* __restrict__ dz, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
+                    uint16_t* __restrict__ dx, float* __restrict__ parts, float alpha, int T, int K, int N, int ldz,
+                    int mtiles, int ntiles, int nsplit) {
+  constexpr int BM = WM * MT * 16, BN = WN * 64;
+  typedef RowStage<BM, BWD_KB, WM * WN> ZStage;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (ZStage::BYTES + WeightStage<BN>::BYTES)];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave / WN, wn = wave % WN;
+  const int tile = xcd_tile(blockIdx.x, mtiles * ntiles * nsplit);
+  const int split = tile % nsplit, nt = tile / nsplit % ntiles, mt0 = tile / nsplit / ntiles;
+  const int m0 = mt0 * BM, k0 = nt * BN;
+  const int stages = (N + BWD_KB - 1) / BWD_KB;
+  const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
+  ZStage zs;
+  zs.init(dz, m0, T, ldz, wave, lane);
+  f32x4 acc[MT][4];
+  tile_zero(acc);
+  backward_tile<MT, WM, WN>(zs, w, s, N, K, k0, ldz, st0, st1, lds, wm, wn, lane, acc);
+  const int r = lane & 15, g = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int t = m0 + wm * MT * 16 + m * 16 + r;
+    const int k = k0 + wn * 64 + 16 * g;  // 16 consecutive columns: 4j + i of tile i, element j
+    if (t >= T || k >= K) continue;       // K is a multiple of 32
+    if (nsplit > 1) {
+      float* p = parts + ((size_t)split * T + t) * (size_t)K + k;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        *reinterpret_cast<f32x4*>(p + 4 * j) = f32x4{acc[m][0][j], acc[m][1][j], acc[m][2][j], acc[m][3][j]};
+    } else {
+      float v[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[j] = alpha * acc[m][j & 3][j >> 2];
+      store_bf16<16>(dx + (size_t)t * K + k, v, true, 16);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) dx_combine_kernel(const float* __restrict__ parts, uint16_t* __restrict__ dx,
+                                                         float alpha, int64_t pieces, int nsplit) {
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= pieces) return;
+  f32x4 a[2] = {};
+  for (int z = 0; z < nsplit; ++z) {
+    const float* p = parts + ((size_t)z * pieces + id) * 8;
+    a[0] += *reinterpret_cast<const f32x4*>(p);
+    a[1] += *reinterpret_cast<const f32x4*>(p + 4);
+  }
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = alpha * a[j >> 2][j & 3];
+  store_bf16<8>(dx + (size_t)id * 8, v, true, 8);
+}
+
+// ------------------------------------------------------------------ launch plans
+
+TilePlan backward_plan(int64_t T, int64_t K, int64_t N) {
+  TilePlan p{};
+  p.mt = T > 1024 ? 8 : T > 64 ? 4 : 2;
+  p.wn = p.mt == 8 ? 4 : 2;
+  const int bm = 32 * p.mt, bn = p.wn * 64;
+  p.mtiles = (int)((T + bm - 1) / bm);
+  p.ntiles = (int)((K + bn - 1) / bn);
+  const int64_t tiles = (int64_t)p.mtiles * p.ntiles, stages = (N + BWD_KB - 1) / BWD_KB;
+  int64_t split = tiles >= GPU_CUS ? 1 : GPU_CUS / tiles;
+  p.nsplit = (int)std::max<int64_t>(1, std::min(split, stages / 4));
+  if (p.nsplit > 1) p.bytes = (size_t)p.nsplit * T * K * 4;
+  return p;
+}
+
+// Rows per strip of the dz launch: enough workgroups for the chip, whole groups of 8 rows.
+int dz_strip_rows(int64_t T, int64_t cols) {
+  const int64_t ctiles = (cols + DZ_COLS - 1) / DZ_COLS;
+  const int64_t want = std::max<int64_t>(1, 4 * GPU_CUS / ctiles);
+  int64_t rows = (T + want - 1) / want;
+  rows = std::max<int64_t>(8, (rows + 7) / 8 * 8);
+  return (int)rows;
+}
+
+BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, bool need_dz, bool dx, bool dbias) {
+  BackwardPlan b{};
+  b.ldz = (int)((N + 7) / 8 * 8);
+  b.strip_rows = dz_strip_rows(T, cols);
+  b.strips = (int)((T + b.strip_rows - 1) / b.strip_rows);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  if (need_dz && dx) b.dz = take((size_t)T * b.ldz * 2);
+  if (dbias) b.bias_parts = take((size_t)b.strips * N * 4);
+  if (dx) {
+    b.tile = backward_plan(T, K, N);
+    b.parts = take(b.tile.bytes);
+  }
+  b.bytes = off;
+  return b;
+}
+
+static int launch_dx(const uint16_t* dz, int ldz, const uint8_t* w, const uint8_t* s, uint16_t* dx, float alpha,
+                     const TilePlan& p, float* parts, int T, int K, int N, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
+#define MX_TILE(MT, WN)                                                                                            \
+  hipLaunchKernelGGL((backward_kernel<MT, 2, WN>), grid, dim3(2 * WN * 64), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, \
+                     ldz, p.mtiles, p.ntiles, p.nsplit)
+  if (p.mt == 8)
+    MX_TILE(8, 4);
+  else if (p.mt == 4)
+    MX_TILE(4, 2);
+  else
+    MX_TILE(2, 2);
+#undef MX_TILE
+  if (p.nsplit > 1) {
+    const int64_t pieces = (int64_t)T * (K / 8);
+    hipLaunchKernelGGL(dx_combine_kernel, dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, stream, parts, dx, alpha,
+                       pieces, p.nsplit);
+  }
+  return hip_status(hipGetLastError());
+}
+
+int launch_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const uint8_t* w, const uint8_t* s, float scale,
+                                 int act, uint16_t* dx, float* dbias, int T, int K, int N, void* workspace,
+                                 hipStream_t stream) {
+  const bool direct = !z && (N & 7) == 0;  // dz = scale * dy: the product reads dy itself
+  const BackwardPlan b = backward_workspace(T, K, N, N, !direct, dx != nullptr, dbias != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* dz = (dx && !direct) ? reinterpret_cast<uint16_t*>(ws + b.dz) : nullptr;
+  float* bp = dbias ? reinterpret_cast<float*>(ws + b.bias_parts) : nullptr;
+  if (dz || bp) {
+    const dim3 grid((N + DZ_COLS - 1) / DZ_COLS, b.strips);
+    hipLaunchKernelGGL((dz_kernel<LinearSlope>), grid, dim3(256), 0, stream, LinearSlope{dy, z, N, act, scale}, dz,
+                       b.ldz, bp, (int64_t)T, b.strip_rows);
+    if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
+  }
+  if (bp) {
+    const int st = launch_strip_sum(bp, b.strips, N, 1, &dbias, stream);
+    if (st != MX_OK) return st;
+  }
+  if (!dx) return MX_OK;
+  return launch_dx(direct ? dy : dz, direct ? N : b.ldz, w, s, dx, direct ? scale : 1.f, b.tile,
+                   reinterpret_cast<float*>(ws + b.parts), T, K, N, stream);
+}
+
+int launch_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t* w, const uint8_t* s, int act,
+                            uint16_t* dx, float* dbias, int T, int H, int I, void* workspace, hipStream_t stream) {
+  const BackwardPlan b = backward_workspace(T, H, 2 * (int64_t)I, I, true, dx != nullptr, dbias != nullptr);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* dz = dx ? reinterpret_cast<uint16_t*>(ws + b.dz) : nullptr;
+  float* bp = dbias ? reinterpret_cast<float*>(ws + b.bias_parts) : nullptr;
+  const dim3 grid((I + DZ_COLS - 1) / DZ_COLS, b.strips);
+  hipLaunchKernelGGL(dz_gated_kernel, grid, dim3(256), 0, stream, dh, z, I, act, dz, b.ldz, bp, (int64_t)T, b.strip_rows);
+  if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
+  if (bp) {
+    const int st = launch_strip_sum(bp, b.strips, 2 * I, 1, &dbias, stream);
+    if (st != MX_OK) return st;
+  }
+  if (!dx) return MX_OK;
+  return launch_dx(dz, b.ldz, w, s, dx, 1.f, b.tile, reinterpret_cast<float*>(ws + b.parts), T, H, 2 * I, stream);
+}
+
+}  // namespace mx

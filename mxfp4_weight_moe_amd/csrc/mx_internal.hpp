@@ -4,6 +4,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/mxmoe.h"
 
 namespace mx {
@@ -136,5 +138,50 @@ bool fused_layer_fits(int T, int E, int k, int H, int I);
 int launch_moe_fused(const uint16_t* x, const float* logits, const uint8_t* wgu, const uint8_t* sgu, const uint8_t* wd,
                      const uint8_t* sd, uint16_t* hbuf, float* dpart, uint16_t* y, int32_t* ctl, int T, int H, int I,
                      int E, int k, hipStream_t stream);
+
+// ------------------------------------------------------------------ dense feed-forward operators
+
+constexpr int GPU_CUS = 256;  // gfx950; launch plans use it, so that workspaces depend on sizes alone
+
+// A tiled product: the workgroup tile (2 waves of mt MFMA tiles by wn waves of 64 columns),
+// the tiles, and over how many workgroups the reduction is split (bytes: their fp32 parts).
+struct TilePlan {
+  int mt, wn, mtiles, ntiles, nsplit;
+  size_t bytes;
+};
+TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated);
+
+int launch_linear_fused(const uint16_t* x, const uint8_t* w, const uint8_t* s, const uint16_t* bias,
+                        const uint16_t* residual, float scale, int act, uint16_t* y, uint16_t* z, int T, int K, int N,
+                        void* workspace, hipStream_t stream);
+int launch_gate_up_dense(const uint16_t* x, const uint8_t* w, const uint8_t* s, const uint16_t* bias, int act,
+                         uint16_t* h, uint16_t* z, int T, int H, int I, void* workspace, hipStream_t stream);
+
+// Workspace of a backward call: byte offsets of dz, of the bias gradient's strip sums and of
+// the product's parts.
+struct BackwardPlan {
+  TilePlan tile;
+  int ldz, strip_rows, strips;
+  size_t dz, bias_parts, parts, bytes;
+};
+// N: rows of W; cols: columns that one dz launch covers (N, or I for gate_up); need_dz: the
+// product reads dz from the workspace, not dy itself
+BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, bool need_dz, bool dx, bool dbias);
+int launch_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const uint8_t* w, const uint8_t* s, float scale,
+                                 int act, uint16_t* dx, float* dbias, int T, int K, int N, void* workspace,
+                                 hipStream_t stream);
+int launch_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t* w, const uint8_t* s, int act,
+                            uint16_t* dx, float* dbias, int T, int H, int I, void* workspace, hipStream_t stream);
+// out[k][c] = sum over strips of parts[strip][k][c], in a fixed order (arrays <= 3)
+int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float* const* out, hipStream_t stream);
+
+int launch_norm_residual(const uint16_t* x, const uint16_t* b, const uint16_t* w_post, const uint16_t* gate,
+                         int gate_mode, float scale, const uint16_t* w_pre, float eps, uint16_t* y, uint16_t* xn, int T,
+                         int H, hipStream_t stream);
+int norm_backward_groups(int64_t T);
+int launch_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const uint16_t* y, const uint16_t* b,
+                                  const uint16_t* w_post, const uint16_t* gate, int gate_mode, float scale,
+                                  const uint16_t* w_pre, float eps, uint16_t* dx, uint16_t* db, void* dgate,
+                                  float* dw_post, float* dw_pre, int T, int H, float* parts, hipStream_t stream);
 
 }  // namespace mx

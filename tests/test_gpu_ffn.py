@@ -1,0 +1,608 @@
+"""GPU parity of the dense feed-forward operators against their definitions in 64 bits.
+
+Tolerances.  u = 2^-24 (half a step of fp32), b = 2^-8 (half a step of bf16).
+  * A dot product of exact terms summed in fp32 in any order is off by at most
+    n u sum|terms| (first order); n + 8 covers the bias and the second order.
+  * The activations are built from 1-ulp exponentials, reciprocals and erf: act(z) and act'(z)
+    are off by at most 2^-20 (1 + |z|), and change by at most 1.13 per unit of z.
+  * A stored bf16 value adds b |value|, and 2^-133 where it is subnormal.
+  * dz is rounded to bf16 for dx where there is an activation: b sum|dz w|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U, B, TINY = 2.0 ** -24, 2.0 ** -8, 2.0 ** -133
+ACT_ERR, ACT_LIP = 2.0 ** -20, 1.13
+ACTS = ["none", "relu", "silu", "gelu", "gelu_tanh", "sigmoid"]
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def mx():
+    assert torch.cuda.is_available(), "GPU tests need an MI355X"
+    import mxfp4_weight_moe_amd
+    return mxfp4_weight_moe_amd
+
+
+DEV = "cuda:0"
+
+
+def say(*a):
+    print(*a, flush=True)
+
+
+def gen(seed):
+    g = torch.Generator()
+    g.manual_seed(seed)
+    return g
+
+
+def bf(*shape, g, std=1.0, mean=0.0):
+    return (torch.randn(shape, generator=g, dtype=torch.float64) * std + mean).to(torch.bfloat16)
+
+
+def weights(rows, K, g, lo=115, hi=122):
+    w = torch.randint(0, 256, (rows, K // 2), generator=g, dtype=torch.uint8)
+    s = torch.randint(lo, hi, (rows, K // 32), generator=g, dtype=torch.uint8)
+    return w, s
+
+
+def decode(w, s):
+    t = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, -0., -.5, -1, -1.5, -2, -3, -4, -6], dtype=torch.float64)
+    v = torch.stack((t[(w & 15).long()], t[(w >> 4).long()]), -1).reshape(w.shape[0], -1, 32)
+    p = torch.where(s == 255, torch.full(s.shape, math.nan, dtype=torch.float64),
+                    torch.ldexp(torch.ones(s.shape, dtype=torch.float64), s.int() - 127))
+    return (v * p[..., None]).flatten(1)
+
+
+def act(z, kind):
+    """(value, slope) in 64 bits."""
+    if kind == "none":
+        return z, torch.ones_like(z)
+    if kind == "relu":
+        return z.clamp(min=0), (z > 0).double()
+    if kind == "gelu":
+        c = 0.5 * torch.erfc(-z / math.sqrt(2))
+        return z * c, c + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    if kind == "gelu_tanh":
+        k = math.sqrt(2 / math.pi)
+        p = torch.sigmoid(2 * k * (z + 0.044715 * z ** 3))
+        return z * p, p + z * p * (1 - p) * 2 * k * (1 + 3 * 0.044715 * z * z)
+    p = torch.sigmoid(z)
+    return (p, p * (1 - p)) if kind == "sigmoid" else (z * p, p + z * p * (1 - p))
+
+
+def within(got, want, tol, what):
+    got, want, tol = got.double().cpu(), want.expand(got.shape), torch.as_tensor(tol).double().expand(got.shape)
+    assert torch.equal(got.isnan(), want.isnan()), f"{what}: NaN at other places"
+    fine = ~want.isnan()
+    inf = fine & (want.isinf() | got.isinf())
+    assert torch.equal(got[inf], want[inf]), f"{what}: Inf at other places"
+    fine &= ~inf
+    r = ((got - want).abs() / (tol + TINY))[fine]
+    worst = float(r.max()) if r.numel() else 0.0
+    assert worst <= 1, f"{what}: {int((r > 1).sum())} of {r.numel()} out of bound, worst {worst:.3g}"
+    return worst
+
+
+def cuda(*ts):
+    return [t.to(DEV) if isinstance(t, torch.Tensor) else t for t in ts]
+
+
+def z_of(x, w, s, bias):
+    """z and the bound of its error."""
+    W = decode(w, s)
+    z = x.double() @ W.T
+    size = x.double().abs() @ W.abs().T
+    if bias is not None:
+        z, size = z + bias.double(), size + bias.double().abs()
+    return z, (x.shape[1] + 8) * U * size
+
+
+def value_error(z, ez, a):
+    return ACT_LIP * ez + ACT_ERR * (1 + z.abs())
+
+
+# ------------------------------------------------------------------ linear
+
+# streaming (T <= 32), then every tile height, odd rows and columns, K tails of 32, 64 and 96
+LINEAR_SHAPES = [(1, 256, 64), (1, 32, 1), (2, 96, 7), (5, 512, 33), (16, 288, 16), (17, 2048, 40), (31, 256, 100),
+                 (32, 160, 264), (33, 128, 8), (40, 32, 1), (64, 544, 130), (65, 256, 64), (77, 2048, 257),
+                 (129, 96, 300), (300, 512, 520), (1025, 192, 264), (1300, 256, 65), (1100, 32, 512)]
+
+
+def linear_inputs(T, K, N, seed):
+    g = gen(seed)
+    return (bf(T, K, g=g), *weights(N, K, g), bf(N, g=g, std=0.5), bf(T, N, g=g))
+
+
+def check_linear(y, z_got, x, w, s, bias, res, scale, kind):
+    z, ez = z_of(x, w, s, bias)
+    a, _ = act(z, kind)
+    want, err = scale * a, abs(scale) * value_error(z, ez, a)
+    if res is not None:
+        want, err = want + res.double(), err + U * (want + res.double()).abs()
+    worst = within(y, want, (1 + B) * err + B * want.abs(), "y")
+    if z_got is not None:
+        within(z_got, z, (1 + B) * ez + B * z.abs(), "z")
+    return worst
+
+
+@pytest.mark.parametrize("T,K,N", LINEAR_SHAPES)
+def test_linear(mx, T, K, N):
+    for i, (kind, has_bias, has_res, scale, save) in enumerate([
+            ("none", False, False, 1.0, False), ("gelu_tanh", True, True, 0.5, True), ("silu", True, False, -2.0, False),
+            ("none", False, True, 0.25, True)]):
+        x, w, s, bias, res = linear_inputs(T, K, N, 100 * T + K + N + i)
+        bias, res = bias if has_bias else None, res if has_res else None
+        say("linear", T, K, N, kind, has_bias, has_res)
+        r = mx.mx_linear_fused(*cuda(x, w, s), *cuda(bias, res), scale, kind, save_z=save)
+        y, z = r if save else (r, None)
+        say("   worst", check_linear(y, z, x, w, s, bias, res, scale, kind))
+
+
+@pytest.mark.parametrize("kind", ACTS)
+@pytest.mark.parametrize("T", [3, 50])
+def test_linear_activations(mx, T, kind):
+    x, w, s, bias, res = linear_inputs(T, 256, 48, 7)
+    x = (x * torch.linspace(0, 12, T)[:, None]).to(torch.bfloat16)  # pre-activations from 0 to beyond 30
+    say("act", kind, T)
+    y, z = mx.mx_linear_fused(*cuda(x, w, s, bias, res), 1.0, kind, save_z=True)
+    check_linear(y, z, x, w, s, bias, res, 1.0, kind)
+
+
+@pytest.mark.parametrize("T", [1, 20, 40, 100, 1030])
+def test_linear_nan_inf_and_neighbours(mx, T):
+    K, N = 288, 72
+    x, w, s, bias, res = linear_inputs(T, K, N, 11)
+    s[5, 3] = 255          # a NaN scale: column 5 alone
+    x[T // 2, 17] = math.nan   # a NaN activation: its row alone
+    if T > 2:
+        x[0, K - 1] = math.inf
+    say("nan", T)
+    xd, wd, sd = cuda(x, w, s)
+    out = torch.full((T + 3, N), 7.0, dtype=torch.bfloat16, device=DEV)
+    y = mx.mx_linear_fused(xd, wd, sd, out=out[:T])
+    z = x.double() @ decode(w, s).T
+    size = (x.double().abs() @ decode(w, s).abs().T).nan_to_num(0, 0, 0)
+    # Inf times a zero weight is NaN in the definition and on the GPU alike
+    within(y, z, (K + 8) * U * 1.01 * size + B * z.abs().nan_to_num(0, 0, 0), "y")
+    assert bool((out[T:] == 7).all()), "rows behind the last were written"
+
+
+def test_linear_in_place_residual_and_repeat(mx):
+    for T, K, N in ((4, 512, 64), (40, 2048, 64), (200, 256, 129), (1100, 256, 264)):
+        x, w, s, bias, res = cuda(*linear_inputs(T, K, N, 21))
+        say("in place", T)
+        a = mx.mx_linear_fused(x, w, s, bias, res, 0.5, "relu")
+        b = mx.mx_linear_fused(x, w, s, bias, res, 0.5, "relu")
+        buf = res.clone()
+        c = mx.mx_linear_fused(x, w, s, bias, buf, 0.5, "relu", out=buf)
+        assert torch.equal(a, b) and torch.equal(a, c) and c.data_ptr() == buf.data_ptr()
+
+
+# ------------------------------------------------------------------ linear, backward
+
+def check_dx(dx, dz, edz, w, s, rounded, N):
+    W = decode(w, s)
+    want, size = dz @ W, dz.abs() @ W.abs()
+    err = edz @ W.abs() + (N + 8) * U * size + (B * size if rounded else 0)
+    return within(dx, want, (1 + B) * err + B * want.abs(), "dx")
+
+
+BWD_SHAPES = [(1, 32, 1), (1, 256, 64), (3, 96, 7), (33, 128, 16), (64, 288, 130), (65, 160, 257), (100, 512, 520),
+              (129, 544, 33), (700, 96, 72), (1025, 256, 264), (1100, 32, 100), (1030, 288, 65)]
+
+
+@pytest.mark.parametrize("T,K,N", BWD_SHAPES)
+def test_linear_backward(mx, T, K, N):
+    for kind, scale in (("none", 0.5), ("silu", 1.0), ("gelu", -2.0)):
+        g = gen(T + K + N)
+        w, s = weights(N, K, g)
+        dy, z = bf(T, N, g=g), bf(T, N, g=g, std=1.5)
+        say("linear backward", T, K, N, kind)
+        dx, db = mx.mx_linear_fused_backward(*cuda(dy, w, s), None if kind == "none" else z.to(DEV), scale, kind)
+        slope = act(z.double(), kind)[1]
+        dz = scale * dy.double() * slope
+        edz = abs(scale) * dy.double().abs() * ((ACT_ERR * (1 + z.double().abs()) if kind != "none" else 0) + 4 * U)
+        say("   worst", check_dx(dx, dz, edz, w, s, kind != "none", N))
+        within(db, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbias")
+        only = mx.mx_linear_fused_backward(*cuda(dy, w, s), z.to(DEV), scale, kind, need_dx=False)
+        assert only[0] is None and torch.equal(only[1], db)
+        again = mx.mx_linear_fused_backward(*cuda(dy, w, s), z.to(DEV), scale, kind, need_dbias=False)
+        assert again[1] is None and torch.equal(again[0], dx)
+
+
+def test_backward_nan_and_neighbours(mx):
+    for T in (2, 70, 1030):
+        g = gen(T)
+        N, K = 72, 96
+        w, s = weights(N, K, g)
+        s[9, 1] = 255
+        dy = bf(T, N, g=g)
+        dy[T // 2, 3] = math.nan
+        say("backward nan", T)
+        dx, db = mx.mx_linear_fused_backward(*cuda(dy, w, s))
+        W = decode(w, s)
+        want = dy.double() @ W
+        size = (dy.double().abs() @ W.abs()).nan_to_num(0)
+        within(dx, want, (N + 8) * U * 1.01 * size + B * want.abs().nan_to_num(0), "dx")
+        assert db.isnan().nonzero().flatten().tolist() == [3]
+
+
+# ------------------------------------------------------------------ gate_up
+
+GATED_SHAPES = [(1, 256, 64), (1, 32, 1), (3, 96, 7), (16, 288, 33), (17, 512, 16), (32, 160, 100), (33, 128, 8),
+                (64, 544, 65), (65, 1024, 130), (130, 96, 257), (1025, 192, 136), (1100, 256, 33), (1030, 32, 264)]
+
+
+@pytest.mark.parametrize("T,H,I", GATED_SHAPES)
+def test_gate_up(mx, T, H, I):
+    for kind, has_bias, save in (("silu", False, False), ("gelu_tanh", True, True), ("none", True, False)):
+        g = gen(T + H + I)
+        x, (w, s), bias = bf(T, H, g=g), weights(2 * I, H, g), bf(2 * I, g=g, std=0.5)
+        bias = bias if has_bias else None
+        say("gate_up", T, H, I, kind)
+        r = mx.mx_gate_up(*cuda(x, w, s, bias), kind, save_z=save)
+        h, z_got = r if save else (r, None)
+        z, ez = z_of(x, w, s, bias)
+        a = act(z[:, :I], kind)[0]
+        want = a * z[:, I:]
+        err = value_error(z[:, :I], ez[:, :I], a) * (z[:, I:].abs() + ez[:, I:]) + a.abs() * ez[:, I:] + U * want.abs()
+        say("   worst", within(h, want, (1 + B) * err + B * want.abs(), "h"))
+        if save:
+            within(z_got, z, (1 + B) * ez + B * z.abs(), "z")
+
+
+@pytest.mark.parametrize("kind", ACTS)
+def test_gate_up_backward(mx, kind):
+    for T, H, I in ((1, 32, 1), (5, 96, 33), (64, 288, 64), (130, 160, 65), (1030, 128, 72), (700, 512, 257)):
+        g = gen(T + H + I)
+        w, s = weights(2 * I, H, g)
+        dh, z = bf(T, I, g=g), bf(T, 2 * I, g=g, std=1.5)
+        say("gate_up backward", T, H, I, kind)
+        dx, db = mx.mx_gate_up_backward(*cuda(dh, z, w, s), kind)
+        gt, up, d = z[:, :I].double(), z[:, I:].double(), dh.double()
+        a, slope = act(gt, kind)
+        dz = torch.cat((d * up * slope, d * a), 1)
+        e = ACT_ERR * (1 + gt.abs()) if kind != "none" else torch.zeros_like(gt)
+        edz = torch.cat((d.abs() * up.abs() * e, d.abs() * e), 1) + 4 * U * dz.abs()
+        say("   worst", check_dx(dx, dz, edz, w, s, True, 2 * I))
+        within(db, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbias")
+        assert torch.equal(mx.mx_gate_up_backward(*cuda(dh, z, w, s), kind, need_dx=False)[1], db)
+
+
+def test_gradients_against_differences():
+    """The gradient formulas used above against central differences of the forward's, in 64 bits."""
+    g = gen(3)
+    T, I = 5, 6
+    z = torch.randn(T, 2 * I, generator=g, dtype=torch.float64)
+    d = torch.randn(T, I, generator=g, dtype=torch.float64)
+    dirn = torch.randn(T, 2 * I, generator=g, dtype=torch.float64)
+    for kind in ACTS:
+        f = lambda v: float((d * act(v[:, :I], kind)[0] * v[:, I:]).sum())  # noqa: B023, E731
+        a, slope = act(z[:, :I], kind)
+        grad = torch.cat((d * z[:, I:] * slope, d * a), 1)
+        h = 1e-5
+        assert abs((f(z + h * dirn) - f(z - h * dirn)) / (2 * h) - float((grad * dirn).sum())) < 1e-7
+    x, b = torch.randn(T, 16, generator=g, dtype=torch.float64), torch.randn(T, 16, generator=g, dtype=torch.float64)
+    wo, wi = torch.rand(16, generator=g, dtype=torch.float64) + 0.5, torch.rand(16, generator=g, dtype=torch.float64) + 0.5
+    gate, c1, c2 = (torch.randn(T, 16, generator=g, dtype=torch.float64) for _ in range(3))
+    args = [x, b, wo, gate, wi]
+
+    def total(x, b, wo, gate, wi):
+        y, xn = norm_forward(x, b, wo, gate, 0.7, wi)
+        return float((c1 * y + c2 * xn).sum())
+
+    y, _ = norm_forward(*args[:4], 0.7, wi)
+    gr = norm_grads(c1, c2, y, b, wo, gate, 0.7, wi, "full")
+    for i, name in enumerate(("dx", "db", "dw_post", "dgate", "dw_pre")):
+        v = torch.randn(args[i].shape, generator=g, dtype=torch.float64)
+        hi, lo = list(args), list(args)
+        hi[i], lo[i] = args[i] + 1e-5 * v, args[i] - 1e-5 * v
+        diff = (total(*hi) - total(*lo)) / 2e-5
+        assert abs(diff - float((gr[name][0] * v).sum())) < 1e-6, name
+
+
+# ------------------------------------------------------------------ norms
+
+def rms(v):
+    return 1 / torch.sqrt((v * v).mean(1, keepdim=True) + EPS)
+
+
+def norm_forward(x, b, w_post, gate, scale, w_pre):
+    """(y, xn) in 64 bits, y not rounded."""
+    y = x
+    if b is not None:
+        n = b if w_post is None else b * rms(b) * w_post
+        y = x + scale * (n if gate is None else n * gate)
+    return y, (None if w_pre is None else y * rms(y) * w_pre)
+
+
+def norm_grads(dy, dxn, y, b, w_post, gate, scale, w_pre, mode):
+    """{name: (gradient, sum of the sizes of its terms)} in 64 bits."""
+    out = {}
+    D = dy if dy is not None else torch.zeros_like(y)
+    size = D.abs()
+    if w_pre is not None:
+        r, t = rms(y), dxn * w_pre
+        out["dw_pre"] = ((dxn * y * r).sum(0), (dxn * y * r).abs().sum(0))
+        D = D + r * (t - y * r * r * (t * y).mean(1, keepdim=True))
+        size = size + r * (t.abs() + y.abs() * r * r * (t * y).abs().mean(1, keepdim=True))
+    out["dx"] = (D, size)
+    if b is None:
+        return out
+    q = rms(b) if w_post is not None else torch.ones_like(y[:, :1])
+    w = w_post if w_post is not None else torch.ones_like(y[0])
+    e, es = scale * D, abs(scale) * size
+    if gate is not None:
+        dg, ds = e * b * q * w, es * (b * q * w).abs()
+        f = {"channel": lambda v: v.sum(0), "token": lambda v: v.sum(1, keepdim=True), "full": lambda v: v}[mode]
+        out["dgate"] = (f(dg), f(ds))
+        e, es = e * gate, es * gate.abs()
+    if w_post is not None:
+        out["dw_post"] = ((e * b * q).sum(0), (es * (b * q).abs()).sum(0))
+        t, ts = e * w, es * w.abs()
+        e = q * (t - b * q * q * (t * b).mean(1, keepdim=True))
+        es = q * (ts + b.abs() * q * q * (ts * b.abs()).mean(1, keepdim=True))
+    out["db"] = (e, es)
+    return out
+
+
+# every kernel width (one wave up to 1024 threads), rows that fill it and odd ones
+NORM_SHAPES = [(1, 8), (3, 64), (5, 512), (2, 520), (33, 1000), (7, 2048), (4, 2056), (9, 4096), (600, 72), (3, 7168),
+               (5, 8200), (2, 16384), (1030, 264), (2100, 40)]
+NORM_KINDS = [("full", True, True), ("none", True, True), ("channel", True, True), ("token", True, False),
+              ("token", False, True), ("channel", False, False), ("none", False, True), (None, False, True)]
+
+
+def norm_inputs(T, H, kind, post, pre, seed):
+    g = gen(seed)
+    x, b = bf(T, H, g=g, std=2.0), bf(T, H, g=g, std=0.7)
+    wo, wi = bf(H, g=g, std=0.1, mean=1.0), bf(H, g=g, std=0.1, mean=1.0)
+    shape = {"full": (T, H), "channel": (H,), "token": (T, 1)}.get(kind)
+    gate = bf(*shape, g=g, std=0.4, mean=0.5) if shape else None
+    if T > 1:
+        b[1] = 0  # a block that gives nothing: the norm divides by sqrt(eps)
+    return x, (b if kind else None), (wo if post else None), gate, (wi if pre else None), bf(T, H, g=g), bf(T, H, g=g)
+
+
+def dbl(t):
+    return None if t is None else t.double()
+
+
+@pytest.mark.parametrize("T,H", NORM_SHAPES)
+def test_norm(mx, T, H):
+    # a mean of H squares in fp32, then a reciprocal root and three products
+    d = (H + 16) * U
+    for kind, post, pre in NORM_KINDS:
+        x, b, wo, gate, wi, _, _ = norm_inputs(T, H, kind, post, pre, T + H)
+        say("norm", T, H, kind, post, pre)
+        y, xn = mx.mx_norm_residual(*cuda(x, b), *cuda(wo, gate), 0.7, wi if wi is None else wi.to(DEV), EPS)
+        want, _ = norm_forward(dbl(x), dbl(b), dbl(wo), dbl(gate), float(np.float32(0.7)), None)
+        if b is not None:
+            err = d * (want - x.double()).abs() + U * want.abs()
+            within(y, want, (1 + B) * err + B * want.abs(), "y")
+        if pre:
+            yy = y.double().cpu()
+            xw = yy * rms(yy) * wi.double()
+            within(xn, xw, ((1 + B) * d + B) * xw.abs(), "xn")
+
+
+@pytest.mark.parametrize("T,H", NORM_SHAPES)
+def test_norm_backward(mx, T, H):
+    # sums of H terms (means) and of T (parameter gradients), each on values off by a few u
+    d = (2 * H + 64) * U
+    for kind, post, pre in NORM_KINDS:
+        y, b, wo, gate, wi, dy, dxn = norm_inputs(T, H, kind, post, pre, 3 * T + H)
+        dy = None if (kind == "none" and pre) else dy
+        dxn = dxn if pre else None
+        say("norm backward", T, H, kind, post, pre)
+        got = mx.mx_norm_residual_backward(*cuda(dy, dxn, y, b), *cuda(wo, gate), 0.7, wi if wi is None else wi.to(DEV), EPS)
+        want = norm_grads(dbl(dy), dbl(dxn), dbl(y), dbl(b), dbl(wo), dbl(gate), float(np.float32(0.7)), dbl(wi), kind)
+        assert {k for k, v in got.items() if v is not None} == set(want)
+        for name, (v, size) in want.items():
+            rounded = B if got[name].dtype == torch.bfloat16 else 0.0
+            extra = (T + 16) * U if name.startswith("dw") or (name == "dgate" and kind == "channel") else 0.0
+            within(got[name], v, (1 + rounded) * (d + extra) * size + rounded * v.abs(), name)
+
+
+def test_norm_in_place_nan_and_neighbours(mx):
+    T, H = 37, 520
+    x, b, wo, gate, wi, dy, dxn = norm_inputs(T, H, "token", True, True, 5)
+    x[3, 7], b[9, 0], x[20, 1] = math.nan, math.inf, math.inf
+    xd, bd, wod, gd, wid = cuda(x, b, wo, gate, wi)
+    say("norm in place")
+    y, xn = mx.mx_norm_residual(xd, bd, wod, gd, 1.0, wid, EPS)
+    buf = torch.full((T + 2, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    buf[:T] = xd
+    y2, xn2 = mx.mx_norm_residual(buf[:T], bd, wod, gd, 1.0, wid, EPS, out=buf[:T])
+    assert torch.equal(y2.view(torch.int16), y.view(torch.int16)) and torch.equal(xn2.view(torch.int16), xn.view(torch.int16))
+    assert bool((buf[T:] == 7).all())
+    bad = {3, 9, 20}
+    rows = [i for i in range(T) if bool((~xn[i].isfinite()).any())]
+    assert set(rows) == bad, rows
+
+
+# ------------------------------------------------------------------ together, streams, graphs
+
+def block_inputs(T, H, I, seed):
+    g = gen(seed)
+    x = bf(T, H, g=g)
+    wgu, sgu = weights(2 * I, H, g)
+    wd, sd = weights(H, I, g)
+    return cuda(x, wgu, sgu, wd, sd, bf(H, g=g, std=0.1, mean=1.0), bf(2 * I, g=g, std=0.3), bf(H, g=g, std=0.3),
+                bf(H, g=g, std=0.1, mean=1.0), bf(T, 1, g=g, mean=0.5))
+
+
+def check_block(mx, T, H, I):
+    x, wgu, sgu, wd, sd, wi, bgu, bd, wo, gate = block_inputs(T, H, I, T + H)
+    _, xn = mx.mx_norm_residual(x, w_pre=wi)
+    h = mx.mx_gate_up(xn, wgu, sgu, bgu, "silu")
+    plain = mx.mx_linear_fused(h, wd, sd, bd, x, 0.5)
+    assert torch.equal(mx.mx_ffn_block(x, wgu, sgu, wd, sd, wi, bgu, bd, scale=0.5), plain)
+    b = mx.mx_linear_fused(h, wd, sd, bd)
+    y, _ = mx.mx_norm_residual(x, b, wo, gate, 0.5)
+    assert torch.equal(mx.mx_ffn_block(x, wgu, sgu, wd, sd, wi, bgu, bd, "silu", wo, gate, 0.5), y)
+    return plain
+
+
+@pytest.mark.parametrize("T,H,I", [(1, 256, 64), (8, 1024, 512), (40, 512, 288), (200, 288, 96), (1100, 256, 160)])
+def test_block_is_its_parts(mx, T, H, I):
+    """The block's path against the separate calls (the same bits), and the whole of it against
+    the definition with the same roundings between the calls."""
+    say("block", T, H, I)
+    plain = check_block(mx, T, H, I)
+    x, wgu, sgu, wd, sd, wi, bgu, bd, _, _ = [t.cpu() for t in block_inputs(T, H, I, T + H)]
+    _, xn = mx.mx_norm_residual(x.to(DEV), w_pre=wi.to(DEV))
+    h = mx.mx_gate_up(*cuda(xn, wgu, sgu, bgu), "silu").cpu()
+    z, ez = z_of(h, wd, sd, bd)
+    want = x.double() + 0.5 * z
+    within(plain, want, (1 + B) * (0.5 * ez + 2 * U * want.abs()) + B * want.abs(), "block")
+
+
+def test_training_step_runs_together(mx):
+    """Forward with saved pre-activations, then the whole backward: the input's gradient of a
+    norm -> gate_up -> down -> norm block against the chain of definitions on the same values."""
+    T, H, I = 70, 256, 96
+    x, wgu, sgu, wd, sd, wi, bgu, bd, wo, gate = block_inputs(T, H, I, 9)
+    dy = bf(T, H, g=gen(1)).to(DEV)
+    say("training step")
+    _, xn = mx.mx_norm_residual(x, w_pre=wi)
+    h, z = mx.mx_gate_up(xn, wgu, sgu, bgu, "silu", save_z=True)
+    b = mx.mx_linear_fused(h, wd, sd, bd)
+    y, _ = mx.mx_norm_residual(x, b, wo, gate, 0.5)
+    post = mx.mx_norm_residual_backward(dy, None, None, b, wo, gate, 0.5)
+    dh, dbd = mx.mx_linear_fused_backward(post["db"], wd, sd)
+    dxn, dbgu = mx.mx_gate_up_backward(dh, z, wgu, sgu, "silu")
+    pre = mx.mx_norm_residual_backward(post["dx"], dxn, x, w_pre=wi)
+    c = [dbl(t.cpu()) for t in (dy, b, wo, gate)]
+    want = norm_grads(c[0], None, c[0], c[1], c[2], c[3], 0.5, None, "token")
+    d = (2 * H + 64) * U
+    within(post["db"], want["db"][0], (1 + B) * d * want["db"][1] + B * want["db"][0].abs(), "db")
+    check_dx(dh.cpu(), post["db"].double().cpu(), torch.zeros(T, H, dtype=torch.float64), wd.cpu(), sd.cpu(), False, H)
+    want = norm_grads(dbl(post["dx"].cpu()), dbl(dxn.cpu()), dbl(x.cpu()), None, None, None, 1.0, dbl(wi.cpu()), "none")
+    within(pre["dx"], want["dx"][0], (1 + B) * d * want["dx"][1] + B * want["dx"][0].abs(), "dx")
+    assert dbd.shape == (H,) and dbgu.shape == (2 * I,)
+
+
+def every_call(mx, T, H, I, seed):
+    """One pass through every operator: its outputs in a list."""
+    x, wgu, sgu, wd, sd, wi, bgu, bd, wo, gate = block_inputs(T, H, I, seed)
+
+    def run():
+        y = mx.mx_ffn_block(x, wgu, sgu, wd, sd, wi, bgu, bd, "gelu", wo, gate, 0.5)
+        h, z = mx.mx_gate_up(x, wgu, sgu, bgu, "silu", save_z=True)
+        l, lz = mx.mx_linear_fused(h, wd, sd, bd, x, 0.5, "gelu_tanh", save_z=True)
+        dh, dbd = mx.mx_linear_fused_backward(x, wd, sd, lz, 0.5, "gelu_tanh")
+        dx, dbgu = mx.mx_gate_up_backward(h, z, wgu, sgu)
+        n = mx.mx_norm_residual_backward(x, y, x, l, wo, gate, 0.5, wi)
+        return [y, h, z, l, lz, dh, dbd, dx, dbgu] + [v for v in n.values() if v is not None]
+
+    return run
+
+
+@pytest.mark.parametrize("T", [3, 45, 150])
+def test_graph_replays(mx, T):
+    """Captured and replayed several times, with eager work between: every replay's outputs."""
+    run = every_call(mx, T, 256, 96, T)
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    say("graph", T)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        outs = run()
+    for k in range(4):
+        for o in outs:
+            o.fill_(math.nan)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), k
+        for a, b in zip(run(), want):  # eager calls between the replays
+            assert torch.equal(a, b), k
+
+
+def test_two_graphs_replayed_at_once(mx):
+    """Each captured call owns its workspace: two graphs on two streams do not share one."""
+    runs = [every_call(mx, T, 256, 96, T) for T in (45, 46)]
+    wants = [[t.clone() for t in r()] for r in runs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for r in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(r())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    say("two graphs")
+    for _ in range(3):
+        for o in outs[0] + outs[1]:
+            o.fill_(math.nan)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, wants):
+            for a, b in zip(o, w):
+                assert torch.equal(a, b)
+
+
+def test_streams(mx):
+    """Calls on two streams at once, each waiting only for its own inputs."""
+    run = every_call(mx, 45, 256, 96, 4)
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    say("streams")
+    for s in streams:
+        with torch.cuda.stream(s):
+            got.append(run())
+    torch.cuda.synchronize()
+    for g in got:
+        for a, b in zip(g, want):
+            assert torch.equal(a, b)
+
+
+def test_caller_workspace(mx):
+    """A caller's workspace with any content, one byte short refused."""
+    T, K, N = 40, 2048, 64
+    x, w, s, bias, res = cuda(*linear_inputs(T, K, N, 2))
+    need = mx.raw().mx_linear_fused_workspace_size(T, K, N)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
+    say("workspace", need)
+    assert torch.equal(mx.mx_linear_fused(x, w, s, bias, ws=ws), mx.mx_linear_fused(x, w, s, bias))
+    with pytest.raises(mx.MxError):
+        mx.mx_linear_fused(x, w, s, bias, ws=ws[:-1])
+
+
+def test_refusals(mx):
+    x, w, s, bias, res = cuda(*linear_inputs(4, 64, 8, 2))
+    for bad in (dict(bias=bias[:4]), dict(residual=res.t()), dict(act="swish"), dict(out=res[:2]), dict(bias=bias.float()),
+                dict(scale=math.inf), dict(residual=res.cpu())):
+        with pytest.raises((ValueError, TypeError)):
+            mx.mx_linear_fused(x, w, s, **bad)
+    for a in ((x[:, :32], w, s), (x, w[:, :16], s), (x, w, s[:, :1]), (x, w[:4], s), (x[:0], w, s), (x[0], w, s)):
+        with pytest.raises((ValueError, TypeError)):
+            mx.mx_linear_fused(*a)
+    with pytest.raises(ValueError):
+        mx.mx_linear_fused_backward(res, w, s, act="silu")
+    with pytest.raises(ValueError):
+        mx.mx_linear_fused_backward(res, w, s, need_dx=False, need_dbias=False)
+    with pytest.raises(ValueError):
+        mx.mx_gate_up(x, w[:7], s[:7])
+    one = torch.ones(64, dtype=torch.bfloat16, device=DEV)
+    for bad in (dict(), dict(w_post=one), dict(w_pre=one, gate=one), dict(b=x, gate=one[:4]), dict(b=x, w_pre=one, eps=0.0),
+                dict(b=x[:2]), dict(w_pre=one[:8])):
+        with pytest.raises((ValueError, TypeError)):
+            mx.mx_norm_residual(x, **bad)
+    for bad in ((x, x, x), (x, None, None, None, one), (x, x, None, None, None, None, 1.0, one)):
+        with pytest.raises((ValueError, TypeError)):
+            mx.mx_norm_residual_backward(*bad)
