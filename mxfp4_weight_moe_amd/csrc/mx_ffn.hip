@@ -5,7 +5,7 @@
 // product, scale and residual are applied to the fp32 sums, and each output is rounded once.
 //
 // Two kernels, by the number of tokens:
-//   * up to STREAM_MAX_T a workgroup owns 16 weight rows (gate_up: 16 gate and the 16 up rows
+//   * up to STREAM_MAX_T (or less than one MX block per lane group, K < 128) a workgroup owns 16 weight rows (gate_up: 16 gate and the 16 up rows
 //     of the same columns), its waves split K, and every weight byte is read once: the time is
 //     the weight bytes' (stream_kernel);
 //   * beyond, tiles of tokens x rows (mx_tile.hpp), where the matrix instructions set the
@@ -39,7 +39,8 @@ __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restri
   __shared__ __attribute__((aligned(16))) uint8_t slabs[W][NS * SLAB_BYTES];
   __shared__ f32x4 red[(W > 1) ? W * NS * MT * 64 : 1];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int n0 = blockIdx.x * SUB_ROWS;
+  const int items = (rows + SUB_ROWS - 1) / SUB_ROWS;
+  const int n0 = blockIdx.x % items * SUB_ROWS, t0 = blockIdx.x / items * (MT * 16);
   StreamLanes<NS, MT> L;
   lanes_init_lds(L, lane);
   const size_t kb = (size_t)(K >> 1), ks = (size_t)(K >> 5);
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restri
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int t = mt * 16 + (lane & 15);
+    const int t = t0 + mt * 16 + (lane & 15);
     L.x[mt] = t < T ? x + (size_t)t * K + 32 * (lane >> 4) : nullptr;
   }
   const int nseg = K / SEG_K, nb_tail = (K % SEG_K) / 32;
@@ -78,96 +79,138 @@ __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restri
   if (wave != 0) return;
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    const int t = mt * 16 + (lane & 15);
+    const int t = t0 + mt * 16 + (lane & 15);
     if (t >= T) continue;
     float v[NS][4];
 #pragma unroll
     for (int i = 0; i < NS; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i][j] = acc[mt][i][j];
+    const int n = n0 + 4 * (lane >> 4);
+    const auto cols = epi.template columns<4>(n);
     if constexpr (GATED)
-      epi.template store<4>(t, n0 + 4 * (lane >> 4), v[0], v[1]);
+      epi.template store<4>(t, n, v[0], v[1], cols);
     else
-      epi.template store<4>(t, n0 + 4 * (lane >> 4), v[0]);
+      epi.template store<4>(t, n, v[0], cols, epi.template fetch<4>(t, n));
   }
 }
 
 // ------------------------------------------------------------------ many tokens: tiles
 
-// Columns per row of the fp32 parts of a split K: each half of gate_up, or all rows of a
-// linear layer, rounded up so that a lane's 8 or 16 consecutive values always fit.
-static inline int part_cols(int rows, bool gated) { return gated ? (rows + 7) / 8 * 8 : (rows + 15) / 16 * 16; }
+// Columns per row of the fp32 parts of a split K (each half of gate_up, or all rows of a
+// linear layer), rounded up so that a lane's 8 consecutive values always fit.
+__host__ __device__ static inline int part_cols(int rows) { return (rows + 7) / 8 * 8; }
 
 // rows: output columns (N, or I for gate_up).  nsplit > 1: part z of K goes to parts[z] as
-// fp32 [T][part columns (x 2)].
-template <int MT, int WM, int WN, bool GATED>
-__global__ void __launch_bounds__(WM * WN * 64, 2)
+// fp32 [T][part columns (x 2)].  A wave's NT MFMA tiles are 32 consecutive weight rows each;
+// for gate_up the first half of them gate rows, the second half the up rows of the same columns.
+template <int MT, int NT, int WM, int WN, bool GATED>
+__global__ void __launch_bounds__(WM * WN * 64, MT == 4 ? 1 : 2)
     forward_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                    typename EpilogueOf<GATED>::type epi, float* __restrict__ parts, int T, int K, int rows, int mtiles,
                    int ntiles, int nsplit) {
-  constexpr int BM = WM * MT * 16, COLS = GATED ? WN * 32 : WN * 64;
-  typedef RowStage<BM, FWD_KB, WM * WN> XStage;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * XStage::BYTES];
+  constexpr int BM = WM * MT * 32, WCOLS = NT * 32 / (GATED ? 2 : 1), HALF = GATED ? NT / 2 : NT;
+  typedef ForwardLds<MT, NT, WM, WN> L;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
   const int tile = xcd_tile(blockIdx.x, mtiles * ntiles * nsplit);
   const int split = tile % nsplit, nt = tile / nsplit % ntiles, mt0 = tile / nsplit / ntiles;
-  const int m0 = mt0 * BM, n0 = nt * COLS;
+  const int m0 = mt0 * BM, n0 = nt * (WN * WCOLS);
   const int stages = (K + FWD_KB - 1) / FWD_KB;
   const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
-  XStage xs;
+  typename L::Rows xs;
   xs.init(x, m0, T, K, wave, lane);
-  const int r = lane & 15, g = lane >> 4;
-  // weight row of MFMA row r of tile i, so that a lane's results are consecutive columns:
-  // linear 16 of them (16g + 4i + j), gate_up 8 gate (i = 0, 1) and 8 up (i = 2, 3)
-  const uint8_t* wrow[4];
-  const uint8_t* srow[4];
+  // Row r of MFMA tile i (of WN * NT), counted from the tile's first row (32-bit offsets) in
+  // the gate or the up half; past the last row the last one again.
+  auto row_of = [&](int lr) {
+    const int i = lr >> 5;
+    return min(i / NT * WCOLS + i % HALF * 32 + (lr & 31), rows - 1 - n0);
+  };
+  auto first_row = [&](int i) { return (size_t)n0 + (i % NT >= HALF ? (size_t)rows : 0); };
+  typename L::Codes cs;
+  cs.init(K, min(WN * WCOLS, rows - n0), wave, lane, [&](int i) { return w + first_row(i) * (size_t)(K >> 1); }, row_of);
+  const uint8_t* sbase[NT];
+  uint32_t soff[NT];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    int n = GATED ? n0 + wn * 32 + 8 * (r >> 2) + 4 * (i & 1) + (r & 3) : n0 + wn * 64 + 16 * (r >> 2) + 4 * i + (r & 3);
-    n = min(n, rows - 1);
-    const size_t row = (GATED && i >= 2) ? (size_t)rows + n : (size_t)n;
-    wrow[i] = w + row * (size_t)(K >> 1);
-    srow[i] = s + row * (size_t)(K >> 5);
+  for (int i = 0; i < NT; ++i) {
+    sbase[i] = s + first_row(i) * (size_t)(K >> 5);
+    soff[i] = (uint32_t)row_of((wn * NT + i) * 32 + (lane & 31)) * (uint32_t)(K >> 5);
   }
-  f32x4 acc[MT][4];
+  f32x16 acc[MT][NT];
   tile_zero(acc);
-  forward_tile<MT, WM, WN>(xs, wrow, srow, K, st0, st1, lds, wm, lane, acc);
-  const int pc = GATED ? (rows + 7) / 8 * 8 : (rows + 15) / 16 * 16;
+  forward_tile<MT, NT, WM, WN>(xs, cs, sbase, soff, K, st0, st1, lds, wm, wn, lane, acc);
+
+  const int pc = part_cols(rows);
+  // MB rows of MFMA tiles at a time through the LDS; then row by row, PIECES lanes a row with 8
+  // columns each, so a lane has the same columns in all its rows.  U rows of a lane go
+  // together, and what the next ones read (the residual) is fetched meanwhile.
+  constexpr int MB = MT < 2 ? 1 : 2;
+  static_assert(WM * WN * MB * NT * 4096 <= L::BYTES, "results of all waves in the stages' LDS");
+  uint8_t* mine = lds + wave * (MB * NT * 4096);
+  constexpr int PIECES = WCOLS / 8, ROWS = 64 / PIECES, ITERS = MB * 32 / ROWS, U = ITERS < 4 ? ITERS : 4;
+  const int p = lane % PIECES, n = n0 + wn * WCOLS + p * 8;
+  const int t0 = m0 + wm * MT * 32 + lane / PIECES;
+  const auto cols = epi.template columns<8>(n);
+  struct Ahead {
+    Piece<8> r[U];
+  };
+  auto fetch = [&](int it) {  // row t0 + it * ROWS and the U - 1 after it
+    Ahead f{};
+    if constexpr (!GATED) {
+      if (nsplit == 1)
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int t = m0 + wm * MT * 16 + m * 16 + r;
-    if (t >= T) continue;
-    if constexpr (GATED) {
-      const int n = n0 + wn * 32 + 8 * g;
-      if (nsplit > 1) {
-        if (n >= pc) continue;
-        float* p = parts + ((size_t)split * T + t) * (2 * (size_t)pc) + n;
-        *reinterpret_cast<f32x4*>(p) = acc[m][0];
-        *reinterpret_cast<f32x4*>(p + 4) = acc[m][1];
-        *reinterpret_cast<f32x4*>(p + pc) = acc[m][2];
-        *reinterpret_cast<f32x4*>(p + pc + 4) = acc[m][3];
-      } else {
-        float a[8], b[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          a[j] = acc[m][j >> 2][j & 3];
-          b[j] = acc[m][2 + (j >> 2)][j & 3];
+        for (int k = 0; k < U; ++k) {
+          const int t = t0 + (it + k) * ROWS;
+          if (t < T) f.r[k] = epi.template fetch<8>(t, n);
         }
-        epi.template store<8>(t, n, a, b);
-      }
-    } else {
-      const int n = n0 + wn * 64 + 16 * g;
-      if (nsplit > 1) {
-        if (n >= pc) continue;
-        float* p = parts + ((size_t)split * T + t) * (size_t)pc + n;
+    }
+    return f;
+  };
+  Ahead next = fetch(0);
+  __syncthreads();  // every wave has read its last fragments
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<f32x4*>(p + 4 * i) = acc[m][i];
-      } else {
-        float v[16];
+  for (int b = 0; b < MT / MB; ++b) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = acc[m][j >> 2][j & 3];
-        epi.template store<16>(t, n, v);
+    for (int m = 0; m < MB; ++m) tile_to_lds<NT>(mine + m * NT * 4096, acc[b * MB + m], lane);
+#pragma unroll 1
+    for (int it = 0; it < ITERS; it += U) {
+      const Ahead now = next;
+      if (b * ITERS + it + U < MT / MB * ITERS) next = fetch(b * ITERS + it + U);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int row = (it + k) * ROWS + lane / PIECES;
+        const int t = t0 + (b * ITERS + it + k) * ROWS;
+        if (t >= T || n >= rows) continue;
+        f32x4 q[GATED ? 4 : 2];
+        q[0] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 2 * p));
+        q[1] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 2 * p + 1));
+        if constexpr (GATED) {
+          q[2] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 4 * NT + 2 * p));
+          q[3] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 4 * NT + 2 * p + 1));
+        }
+        if (nsplit > 1) {
+          f32x4* o = reinterpret_cast<f32x4*>(parts + ((size_t)split * T + t) * ((GATED ? 2 : 1) * (size_t)pc) + n);
+          o[0] = q[0];
+          o[1] = q[1];
+          if constexpr (GATED) {
+            o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(o) + pc);
+            o[0] = q[2];
+            o[1] = q[3];
+          }
+        } else {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = q[j >> 2][j & 3];
+          if constexpr (GATED) {
+            float u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) u[j] = q[2 + (j >> 2)][j & 3];
+            epi.template store<8>(t, n, v, u, cols);
+          } else {
+            epi.template store<8>(t, n, v, cols, now.r[k]);
+          }
+        }
       }
     }
   }
@@ -196,10 +239,11 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
   float v[8], u[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = a[j >> 2][j & 3], u[j] = b[j >> 2][j & 3];
+  const auto cols = epi.template columns<8>(n);
   if constexpr (GATED)
-    epi.template store<8>(t, n, v, u);
+    epi.template store<8>(t, n, v, u, cols);
   else
-    epi.template store<8>(t, n, v);
+    epi.template store<8>(t, n, v, cols, epi.template fetch<8>(t, n));
 }
 
 // ------------------------------------------------------------------ launch plans
@@ -208,16 +252,16 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 // call needs does too.
 TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated) {
   TilePlan p{};
-  if (T <= STREAM_MAX_T) return p;
-  p.mt = T > 1024 ? 8 : T > 64 ? 4 : 2;
-  p.wn = p.mt == 8 ? 4 : 2;
-  const int bm = 32 * p.mt, cols = gated ? p.wn * 32 : p.wn * 64;
+  if (T <= STREAM_MAX_T || K < FWD_KB) return p;
+  p.mt = T > 1024 ? 4 : T > 64 ? 2 : 1;
+  p.nt = p.mt == 4 ? 4 : 2;
+  const int bm = 64 * p.mt, cols = (gated ? 32 : 64) * p.nt;
   p.mtiles = (int)((T + bm - 1) / bm);
   p.ntiles = (int)((rows + cols - 1) / cols);
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles, stages = (K + FWD_KB - 1) / FWD_KB;
   int64_t split = tiles >= GPU_CUS ? 1 : GPU_CUS / tiles;
   p.nsplit = (int)std::max<int64_t>(1, std::min(split, stages / 2));
-  if (p.nsplit > 1) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows, gated) * (gated ? 2 : 1) * 4;
+  if (p.nsplit > 1) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows) * (gated ? 2 : 1) * 4;
   return p;
 }
 
@@ -225,12 +269,12 @@ template <bool GATED>
 static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
                           const typename EpilogueOf<GATED>::type& epi, void* workspace, int T, int K, int rows,
                           hipStream_t stream) {
-  if (T <= STREAM_MAX_T) {
+  if (T <= STREAM_MAX_T || K < FWD_KB) {
     const int items = (rows + SUB_ROWS - 1) / SUB_ROWS, nseg = K / SEG_K;
     int W = 1;
     while (W < 8 && 2 * W <= nseg && items * W < 2048) W *= 2;
     if (T > 16 && GATED) W = std::min(W, 4);
-    const dim3 grid(items), block(W * 64);
+    const dim3 grid(items * ((T + STREAM_MAX_T - 1) / STREAM_MAX_T)), block(W * 64);
 #define MX_STREAM(WW, M, SB) \
   hipLaunchKernelGGL((stream_kernel<WW, M, GATED, SB>), grid, block, 0, stream, x, w, s, epi, T, K, rows)
 #define MX_STREAM_W(WW)         \
@@ -260,18 +304,18 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   const TilePlan p = forward_plan(T, K, rows, GATED);
   float* parts = static_cast<float*>(workspace);
   const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE(MT, WN)                                                                                           \
-  hipLaunchKernelGGL((forward_kernel<MT, 2, WN, GATED>), grid, dim3(2 * WN * 64), 0, stream, x, w, s, epi, parts, T, K, \
-                     rows, p.mtiles, p.ntiles, p.nsplit)
-  if (p.mt == 8)
-    MX_TILE(8, 4);
-  else if (p.mt == 4)
-    MX_TILE(4, 2);
-  else
+#define MX_TILE(MT, NT)                                                                                           \
+  hipLaunchKernelGGL((forward_kernel<MT, NT, 2, 2, GATED>), grid, dim3(256), 0, stream, x, w, s, epi, parts, T, K, rows, \
+                     p.mtiles, p.ntiles, p.nsplit)
+  if (p.mt == 4)
+    MX_TILE(4, 4);
+  else if (p.mt == 2)
     MX_TILE(2, 2);
+  else
+    MX_TILE(1, 2);
 #undef MX_TILE
   if (p.nsplit > 1) {
-    const int pc = part_cols(rows, GATED);
+    const int pc = part_cols(rows);
     const int64_t pieces = (int64_t)T * (pc / 8);
     hipLaunchKernelGGL((combine_kernel<GATED>), dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, stream, parts,
                        epi, T, pc, p.nsplit);

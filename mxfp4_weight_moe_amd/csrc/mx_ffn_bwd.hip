@@ -23,14 +23,11 @@ struct LinearSlope {
   __device__ __forceinline__ void dz(int64_t t, int n, float (&v)[8], bool wide, int left) const {
     load_bf16<8>(dy + (size_t)t * N + n, v, wide, left);
     if (z) {
-      float zv[8];
+      float zv[8], a[8], d[8];
       load_bf16<8>(z + (size_t)t * N + n, zv, wide, left);
+      act_values_slopes(act, zv, a, d);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float a, d;
-        act_value_slope(act, zv[i], a, d);
-        v[i] *= d;
-      }
+      for (int i = 0; i < 8; ++i) v[i] *= d[i];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= scale;
@@ -50,7 +47,7 @@ __global__ void __launch_bounds__(256) dz_kernel(Slope f, uint16_t* __restrict__
   const bool wide = n + 8 <= N && (N & 7) == 0;
   const int left = N - n;
   float sum[8] = {};
-  if (n < (dz ? ldz : N)) {
+  if (n < (dz ? ldz : N)) {  // columns N .. ldz read as 0
     for (int64_t t = t0 + ry; t < t1; t += 8) {
       float v[8];
       f.dz(t, n, v, wide, left);
@@ -89,15 +86,14 @@ __global__ void __launch_bounds__(256) dz_gated_kernel(const uint16_t* __restric
       load_bf16<8>(dh + (size_t)t * I + n, d, wide, left);
       load_bf16<8>(z + (size_t)t * 2 * I + n, g, wide, left);
       load_bf16<8>(z + (size_t)t * 2 * I + I + n, u, wide, left);
+      float a[8], slope[8];
+      act_values_slopes(act, g, a, slope);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float a, sl;
-        act_value_slope(act, g[i], a, sl);
-        const float du = d[i] * a;
-        g[i] = d[i] * u[i] * sl;
-        u[i] = du;
+        g[i] = d[i] * u[i] * slope[i];
+        u[i] = d[i] * a[i];
         sg[i] += g[i];
-        su[i] += du;
+        su[i] += u[i];
       }
       if (dz) {
         store_bf16<8>(dz + (size_t)t * ldz + n, g, wide, left);
@@ -158,42 +154,48 @@ int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float
 
 // ------------------------------------------------------------------ dx = alpha * dz W
 
-template <int MT, int WM, int WN>
-__global__ void __launch_bounds__(WM * WN * 64, 2)
+template <int MT, int NT>
+__global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
     backward_kernel(const uint16_t* __restrict__ dz, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                     uint16_t* __restrict__ dx, float* __restrict__ parts, float alpha, int T, int K, int N, int ldz,
                     int mtiles, int ntiles, int nsplit) {
-  constexpr int BM = WM * MT * 16, BN = WN * 64;
-  typedef RowStage<BM, BWD_KB, WM * WN> ZStage;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * (ZStage::BYTES + WeightStage<BN>::BYTES)];
+  constexpr int BM = 2 * MT * 32, BN = 2 * NT * 32;
+  typedef BackwardLds<MT, NT> L;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wm = wave / WN, wn = wave % WN;
+  const int wm = wave >> 1, wn = wave & 1;
   const int tile = xcd_tile(blockIdx.x, mtiles * ntiles * nsplit);
   const int split = tile % nsplit, nt = tile / nsplit % ntiles, mt0 = tile / nsplit / ntiles;
   const int m0 = mt0 * BM, k0 = nt * BN;
   const int stages = (N + BWD_KB - 1) / BWD_KB;
   const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
-  ZStage zs;
+  typename L::Rows zs;
   zs.init(dz, m0, T, ldz, wave, lane);
-  f32x4 acc[MT][4];
+  f32x16 acc[MT][NT];
   tile_zero(acc);
-  backward_tile<MT, WM, WN>(zs, w, s, N, K, k0, ldz, st0, st1, lds, wm, wn, lane, acc);
-  const int r = lane & 15, g = lane >> 4;
+  backward_tile<MT, NT>(zs, w, s, N, K, k0, st0, st1, lds, wm, wn, lane, acc);
+  const int r = lane & 31, g = lane >> 5;
+  constexpr int CPT = ColumnStage<NT>::CPT;
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    const int t = m0 + wm * MT * 16 + m * 16 + r;
-    const int k = k0 + wn * 64 + 16 * g;  // 16 consecutive columns: 4j + i of tile i, element j
-    if (t >= T || k >= K) continue;       // K is a multiple of 32
-    if (nsplit > 1) {
-      float* p = parts + ((size_t)split * T + t) * (size_t)K + k;
+    const int t = m0 + (wm * MT + m) * 32 + r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<f32x4*>(p + 4 * j) = f32x4{acc[m][0][j], acc[m][1][j], acc[m][2][j], acc[m][3][j]};
-    } else {
-      float v[16];
+    for (int j = 0; j < 8; ++j) {
+      // MFMA rows R = 8 (j >> 2) + 4 g + (j & 3) and R + 16 of all tiles: CPT columns
+      const int k = k0 + wn * (NT * 32) + CPT * (8 * (j >> 2) + 4 * g + (j & 3));
+      if (t >= T || k >= K) continue;  // K is a multiple of 32
+      float v[CPT];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) v[j] = alpha * acc[m][j & 3][j >> 2];
-      store_bf16<16>(dx + (size_t)t * K + k, v, true, 16);
+      for (int c = 0; c < CPT; ++c) v[c] = acc[m][c >> 1][j + 8 * (c & 1)];
+      if (nsplit > 1) {
+        float* p = parts + ((size_t)split * T + t) * (size_t)K + k;
+#pragma unroll
+        for (int c = 0; c < CPT; c += 4) *reinterpret_cast<f32x4*>(p + c) = f32x4{v[c], v[c + 1], v[c + 2], v[c + 3]};
+      } else {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) v[c] *= alpha;
+        store_bf16<CPT>(dx + (size_t)t * K + k, v, true, CPT);
+      }
     }
   }
 }
@@ -218,9 +220,9 @@ __global__ void __launch_bounds__(256) dx_combine_kernel(const float* __restrict
 
 TilePlan backward_plan(int64_t T, int64_t K, int64_t N) {
   TilePlan p{};
-  p.mt = T > 1024 ? 8 : T > 64 ? 4 : 2;
-  p.wn = p.mt == 8 ? 4 : 2;
-  const int bm = 32 * p.mt, bn = p.wn * 64;
+  p.mt = T > 1024 ? 4 : T > 64 ? 2 : 1;
+  p.nt = p.mt == 4 ? 4 : 2;
+  const int bm = 64 * p.mt, bn = 64 * p.nt;
   p.mtiles = (int)((T + bm - 1) / bm);
   p.ntiles = (int)((K + bn - 1) / bn);
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles, stages = (N + BWD_KB - 1) / BWD_KB;
@@ -241,7 +243,7 @@ int dz_strip_rows(int64_t T, int64_t cols) {
 
 BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, bool need_dz, bool dx, bool dbias) {
   BackwardPlan b{};
-  b.ldz = (int)((N + 7) / 8 * 8);
+  b.ldz = (int)((N + BWD_KB - 1) / BWD_KB * BWD_KB);  // whole stages, zeros past N
   b.strip_rows = dz_strip_rows(T, cols);
   b.strips = (int)((T + b.strip_rows - 1) / b.strip_rows);
   size_t off = 0;
@@ -263,15 +265,15 @@ BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, b
 static int launch_dx(const uint16_t* dz, int ldz, const uint8_t* w, const uint8_t* s, uint16_t* dx, float alpha,
                      const TilePlan& p, float* parts, int T, int K, int N, hipStream_t stream) {
   const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE(MT, WN)                                                                                            \
-  hipLaunchKernelGGL((backward_kernel<MT, 2, WN>), grid, dim3(2 * WN * 64), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, \
-                     ldz, p.mtiles, p.ntiles, p.nsplit)
-  if (p.mt == 8)
-    MX_TILE(8, 4);
-  else if (p.mt == 4)
-    MX_TILE(4, 2);
-  else
+#define MX_TILE(MT, NT)                                                                                              \
+  hipLaunchKernelGGL((backward_kernel<MT, NT>), grid, dim3(256), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, ldz, \
+                     p.mtiles, p.ntiles, p.nsplit)
+  if (p.mt == 4)
+    MX_TILE(4, 4);
+  else if (p.mt == 2)
     MX_TILE(2, 2);
+  else
+    MX_TILE(1, 2);
 #undef MX_TILE
   if (p.nsplit > 1) {
     const int64_t pieces = (int64_t)T * (K / 8);
@@ -284,13 +286,13 @@ static int launch_dx(const uint16_t* dz, int ldz, const uint8_t* w, const uint8_
 int launch_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const uint8_t* w, const uint8_t* s, float scale,
                                  int act, uint16_t* dx, float* dbias, int T, int K, int N, void* workspace,
                                  hipStream_t stream) {
-  const bool direct = !z && (N & 7) == 0;  // dz = scale * dy: the product reads dy itself
+  const bool direct = !z && N % BWD_KB == 0;  // dz = scale * dy: the product reads dy itself
   const BackwardPlan b = backward_workspace(T, K, N, N, !direct, dx != nullptr, dbias != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* dz = (dx && !direct) ? reinterpret_cast<uint16_t*>(ws + b.dz) : nullptr;
   float* bp = dbias ? reinterpret_cast<float*>(ws + b.bias_parts) : nullptr;
   if (dz || bp) {
-    const dim3 grid((N + DZ_COLS - 1) / DZ_COLS, b.strips);
+    const dim3 grid((b.ldz + DZ_COLS - 1) / DZ_COLS, b.strips);
     hipLaunchKernelGGL((dz_kernel<LinearSlope>), grid, dim3(256), 0, stream, LinearSlope{dy, z, N, act, scale}, dz,
                        b.ldz, bp, (int64_t)T, b.strip_rows);
     if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;

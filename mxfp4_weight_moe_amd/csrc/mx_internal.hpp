@@ -143,10 +143,10 @@ int launch_moe_fused(const uint16_t* x, const float* logits, const uint8_t* wgu,
 
 constexpr int GPU_CUS = 256;  // gfx950; launch plans use it, so that workspaces depend on sizes alone
 
-// A tiled product: the workgroup tile (2 waves of mt MFMA tiles by wn waves of 64 columns),
-// the tiles, and over how many workgroups the reduction is split (bytes: their fp32 parts).
+// A tiled product: the MFMA tiles of each of a workgroup's 2 x 2 waves (mt x nt of 32 x 32), the
+// workgroup tiles, and over how many workgroups the reduction is split (bytes: their fp32 parts).
 struct TilePlan {
-  int mt, wn, mtiles, ntiles, nsplit;
+  int mt, nt, mtiles, ntiles, nsplit;
   size_t bytes;
 };
 TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated);

@@ -1,25 +1,40 @@
 // Tiled products of bf16 rows with MXFP4 weights for more tokens than one weight-streaming
 // pass covers: the shared pieces of the forward (x W^T) and the backward (dz W) kernels.
 //
-// A workgroup of WM x WN waves owns a tile of WM*MT*16 tokens by WN*64 weight rows (forward)
-// or columns (backward).  Each wave holds MT x 4 MFMA tiles (16x16x32 bf16) in registers.
+// A workgroup of WM x WN waves owns a tile of WM*MT*32 tokens by WN*NT*32 weight rows (forward)
+// or columns (backward).  Each wave holds MT x NT MFMA tiles (32x32x16 bf16) in registers: a
+// wave issues an instruction about every 8 cycles, and a 32x32x16 product takes 32, which
+// leaves room for three others beside it (16x16x32: 16 cycles, room for one; with it the same
+// tile of 128 x 128 a wave ran at 47% of the matrix rate instead).
 // The activation tile goes from global memory to LDS without passing through registers
-// (global_load_lds, 16 bytes a lane) into the buffer that the waves are not reading, one
+// (buffer loads to LDS, 16 bytes a lane) into the buffer that the waves are not reading, one
 // barrier a stage.  The weights stay 4-bit until they are in the registers of the wave that
-// multiplies with them: a wave decodes 4 fragments (16 conversions) for 4*MT matrix
-// instructions, so decoding costs a quarter of the issue slots at MT = 4 and an eighth at 8.
+// multiplies with them: 4 conversions decode a fragment that MT matrix instructions use.
+//
+// 16-byte LDS reads go 16 lanes at a time over 64 banks, in the lane groups 0-3, 12-15, 20-23,
+// 24-27 and 4-7, 8-11, 16-19, 28-31 (and the same 32 lanes on); the layouts below give the 16
+// lanes of a group 16 different 16-byte columns.
 #pragma once
+#include <utility>
+
 #include "mx_device.hpp"
 #include "mx_internal.hpp"
 
 namespace mx {
 
-typedef __attribute__((address_space(1))) const void* global_cptr;
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// 16 bytes a lane from global memory to LDS: lane l's bytes land at `lds` + 16 * l.
-__device__ __forceinline__ void copy16_to_lds(const void* g, void* lds) {
-  __builtin_amdgcn_global_load_lds((global_cptr)g, (lds_ptr)lds, 16, 0, 0);
+// A buffer of up to 4 GB from a uniform address: its loads take a 32-bit offset per lane and a
+// uniform one, no address arithmetic per lane; what lies past its end reads as zero.
+typedef __amdgpu_buffer_rsrc_t buffer;
+__device__ __forceinline__ buffer make_buffer(const void* base, uint64_t bytes) {
+  const uint32_t n = bytes < 0xFFFFFFFFull ? (uint32_t)bytes : 0xFFFFFFFFu;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);  // 32-bit data, no stride
+}
+// 16 bytes a lane from memory to LDS: lane l's bytes land at `lds` + 16 * l.
+__device__ __forceinline__ void copy16_to_lds(buffer b, uint32_t lane_offset, uint32_t offset, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 16, lane_offset, offset, 0, 0);
 }
 
 // This wave's copies to LDS have landed (they count as vector memory operations, which a
@@ -34,12 +49,38 @@ __device__ __forceinline__ int xcd_tile(int b, int total) {
   return x * q + min(x, r) + i;
 }
 
+// A value that the compiler must compute where it stands instead of keeping it in a register
+// across the main loop.
+__device__ __forceinline__ uint32_t here(uint32_t v) {
+  asm volatile("" : "+v"(v));
+  return v;
+}
+
+// No instruction moves across: the compiler otherwise puts the reads of the next step right
+// before their use, to save registers.
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0); }
+
+// f(integral_constant<int, 0>), f(integral_constant<int, 1>), ... f(N - 1): a loop whose
+// every iteration is its own code, however long (the compiler gives up unrolling a long one,
+// and arrays indexed by its counter then leave the registers).
+template <class F, int... I>
+__device__ __forceinline__ void unrolled(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+  unrolled(f, std::make_integer_sequence<int, N>{});
+}
+
 // ------------------------------------------------------------------ activation stages
 
-// A stage is KB reduction values of BM rows: rows of KB * 2 bytes in 16-byte chunks, chunk c
-// of row r stored at chunk position c ^ (r & (C - 1) & 15), so that 16 rows' reads of one
-// logical chunk spread over all banks.  The copy to LDS writes 1 KB a wave at consecutive
-// addresses; the permutation is in which chunk of its row each lane fetches.
+// A stage is KB reduction values of BM rows: rows of KB * 2 bytes in C = KB / 8 chunks of 16
+// bytes, chunk c of row r at position c ^ row_key<C>(r).  The copy to LDS writes 1 KB a wave at
+// consecutive addresses; the permutation is in which chunk of its row each lane fetches.
+template <int C>
+__device__ __forceinline__ int row_key(int r) {
+  return C == 16 ? r & 15 : (r >> 1) & 7;  // rows of 256 bytes; of 128 (two to a line of banks)
+}
 template <int BM, int KB, int NW>
 struct RowStage {
   static constexpr int C = KB / 8;                 // chunks per row
@@ -48,216 +89,472 @@ struct RowStage {
   static constexpr int COPIES = BM / ROWS_PER_COPY / NW;  // wave-wide copies per wave
   static_assert(BM % (ROWS_PER_COPY * NW) == 0, "whole copies");
 
-  uint32_t off[COPIES];  // byte offset of this lane's chunk from the tile's first row, stage 0
-  const uint8_t* base;
-  int wave, lane;
+  const uint8_t* base;   // the tile's first row
+  buffer buf_;           // the tile's rows
+  uint32_t off[COPIES];  // byte offset of this lane's chunk in each copy
+  int chunk, wave, lane;
+  static_assert(NW * ROWS_PER_COPY % 16 == 0, "a lane's chunk is the same in all its copies");
 
   // Rows past `rows` fetch the last row again; their results are never stored.
   __device__ __forceinline__ void init(const uint16_t* x, int m0, int rows, int64_t ld, int wave_, int lane_) {
     wave = wave_, lane = lane_;
     base = reinterpret_cast<const uint8_t*>(x + (size_t)m0 * ld);
+    buf_ = make_buffer(base, (uint64_t)min(BM, rows - m0) * (uint64_t)(ld * 2));
+    const int r = wave * ROWS_PER_COPY + lane / C;
+    chunk = (lane % C) ^ row_key<C>(r);
 #pragma unroll
-    for (int q = 0; q < COPIES; ++q) {
-      const int r = (q * NW + wave) * ROWS_PER_COPY + lane / C;
-      const int c = (lane % C) ^ (r & (C - 1));
-      off[q] = (uint32_t)min(r, rows - 1 - m0) * (uint32_t)(ld * 2) + c * 16;
-    }
+    for (int q = 0; q < COPIES; ++q)
+      off[q] = (uint32_t)min(r + q * (NW * ROWS_PER_COPY), rows - 1 - m0) * (uint32_t)(ld * 2) + chunk * 16;
+  }
+  // copy q of COPIES of this wave
+  __device__ __forceinline__ void copy_one(uint8_t* buf, int stage, int q) const {
+    copy16_to_lds(buf_, off[q], (uint32_t)stage * (KB * 2), buf + (q * NW + wave) * 1024);
   }
   __device__ __forceinline__ void copy(uint8_t* buf, int stage) const {
-    const uint8_t* p = base + (size_t)stage * (KB * 2);
 #pragma unroll
-    for (int q = 0; q < COPIES; ++q) copy16_to_lds(p + off[q], buf + (q * NW + wave) * 1024);
+    for (int q = 0; q < COPIES; ++q) copy_one(buf, stage, q);
   }
   // The last, partial stage: `valid` (< KB, a multiple of 8) values of each row, zeros beyond.
   __device__ __forceinline__ void copy_tail(uint8_t* buf, int stage, int valid) const {
     const uint8_t* p = base + (size_t)stage * (KB * 2);
 #pragma unroll
     for (int q = 0; q < COPIES; ++q) {
-      const int r = (q * NW + wave) * ROWS_PER_COPY + lane / C;
-      const int c = (lane % C) ^ (r & (C - 1));
-      const u32x4 v = c * 8 < valid ? ld16(p + off[q]) : u32x4{0u, 0u, 0u, 0u};
+      const u32x4 v = chunk * 8 < valid ? ld16(p + here(off[q])) : u32x4{0u, 0u, 0u, 0u};
       *reinterpret_cast<u32x4*>(buf + (q * NW + wave) * 1024 + lane * 16) = v;
     }
   }
 };
 
-template <int MT>
-__device__ __forceinline__ void tile_zero(f32x4 (&acc)[MT][4]) {
+template <int MT, int NT>
+__device__ __forceinline__ void tile_zero(f32x16 (&acc)[MT][NT]) {
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[m][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) acc[m][i][j] = 0.f;
+}
+
+// ------------------------------------------------------------------ matrix instructions
+
+// acc += a x b in place: lane (r = lane & 31, g = lane >> 5) gives values 8g .. 8g + 7 of row r
+// of a and of column r of b, and holds rows 8 (j >> 2) + 4 g + (j & 3) of column r of acc.
+// The compiler's own choice of registers for accumulators that fill all 256 accumulation
+// registers moves them about between matrix instructions (as many moves as products); tied
+// operands cannot move.  See settle_mfma and operands_ready.
+__device__ __forceinline__ void mfma_in_place(f32x16& acc, u32x4 a, u32x4 b) {
+  asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
+}
+// The compiler does not see that the instructions above multiply, so it keeps none of their
+// distances.  Before their accumulators are written or read otherwise, this waits out the
+// longest of them (18 wait states).
+__device__ __forceinline__ void settle_mfma() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+// Two wait states between a vector instruction that writes an operand and the product.
+__device__ __forceinline__ void operands_ready() { asm volatile("s_nop 1"); }
+
+// Value pair Q of 8 codes.
+template <int Q>
+__device__ __forceinline__ uint32_t decode2(uint32_t codes, float scale) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, Q));
 }
 
 // ------------------------------------------------------------------ forward: x W^T
 
-constexpr int FWD_KB = 128;  // reduction values per stage: one MX block per MFMA lane group
+constexpr int FWD_KB = 128;  // reduction values per stage: 4 MX blocks, two per MFMA lane group
 
-// acc[m][i] += W rows (as the MFMA's rows) x activation rows (its columns) over the stages
-// [st0, st1) of K.  Lane (r = lane & 15, g = lane >> 4) holds MX block g of the stage of
-// weight row wrow[i], 16 code bytes and a scale byte; MFMA step c takes values 8c .. 8c + 7 of
-// every lane's block, and the activations are read in the same order.
-template <int MT, int WM, int WN>
-__device__ __forceinline__ void forward_tile(const RowStage<WM * MT * 16, FWD_KB, WM * WN>& rows,
-                                             const uint8_t* const (&wrow)[4], const uint8_t* const (&srow)[4], int K,
-                                             int st0, int st1, uint8_t* lds, int wm, int lane, f32x4 (&acc)[MT][4]) {
-  using Stage = RowStage<WM * MT * 16, FWD_KB, WM * WN>;
-  const int r = lane & 15, g = lane >> 4, blocks = K >> 5;
-  u32x4 codes[4];
-  uint32_t sb[4];
-  // blocks past K read as zero codes with scale 1
-  auto load_w = [&](int st) {
-    const int b = st * 4 + g;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool ok = b < blocks;
-      codes[i] = ok ? ld16(wrow[i] + (size_t)b * 16) : u32x4{0u, 0u, 0u, 0u};
-      sb[i] = ok ? srow[i][b] : 127u;
-    }
-  };
-  auto load_x = [&](int st, uint8_t* buf) {
-    const int valid = K - st * FWD_KB;
-    if (valid >= FWD_KB)
-      rows.copy(buf, st);
-    else
-      rows.copy_tail(buf, st, valid);
-  };
-  uint32_t at[4];  // LDS byte offset of this lane's activation chunk at step c, first MFMA tile
-#pragma unroll
-  for (int c = 0; c < 4; ++c) at[c] = (uint32_t)(wm * MT * 16 + r) * 256 + (((4 * g + c) ^ r) << 4);
+// The weight codes of a stage: BN rows of 64 bytes (4 MX blocks); LDS row 32 i + r is MFMA row
+// r of the workgroup's MFMA tile i.  Block b of row r sits at chunk b ^ (r >> 3).
+template <int BN, int NW>
+struct CodeStage {
+  static constexpr int BYTES = BN * 64;
+  static constexpr int COPIES = BN / 16 / NW;  // wave-wide copies of 16 rows per wave
+  static_assert(BN % (16 * NW) == 0, "whole copies");
+  const uint8_t* base[COPIES];  // the first weight row of the copy's half (the same in a wave)
+  buffer buf_[COPIES];          // that half's rows of the tile
+  uint32_t off[COPIES];         // this lane's chunk from there, stage 0
+  int wave, lane;
 
-  load_x(st0, lds);
-  load_w(st0);
-  for (int st = st0; st < st1; ++st) {
-    uint8_t* cur = lds + ((st - st0) & 1) * Stage::BYTES;
-    uint8_t* nxt = lds + ((st - st0 + 1) & 1) * Stage::BYTES;
-    u32x4 wc[4];
-    float sc[4];
+  // which of a stage's 4 blocks the lane copies
+  __device__ __forceinline__ int block(int q) const {
+    return (lane & 3) ^ ((((q * NW + wave) * 16 + (lane >> 2)) >> 3) & 3);
+  }
+  // half_of(MFMA tile) = first row of that tile's half, of which the tile has tile_rows;
+  // row_of(LDS row) = row within it
+  template <class F, class G>
+  __device__ __forceinline__ void init(int K, int tile_rows, int wave_, int lane_, F half_of, G row_of) {
+    wave = wave_, lane = lane_;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      wc[i] = codes[i];
-      sc[i] = e8m0_scale_operand(sb[i]);
-    }
-    wait_copies();
-    __syncthreads();  // this stage is in LDS, and nobody reads the other buffer any more
-    if (st + 1 < st1) {
-      load_x(st + 1, nxt);
-      load_w(st + 1);
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      bf16x8 w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = decode8(wc[i][c], sc[i]);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const bf16x8 a = as_bf16x8(ld16(cur + at[c] + m * 4096));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(w[i], a, acc[m][i]);
-      }
+    for (int q = 0; q < COPIES; ++q) {
+      base[q] = half_of((q * NW + wave) >> 1);
+      buf_[q] = make_buffer(base[q], (uint64_t)tile_rows * (uint64_t)(K >> 1));
+      off[q] = (uint32_t)row_of((q * NW + wave) * 16 + (lane >> 2)) * (uint32_t)(K >> 1) + block(q) * 16;
     }
   }
+  __device__ __forceinline__ void copy_one(uint8_t* buf, int stage, int q) const {
+    copy16_to_lds(buf_[q], off[q], (uint32_t)stage * 64, buf + (q * NW + wave) * 1024);
+  }
+  __device__ __forceinline__ void copy(uint8_t* buf, int stage) const {
+#pragma unroll
+    for (int q = 0; q < COPIES; ++q) copy_one(buf, stage, q);
+  }
+  // The last, partial stage: `valid` (< 4) blocks of each row, zero codes beyond.
+  __device__ __forceinline__ void copy_tail(uint8_t* buf, int stage, int valid) const {
+#pragma unroll
+    for (int q = 0; q < COPIES; ++q) {
+      const u32x4 v = block(q) < valid ? ld16(base[q] + (size_t)stage * 64 + here(off[q])) : u32x4{0u, 0u, 0u, 0u};
+      *reinterpret_cast<u32x4*>(buf + (q * NW + wave) * 1024 + lane * 16) = v;
+    }
+  }
+};
+
+template <int MT, int NT, int WM, int WN>
+struct ForwardLds {
+  typedef RowStage<WM * MT * 32, FWD_KB, WM * WN> Rows;
+  typedef CodeStage<WN * NT * 32, WM * WN> Codes;
+  static constexpr int ONE = Rows::BYTES + Codes::BYTES;
+  static constexpr int BYTES = 2 * ONE;
+};
+
+// acc[m][i] += W rows (as the MFMA's rows) x activation rows (its columns) over the stages
+// [st0, st1) of K (K >= FWD_KB).  Lane (r = lane & 31, g = lane >> 5) holds MX blocks g and
+// g + 2 of the stage of MFMA row r of tile i, 16 code bytes and a scale byte each.  A stage is
+// 8 steps; step u multiplies values 8 (u & 3) .. + 7 of every lane's block g + 2 (u >> 2), and
+// the activations are read in the same order.
+//
+// Between the matrix instructions of a step, in slots that they leave free, the wave reads the
+// activation fragments and decodes the weights of the next step and, early in the stage,
+// copies the next stage to LDS.  The stage's only barrier stands before its last step, whose
+// operands are already in registers.
+template <int MT, int NT, int WM, int WN>
+__device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, WM, WN>::Rows& rows,
+                                             const typename ForwardLds<MT, NT, WM, WN>::Codes& codes,
+                                             const uint8_t* const (&sbase)[NT], const uint32_t (&soff)[NT], int K,
+                                             int st0, int st1, uint8_t* lds, int wm, int wn, int lane,
+                                             f32x16 (&acc)[MT][NT]) {
+  typedef ForwardLds<MT, NT, WM, WN> L;
+  constexpr int STEPS = 8, SLOTS = MT * NT;
+  constexpr int XC = L::Rows::COPIES, COPIES = XC + L::Codes::COPIES;
+  constexpr int COPY_SLOTS = (STEPS - 3) * SLOTS / COPIES < 3 ? (STEPS - 3) * SLOTS / COPIES : 3;
+  constexpr int COPIES_AT_ONCE = COPY_SLOTS ? 1 : (COPIES + (STEPS - 3) * SLOTS - 1) / ((STEPS - 3) * SLOTS);
+  constexpr int COPY_EVERY = COPY_SLOTS ? COPY_SLOTS : 1;
+  const int r = lane & 31, g = lane >> 5, blocks = K >> 5;
+  const int full = K / FWD_KB;  // stages of FWD_KB values
+  const uint32_t xrow = (uint32_t)(wm * MT * 32 + r) * 256;
+  const uint32_t wrow = L::Rows::BYTES + (uint32_t)(wn * NT * 32 + r) * 64;
+  uint32_t at[8];  // LDS byte offset of this lane's activation chunk at step u, first tile
+#pragma unroll
+  for (int u = 0; u < 8; ++u) at[u] = xrow + (((8 * (u >> 2) + 4 * g + (u & 3)) ^ (r & 15)) << 4);
+  uint32_t wat[2];  // and of its blocks
+#pragma unroll
+  for (int b = 0; b < 2; ++b) wat[b] = wrow + (((2 * b + g) ^ (r >> 3)) << 4);
+  u32x4 wc[2][NT], frag[2][MT], w[2][NT];
+  uint32_t sb[2][NT];
+  float sc[2][NT];
+  auto load_tail = [&](uint8_t* buf) {
+    rows.copy_tail(buf, full, K - full * FWD_KB);
+    codes.copy_tail(buf + L::Rows::BYTES, full, blocks & 3);
+  };
+  // blocks past K have zero codes; their scale is 1
+  auto load_scales = [&](int st) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int k = st * 4 + 2 * b + g;
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint32_t v = sbase[i][soff[i] + min(k, blocks - 1)];
+        sb[b][i] = k < blocks ? v : 127u;
+      }
+    }
+  };
+  auto use_scales = [&]() {
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) sc[b][i] = e8m0_scale_operand(sb[b][i]);
+  };
+  uint8_t* cur = lds;
+  uint8_t* nxt = lds + L::ONE;
+  if (st0 < full) {
+    rows.copy(cur, st0);
+    codes.copy(cur + L::Rows::BYTES, st0);
+  } else {
+    load_tail(cur);
+  }
+  load_scales(st0);
+  wait_copies();
+  __syncthreads();
+  use_scales();
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+#pragma unroll
+    for (int b = 0; b < 2; ++b) wc[b][i] = ld16(cur + wat[b] + i * 2048);
+    w[0][i] = __builtin_bit_cast(u32x4, decode8(wc[0][i][0], sc[0][i]));
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) frag[0][m] = ld16(cur + at[0] + m * 8192);
+  settle_mfma();  // the accumulators have been cleared
+  for (int st = st0; st < st1; ++st) {
+    // The stage that is copied meanwhile.  Past the last full one its copy repeats that one:
+    // the partial stage is written over it, and after the last stage nothing reads it.
+    const int cs = min(st + 1, full - 1);
+    unrolled<STEPS>([&](auto U) __attribute__((always_inline)) {
+      constexpr int u = U, next = (u + 1) % STEPS;
+      constexpr bool last = u == STEPS - 1;
+      if constexpr (last) {
+        wait_copies();  // the next stage has landed
+        if (st + 1 == full && st + 1 < st1) load_tail(nxt);
+        __syncthreads();  // for every wave, and no wave reads `cur` any more
+        use_scales();
+      }
+      // The slots' reads and conversions; in the last step the reads, which the conversions
+      // wait for, fill the first half.
+      constexpr int reads = MT + (last ? 2 * NT : 0), converts = 4 * NT;
+      constexpr int first = last ? SLOTS / 2 : 0;  // slot of the first conversion
+      constexpr int per_read = (reads + (last ? (SLOTS + 1) / 2 : SLOTS) - 1) / (last ? (SLOTS + 1) / 2 : SLOTS);
+      constexpr int per_convert = (converts + SLOTS - first - 1) / (SLOTS - first);
+      operands_ready();
+      unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
+        constexpr int k = S, m = k / NT, i = k % NT;
+        mfma_in_place(acc[m][i], w[u & 1][i], frag[u & 1][m]);
+        unrolled<per_read>([&](auto E) __attribute__((always_inline)) {
+          constexpr int e = k * per_read + E, codes_first = last ? 2 * NT : 0;
+          if constexpr (e < codes_first)
+            wc[e / NT][e % NT] = ld16(nxt + wat[e / NT] + (e % NT) * 2048);
+          else if constexpr (e < reads)
+            frag[next & 1][e - codes_first] = ld16((last ? nxt : cur) + at[next] + (e - codes_first) * 8192);
+        });
+        unrolled<per_convert>([&](auto E) __attribute__((always_inline)) {
+          constexpr int e = (k - first) * per_convert + E;
+          if constexpr (e >= 0 && e < converts) {
+            constexpr int j = e / 4, q = e & 3;
+            w[next & 1][j][q] = decode2<q>(wc[next >> 2][j][next & 3], sc[next >> 2][j]);
+          }
+        });
+        // copies, one every few slots from the stage's first on; then the next stage's scales
+        constexpr int n = u * SLOTS + k;
+        if constexpr (n % COPY_EVERY == COPY_EVERY - 1)
+          unrolled<COPIES_AT_ONCE>([&](auto E) __attribute__((always_inline)) {
+            constexpr int q = n / COPY_EVERY * COPIES_AT_ONCE + E;
+            if constexpr (q < XC)
+              rows.copy_one(nxt, cs, q);
+            else if constexpr (q < COPIES)
+              codes.copy_one(nxt + L::Rows::BYTES, cs, q - XC);
+          });
+        if constexpr (n == COPY_EVERY * ((COPIES + COPIES_AT_ONCE - 1) / COPIES_AT_ONCE))
+          load_scales(min(st + 1, st1 - 1));
+        keep_order();
+      });
+    });
+    uint8_t* t = cur;
+    cur = nxt;
+    nxt = t;
+  }
+  settle_mfma();
+}
+
+// A wave's results, one row of MFMA tiles (32 tokens) at a time, through its own part of the
+// LDS (free after the main loop and a barrier): rows of NT * 32 floats, 4 to a chunk.  The
+// epilogue then reads them back by rows, so that its accesses to memory are whole lines.
+template <int NT>
+__device__ __forceinline__ uint32_t out_at(int row, int chunk) {
+  return (uint32_t)row * (NT * 128) + ((chunk ^ (row & 15)) << 4);
+}
+// Writes tile row m of acc there.
+template <int NT>
+__device__ __forceinline__ void tile_to_lds(uint8_t* mine, const f32x16 (&acc)[NT], int lane) {
+  const int r = lane & 31, g = lane >> 5;
+#pragma unroll
+  for (int i = 0; i < NT; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<f32x4*>(mine + out_at<NT>(r, 8 * i + 2 * j + g)) =
+          f32x4{acc[i][4 * j], acc[i][4 * j + 1], acc[i][4 * j + 2], acc[i][4 * j + 3]};
 }
 
 // ------------------------------------------------------------------ backward: dz W
 
 constexpr int BWD_KB = 64;  // reduction values (weight rows) per stage
 
-// The weight side of a stage: 64 weight rows n of BN columns.  MFMA lane (r, g) takes columns
-// 4r .. 4r + 3 of its wave's 64 (one for each of the 4 tiles) and the 8 rows of octet g, which
-// it finds as 16 consecutive bytes: the 2-byte code quads of 8 rows, gathered by the threads
-// that load them.  Scales are kept as fp32 per (block of 32 columns, row).
-template <int BN>
-struct WeightStage {
-  static constexpr int QUADS = BN / 4;
-  static constexpr int CODE_BYTES = BWD_KB * BN / 2;
-  static constexpr int BLOCKS = BN / 32;
-  static constexpr int SCALE_LD = BWD_KB + 16;
-  static constexpr int BYTES = CODE_BYTES + BLOCKS * SCALE_LD * 4;
+// Here the reduction runs over weight rows, across the packing and the scales (a block of 32
+// shares one along the columns).  A thread takes CPT columns (CPT / 2 bytes) of 8 consecutive
+// weight rows, an octet, of the stage, decodes each row's pairs with that row's scale and
+// exchanges halves between two rows, and writes each column's 8 bf16 values as one 16-byte
+// chunk, so that every weight is decoded once a workgroup and the LDS holds both operands in
+// the same form: rows of 64 reduction values.  (Decoding in the registers of each wave that
+// multiplies takes twice the conversions and as many LDS reads: 64 x 256 weights a stage.)
+// Column CPT (R & 15) + 2 i + (R >> 4) of a wave's is MFMA row R of its tile i: the threads'
+// writes then go to consecutive LDS rows, and a lane's results are CPT consecutive columns.
+template <int NT>
+struct ColumnStage {
+  static constexpr int CPT = 2 * NT;              // columns of a thread: WN * NT * 32 over 32 threads
+  static constexpr int BYTES = 2 * NT * 32 * 128;  // two wave columns
 };
 
-template <int MT, int WM, int WN>
-__device__ __forceinline__ void backward_tile(const RowStage<WM * MT * 16, BWD_KB, WM * WN>& rows,
+template <int MT, int NT>
+struct BackwardLds {
+  typedef RowStage<2 * MT * 32, BWD_KB, 4> Rows;
+  static constexpr int ONE = Rows::BYTES + ColumnStage<NT>::BYTES;
+  static constexpr int BYTES = 2 * ONE;
+};
+
+// acc[m][i] += W columns (as the MFMA's rows) x dz rows (its columns) over the stages
+// [st0, st1) of weight rows, for a workgroup of 2 x 2 waves.  dz has a multiple of 64 columns,
+// those past N zero.  As in forward_tile, what prepares the next step and the next stage goes
+// between the matrix instructions: reads of both operands' fragments, decoding the weights of
+// the next stage, whose codes were loaded a stage before, and copies of its dz rows.
+template <int MT, int NT>
+__device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>::Rows& rows,
                                               const uint8_t* __restrict__ w, const uint8_t* __restrict__ s, int N,
-                                              int K, int k0, int valid_n, int st0, int st1, uint8_t* lds, int wm,
-                                              int wn, int lane, f32x4 (&acc)[MT][4]) {
-  using Stage = RowStage<WM * MT * 16, BWD_KB, WM * WN>;
-  using WS = WeightStage<WN * 64>;
-  constexpr int ONE = Stage::BYTES + WS::BYTES;
-  static_assert(WM * WN * 64 == 8 * WS::QUADS && WM * WN * 64 == BWD_KB * WS::BLOCKS, "one gather per thread");
-  const int tid = threadIdx.x;
-  const int r = lane & 15, g = lane >> 4;
-  // codes: octet o of the stage's rows, column quad q of the tile (clamped inside K)
-  const int o = tid / WS::QUADS, q = tid % WS::QUADS;
-  const uint8_t* wp = w + (min(k0 + 4 * q, K - 4) >> 1);
-  const size_t wld = (size_t)(K >> 1), sld = (size_t)(K >> 5);
-  // scales: row sn, column block sk
-  const int sn = tid / WS::BLOCKS, sk = tid % WS::BLOCKS;
-  const uint8_t* sp = s + min((k0 >> 5) + sk, (K >> 5) - 1);
-  uint32_t quad[8];
-  uint32_t sb;
-  // rows past N read as zero codes with scale 1
-  auto load_w = [&](int st) {
-    const int n = st * BWD_KB;
+                                              int K, int k0, int st0, int st1, uint8_t* lds, int wm, int wn, int lane,
+                                              f32x16 (&acc)[MT][NT]) {
+  typedef BackwardLds<MT, NT> L;
+  constexpr int STEPS = 4, SLOTS = MT * NT, CPT = ColumnStage<NT>::CPT, COPIES = L::Rows::COPIES;
+  constexpr int READS = MT + NT;
+  const int r = lane & 31, g = lane >> 5, o = threadIdx.x >> 5, q = threadIdx.x & 31;
+  const int wld = K >> 1, sld = K >> 5;
+  const int col = min(k0 + CPT * q, K - CPT);  // columns past K: the last ones again, never stored
+  // byte offsets of this thread's 8 rows from the stage's first
+  uint32_t woff[8], soff[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    woff[i] = (uint32_t)((o * 8 + i) * wld + (col >> 1));
+    soff[i] = (uint32_t)((o * 8 + i) * sld + (col >> 5));
+  }
+  uint32_t at[4], wat[4];  // LDS byte offsets of this lane's chunks at step u, first tile
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    at[u] = (uint32_t)(wm * MT * 32 + r) * 128 + (((2 * u + g) ^ row_key<8>(r)) << 4);
+    wat[u] = L::Rows::BYTES + (uint32_t)(wn * NT * 32 + r) * 128 + (((2 * u + g) ^ row_key<8>(r)) << 4);
+  }
+  // where this thread's columns go: LDS row 16 i + (q & 15) of its wave column, chunk o
+  const uint32_t put = L::Rows::BYTES + (uint32_t)((q >> 4) * NT * 32 + (q & 15)) * 128 + ((o ^ row_key<8>(q & 15)) << 4);
+  uint32_t code[8], sb[8];  // of the stage after the current one
+  u32x4 frag[2][MT], wf[2][NT], column[2];
+  auto load_one = [&](int st, int i) {
+    const uint8_t* wb = w + (size_t)st * BWD_KB * wld;
+    if constexpr (CPT == 8)
+      code[i] = *reinterpret_cast<const uint32_t*>(wb + woff[i]);
+    else
+      code[i] = *reinterpret_cast<const uint16_t*>(wb + woff[i]);
+    sb[i] = (s + (size_t)st * BWD_KB * sld)[soff[i]];
+  };
+  // Rows past N (in the last stage): their addresses are moved to row N - 1 before they are
+  // loaded, and their values replaced by zero codes with scale 1 before they are used.
+  const int last_stage = (N - 1) / BWD_KB, left = N - last_stage * BWD_KB;
+  auto clamp_rows = [&]() {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int row = n + o * 8 + i;
-      quad[i] = row < N ? *reinterpret_cast<const uint16_t*>(wp + (size_t)row * wld) : 0u;
+      const int row = min(o * 8 + i, left - 1);
+      woff[i] = (uint32_t)(row * wld + (col >> 1));
+      soff[i] = (uint32_t)(row * sld + (col >> 5));
     }
-    sb = n + sn < N ? sp[(size_t)(n + sn) * sld] : 127u;
   };
-  auto store_w = [&](uint8_t* buf) {
-    *reinterpret_cast<u32x4*>(buf + Stage::BYTES + (o * WS::QUADS + q) * 16) =
-        u32x4{quad[0] | quad[1] << 16, quad[2] | quad[3] << 16, quad[4] | quad[5] << 16, quad[6] | quad[7] << 16};
-    reinterpret_cast<float*>(buf + Stage::BYTES + WS::CODE_BYTES)[sk * WS::SCALE_LD + sn] = e8m0_scale_operand(sb);
+  auto clear_rows = [&]() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (o * 8 + i >= left) code[i] = 0u, sb[i] = 127u;
   };
-  auto load_x = [&](int st, uint8_t* buf) {
-    const int valid = valid_n - st * BWD_KB;
-    if (valid >= BWD_KB)
-      rows.copy(buf, st);
+  // half of column pair b, row pair p2: rows 2 p2 and 2 p2 + 1
+  auto decode_pair = [&](auto B, auto P2) __attribute__((always_inline)) {
+    constexpr int b = B, p2 = P2;
+    const uint32_t lo = decode2<b>(code[2 * p2], e8m0_scale_operand(sb[2 * p2]));
+    const uint32_t hi = decode2<b>(code[2 * p2 + 1], e8m0_scale_operand(sb[2 * p2 + 1]));
+    column[0][p2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);  // low halves: column 2b
+    column[1][p2] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+  };
+  auto put_column = [&](uint8_t* buf, int b, int h) {
+    *reinterpret_cast<u32x4*>(buf + put + (2 * b + h) * 2048) = column[h];
+  };
+  auto read_one = [&](const uint8_t* buf, int u, int e) {  // operand e of step u
+    if (e < MT)
+      frag[u & 1][e] = ld16(buf + at[u] + e * 4096);
     else
-      rows.copy_tail(buf, st, valid);
+      wf[u & 1][e - MT] = ld16(buf + wat[u] + (e - MT) * 4096);
   };
-  load_x(st0, lds);
-  load_w(st0);
-  store_w(lds);
+
+  // the first stage's operands and the second's codes
+  const bool ragged = left < BWD_KB;
+  if (ragged && st0 == last_stage) clamp_rows();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load_one(st0, i);
+  rows.copy(lds, st0);
+  if (ragged && st0 == last_stage) clear_rows();
+  unrolled<NT>([&](auto B) __attribute__((always_inline)) {
+    unrolled<4>([&](auto P2) __attribute__((always_inline)) { decode_pair(B, P2); });
+    put_column(lds, B, 0);
+    put_column(lds, B, 1);
+  });
+  const int second = min(st0 + 1, st1 - 1);
+  if (ragged && second == last_stage) clamp_rows();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) load_one(second, i);
+  wait_copies();
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < READS; ++e) read_one(lds, 0, e);
+  settle_mfma();  // the accumulators have been cleared
+
+  uint8_t* cur = lds;
+  uint8_t* nxt = lds + L::ONE;
   for (int st = st0; st < st1; ++st) {
-    uint8_t* cur = lds + ((st - st0) & 1) * ONE;
-    uint8_t* nxt = lds + ((st - st0 + 1) & 1) * ONE;
-    wait_copies();
-    __syncthreads();
-    if (st + 1 < st1) {
-      load_x(st + 1, nxt);
-      load_w(st + 1);
+    // the stages that are decoded and copied, and loaded, meanwhile; past the last one that one
+    // again, which nothing uses
+    const int cs = min(st + 1, st1 - 1), ls = min(st + 2, st1 - 1);
+    if (ragged) {
+      if (cs == last_stage) clear_rows();
+      if (ls == last_stage) clamp_rows();
     }
-    const float* scales = reinterpret_cast<const float*>(cur + Stage::BYTES + WS::CODE_BYTES);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const u32x4 d = ld16(cur + Stage::BYTES + ((4 * c + g) * WS::QUADS + wn * 16 + r) * 16);
-      const float* sf = scales + (wn * 2 + (r >> 3)) * WS::SCALE_LD + c * 32 + g * 8;
-      u32x4 frag[4];  // the 8 rows of columns 4r + i
-#pragma unroll
-      for (int p = 0; p < 4; ++p) {  // rows 2p and 2p + 1
-        const float s0 = sf[2 * p], s1 = sf[2 * p + 1];
-        const uint32_t a0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[p], s0, 0));
-        const uint32_t a1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[p], s0, 1));
-        const uint32_t b0 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[p], s1, 2));
-        const uint32_t b1 = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d[p], s1, 3));
-        frag[0][p] = __builtin_amdgcn_perm(b0, a0, 0x05040100u);  // low halves: column 4r
-        frag[1][p] = __builtin_amdgcn_perm(b0, a0, 0x07060302u);
-        frag[2][p] = __builtin_amdgcn_perm(b1, a1, 0x05040100u);
-        frag[3][p] = __builtin_amdgcn_perm(b1, a1, 0x07060302u);
+    unrolled<STEPS>([&](auto U) __attribute__((always_inline)) {
+      constexpr int u = U, next = (u + 1) % STEPS;
+      constexpr bool last = u == STEPS - 1;
+      if constexpr (last) {
+        wait_copies();
+        __syncthreads();  // the next stage is whole, and no wave reads `cur` any more
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int row = wm * MT * 16 + m * 16 + r;
-        const bf16x8 a = as_bf16x8(ld16(cur + row * 128 + (((4 * c + g) ^ (r & 7)) << 4)));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(as_bf16x8(frag[i]), a, acc[m][i]);
-      }
-    }
-    if (st + 1 < st1) store_w(nxt);
+      unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
+        constexpr int k = S, m = k / NT, i = k % NT, n = u * SLOTS + k;
+        mfma_in_place(acc[m][i], wf[u & 1][i], frag[u & 1][m]);
+        constexpr int per_read = (READS + SLOTS - 1) / SLOTS;
+        unrolled<per_read>([&](auto E) __attribute__((always_inline)) {
+          constexpr int e = k * per_read + E;
+          if constexpr (e < READS) read_one(last ? nxt : cur, next, e);
+        });
+        // copies of the next stage's dz rows: steps 0 and 1
+        constexpr int per_copy = (COPIES + 2 * SLOTS - 1) / (2 * SLOTS);
+        unrolled<per_copy>([&](auto E) __attribute__((always_inline)) {
+          constexpr int e = n * per_copy + E;
+          if constexpr (e < COPIES) rows.copy_one(nxt, cs, e);
+        });
+        // decoding the next stage: steps 1 and 2, a column pair's 4 row pairs, then its writes
+        constexpr int units = 4 * NT, per_unit = (units + 2 * SLOTS - 1) / (2 * SLOTS);
+        constexpr int every = per_unit > 1 ? 1 : 2 * SLOTS / units;
+        if constexpr (u > 0 && !last && n % every == 0)
+          unrolled<per_unit>([&](auto E) __attribute__((always_inline)) {
+            constexpr int e = (n - SLOTS) / every * per_unit + E;
+            if constexpr (e < units) {
+              decode_pair(std::integral_constant<int, e / 4>{}, std::integral_constant<int, e % 4>{});
+              if constexpr (e % 4 == 3) {
+                put_column(nxt, e / 4, 0);
+                put_column(nxt, e / 4, 1);
+              }
+            }
+          });
+        // the codes of the stage after next: step 3, used from the next stage's step 1 on
+        if constexpr (last) {
+          constexpr int per_load = (8 + SLOTS - 1) / SLOTS;
+          unrolled<per_load>([&](auto E) __attribute__((always_inline)) {
+            constexpr int e = k * per_load + E;
+            if constexpr (e < 8) load_one(ls, e);
+          });
+        }
+        keep_order();
+      });
+    });
+    uint8_t* t = cur;
+    cur = nxt;
+    nxt = t;
   }
+  settle_mfma();
 }
 
 }  // namespace mx
