@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 ? 1 : 2)
   }
   f32x16 acc[MT][NT];
   tile_zero(acc);
-  forward_tile<MT, NT, WM, WN>(xs, cs, sbase, soff, K, st0, st1, lds, wm, wn, lane, acc);
+  forward_tile<MT, NT, WM, WN>(xs, cs, sbase, (uint32_t)(min(WN * WCOLS, rows - n0) * (K >> 5)), soff, K, st0, st1, lds, wm, wn, lane, acc);
 
   const int pc = part_cols(rows);
   // MB rows of MFMA tiles at a time through the LDS; then row by row, PIECES lanes a row with 8

@@ -146,11 +146,31 @@ __device__ __forceinline__ void mfma_in_place(f32x16& acc, u32x4 a, u32x4 b) {
   asm volatile("v_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+a"(acc) : "v"(a), "v"(b));
 }
 // The compiler does not see that the instructions above multiply, so it keeps none of their
-// distances.  Before their accumulators are written or read otherwise, this waits out the
-// longest of them (18 wait states).
-__device__ __forceinline__ void settle_mfma() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
-// Two wait states between a vector instruction that writes an operand and the product.
-__device__ __forceinline__ void operands_ready() { asm volatile("s_nop 1"); }
+// distances.  This stands between them and what writes or reads their accumulators otherwise
+// (before the first and after the last): it waits out the longest of them (18 wait states),
+// and the ties keep those writes and reads on their side of it.
+template <int MT, int NT>
+__device__ __forceinline__ void settle_mfma(f32x16 (&acc)[MT][NT]) {
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) asm volatile("" : "+a"(acc[m][i]));
+  asm volatile("s_nop 15\n\ts_nop 15" ::: "memory");
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) asm volatile("" : "+a"(acc[m][i]));
+}
+// Two wait states between the vector instructions that write these operands and the product.
+// The operands are tied: what computes them cannot move behind this.
+template <int NT>
+__device__ __forceinline__ void operands_ready(u32x4 (&w)[NT]) {
+  static_assert(NT == 2 || NT == 4, "tiles of a wave");
+  if constexpr (NT == 2)
+    asm volatile("s_nop 1" : "+v"(w[0]), "+v"(w[1]));
+  else
+    asm volatile("s_nop 1" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]));
+}
 
 // Value pair Q of 8 codes.
 template <int Q>
@@ -228,15 +248,16 @@ struct ForwardLds {
 template <int MT, int NT, int WM, int WN>
 __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, WM, WN>::Rows& rows,
                                              const typename ForwardLds<MT, NT, WM, WN>::Codes& codes,
-                                             const uint8_t* const (&sbase)[NT], const uint32_t (&soff)[NT], int K,
-                                             int st0, int st1, uint8_t* lds, int wm, int wn, int lane,
-                                             f32x16 (&acc)[MT][NT]) {
+                                             const uint8_t* const (&sbase)[NT], uint32_t scale_bytes,
+                                             const uint32_t (&soff)[NT], int K, int st0, int st1, uint8_t* lds,
+                                             int wm, int wn, int lane, f32x16 (&acc)[MT][NT]) {
   typedef ForwardLds<MT, NT, WM, WN> L;
   constexpr int STEPS = 8, SLOTS = MT * NT;
   constexpr int XC = L::Rows::COPIES, COPIES = XC + L::Codes::COPIES;
-  constexpr int COPY_SLOTS = (STEPS - 3) * SLOTS / COPIES < 3 ? (STEPS - 3) * SLOTS / COPIES : 3;
-  constexpr int COPIES_AT_ONCE = COPY_SLOTS ? 1 : (COPIES + (STEPS - 3) * SLOTS - 1) / ((STEPS - 3) * SLOTS);
-  constexpr int COPY_EVERY = COPY_SLOTS ? COPY_SLOTS : 1;
+  // loads from memory: one every COPY_EVERY slots of the first five steps, or several a slot
+  constexpr int LOADS = COPIES + NT, LOAD_SLOTS = 5 * SLOTS;
+  constexpr int COPIES_AT_ONCE = (LOADS + LOAD_SLOTS - 1) / LOAD_SLOTS;
+  constexpr int COPY_EVERY = LOADS > LOAD_SLOTS ? 1 : LOAD_SLOTS / LOADS < 3 ? LOAD_SLOTS / LOADS : 3;
   const int r = lane & 31, g = lane >> 5, blocks = K >> 5;
   const int full = K / FWD_KB;  // stages of FWD_KB values
   const uint32_t xrow = (uint32_t)(wm * MT * 32 + r) * 256;
@@ -248,51 +269,57 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
 #pragma unroll
   for (int b = 0; b < 2; ++b) wat[b] = wrow + (((2 * b + g) ^ (r >> 3)) << 4);
   u32x4 wc[2][NT], frag[2][MT], w[2][NT];
-  uint32_t sb[2][NT];
+  uint32_t sd[NT];  // a stage's 4 scale bytes of the row of tile i
   float sc[2][NT];
   auto load_tail = [&](uint8_t* buf) {
     rows.copy_tail(buf, full, K - full * FWD_KB);
     codes.copy_tail(buf + L::Rows::BYTES, full, blocks & 3);
   };
-  // blocks past K have zero codes; their scale is 1
-  auto load_scales = [&](int st) {
+  buffer sbuf[NT];
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int k = st * 4 + 2 * b + g;
+  for (int i = 0; i < NT; ++i) sbuf[i] = make_buffer(sbase[i], scale_bytes);
+  auto load_scale = [&](int st, int i) { sd[i] = __builtin_amdgcn_raw_buffer_load_b32(sbuf[i], soff[i], st * 4, 0); };
+  // The partial stage's scales byte by byte (a row may end with the tensor); blocks past K have
+  // zero codes and scale 1.
+  auto load_tail_scales = [&]() {
 #pragma unroll
-      for (int i = 0; i < NT; ++i) {
-        const uint32_t v = sbase[i][soff[i] + min(k, blocks - 1)];
-        sb[b][i] = k < blocks ? v : 127u;
-      }
+    for (int i = 0; i < NT; ++i) {
+      uint32_t d = 0x7F7F7F7Fu;
+      for (int b = 0; b < (blocks & 3); ++b)
+        d = (d & ~(0xFFu << (8 * b))) | (uint32_t)sbase[i][soff[i] + full * 4 + b] << (8 * b);
+      sd[i] = d;
     }
   };
-  auto use_scales = [&]() {
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < NT; ++i) sc[b][i] = e8m0_scale_operand(sb[b][i]);
+  // of tile i: this lane's blocks g and g + 2
+  auto use_scale = [&](int i) {
+    const uint32_t d = sd[i] >> (8 * g);
+    sc[0][i] = e8m0_scale_operand(d & 0xFFu);
+    sc[1][i] = e8m0_scale_operand((d >> 16) & 0xFFu);
   };
   uint8_t* cur = lds;
   uint8_t* nxt = lds + L::ONE;
   if (st0 < full) {
     rows.copy(cur, st0);
     codes.copy(cur + L::Rows::BYTES, st0);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) load_scale(st0, i);
   } else {
     load_tail(cur);
+    load_tail_scales();
   }
-  load_scales(st0);
   wait_copies();
   __syncthreads();
-  use_scales();
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
+    use_scale(i);
 #pragma unroll
     for (int b = 0; b < 2; ++b) wc[b][i] = ld16(cur + wat[b] + i * 2048);
     w[0][i] = __builtin_bit_cast(u32x4, decode8(wc[0][i][0], sc[0][i]));
   }
 #pragma unroll
   for (int m = 0; m < MT; ++m) frag[0][m] = ld16(cur + at[0] + m * 8192);
-  settle_mfma();  // the accumulators have been cleared
+  settle_mfma(acc);  // the accumulators have been cleared
+  operands_ready<NT>(w[0]);
   for (int st = st0; st < st1; ++st) {
     // The stage that is copied meanwhile.  Past the last full one its copy repeats that one:
     // the partial stage is written over it, and after the last stage nothing reads it.
@@ -302,9 +329,11 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
       constexpr bool last = u == STEPS - 1;
       if constexpr (last) {
         wait_copies();  // the next stage has landed
-        if (st + 1 == full && st + 1 < st1) load_tail(nxt);
+        if (st + 1 == full && st + 1 < st1) {
+          load_tail(nxt);
+          load_tail_scales();
+        }
         __syncthreads();  // for every wave, and no wave reads `cur` any more
-        use_scales();
       }
       // The slots' reads and conversions; in the last step the reads, which the conversions
       // wait for, fill the first half.
@@ -312,7 +341,6 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
       constexpr int first = last ? SLOTS / 2 : 0;  // slot of the first conversion
       constexpr int per_read = (reads + (last ? (SLOTS + 1) / 2 : SLOTS) - 1) / (last ? (SLOTS + 1) / 2 : SLOTS);
       constexpr int per_convert = (converts + SLOTS - first - 1) / (SLOTS - first);
-      operands_ready();
       unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
         constexpr int k = S, m = k / NT, i = k % NT;
         mfma_in_place(acc[m][i], w[u & 1][i], frag[u & 1][m]);
@@ -323,6 +351,13 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
           else if constexpr (e < reads)
             frag[next & 1][e - codes_first] = ld16((last ? nxt : cur) + at[next] + (e - codes_first) * 8192);
         });
+        // the next stage's scales, before its first conversion
+        constexpr int per_scale = (NT + (SLOTS + 1) / 2 - 1) / ((SLOTS + 1) / 2);
+        if constexpr (last)
+          unrolled<per_scale>([&](auto E) __attribute__((always_inline)) {
+            constexpr int i2 = k * per_scale + E;
+            if constexpr (i2 < NT) use_scale(i2);
+          });
         unrolled<per_convert>([&](auto E) __attribute__((always_inline)) {
           constexpr int e = (k - first) * per_convert + E;
           if constexpr (e >= 0 && e < converts) {
@@ -330,7 +365,7 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
             w[next & 1][j][q] = decode2<q>(wc[next >> 2][j][next & 3], sc[next >> 2][j]);
           }
         });
-        // copies, one every few slots from the stage's first on; then the next stage's scales
+        // copies, one every few slots from the stage's first on; the next stage's scales last
         constexpr int n = u * SLOTS + k;
         if constexpr (n % COPY_EVERY == COPY_EVERY - 1)
           unrolled<COPIES_AT_ONCE>([&](auto E) __attribute__((always_inline)) {
@@ -339,17 +374,18 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
               rows.copy_one(nxt, cs, q);
             else if constexpr (q < COPIES)
               codes.copy_one(nxt + L::Rows::BYTES, cs, q - XC);
+            else if constexpr (q < COPIES + NT)
+              load_scale(cs, q - COPIES);
           });
-        if constexpr (n == COPY_EVERY * ((COPIES + COPIES_AT_ONCE - 1) / COPIES_AT_ONCE))
-          load_scales(min(st + 1, st1 - 1));
         keep_order();
       });
+      operands_ready<NT>(w[next & 1]);
     });
     uint8_t* t = cur;
     cur = nxt;
     nxt = t;
   }
-  settle_mfma();
+  settle_mfma(acc);
 }
 
 // A wave's results, one row of MFMA tiles (32 tokens) at a time, through its own part of the
@@ -492,7 +528,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   __syncthreads();
 #pragma unroll
   for (int e = 0; e < READS; ++e) read_one(lds, 0, e);
-  settle_mfma();  // the accumulators have been cleared
+  settle_mfma(acc);  // the accumulators have been cleared
 
   uint8_t* cur = lds;
   uint8_t* nxt = lds + L::ONE;
@@ -554,7 +590,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
     cur = nxt;
     nxt = t;
   }
-  settle_mfma();
+  settle_mfma(acc);
 }
 
 }  // namespace mx
