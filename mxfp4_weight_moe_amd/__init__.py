@@ -565,11 +565,18 @@ def _act_code(act: str) -> int:
     return code
 
 
+# A decode step's call is a few microseconds of GPU time, so the checks below take their fast
+# way in one expression and leave naming what is wrong to _check; the raw stream handle saves
+# building a Stream object (2 us of the 12 that a call took).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _tensor(t, name: str, dtype, shape, dev):
     """_check with the whole shape at once."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.device != dev or not t.is_cuda or not t.is_contiguous():
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape and t.device == dev
+            and t.is_contiguous()):
         _check(t, name, dtype, None, dev)
-    if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
@@ -589,20 +596,21 @@ def _scratch(nbytes: int, dev, ws):
     return ws, ws.data_ptr(), nbytes
 
 
-def _call(name: str, dev, *args):
-    """The C call `name` on dev's current stream, which is its last argument."""
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
-        st = getattr(_lib, name)(*args, stream)
+def _call(fn, dev, *args):
+    """The C call `fn` on dev's current stream, which is its last argument."""
+    index = dev.index
+    stream = _raw_stream(index)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
-            st = getattr(_lib, name)(*args, stream)
+            st = fn(*args, stream)
     if st != MX_OK:
-        _raise(st, name)
+        _raise(st, fn.__name__)
 
 
 def _bf16_rows(t, name: str):
-    if not isinstance(t, torch.Tensor) or t.dtype != _BF16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 2:
+    if not (isinstance(t, torch.Tensor) and t.dtype is _BF16 and t.is_cuda and t.dim() == 2 and t.is_contiguous()):
         _check(t, name, _BF16, 2)
     if t.numel() == 0:
         raise ValueError(f"{name} is empty: {list(t.shape)}")
@@ -610,7 +618,10 @@ def _bf16_rows(t, name: str):
 
 
 def _weights(codes, scales, name: str, rows: int | None, K: int, dev) -> int:
-    rows = codes.shape[0] if rows is None and isinstance(codes, torch.Tensor) and codes.dim() else rows
+    if rows is None:
+        if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
+            raise ValueError(f"{name} codes must be a 2-d tensor")
+        rows = codes.shape[0]
     if K % 32:
         raise ValueError(f"the reduction length {K} must be a multiple of 32")
     _tensor(codes, f"{name} codes", _U8, (rows, K // 2), dev)
@@ -633,12 +644,12 @@ def mx_linear_fused(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tens
         _tensor(residual, "residual", _BF16, (T, N), dev)
     code = _act_code(act)
     if out is None:
-        out = torch.empty((T, N), dtype=_BF16, device=dev)
+        out = x.new_empty((T, N))
     else:
         _tensor(out, "out", _BF16, (T, N), dev)
     z = torch.empty((T, N), dtype=_BF16, device=dev) if save_z else None
     ws, wp, wn = _scratch(_lib.mx_linear_fused_workspace_size(T, K, N), dev, ws)
-    _call("mx_linear_fused", dev, x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), _opt(bias), _opt(residual),
+    _call(_lib.mx_linear_fused, dev, x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), _opt(bias), _opt(residual),
           scale, code, out.data_ptr(), _opt(z), T, K, N, wp, wn)
     return (out, z) if save_z else out
 
@@ -664,7 +675,7 @@ def mx_linear_fused_backward(dy: torch.Tensor, w_codes: torch.Tensor, w_scales: 
     dx = torch.empty((T, K), dtype=_BF16, device=dev) if need_dx else None
     dbias = torch.empty(N, dtype=_F32, device=dev) if need_dbias else None
     ws, wp, wn = _scratch(_lib.mx_linear_fused_backward_workspace_size(T, K, N), dev, ws)
-    _call("mx_linear_fused_backward", dev, dy.data_ptr(), _opt(z), w_codes.data_ptr(), w_scales.data_ptr(), scale, code,
+    _call(_lib.mx_linear_fused_backward, dev, dy.data_ptr(), _opt(z), w_codes.data_ptr(), w_scales.data_ptr(), scale, code,
           _opt(dx), _opt(dbias), T, K, N, wp, wn)
     return dx, dbias
 
@@ -685,12 +696,12 @@ def mx_gate_up(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor
         _tensor(bias, "bias", _BF16, (two_i,), dev)
     code = _act_code(act)
     if out is None:
-        out = torch.empty((T, I), dtype=_BF16, device=dev)
+        out = x.new_empty((T, I))
     else:
         _tensor(out, "out", _BF16, (T, I), dev)
     z = torch.empty((T, two_i), dtype=_BF16, device=dev) if save_z else None
     ws, wp, wn = _scratch(_lib.mx_gate_up_workspace_size(T, H, I), dev, ws)
-    _call("mx_gate_up", dev, x.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), _opt(bias), code, out.data_ptr(),
+    _call(_lib.mx_gate_up, dev, x.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), _opt(bias), code, out.data_ptr(),
           _opt(z), T, H, I, wp, wn)
     return (out, z) if save_z else out
 
@@ -713,7 +724,7 @@ def mx_gate_up_backward(dh: torch.Tensor, z: torch.Tensor, W_gate_up: torch.Tens
     dx = torch.empty((T, H), dtype=_BF16, device=dev) if need_dx else None
     dbias = torch.empty(2 * I, dtype=_F32, device=dev) if need_dbias else None
     ws, wp, wn = _scratch(_lib.mx_gate_up_backward_workspace_size(T, H, I), dev, ws)
-    _call("mx_gate_up_backward", dev, dh.data_ptr(), z.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), code,
+    _call(_lib.mx_gate_up_backward, dev, dh.data_ptr(), z.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), code,
           _opt(dx), _opt(dbias), T, H, I, wp, wn)
     return dx, dbias
 
@@ -752,7 +763,7 @@ def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: tor
         else:
             _tensor(y, "out", _BF16, (T, H), dev)
     xn = torch.empty((T, H), dtype=_BF16, device=dev) if w_pre is not None else None
-    _call("mx_norm_residual", dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale, _opt(w_pre), eps,
+    _call(_lib.mx_norm_residual, dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale, _opt(w_pre), eps,
           _opt(y), _opt(xn), T, H)
     return (x if y is None else y), xn
 
@@ -787,7 +798,7 @@ def mx_norm_residual_backward(dy: torch.Tensor | None, dxn: torch.Tensor | None,
     dw_post = torch.empty(H, dtype=_F32, device=dev) if w_post is not None else None
     dw_pre = torch.empty(H, dtype=_F32, device=dev) if w_pre is not None else None
     ws, wp, wn = _scratch(_lib.mx_norm_residual_backward_workspace_size(T, H), dev, ws)
-    _call("mx_norm_residual_backward", dev, _opt(dy), _opt(dxn), _opt(y), _opt(b), _opt(w_post), _opt(gate), mode,
+    _call(_lib.mx_norm_residual_backward, dev, _opt(dy), _opt(dxn), _opt(y), _opt(b), _opt(w_post), _opt(gate), mode,
           scale, _opt(w_pre), eps, dx.data_ptr(), _opt(db), _opt(dgate), _opt(dw_post), _opt(dw_pre), T, H, wp, wn)
     return dict(dx=dx, db=db, dgate=dgate, dw_post=dw_post, dw_pre=dw_pre)
 
@@ -818,7 +829,7 @@ def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tens
     else:
         _tensor(out, "out", _BF16, (T, H), dev)
     ws, wp, wn = _scratch(_lib.mx_ffn_block_workspace_size(T, H, I), dev, ws)
-    _call("mx_ffn_block", dev, x.data_ptr(), _opt(w_pre), W_gate_up.data_ptr(), S_gate_up.data_ptr(),
+    _call(_lib.mx_ffn_block, dev, x.data_ptr(), _opt(w_pre), W_gate_up.data_ptr(), S_gate_up.data_ptr(),
           _opt(bias_gate_up), code, W_down.data_ptr(), S_down.data_ptr(), _opt(bias_down), _opt(w_post), _opt(gate), mode,
           scale, eps, out.data_ptr(), T, H, I, wp, wn)
     return out

@@ -104,13 +104,14 @@ __host__ __device__ static inline int part_cols(int rows) { return (rows + 7) / 
 // rows: output columns (N, or I for gate_up).  nsplit > 1: part z of K goes to parts[z] as
 // fp32 [T][part columns (x 2)].  A wave's NT MFMA tiles are 32 consecutive weight rows each;
 // for gate_up the first half of them gate rows, the second half the up rows of the same columns.
-template <int MT, int NT, int WM, int WN, bool GATED>
-__global__ void __launch_bounds__(WM * WN * 64, MT == 4 ? 1 : 2)
+// D: stages in the LDS (mx_tile.hpp).
+template <int MT, int NT, int WM, int WN, int D, bool GATED>
+__global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
     forward_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                    typename EpilogueOf<GATED>::type epi, float* __restrict__ parts, int T, int K, int rows, int mtiles,
                    int ntiles, int nsplit) {
   constexpr int BM = WM * MT * 32, WCOLS = NT * 32 / (GATED ? 2 : 1), HALF = GATED ? NT / 2 : NT;
-  typedef ForwardLds<MT, NT, WM, WN> L;
+  typedef ForwardLds<MT, NT, WM, WN, D> L;
   __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave / WN, wn = wave % WN;
@@ -137,9 +138,19 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 ? 1 : 2)
     sbase[i] = s + first_row(i) * (size_t)(K >> 5);
     soff[i] = (uint32_t)row_of((wn * NT + i) * 32 + (lane & 31)) * (uint32_t)(K >> 5);
   }
+  typename L::Scales ss;
+  if constexpr (D > 2) {  // 32-bit offsets from the first gate row to the up rows (forward_deep)
+    ss.wave = wave;
+    ss.buf_ = make_buffer(sbase[0], ((uint64_t)min(WN * WCOLS, rows - n0) + (GATED ? rows : 0)) * (uint64_t)(K >> 5));
+#pragma unroll
+    for (int q = 0; q < L::Scales::COPIES; ++q) {
+      const int i = 2 * q + (lane >> 5);
+      ss.off[q] = ((uint32_t)row_of((wn * NT + i) * 32 + (lane & 31)) + (i >= HALF ? (uint32_t)rows : 0u)) * (uint32_t)(K >> 5);
+    }
+  }
   f32x16 acc[MT][NT];
   tile_zero(acc);
-  forward_tile<MT, NT, WM, WN>(xs, cs, sbase, (uint32_t)(min(WN * WCOLS, rows - n0) * (K >> 5)), soff, K, st0, st1, lds, wm, wn, lane, acc);
+  forward_tile<MT, NT, WM, WN, D>(xs, cs, ss, sbase, (uint32_t)(min(WN * WCOLS, rows - n0) * (K >> 5)), soff, K, st0, st1, lds, wm, wn, lane, acc);
 
   const int pc = part_cols(rows);
   // MB rows of MFMA tiles at a time through the LDS; then row by row, PIECES lanes a row with 8
@@ -304,15 +315,23 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   const TilePlan p = forward_plan(T, K, rows, GATED);
   float* parts = static_cast<float*>(workspace);
   const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE(MT, NT)                                                                                           \
-  hipLaunchKernelGGL((forward_kernel<MT, NT, 2, 2, GATED>), grid, dim3(256), 0, stream, x, w, s, epi, parts, T, K, rows, \
-                     p.mtiles, p.ntiles, p.nsplit)
+  // One tile a CU and K in whole stages: more stages in the LDS.  Measured at T = 128 with
+  // H = 7168, I = 2048 (7 stages a workgroup); see forward_tile.
+  const bool deep = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS && K % FWD_KB == 0 && aligned(s, 4) &&
+                    (int64_t)rows * (K >> 5) < ((int64_t)1 << 31);
+#define MX_TILE(MT, NT, D)                                                                                           \
+  hipLaunchKernelGGL((forward_kernel<MT, NT, 2, 2, D, GATED>), grid, dim3(256), 0, stream, x, w, s, epi, parts, T, K, \
+                     rows, p.mtiles, p.ntiles, p.nsplit)
   if (p.mt == 4)
-    MX_TILE(4, 4);
+    MX_TILE(4, 4, 2);
+  else if (p.mt == 2 && deep)
+    MX_TILE(2, 2, 3);
   else if (p.mt == 2)
-    MX_TILE(2, 2);
+    MX_TILE(2, 2, 2);
+  else if (deep)
+    MX_TILE(1, 2, 6);
   else
-    MX_TILE(1, 2);
+    MX_TILE(1, 2, 2);
 #undef MX_TILE
   if (p.nsplit > 1) {
     const int pc = part_cols(rows);

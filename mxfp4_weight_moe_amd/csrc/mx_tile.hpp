@@ -32,14 +32,22 @@ __device__ __forceinline__ buffer make_buffer(const void* base, uint64_t bytes) 
   const uint32_t n = bytes < 0xFFFFFFFFull ? (uint32_t)bytes : 0xFFFFFFFFu;
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, n, 0x00020000);  // 32-bit data, no stride
 }
-// 16 bytes a lane from memory to LDS: lane l's bytes land at `lds` + 16 * l.
+// 16 (4) bytes a lane from memory to LDS: lane l's bytes land at `lds` + 16 (4) * l.
 __device__ __forceinline__ void copy16_to_lds(buffer b, uint32_t lane_offset, uint32_t offset, void* lds) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 16, lane_offset, offset, 0, 0);
+}
+__device__ __forceinline__ void copy4_to_lds(buffer b, uint32_t lane_offset, uint32_t offset, void* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(b, (lds_ptr)lds, 4, lane_offset, offset, 0, 0);
 }
 
 // This wave's copies to LDS have landed (they count as vector memory operations, which a
 // barrier alone does not wait for).
-__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// LATER: all but the last LATER vector memory operations, which return in order.
+template <int LATER = 0>
+__device__ __forceinline__ void wait_copies() {
+  static_assert(LATER < 64, "the counter's width");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LATER) : "memory");
+}
 
 // Consecutive tiles go to one XCD (workgroups are dealt to the 8 XCDs in turn), so that the
 // tiles that share activation rows share an L2.
@@ -227,12 +235,28 @@ struct CodeStage {
   }
 };
 
-template <int MT, int NT, int WM, int WN>
+// The scale bytes of a stage (4 a row) of a wave's weight rows, where they pass through the
+// LDS: 64 rows a copy, each wave its own.
+template <int NT, int NW>
+struct ScaleStage {
+  static constexpr int COPIES = NT / 2, BYTES = NW * COPIES * 256;
+  buffer buf_;
+  uint32_t off[COPIES];
+  int wave;
+  __device__ __forceinline__ void copy_one(uint8_t* buf, int stage, int q) const {
+    copy4_to_lds(buf_, off[q], (uint32_t)stage * 4, buf + (wave * COPIES + q) * 256);
+  }
+};
+
+// D: stages in the LDS.
+template <int MT, int NT, int WM, int WN, int D>
 struct ForwardLds {
   typedef RowStage<WM * MT * 32, FWD_KB, WM * WN> Rows;
   typedef CodeStage<WN * NT * 32, WM * WN> Codes;
-  static constexpr int ONE = Rows::BYTES + Codes::BYTES;
-  static constexpr int BYTES = 2 * ONE;
+  typedef ScaleStage<NT, WM * WN> Scales;
+  static constexpr int CODES_AT = Rows::BYTES, SCALES_AT = CODES_AT + Codes::BYTES;
+  static constexpr int ONE = SCALES_AT + (D > 2 ? Scales::BYTES : 0);
+  static constexpr int BYTES = D * ONE;
 };
 
 // acc[m][i] += W rows (as the MFMA's rows) x activation rows (its columns) over the stages
@@ -243,45 +267,62 @@ struct ForwardLds {
 //
 // Between the matrix instructions of a step, in slots that they leave free, the wave reads the
 // activation fragments and decodes the weights of the next step and, early in the stage,
-// copies the next stage to LDS.  The stage's only barrier stands before its last step, whose
+// copies a later stage to LDS.  The stage's only barrier stands before its last step, whose
 // operands are already in registers.
-template <int MT, int NT, int WM, int WN>
-__device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, WM, WN>::Rows& rows,
-                                             const typename ForwardLds<MT, NT, WM, WN>::Codes& codes,
+//
+// D = 2 (the tiles of 256 x 256 fill the LDS with that): copies are one stage ahead, scales
+// are loaded to registers.  D > 2, for products with one small tile a CU and few stages, which
+// wait for memory: copies are D - 1 stages ahead, scales among them; K % FWD_KB == 0 then, and
+// scale rows are 4-byte aligned.
+template <int MT, int NT, int WM, int WN, int D>
+__device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, WM, WN, D>::Rows& rows,
+                                             const typename ForwardLds<MT, NT, WM, WN, D>::Codes& codes,
+                                             const typename ForwardLds<MT, NT, WM, WN, D>::Scales& scales,
                                              const uint8_t* const (&sbase)[NT], uint32_t scale_bytes,
                                              const uint32_t (&soff)[NT], int K, int st0, int st1, uint8_t* lds,
                                              int wm, int wn, int lane, f32x16 (&acc)[MT][NT]) {
-  typedef ForwardLds<MT, NT, WM, WN> L;
+  typedef ForwardLds<MT, NT, WM, WN, D> L;
+  constexpr bool DEEP = D > 2;
   constexpr int STEPS = 8, SLOTS = MT * NT;
-  constexpr int XC = L::Rows::COPIES, COPIES = XC + L::Codes::COPIES;
-  // loads from memory: one every COPY_EVERY slots of the first five steps, or several a slot
-  constexpr int LOADS = COPIES + NT, LOAD_SLOTS = 5 * SLOTS;
-  constexpr int COPIES_AT_ONCE = (LOADS + LOAD_SLOTS - 1) / LOAD_SLOTS;
-  constexpr int COPY_EVERY = LOADS > LOAD_SLOTS ? 1 : LOAD_SLOTS / LOADS < 3 ? LOAD_SLOTS / LOADS : 3;
+  constexpr int XC = L::Rows::COPIES, WC = L::Codes::COPIES;
+  // loads from memory: one every LOAD_EVERY slots of the first five steps, or several a slot
+  constexpr int LOADS = XC + WC + (DEEP ? L::Scales::COPIES : NT), LOAD_SLOTS = 5 * SLOTS;
+  constexpr int LOADS_AT_ONCE = (LOADS + LOAD_SLOTS - 1) / LOAD_SLOTS;
+  constexpr int LOAD_EVERY = LOADS > LOAD_SLOTS ? 1 : LOAD_SLOTS / LOADS < 3 ? LOAD_SLOTS / LOADS : 3;
   const int r = lane & 31, g = lane >> 5, blocks = K >> 5;
   const int full = K / FWD_KB;  // stages of FWD_KB values
   const uint32_t xrow = (uint32_t)(wm * MT * 32 + r) * 256;
-  const uint32_t wrow = L::Rows::BYTES + (uint32_t)(wn * NT * 32 + r) * 64;
+  const uint32_t wrow = L::CODES_AT + (uint32_t)(wn * NT * 32 + r) * 64;
   uint32_t at[8];  // LDS byte offset of this lane's activation chunk at step u, first tile
 #pragma unroll
   for (int u = 0; u < 8; ++u) at[u] = xrow + (((8 * (u >> 2) + 4 * g + (u & 3)) ^ (r & 15)) << 4);
-  uint32_t wat[2];  // and of its blocks
+  uint32_t wat[2];  // of its blocks
 #pragma unroll
   for (int b = 0; b < 2; ++b) wat[b] = wrow + (((2 * b + g) ^ (r >> 3)) << 4);
+  const uint32_t sat = L::SCALES_AT + (uint32_t)(wm * WN + wn) * (L::Scales::COPIES * 256) + r * 4;  // of its scales
   u32x4 wc[2][NT], frag[2][MT], w[2][NT];
   uint32_t sd[NT];  // a stage's 4 scale bytes of the row of tile i
   float sc[2][NT];
-  auto load_tail = [&](uint8_t* buf) {
-    rows.copy_tail(buf, full, K - full * FWD_KB);
-    codes.copy_tail(buf + L::Rows::BYTES, full, blocks & 3);
-  };
   buffer sbuf[NT];
 #pragma unroll
   for (int i = 0; i < NT; ++i) sbuf[i] = make_buffer(sbase[i], scale_bytes);
-  auto load_scale = [&](int st, int i) { sd[i] = __builtin_amdgcn_raw_buffer_load_b32(sbuf[i], soff[i], st * 4, 0); };
-  // The partial stage's scales byte by byte (a row may end with the tensor); blocks past K have
-  // zero codes and scale 1.
-  auto load_tail_scales = [&]() {
+  // load q of LOADS of a stage
+  auto load = [&](uint8_t* buf, int st, auto Q) __attribute__((always_inline)) {
+    constexpr int q = Q;
+    if constexpr (q < XC)
+      rows.copy_one(buf, st, q);
+    else if constexpr (q < XC + WC)
+      codes.copy_one(buf + L::CODES_AT, st, q - XC);
+    else if constexpr (DEEP)
+      scales.copy_one(buf + L::SCALES_AT, st, q - XC - WC);
+    else
+      sd[q - XC - WC] = __builtin_amdgcn_raw_buffer_load_b32(sbuf[q - XC - WC], soff[q - XC - WC], st * 4, 0);
+  };
+  // The partial stage, through registers, and its scales byte by byte (a row may end with the
+  // tensor); blocks past K have zero codes and scale 1.
+  auto load_tail = [&](uint8_t* buf) {
+    rows.copy_tail(buf, full, K - full * FWD_KB);
+    codes.copy_tail(buf + L::CODES_AT, full, blocks & 3);
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       uint32_t d = 0x7F7F7F7Fu;
@@ -290,27 +331,31 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
       sd[i] = d;
     }
   };
+  auto read_scale = [&](const uint8_t* buf, int i) {
+    if constexpr (DEEP) sd[i] = *reinterpret_cast<const uint32_t*>(buf + sat + (i >> 1) * 256 + (i & 1) * 128);
+  };
   // of tile i: this lane's blocks g and g + 2
   auto use_scale = [&](int i) {
     const uint32_t d = sd[i] >> (8 * g);
     sc[0][i] = e8m0_scale_operand(d & 0xFFu);
     sc[1][i] = e8m0_scale_operand((d >> 16) & 0xFFu);
   };
+  // the buffers of the current and of the next stage, and the one that is filled meanwhile
   uint8_t* cur = lds;
   uint8_t* nxt = lds + L::ONE;
-  if (st0 < full) {
-    rows.copy(cur, st0);
-    codes.copy(cur + L::Rows::BYTES, st0);
-#pragma unroll
-    for (int i = 0; i < NT; ++i) load_scale(st0, i);
+  uint8_t* fill = lds + (D - 1) * L::ONE;
+  if (DEEP || st0 < full) {
+    unrolled<D - 1>([&](auto J) __attribute__((always_inline)) {
+      unrolled<LOADS>([&](auto Q) __attribute__((always_inline)) { load(lds + J * L::ONE, min(st0 + J, full - 1), Q); });
+    });
   } else {
     load_tail(cur);
-    load_tail_scales();
   }
-  wait_copies();
+  wait_copies<(D - 2) * LOADS>();
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
+    read_scale(cur, i);
     use_scale(i);
 #pragma unroll
     for (int b = 0; b < 2; ++b) wc[b][i] = ld16(cur + wat[b] + i * 2048);
@@ -323,21 +368,21 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
   for (int st = st0; st < st1; ++st) {
     // The stage that is copied meanwhile.  Past the last full one its copy repeats that one:
     // the partial stage is written over it, and after the last stage nothing reads it.
-    const int cs = min(st + 1, full - 1);
+    const int cs = min(st + D - 1, full - 1);
     unrolled<STEPS>([&](auto U) __attribute__((always_inline)) {
       constexpr int u = U, next = (u + 1) % STEPS;
       constexpr bool last = u == STEPS - 1;
       if constexpr (last) {
-        wait_copies();  // the next stage has landed
-        if (st + 1 == full && st + 1 < st1) {
-          load_tail(nxt);
-          load_tail_scales();
+        wait_copies<(D - 2) * LOADS>();  // the next stage has landed
+        if constexpr (!DEEP) {
+          if (st + 1 == full && st + 1 < st1) load_tail(nxt);
         }
         __syncthreads();  // for every wave, and no wave reads `cur` any more
       }
       // The slots' reads and conversions; in the last step the reads, which the conversions
       // wait for, fill the first half.
-      constexpr int reads = MT + (last ? 2 * NT : 0), converts = 4 * NT;
+      constexpr int SR = last && DEEP ? NT : 0, CR = last ? 2 * NT : 0;
+      constexpr int reads = SR + CR + MT, converts = 4 * NT;
       constexpr int first = last ? SLOTS / 2 : 0;  // slot of the first conversion
       constexpr int per_read = (reads + (last ? (SLOTS + 1) / 2 : SLOTS) - 1) / (last ? (SLOTS + 1) / 2 : SLOTS);
       constexpr int per_convert = (converts + SLOTS - first - 1) / (SLOTS - first);
@@ -345,19 +390,24 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
         constexpr int k = S, m = k / NT, i = k % NT;
         mfma_in_place(acc[m][i], w[u & 1][i], frag[u & 1][m]);
         unrolled<per_read>([&](auto E) __attribute__((always_inline)) {
-          constexpr int e = k * per_read + E, codes_first = last ? 2 * NT : 0;
-          if constexpr (e < codes_first)
-            wc[e / NT][e % NT] = ld16(nxt + wat[e / NT] + (e % NT) * 2048);
+          constexpr int e = k * per_read + E;
+          if constexpr (e < SR)
+            read_scale(nxt, e);
+          else if constexpr (e < SR + CR)
+            wc[(e - SR) / NT][(e - SR) % NT] = ld16(nxt + wat[(e - SR) / NT] + ((e - SR) % NT) * 2048);
           else if constexpr (e < reads)
-            frag[next & 1][e - codes_first] = ld16((last ? nxt : cur) + at[next] + (e - codes_first) * 8192);
+            frag[next & 1][e - SR - CR] = ld16((last ? nxt : cur) + at[next] + (e - SR - CR) * 8192);
         });
         // the next stage's scales, before its first conversion
-        constexpr int per_scale = (NT + (SLOTS + 1) / 2 - 1) / ((SLOTS + 1) / 2);
-        if constexpr (last)
-          unrolled<per_scale>([&](auto E) __attribute__((always_inline)) {
-            constexpr int i2 = k * per_scale + E;
-            if constexpr (i2 < NT) use_scale(i2);
-          });
+        if constexpr (last && DEEP && k == first) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j) use_scale(j);
+        }
+        if constexpr (last && !DEEP && k < SLOTS / 2) {
+          constexpr int per_scale = (NT + SLOTS / 2 - 1) / (SLOTS / 2);
+#pragma unroll
+          for (int j = k * per_scale; j < (k + 1) * per_scale && j < NT; ++j) use_scale(j);
+        }
         unrolled<per_convert>([&](auto E) __attribute__((always_inline)) {
           constexpr int e = (k - first) * per_convert + E;
           if constexpr (e >= 0 && e < converts) {
@@ -365,27 +415,23 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
             w[next & 1][j][q] = decode2<q>(wc[next >> 2][j][next & 3], sc[next >> 2][j]);
           }
         });
-        // copies, one every few slots from the stage's first on; the next stage's scales last
+        // loads, one every few slots from the stage's first on
         constexpr int n = u * SLOTS + k;
-        if constexpr (n % COPY_EVERY == COPY_EVERY - 1)
-          unrolled<COPIES_AT_ONCE>([&](auto E) __attribute__((always_inline)) {
-            constexpr int q = n / COPY_EVERY * COPIES_AT_ONCE + E;
-            if constexpr (q < XC)
-              rows.copy_one(nxt, cs, q);
-            else if constexpr (q < COPIES)
-              codes.copy_one(nxt + L::Rows::BYTES, cs, q - XC);
-            else if constexpr (q < COPIES + NT)
-              load_scale(cs, q - COPIES);
+        if constexpr (n % LOAD_EVERY == LOAD_EVERY - 1)
+          unrolled<LOADS_AT_ONCE>([&](auto E) __attribute__((always_inline)) {
+            constexpr int q = n / LOAD_EVERY * LOADS_AT_ONCE + E;
+            if constexpr (q < LOADS) load(fill, cs, std::integral_constant<int, q>{});
           });
         keep_order();
       });
       operands_ready<NT>(w[next & 1]);
     });
-    uint8_t* t = cur;
+    fill = cur;
     cur = nxt;
-    nxt = t;
+    nxt = nxt == lds + (D - 1) * L::ONE ? lds : nxt + L::ONE;
   }
   settle_mfma(acc);
+  if constexpr (DEEP) wait_copies();  // the last stages' repeated copies: the LDS is used again
 }
 
 // A wave's results, one row of MFMA tiles (32 tokens) at a time, through its own part of the
