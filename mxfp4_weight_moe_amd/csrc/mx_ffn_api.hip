@@ -26,7 +26,7 @@ int workspace_ok(const void* ws, size_t have, size_t need) {
   return (!ws || !aligned(ws, 256) || have < need) ? MX_ERR_WORKSPACE : MX_OK;
 }
 size_t norm_backward_bytes(int64_t T, int64_t H, int arrays) {
-  return (size_t)norm_backward_groups(T) * (size_t)H * arrays * 4;
+  return (size_t)norm_backward_groups(T, H) * (size_t)H * arrays * 4;
 }
 bool norm_sizes_ok(int64_t T, int64_t H) {
   return T >= 1 && T <= MAX_T && H >= 8 && H <= MX_NORM_MAX_H && H % 8 == 0;

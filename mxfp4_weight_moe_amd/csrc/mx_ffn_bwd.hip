@@ -124,37 +124,50 @@ __global__ void __launch_bounds__(256) dz_gated_kernel(const uint16_t* __restric
 }
 
 // out[k][c] = sum over strips, in a fixed order, of parts[strip][k][c] for the k whose out is
-// set: a workgroup takes 64 columns of one k, its 4 waves a quarter of the strips each.
+// set: a workgroup takes 64 columns of one k, each of its 16 waves a sixteenth of the strips,
+// 8 loads at a time (4 waves with one load at a time took 35 us for 512 strips of 3 x 7168).
 struct StripOut {
   float* p[3];
 };
 
-__global__ void __launch_bounds__(256) strip_sum_kernel(const float* __restrict__ parts, StripOut out, int strips,
-                                                        int cols, int arrays) {
-  __shared__ float red[4][64];
+__global__ void __launch_bounds__(1024) strip_sum_kernel(const float* __restrict__ parts, StripOut out, int strips,
+                                                         int cols, int arrays) {
+  __shared__ float red[16][64];
   const int k = blockIdx.y;
   if (!out.p[k]) return;
-  const int c = blockIdx.x * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  const float* p = parts + (size_t)k * cols + min(c, cols - 1);
+  const size_t step = (size_t)arrays * cols;
+  const int i1 = strips * (q + 1) / 16;
   float a = 0.f;
-  if (c < cols)
-    for (int i = strips * q / 4; i < strips * (q + 1) / 4; ++i) a += parts[((size_t)i * arrays + k) * cols + c];
-  red[q][threadIdx.x & 63] = a;
+  for (int i = strips * q / 16; i < i1; i += 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = p[min(i + u, i1 - 1) * step];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a += i + u < i1 ? v[u] : 0.f;
+  }
+  red[q][lane] = a;
   __syncthreads();
-  if (q == 0 && c < cols)
-    out.p[k][c] = red[0][threadIdx.x] + red[1][threadIdx.x] + red[2][threadIdx.x] + red[3][threadIdx.x];
+  if (q == 0 && c < cols) {
+    float s = red[0][lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    out.p[k][c] = s;
+  }
 }
 
 int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float* const* out, hipStream_t stream) {
   StripOut o{};
   for (int k = 0; k < arrays; ++k) o.p[k] = out[k];
-  hipLaunchKernelGGL(strip_sum_kernel, dim3((cols + 63) / 64, arrays), dim3(256), 0, stream, parts, o, strips, cols,
+  hipLaunchKernelGGL(strip_sum_kernel, dim3((cols + 63) / 64, arrays), dim3(1024), 0, stream, parts, o, strips, cols,
                      arrays);
   return hip_status(hipGetLastError());
 }
 
 // ------------------------------------------------------------------ dx = alpha * dz W
 
-template <int MT, int NT>
+template <int MT, int NT, bool S4>
 __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
     backward_kernel(const uint16_t* __restrict__ dz, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                     uint16_t* __restrict__ dx, float* __restrict__ parts, float alpha, int T, int K, int N, int ldz,
@@ -173,7 +186,7 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
   zs.init(dz, m0, T, ldz, wave, lane);
   f32x16 acc[MT][NT];
   tile_zero(acc);
-  backward_tile<MT, NT>(zs, w, s, N, K, k0, st0, st1, lds, wm, wn, lane, acc);
+  backward_tile<MT, NT, S4>(zs, w, s, N, K, k0, st0, st1, lds, wm, wn, lane, acc);
   const int r = lane & 31, g = lane >> 5;
   constexpr int CPT = ColumnStage<NT>::CPT;
 #pragma unroll
@@ -182,7 +195,7 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       // MFMA rows R = 8 (j >> 2) + 4 g + (j & 3) and R + 16 of all tiles: CPT columns
-      const int k = k0 + wn * (NT * 32) + CPT * (8 * (j >> 2) + 4 * g + (j & 3));
+      const int k = k0 + wn * (NT * 32) + CPT * column_of_row(8 * (j >> 2) + 4 * g + (j & 3));
       if (t >= T || k >= K) continue;  // K is a multiple of 32
       float v[CPT];
 #pragma unroll
@@ -265,15 +278,23 @@ BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, b
 static int launch_dx(const uint16_t* dz, int ldz, const uint8_t* w, const uint8_t* s, uint16_t* dx, float alpha,
                      const TilePlan& p, float* parts, int T, int K, int N, hipStream_t stream) {
   const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE(MT, NT)                                                                                              \
-  hipLaunchKernelGGL((backward_kernel<MT, NT>), grid, dim3(256), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, ldz, \
-                     p.mtiles, p.ntiles, p.nsplit)
-  if (p.mt == 4)
+  const bool s4 = K % 128 == 0 && aligned(s, 4);
+#define MX_TILE1(MT, NT, S4)                                                                                       \
+  hipLaunchKernelGGL((backward_kernel<MT, NT, S4>), grid, dim3(256), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, \
+                     ldz, p.mtiles, p.ntiles, p.nsplit)
+#define MX_TILE(MT, NT)        \
+  if (s4)                      \
+    MX_TILE1(MT, NT, true);    \
+  else                         \
+    MX_TILE1(MT, NT, false)
+  if (p.mt == 4) {
     MX_TILE(4, 4);
-  else if (p.mt == 2)
+  } else if (p.mt == 2) {
     MX_TILE(2, 2);
-  else
+  } else {
     MX_TILE(1, 2);
+  }
+#undef MX_TILE1
 #undef MX_TILE
   if (p.nsplit > 1) {
     const int64_t pieces = (int64_t)T * (K / 8);

@@ -178,7 +178,7 @@ int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float
 int launch_norm_residual(const uint16_t* x, const uint16_t* b, const uint16_t* w_post, const uint16_t* gate,
                          int gate_mode, float scale, const uint16_t* w_pre, float eps, uint16_t* y, uint16_t* xn, int T,
                          int H, hipStream_t stream);
-int norm_backward_groups(int64_t T);
+int norm_backward_groups(int64_t T, int64_t H);
 int launch_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const uint16_t* y, const uint16_t* b,
                                   const uint16_t* w_post, const uint16_t* gate, int gate_mode, float scale,
                                   const uint16_t* w_pre, float eps, uint16_t* dx, uint16_t* db, void* dgate,

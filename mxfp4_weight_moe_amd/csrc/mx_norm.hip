@@ -45,26 +45,45 @@ __device__ __forceinline__ u32x4 pack8(const float (&v)[8]) {
   return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
 
-// Sums of S values over the workgroup, in every thread; a fixed order.  `red` is used once per
-// parity, so that one barrier is enough.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_value(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
+}
+
+// Sum over groups of N consecutive lanes (N = 4, 8 or 16), in every lane, in a fixed order: the
+// lanes exchange in the vector unit (a shuffle through the LDS takes some 60 cycles).
+template <int N>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v += dpp<0xB1>(v);                        // lane ^ 1
+  v += dpp<0x4E>(v);                        // lane ^ 2
+  if constexpr (N >= 8) v += dpp<0x141>(v);   // mirrored within 8: the other 4
+  if constexpr (N >= 16) v += dpp<0x140>(v);  // mirrored within 16: the other 8
+  return v;
+}
+// Sum over the wave, in every lane: the rows of 16 lanes are read as scalars.
+__device__ __forceinline__ float wave_sum(float v) {
+  v = lanes_sum<16>(v);
+  return (lane_value(v, 0) + lane_value(v, 16)) + (lane_value(v, 32) + lane_value(v, 48));
+}
+
+// Sums of S values over the workgroup, in every thread; a fixed order.  The caller leaves a
+// barrier between two uses of the same `red`.
 template <int NT, int S>
-__device__ __forceinline__ void block_sum(float (&v)[S], float (*red)[S]) {
+__device__ __forceinline__ void block_sum(float (&v)[S], float (*red)[NT / 64]) {
 #pragma unroll
-  for (int k = 0; k < S; ++k)
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) v[k] += __shfl_xor(v[k], o, 64);
+  for (int k = 0; k < S; ++k) v[k] = wave_sum(v[k]);
   if constexpr (NT > 64) {
+    constexpr int W = NT / 64;
     const int wave = threadIdx.x >> 6;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
-      for (int k = 0; k < S; ++k) red[wave][k] = v[k];
+      for (int k = 0; k < S; ++k) red[k][wave] = v[k];
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      v[k] = red[0][k];
-#pragma unroll
-      for (int i = 1; i < NT / 64; ++i) v[k] += red[i][k];
-    }
+    for (int k = 0; k < S; ++k) v[k] = lanes_sum<W>(red[k][threadIdx.x & (W - 1)]);
   }
 }
 
@@ -73,7 +92,7 @@ constexpr u32x4 ZERO4 = {0u, 0u, 0u, 0u};
 // BLK: there is a block output; POST: it is normalized; PRE: y is normalized.
 template <int NT, int V, bool BLK, bool POST, bool PRE>
 __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
-  __shared__ float red[2][NT / 64][1];
+  __shared__ float red[2][NT / 64];
   const int vecs = a.H / 8;
   u32x4 wpost[V], wpre[V], gch[V];
   int at[V];
@@ -109,7 +128,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) ss[0] = __builtin_fmaf(v[j], v[j], ss[0]);
         }
-        block_sum<NT, 1>(ss, red[0]);
+        block_sum<NT, 1>(ss, &red[0]);
         q = rsqrtf(ss[0] * inv_h + a.eps);
       }
       float tok = a.scale;
@@ -140,7 +159,7 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss[0] = __builtin_fmaf(v[j], v[j], ss[0]);
       }
-      block_sum<NT, 1>(ss, red[1]);
+      block_sum<NT, 1>(ss, &red[1]);
       const float q = rsqrtf(ss[0] * inv_h + a.eps);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -156,48 +175,74 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
   }
 }
 
-template <int NT, int V, bool BLK, bool POST, bool PRE>
+// The rows of the backward pass's inputs that one thread holds.
+template <int V>
+struct NormRow {
+  u32x4 d[V], y[V], n[V], b[V];  // dy, y, dxn, b
+};
+
+// What was unpacked from p before is unpacked again: 4 packed registers live on, not 8 floats.
+__device__ __forceinline__ void repack(u32x4& p) { asm volatile("" : "+v"(p)); }
+
+// AHEAD: the next row is loaded while this one is worked on (a workgroup of 8 waves is alone on
+// its CU with the registers this takes; without it the CU waited for memory at each row:
+// 101 us instead of 71 at T = 4096, H = 7168).
+template <int NT, int V, bool BLK, bool POST, bool PRE, bool AHEAD>
 __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
-  __shared__ float red1[NT / 64][3];
-  __shared__ float red2[NT / 64][2];
+  __shared__ float red1[3][NT / 64];
+  __shared__ float red2[2][NT / 64];
   const int vecs = a.H / 8;
   int at[V];
   bool ok[V];
   float gpre[PRE ? V : 1][8] = {}, gpost[POST ? V : 1][8] = {}, ggate[BLK ? V : 1][8] = {};
+  u32x4 wpre[V], wpost[V], gch[V];
+  const bool channel = BLK && a.gate_mode == MX_GATE_CHANNEL, full = BLK && a.gate_mode == MX_GATE_FULL;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     at[i] = i * NT + threadIdx.x;
     ok[i] = at[i] < vecs;
+    wpre[i] = (PRE && ok[i]) ? ld16(a.w_pre + at[i] * 8) : ZERO4;
+    wpost[i] = (POST && ok[i]) ? ld16(a.w_post + at[i] * 8) : ZERO4;
+    gch[i] = (channel && ok[i]) ? ld16(a.gate + at[i] * 8) : ZERO4;
   }
-  const float inv_h = 1.f / (float)a.H;
-  const bool channel = BLK && a.gate_mode == MX_GATE_CHANNEL;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+  auto load_row = [&](int t) {
+    NormRow<V> r;
     const size_t row = (size_t)t * a.H;
-    u32x4 dv[V], yv[V], nv[V], bv[V], gv[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const size_t p = row + at[i] * 8;
-      dv[i] = (a.dy && ok[i]) ? ld16(a.dy + p) : ZERO4;
+      r.d[i] = (a.dy && ok[i]) ? ld16(a.dy + p) : ZERO4;
       if constexpr (PRE) {
-        yv[i] = ok[i] ? ld16(a.x + p) : ZERO4;
-        nv[i] = ok[i] ? ld16(a.dxn + p) : ZERO4;
+        r.y[i] = ok[i] ? ld16(a.x + p) : ZERO4;
+        r.n[i] = ok[i] ? ld16(a.dxn + p) : ZERO4;
       }
-      if constexpr (BLK) {
-        bv[i] = ok[i] ? ld16(a.b + p) : ZERO4;
-        gv[i] = !ok[i] ? ZERO4
-                : channel ? ld16(a.gate + at[i] * 8)
-                : a.gate_mode == MX_GATE_FULL ? ld16(a.gate + p) : ZERO4;
-      }
+      if constexpr (BLK) r.b[i] = ok[i] ? ld16(a.b + p) : ZERO4;
     }
+    return r;
+  };
+  const float inv_h = 1.f / (float)a.H;
+  NormRow<V> cur;
+  if (AHEAD) cur = load_row(blockIdx.x);
+  for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    const size_t row = (size_t)t * a.H;
+    NormRow<V> next;
+    if (full) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) gch[i] = ok[i] ? ld16(a.gate + row + at[i] * 8) : ZERO4;
+    }
+    if constexpr (AHEAD)
+      next = load_row(min(t + (int)gridDim.x, a.T - 1));
+    else
+      cur = load_row(t);
     // reduction 1: sum y^2, sum dxn w_pre y, sum b^2
     float s1[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if constexpr (PRE) {
         float y[8], d[8], w[8];
-        unpack8(yv[i], y);
-        unpack8(nv[i], d);
-        unpack8(ok[i] ? ld16(a.w_pre + at[i] * 8) : ZERO4, w);
+        unpack8(cur.y[i], y);
+        unpack8(cur.n[i], d);
+        unpack8(wpre[i], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           s1[0] = __builtin_fmaf(y[j], y[j], s1[0]);
@@ -206,7 +251,7 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
       }
       if constexpr (POST) {
         float b[8];
-        unpack8(bv[i], b);
+        unpack8(cur.b[i], b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) s1[2] = __builtin_fmaf(b[j], b[j], s1[2]);
       }
@@ -214,6 +259,11 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
     float r = 0.f, rc = 0.f, q = 1.f;
     if constexpr (PRE || POST) {
       block_sum<NT, 3>(s1, red1);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        if constexpr (PRE) repack(cur.y[i]), repack(cur.n[i]), repack(wpre[i]);
+        if constexpr (POST) repack(cur.b[i]);
+      }
       r = rsqrtf(s1[0] * inv_h + a.eps);
       rc = r * r * s1[1] * inv_h;
       q = rsqrtf(s1[2] * inv_h + a.eps);
@@ -224,12 +274,12 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
     float s2[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      unpack8(dv[i], e[i]);
+      unpack8(cur.d[i], e[i]);
       if constexpr (PRE) {
         float y[8], d[8], w[8];
-        unpack8(yv[i], y);
-        unpack8(nv[i], d);
-        unpack8(ok[i] ? ld16(a.w_pre + at[i] * 8) : ZERO4, w);
+        unpack8(cur.y[i], y);
+        unpack8(cur.n[i], d);
+        unpack8(wpre[i], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           gpre[i][j] = __builtin_fmaf(d[j], y[j] * r, gpre[i][j]);
@@ -239,9 +289,9 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
       if (ok[i]) *reinterpret_cast<u32x4*>(a.y + row + at[i] * 8) = pack8(e[i]);
       if constexpr (BLK) {
         float b[8], g[8], w[8];
-        unpack8(bv[i], b);
-        unpack8(gv[i], g);
-        if constexpr (POST) unpack8(ok[i] ? ld16(a.w_post + at[i] * 8) : ZERO4, w);
+        unpack8(cur.b[i], b);
+        unpack8(gch[i], g);
+        if constexpr (POST) unpack8(wpost[i], w);
         float dg[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -258,19 +308,23 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
             s2[0] = __builtin_fmaf(e[i][j], b[j], s2[0]);
           }
         }
-        if (a.gate_mode == MX_GATE_FULL && a.dgate && ok[i])
+        if (full && a.dgate && ok[i])
           *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.dgate) + row + at[i] * 8) = pack8(dg);
       }
     }
     if constexpr (BLK) {
       if (POST || a.gate_mode == MX_GATE_TOKEN) block_sum<NT, 2>(s2, red2);
+      if constexpr (POST) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) repack(cur.b[i]);
+      }
       if (a.gate_mode == MX_GATE_TOKEN && a.dgate && threadIdx.x == 0) static_cast<float*>(a.dgate)[t] = s2[1];
       const float qc = q * q * s2[0] * inv_h;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if constexpr (POST) {
           float b[8];
-          unpack8(bv[i], b);
+          unpack8(cur.b[i], b);
 #pragma unroll
           for (int j = 0; j < 8; ++j) e[i][j] = q * (e[i][j] - b[j] * qc);
         }
@@ -278,6 +332,7 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
       }
     }
     if constexpr (NT > 64) __syncthreads();
+    if constexpr (AHEAD) cur = next;
   }
   if (!a.parts) return;
   float* p = a.parts + (size_t)blockIdx.x * a.arrays * a.H;
@@ -305,32 +360,37 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
 // ------------------------------------------------------------------ launches
 
 // Threads and 16-byte pieces per thread for a row of H values.
-#define MX_NORM_SIZES(CALL)    \
-  const int vecs = a.H / 8;    \
-  if (vecs <= 64)              \
-    CALL(64, 1);               \
-  else if (vecs <= 256)        \
-    CALL(256, 1);              \
-  else if (vecs <= 512)        \
-    CALL(256, 2);              \
-  else if (vecs <= 1024)       \
-    CALL(512, 2);              \
-  else                         \
-    CALL(1024, 2)
+#define MX_NORM_SIZES_8192(CALL) \
+  if (a.H <= 512)                \
+    CALL(64, 1);                 \
+  else if (a.H <= 2048)          \
+    CALL(256, 1);                \
+  else if (a.H <= 4096)          \
+    CALL(512, 1);                \
+  else                           \
+    CALL(1024, 1)
 
 template <bool BLK, bool POST, bool PRE>
 static void norm_forward(const NormArgs& a, hipStream_t stream) {
   const dim3 grid((unsigned)std::min(a.T, 8 * GPU_CUS));
 #define MX_CALL(NT, V) hipLaunchKernelGGL((norm_kernel<NT, V, BLK, POST, PRE>), grid, dim3(NT), 0, stream, a)
-  MX_NORM_SIZES(MX_CALL);
+  if (a.H > 8192)
+    MX_CALL(1024, 2);
+  else
+    MX_NORM_SIZES_8192(MX_CALL);
 #undef MX_CALL
 }
 
+// Beyond 8192 values a thread has two pieces of a row, and no registers for the row ahead.
 template <bool BLK, bool POST, bool PRE>
 static void norm_backward(const NormArgs& a, int groups, hipStream_t stream) {
 #define MX_CALL(NT, V) \
-  hipLaunchKernelGGL((norm_backward_kernel<NT, V, BLK, POST, PRE>), dim3(groups), dim3(NT), 0, stream, a)
-  MX_NORM_SIZES(MX_CALL);
+  hipLaunchKernelGGL((norm_backward_kernel<NT, V, BLK, POST, PRE, true>), dim3(groups), dim3(NT), 0, stream, a)
+  if (a.H > 8192) {
+    hipLaunchKernelGGL((norm_backward_kernel<1024, 2, BLK, POST, PRE, false>), dim3(groups), dim3(1024), 0, stream, a);
+    return;
+  }
+  MX_NORM_SIZES_8192(MX_CALL);
 #undef MX_CALL
 }
 
@@ -349,8 +409,10 @@ int launch_norm_residual(const uint16_t* x, const uint16_t* b, const uint16_t* w
   return hip_status(hipGetLastError());
 }
 
-// Workgroups of the backward launch: two per CU, each with T / groups rows.
-int norm_backward_groups(int64_t T) { return (int)std::min<int64_t>(T, 2 * GPU_CUS); }
+// Workgroups of the backward launch, each with T / groups rows: what the CUs hold at once.
+int norm_backward_groups(int64_t T, int64_t H) {
+  return (int)std::min<int64_t>(T, H <= 512 ? 4 * GPU_CUS : H <= 4096 ? 2 * GPU_CUS : GPU_CUS);
+}
 
 int launch_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const uint16_t* y, const uint16_t* b,
                                   const uint16_t* w_post, const uint16_t* gate, int gate_mode, float scale,
@@ -370,7 +432,7 @@ int launch_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const
   bool any = false;
   for (int i = 0; i < n; ++i) any = any || out[i];
   a.parts = any ? parts : nullptr;
-  const int groups = norm_backward_groups(T);
+  const int groups = norm_backward_groups(T, H);
   if (!b)
     norm_backward<false, false, true>(a, groups, stream);
   else if (w_post)

@@ -12,8 +12,9 @@
 // multiplies with them: 4 conversions decode a fragment that MT matrix instructions use.
 //
 // 16-byte LDS reads go 16 lanes at a time over 64 banks, in the lane groups 0-3, 12-15, 20-23,
-// 24-27 and 4-7, 8-11, 16-19, 28-31 (and the same 32 lanes on); the layouts below give the 16
-// lanes of a group 16 different 16-byte columns.
+// 24-27 and 4-7, 8-11, 16-19, 28-31 (and the same 32 lanes on), 16-byte writes 8 consecutive
+// lanes at a time over 32 banks (as the conflict counter has it for test patterns); the layouts
+// below give the lanes of a group different 16-byte columns.
 #pragma once
 #include <utility>
 
@@ -464,8 +465,11 @@ constexpr int BWD_KB = 64;  // reduction values (weight rows) per stage
 // chunk, so that every weight is decoded once a workgroup and the LDS holds both operands in
 // the same form: rows of 64 reduction values.  (Decoding in the registers of each wave that
 // multiplies takes twice the conversions and as many LDS reads: 64 x 256 weights a stage.)
-// Column CPT (R & 15) + 2 i + (R >> 4) of a wave's is MFMA row R of its tile i: the threads'
-// writes then go to consecutive LDS rows, and a lane's results are CPT consecutive columns.
+// Column CPT q + 2 i + (R >> 4) of a wave's, with R & 15 = column_row(q), is MFMA row R of its
+// tile i: a lane's results are then CPT consecutive columns, and the rows that 8 consecutive
+// threads write (every other one) have different keys.
+__device__ __forceinline__ int column_row(int q) { return ((q & 7) << 1) | (q >> 3); }   // q < 16
+__device__ __forceinline__ int column_of_row(int r) { return (r >> 1) | ((r & 1) << 3); }  // its inverse
 template <int NT>
 struct ColumnStage {
   static constexpr int CPT = 2 * NT;              // columns of a thread: WN * NT * 32 over 32 threads
@@ -484,7 +488,10 @@ struct BackwardLds {
 // those past N zero.  As in forward_tile, what prepares the next step and the next stage goes
 // between the matrix instructions: reads of both operands' fragments, decoding the weights of
 // the next stage, whose codes were loaded a stage before, and copies of its dz rows.
-template <int MT, int NT>
+// S4: K % 128 == 0 and s is 4-byte aligned; a row's scale then comes with the 4 bytes around
+// it.  (A loaded byte is widened where the loop begins, long before its use, and the wave
+// waits for it there.)
+template <int MT, int NT, bool S4>
 __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>::Rows& rows,
                                               const uint8_t* __restrict__ w, const uint8_t* __restrict__ s, int N,
                                               int K, int k0, int st0, int st1, uint8_t* lds, int wm, int wn, int lane,
@@ -495,12 +502,13 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   const int r = lane & 31, g = lane >> 5, o = threadIdx.x >> 5, q = threadIdx.x & 31;
   const int wld = K >> 1, sld = K >> 5;
   const int col = min(k0 + CPT * q, K - CPT);  // columns past K: the last ones again, never stored
+  const int block = col >> 5, sshift = S4 ? 8 * (block & 3) : 0, sfirst = S4 ? block & ~3 : block;
   // byte offsets of this thread's 8 rows from the stage's first
   uint32_t woff[8], soff[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     woff[i] = (uint32_t)((o * 8 + i) * wld + (col >> 1));
-    soff[i] = (uint32_t)((o * 8 + i) * sld + (col >> 5));
+    soff[i] = (uint32_t)((o * 8 + i) * sld + sfirst);
   }
   uint32_t at[4], wat[4];  // LDS byte offsets of this lane's chunks at step u, first tile
 #pragma unroll
@@ -508,17 +516,27 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
     at[u] = (uint32_t)(wm * MT * 32 + r) * 128 + (((2 * u + g) ^ row_key<8>(r)) << 4);
     wat[u] = L::Rows::BYTES + (uint32_t)(wn * NT * 32 + r) * 128 + (((2 * u + g) ^ row_key<8>(r)) << 4);
   }
-  // where this thread's columns go: LDS row 16 i + (q & 15) of its wave column, chunk o
-  const uint32_t put = L::Rows::BYTES + (uint32_t)((q >> 4) * NT * 32 + (q & 15)) * 128 + ((o ^ row_key<8>(q & 15)) << 4);
+  // where this thread's columns go: LDS row 16 i + column_row(q & 15) of its wave column, chunk o
+  const int qrow = column_row(q & 15);
+  const uint32_t put = L::Rows::BYTES + (uint32_t)((q >> 4) * NT * 32 + qrow) * 128 + ((o ^ row_key<8>(qrow)) << 4);
   uint32_t code[8], sb[8];  // of the stage after the current one
   u32x4 frag[2][MT], wf[2][NT], column[2];
-  auto load_one = [&](int st, int i) {
-    const uint8_t* wb = w + (size_t)st * BWD_KB * wld;
+  // The first weight row of the stage that load_one loads from, moved on a stage at a time.
+  const uint8_t* wstage = w + (size_t)st0 * BWD_KB * wld;
+  const uint8_t* sstage = s + (size_t)st0 * BWD_KB * sld;
+  auto load_one = [&](int i) {
     if constexpr (CPT == 8)
-      code[i] = *reinterpret_cast<const uint32_t*>(wb + woff[i]);
+      code[i] = *reinterpret_cast<const uint32_t*>(wstage + woff[i]);
     else
-      code[i] = *reinterpret_cast<const uint16_t*>(wb + woff[i]);
-    sb[i] = (s + (size_t)st * BWD_KB * sld)[soff[i]];
+      code[i] = *reinterpret_cast<const uint16_t*>(wstage + woff[i]);
+    if constexpr (S4)
+      sb[i] = *reinterpret_cast<const uint32_t*>(sstage + soff[i]);
+    else
+      sb[i] = sstage[soff[i]];
+  };
+  auto move_on = [&](bool yes) {
+    wstage += yes ? BWD_KB * wld : 0;
+    sstage += yes ? BWD_KB * sld : 0;
   };
   // Rows past N (in the last stage): their addresses are moved to row N - 1 before they are
   // loaded, and their values replaced by zero codes with scale 1 before they are used.
@@ -528,19 +546,20 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
     for (int i = 0; i < 8; ++i) {
       const int row = min(o * 8 + i, left - 1);
       woff[i] = (uint32_t)(row * wld + (col >> 1));
-      soff[i] = (uint32_t)(row * sld + (col >> 5));
+      soff[i] = (uint32_t)(row * sld + sfirst);
     }
   };
   auto clear_rows = [&]() {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (o * 8 + i >= left) code[i] = 0u, sb[i] = 127u;
+      if (o * 8 + i >= left) code[i] = 0u, sb[i] = 127u << sshift;
   };
   // half of column pair b, row pair p2: rows 2 p2 and 2 p2 + 1
   auto decode_pair = [&](auto B, auto P2) __attribute__((always_inline)) {
     constexpr int b = B, p2 = P2;
-    const uint32_t lo = decode2<b>(code[2 * p2], e8m0_scale_operand(sb[2 * p2]));
-    const uint32_t hi = decode2<b>(code[2 * p2 + 1], e8m0_scale_operand(sb[2 * p2 + 1]));
+    auto scale = [&](int i) { return e8m0_scale_operand(S4 ? (sb[i] >> sshift) & 0xFFu : sb[i]); };
+    const uint32_t lo = decode2<b>(code[2 * p2], scale(2 * p2));
+    const uint32_t hi = decode2<b>(code[2 * p2 + 1], scale(2 * p2 + 1));
     column[0][p2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);  // low halves: column 2b
     column[1][p2] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
   };
@@ -558,7 +577,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   const bool ragged = left < BWD_KB;
   if (ragged && st0 == last_stage) clamp_rows();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_one(st0, i);
+  for (int i = 0; i < 8; ++i) load_one(i);
   rows.copy(lds, st0);
   if (ragged && st0 == last_stage) clear_rows();
   unrolled<NT>([&](auto B) __attribute__((always_inline)) {
@@ -567,9 +586,10 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
     put_column(lds, B, 1);
   });
   const int second = min(st0 + 1, st1 - 1);
+  move_on(second > st0);
   if (ragged && second == last_stage) clamp_rows();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_one(second, i);
+  for (int i = 0; i < 8; ++i) load_one(i);
   wait_copies();
   __syncthreads();
 #pragma unroll
@@ -582,6 +602,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
     // the stages that are decoded and copied, and loaded, meanwhile; past the last one that one
     // again, which nothing uses
     const int cs = min(st + 1, st1 - 1), ls = min(st + 2, st1 - 1);
+    move_on(ls > cs);
     if (ragged) {
       if (cs == last_stage) clear_rows();
       if (ls == last_stage) clamp_rows();
@@ -626,7 +647,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
           constexpr int per_load = (8 + SLOTS - 1) / SLOTS;
           unrolled<per_load>([&](auto E) __attribute__((always_inline)) {
             constexpr int e = k * per_load + E;
-            if constexpr (e < 8) load_one(ls, e);
+            if constexpr (e < 8) load_one(e);
           });
         }
         keep_order();
