@@ -399,8 +399,8 @@ MX_API int moe_mxfp4_forward_persistent(const uint16_t* x, const float* router_l
  *   - 1 <= T <= 2^24; a reduction length K (or H, I where they are one) is a multiple of 32
  *     with 32 <= K <= 2^20; weight rows N (or 2I) <= 2^22, any number; no activation tensor
  *     has more than 2^38 values.  MX_ERR_SHAPE otherwise.
- *   - bf16 tensors are 16-byte aligned, weight codes 16, fp32 outputs 4; weight scales 8 where
- *     the reduction length of a forward call is a multiple of 256 (else 1).
+ *   - bf16 tensors are 16-byte aligned, weight codes 16, fp32 outputs 4; weight scales of a
+ *     forward call 8 where its reduction length is a multiple of 256, 4 where it is one of 128.
  *   - `workspace` is scratch of at least the size that the call's *_workspace_size gives (0:
  *     it may be NULL), 256-byte aligned; it needs no initialization, and calls that share one
  *     must not overlap in time.  *_workspace_size returns 0 for sizes that the call rejects.

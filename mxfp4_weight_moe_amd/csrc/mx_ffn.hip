@@ -227,24 +227,182 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
   }
 }
 
+// ------------------------------------------------------------------ 33 to 128 tokens: thin tiles
+
+// A workgroup takes 32 NT weight rows (gate_up: half of them gate rows, half the up rows of the
+// same columns) and a wave each 32 tokens.  A wave loads everything it needs by itself, its
+// activation rows and its own copy of the codes and scales, into a ring of its own in the LDS:
+// no barriers.  With N >= 6144 or so and NT = 1 there is no split of K either, whose second
+// launch costs 3 to 4 us at these sizes; with fewer rows NT = 2 halves the activations that a
+// CU reads beside the same weights, and K is split.
+constexpr int THIN_MAX_T = 128;
+template <int NT>
+struct ThinStage {
+  static constexpr int D = 3;  // stages in the ring
+  static constexpr int CODES = 32 * 256, SCALES = CODES + NT * 32 * 64, BYTES = SCALES + 256;
+  static constexpr int LOADS = 8 + 2 * NT + 1;  // a stage's copies to LDS
+};
+
+template <int NT, bool GATED>
+__global__ void __launch_bounds__(256, 1)
+    thin_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
+                typename EpilogueOf<GATED>::type epi, float* __restrict__ parts, int T, int K, int rows, int ntiles,
+                int nsplit) {
+  typedef ThinStage<NT> L;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[4 * L::D * L::BYTES];
+  constexpr int COLS = GATED ? 16 * NT : 32 * NT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int tile = xcd_tile(blockIdx.x, ntiles * nsplit);
+  const int split = tile % nsplit, n0 = tile / nsplit * COLS, m0 = wave * 32;
+  const int stages = K / FWD_KB;
+  const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
+  uint8_t* ring = lds + wave * (L::D * L::BYTES);
+
+  // Rows that do not exist lie past the end of their buffers and read as zero.
+  const buffer xbuf = make_buffer(x + (size_t)m0 * K, (uint64_t)min(32, T - m0) * (uint64_t)K * 2);
+  uint32_t xoff[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const int r = q * 4 + (lane >> 4);
+    xoff[q] = (uint32_t)r * (uint32_t)(K * 2) + (((lane & 15) ^ (r & 15)) << 4);
+  }
+  // Row lr of the workgroup's 32 NT: weight row n0 + lr, or column n0 + lr % COLS of half lr / COLS.
+  buffer wbuf[2 * NT];
+  uint32_t woff[2 * NT];
+#pragma unroll
+  for (int q = 0; q < 2 * NT; ++q) {
+    const int r = q * 16 + (lane >> 2), c = GATED ? q * 16 % COLS : q * 16;
+    const int have = max(0, min(16, rows - n0 - c));
+    const size_t first = (size_t)n0 + c + (GATED && q >= NT ? (size_t)rows : 0);
+    wbuf[q] = make_buffer(w + first * (size_t)(K >> 1), (uint64_t)have * (uint64_t)(K >> 1));
+    woff[q] = (uint32_t)(lane >> 2) * (uint32_t)(K >> 1) + (((lane & 3) ^ ((r >> 3) & 3)) << 4);
+  }
+  const buffer sbuf = make_buffer(s + (size_t)n0 * (K >> 5),
+                                  ((uint64_t)min(COLS, rows - n0) + (GATED ? rows : 0)) * (uint64_t)(K >> 5));
+  const int slr = lane & (32 * NT - 1);
+  const uint32_t soff = (GATED && slr >= COLS ? (uint32_t)rows + slr - COLS : (uint32_t)slr) * (uint32_t)(K >> 5);
+  auto load = [&](int st, uint8_t* buf) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) copy16_to_lds(xbuf, xoff[q], (uint32_t)st * 256, buf + q * 1024);
+#pragma unroll
+    for (int q = 0; q < 2 * NT; ++q) copy16_to_lds(wbuf[q], woff[q], (uint32_t)st * 64, buf + L::CODES + q * 1024);
+    copy4_to_lds(sbuf, soff, (uint32_t)st * 4, buf + L::SCALES);
+  };
+  const int r = lane & 31, g = lane >> 5;
+  struct Operands {
+    u32x4 x[8], code[NT][2];
+    uint32_t scale[NT];
+  };
+  auto read = [&](const uint8_t* buf) {
+    Operands o;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      o.scale[i] = *reinterpret_cast<const uint32_t*>(buf + L::SCALES + (i * 32 + r) * 4);
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        o.code[i][b] = ld16(buf + L::CODES + (i * 32 + r) * 64 + (((2 * b + g) ^ (r >> 3)) << 4));
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) o.x[u] = ld16(buf + r * 256 + (((8 * (u >> 2) + 4 * g + (u & 3)) ^ (r & 15)) << 4));
+    return o;
+  };
+  f32x16 acc[2][NT] = {};  // even and odd steps: chains of products that do not wait for one another
+  uint8_t* cur = ring;
+  uint8_t* nxt = ring + L::BYTES;
+  uint8_t* fill = ring + 2 * L::BYTES;
+  static_assert(L::D == 3, "three buffers");
+  load(st0, cur);
+  load(min(st0 + 1, st1 - 1), nxt);
+  wait_copies<L::LOADS>();
+  Operands o = read(cur);
+  for (int st = st0; st < st1; ++st) {
+    load(min(st + 2, st1 - 1), fill);  // its last content was used two stages ago
+    wait_copies<L::LOADS>();           // the next stage has landed
+    const Operands next = read(nxt);
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+#pragma unroll
+      for (int i = 0; i < NT; ++i) {
+        const uint32_t d = o.scale[i] >> (8 * g);
+        const float sc = e8m0_scale_operand(u < 4 ? d & 0xFFu : (d >> 16) & 0xFFu);
+        acc[u & 1][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(decode8(o.code[i][u >> 2][u & 3], sc),
+                                                                as_bf16x8(o.x[u]), acc[u & 1][i], 0, 0, 0);
+      }
+    o = next;
+    uint8_t* t = cur;
+    cur = nxt;
+    nxt = fill;
+    fill = t;
+  }
+  wait_copies();  // the repeated copies of the last stages: the ring is used again
+#pragma unroll
+  for (int i = 0; i < NT; ++i) acc[0][i] += acc[1][i];
+  tile_to_lds<NT>(ring, acc[0], lane);
+  const int pc = part_cols(rows);
+  constexpr int PIECES = COLS / 8, ROWS = 64 / PIECES;
+  const int p = lane % PIECES, n = n0 + p * 8;
+  const auto cols = epi.template columns<8>(n);
+#pragma unroll
+  for (int it = 0; it < 32 / ROWS; ++it) {
+    const int row = it * ROWS + lane / PIECES, t = m0 + row;
+    if (t >= T || n >= rows) continue;
+    f32x4 q[GATED ? 4 : 2];
+#pragma unroll
+    for (int j = 0; j < (GATED ? 4 : 2); ++j)
+      q[j] = *reinterpret_cast<const f32x4*>(ring + out_at<NT>(row, 2 * p + (j & 1) + (j >> 1) * (4 * NT)));
+    if (nsplit > 1) {
+      float* o2 = parts + ((size_t)split * T + t) * ((GATED ? 2 : 1) * (size_t)pc) + n;
+#pragma unroll
+      for (int j = 0; j < (GATED ? 4 : 2); ++j) *reinterpret_cast<f32x4*>(o2 + (j >> 1) * pc + (j & 1) * 4) = q[j];
+      continue;
+    }
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = q[j >> 2][j & 3];
+    if constexpr (GATED) {
+      float u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = q[2 + (j >> 2)][j & 3];
+      epi.template store<8>(t, n, v, u, cols);
+    } else {
+      epi.template store<8>(t, n, v, cols, epi.template fetch<8>(t, n));
+    }
+  }
+}
+
 // Sums the parts of a split K in ascending order and applies the epilogue: 8 columns a thread.
 template <bool GATED>
-__global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ parts,
+__global__ void __launch_bounds__(64) combine_kernel(const float* __restrict__ parts,
                                                       typename EpilogueOf<GATED>::type epi, int T, int pc, int nsplit) {
   const int per_row = pc / 8;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
   if (id >= (int64_t)T * per_row) return;
   const int t = (int)(id / per_row), n = (int)(id % per_row) * 8;
   const size_t ld = GATED ? 2 * (size_t)pc : (size_t)pc;
   const float* p = parts + (size_t)t * ld + n;
   const size_t step = (size_t)T * ld;
   f32x4 a[2] = {}, b[2] = {};
-  for (int z = 0; z < nsplit; ++z, p += step) {
-    a[0] += *reinterpret_cast<const f32x4*>(p);
-    a[1] += *reinterpret_cast<const f32x4*>(p + 4);
-    if constexpr (GATED) {
-      b[0] += *reinterpret_cast<const f32x4*>(p + pc);
-      b[1] += *reinterpret_cast<const f32x4*>(p + pc + 4);
+  for (int z0 = 0; z0 < nsplit; z0 += 4) {  // four parts' loads at a time
+    f32x4 q[4][GATED ? 4 : 2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* r = p + min(z0 + k, nsplit - 1) * step;
+      q[k][0] = *reinterpret_cast<const f32x4*>(r);
+      q[k][1] = *reinterpret_cast<const f32x4*>(r + 4);
+      if constexpr (GATED) {
+        q[k][2] = *reinterpret_cast<const f32x4*>(r + pc);
+        q[k][3] = *reinterpret_cast<const f32x4*>(r + pc + 4);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (z0 + k >= nsplit) break;
+      a[0] += q[k][0];
+      a[1] += q[k][1];
+      if constexpr (GATED) {
+        b[0] += q[k][2];
+        b[1] += q[k][3];
+      }
     }
   }
   float v[8], u[8];
@@ -264,14 +422,26 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* __restrict__ 
 TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated) {
   TilePlan p{};
   if (T <= STREAM_MAX_T || K < FWD_KB) return p;
-  p.mt = T > 1024 ? 4 : T > 64 ? 2 : 1;
-  p.nt = p.mt == 4 ? 4 : 2;
-  const int bm = 64 * p.mt, cols = (gated ? 32 : 64) * p.nt;
-  p.mtiles = (int)((T + bm - 1) / bm);
-  p.ntiles = (int)((rows + cols - 1) / cols);
-  const int64_t tiles = (int64_t)p.mtiles * p.ntiles, stages = (K + FWD_KB - 1) / FWD_KB;
-  int64_t split = tiles >= GPU_CUS ? 1 : GPU_CUS / tiles;
-  p.nsplit = (int)std::max<int64_t>(1, std::min(split, stages / 2));
+  const int64_t stages = (K + FWD_KB - 1) / FWD_KB;
+  int64_t split;
+  if (T <= THIN_MAX_T && K % FWD_KB == 0 && rows * (K >> 5) < ((int64_t)1 << 31)) {
+    p.mtiles = 1;
+    p.thin = 1;
+    p.ntiles = (int)((rows + (gated ? 15 : 31)) / (gated ? 16 : 32));
+    if (4 * p.ntiles < 3 * GPU_CUS) {  // measured: H = 7168, I = 2048, T = 128
+      p.thin = 2;
+      p.ntiles = (p.ntiles + 1) / 2;
+    }
+    split = std::min<int64_t>(GPU_CUS / p.ntiles, stages / 4);
+  } else {
+    p.mt = T > 1024 ? 4 : T > 64 ? 2 : 1;
+    p.nt = p.mt == 4 ? 4 : 2;
+    const int bm = 64 * p.mt, cols = (gated ? 32 : 64) * p.nt;
+    p.mtiles = (int)((T + bm - 1) / bm);
+    p.ntiles = (int)((rows + cols - 1) / cols);
+    split = std::min<int64_t>(GPU_CUS / std::max<int64_t>(1, (int64_t)p.mtiles * p.ntiles), stages / 2);
+  }
+  p.nsplit = (int)std::max<int64_t>(1, split);
   if (p.nsplit > 1) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows) * (gated ? 2 : 1) * 4;
   return p;
 }
@@ -317,12 +487,19 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
   // One tile a CU and K in whole stages: more stages in the LDS.  Measured at T = 128 with
   // H = 7168, I = 2048 (7 stages a workgroup); see forward_tile.
-  const bool deep = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS && K % FWD_KB == 0 && aligned(s, 4) &&
+  const bool deep = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS && K % FWD_KB == 0 &&
                     (int64_t)rows * (K >> 5) < ((int64_t)1 << 31);
 #define MX_TILE(MT, NT, D)                                                                                           \
   hipLaunchKernelGGL((forward_kernel<MT, NT, 2, 2, D, GATED>), grid, dim3(256), 0, stream, x, w, s, epi, parts, T, K, \
                      rows, p.mtiles, p.ntiles, p.nsplit)
-  if (p.mt == 4)
+#define MX_THIN(NT)                                                                                                     \
+  hipLaunchKernelGGL((thin_kernel<NT, GATED>), grid, dim3(64 * ((T + 31) / 32)), 0, stream, x, w, s, epi, parts, T, K, rows, \
+                     p.ntiles, p.nsplit)
+  if (p.thin == 1)
+    MX_THIN(1);
+  else if (p.thin == 2)
+    MX_THIN(2);
+  else if (p.mt == 4)
     MX_TILE(4, 4, 2);
   else if (p.mt == 2 && deep)
     MX_TILE(2, 2, 3);
@@ -333,10 +510,11 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   else
     MX_TILE(1, 2, 2);
 #undef MX_TILE
+#undef MX_THIN
   if (p.nsplit > 1) {
     const int pc = part_cols(rows);
     const int64_t pieces = (int64_t)T * (pc / 8);
-    hipLaunchKernelGGL((combine_kernel<GATED>), dim3((unsigned)((pieces + 255) / 256)), dim3(256), 0, stream, parts,
+    hipLaunchKernelGGL((combine_kernel<GATED>), dim3((unsigned)((pieces + 63) / 64)), dim3(64), 0, stream, parts,
                        epi, T, pc, p.nsplit);
   }
   return hip_status(hipGetLastError());

@@ -19,8 +19,10 @@ bool gated_ok(int64_t T, int64_t H, int64_t I) { return I >= 1 && I <= MAX_N / 2
 bool block_ok(int64_t T, int64_t H, int64_t I) { return gated_ok(T, H, I) && sizes_ok(T, I, H); }
 bool act_ok(int act) { return act >= MX_ACT_NONE && act <= MX_ACT_SIGMOID; }
 bool opt_aligned(const void* p, size_t a) { return !p || aligned(p, a); }
-// 8-byte scale loads where a row's scales are a multiple of 8 bytes
-bool scales_aligned(const uint8_t* s, int64_t K) { return K % 256 != 0 || aligned(s, 8); }
+// 8-byte scale loads where a row's scales are a multiple of 8 bytes, 4-byte copies of 4
+bool scales_aligned(const uint8_t* s, int64_t K) {
+  return K % 256 == 0 ? aligned(s, 8) : K % 128 != 0 || aligned(s, 4);
+}
 int workspace_ok(const void* ws, size_t have, size_t need) {
   if (need == 0) return MX_OK;
   return (!ws || !aligned(ws, 256) || have < need) ? MX_ERR_WORKSPACE : MX_OK;

@@ -440,7 +440,7 @@ __device__ __forceinline__ void forward_tile(const typename ForwardLds<MT, NT, W
 // epilogue then reads them back by rows, so that its accesses to memory are whole lines.
 template <int NT>
 __device__ __forceinline__ uint32_t out_at(int row, int chunk) {
-  return (uint32_t)row * (NT * 128) + ((chunk ^ (row & 15)) << 4);
+  return (uint32_t)row * (NT * 128) + ((chunk ^ (row & 15 & (NT * 8 - 1))) << 4);
 }
 // Writes tile row m of acc there.
 template <int NT>
