@@ -4,13 +4,14 @@
 // All products are exact in fp32 (bf16 x E2M1 * 2^s) and accumulate in fp32; bias, activation,
 // product, scale and residual are applied to the fp32 sums, and each output is rounded once.
 //
-// Two kernels, by the number of tokens:
-//   * up to STREAM_MAX_T (or less than one MX block per lane group, K < 128) a workgroup owns 16 weight rows (gate_up: 16 gate and the 16 up rows
-//     of the same columns), its waves split K, and every weight byte is read once: the time is
-//     the weight bytes' (stream_kernel);
-//   * beyond, tiles of tokens x rows (mx_tile.hpp), where the matrix instructions set the
-//     time; K is split over several workgroups while there are fewer tiles than CUs, and the
-//     fp32 parts are summed in a fixed order by a second launch (combine_kernel).
+// Three kernels, by the number of tokens:
+//   * up to STREAM_MAX_T (and for K < 128) a workgroup owns 16 weight rows, its waves split K,
+//     and every weight byte is read once (stream_kernel);
+//   * up to THIN_MAX_T a wave takes 32 tokens and 32 or 64 weight rows (thin_kernel);
+//   * beyond, tiles of tokens x rows (mx_tile.hpp), where the matrix instructions set the time
+//     (forward_kernel).
+// In the last two K is split over several workgroups while there are fewer tiles than CUs; the
+// fp32 parts are then summed in a fixed order by a second launch (combine_kernel).
 #include "mx_epilogue.hpp"
 #include "mx_tile.hpp"
 
@@ -29,69 +30,92 @@ struct EpilogueOf<true> {
   typedef GatedEpilogue type;
 };
 
+// A workgroup has one MFMA tile of 16 weight rows: 16 rows of a linear layer, or 8 gate rows and
+// the 8 up rows of the same columns (a tile of each would leave half the CUs idle at I = 2048:
+// 9.9 us at T = 8 with H = 7168).
 // SBYTE: scale rows whose length is no multiple of 8 bytes (K % 256 != 0) go byte by byte.
-template <int W, int MT, bool GATED, bool SBYTE>
+// XL: the workgroup first copies x to LDS (dynamic, T * K bf16); read from memory, only T of
+// every 16 lanes of a fragment load are active.
+constexpr int STREAM_XL = 65536;  // values of x that fit beside the slabs
+template <int W, int MT, bool GATED, bool SBYTE, bool XL>
 __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w,
                                                         const uint8_t* __restrict__ s,
                                                         typename EpilogueOf<GATED>::type epi, int T, int K, int rows) {
-  constexpr int NS = GATED ? 2 : 1;
-  constexpr int D = (MT * NS == 1) ? 4 : 2;
-  __shared__ __attribute__((aligned(16))) uint8_t slabs[W][NS * SLAB_BYTES];
-  __shared__ f32x4 red[(W > 1) ? W * NS * MT * 64 : 1];
+  constexpr int D = MT == 1 ? 4 : 2, COLS = GATED ? SUB_ROWS / 2 : SUB_ROWS;
+  __shared__ __attribute__((aligned(16))) uint8_t slabs[W][SLAB_BYTES];
+  __shared__ f32x4 red[(W > 1) ? W * MT * 64 : 1];
+  extern __shared__ u32x4 xdyn[];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int items = (rows + SUB_ROWS - 1) / SUB_ROWS;
-  const int n0 = blockIdx.x % items * SUB_ROWS, t0 = blockIdx.x / items * (MT * 16);
-  StreamLanes<NS, MT> L;
-  lanes_init_lds(L, lane);
+  const int items = (rows + COLS - 1) / COLS;
+  const int n0 = blockIdx.x % items * COLS, t0 = blockIdx.x / items * (MT * 16);
   const size_t kb = (size_t)(K >> 1), ks = (size_t)(K >> 5);
+  // weight row of MFMA row r; past the last row the last one again
+  auto weight_row = [&](int r) {
+    if (GATED) return (size_t)min(n0 + (r & 7), rows - 1) + (r >= 8 ? (size_t)rows : 0);
+    return (size_t)min(n0 + r, rows - 1);
+  };
+  StreamLanes<1, MT> L;
+  lanes_init_lds(L, lane);
 #pragma unroll
-  for (int i = 0; i < NS; ++i) {
-    const size_t first = (size_t)i * rows;  // up rows follow the gate rows
+  for (int q = 0; q < 2; ++q) L.w[0][q] = w + weight_row((lane >> 3) + 8 * q) * kb + (lane & 7) * 16;
+  L.s[0] = s + weight_row(lane & 15) * ks;
+  const uint16_t* xs = x;
+  if constexpr (XL) {
+    static_assert(MT == 1 && !SBYTE, "one tile of tokens, whole segments");
+    // 8 loads of a thread in flight at once; a piece past the end is the last piece again
+    const int n16 = T * K / 8, nt = W * 64, t = threadIdx.x;
+    const u32x4* xv = reinterpret_cast<const u32x4*>(x);
+    for (int i0 = t; i0 < n16; i0 += 8 * nt) {
+      u32x4 v[8];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
-      L.w[i][q] = w + (first + min(n0 + (lane >> 3) + 8 * q, rows - 1)) * kb + (lane & 7) * 16;
-    L.s[i] = s + (first + min(n0 + (lane & 15), rows - 1)) * ks;
+      for (int u = 0; u < 8; ++u) v[u] = xv[min(i0 + u * nt, n16 - 1)];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) xdyn[min(i0 + u * nt, n16 - 1)] = v[u];
+    }
+    __syncthreads();
+    xs = reinterpret_cast<const uint16_t*>(xdyn);
   }
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int t = t0 + mt * 16 + (lane & 15);
-    L.x[mt] = t < T ? x + (size_t)t * K + 32 * (lane >> 4) : nullptr;
+    L.x[mt] = t < T ? xs + (size_t)t * K + 32 * (lane >> 4) : nullptr;
   }
   const int nseg = K / SEG_K, nb_tail = (K % SEG_K) / 32;
   const int sg0 = (int)((long)nseg * wave / W), sg1 = (int)((long)nseg * (wave + 1) / W);
-  f32x4 acc[MT][NS];
+  f32x4 acc[MT][1];
   acc_zero(acc);
-  if (SBYTE) {
-    Stage<NS, MT> st;
+  if constexpr (SBYTE) {
+    Stage<1, MT> st;
     stage_zero_x(st);
     for (int sg = sg0; sg < sg1; ++sg) {
-      stage_load_tail<NS, MT>(st, L, sg, 8, lane);
+      stage_load_tail<1, MT>(st, L, sg, 8, lane);
       stage_compute(st, L, slabs[wave], acc);
     }
     if (wave == W - 1 && nb_tail > 0) {
-      stage_load_tail<NS, MT>(st, L, nseg, nb_tail, lane);
+      stage_load_tail<1, MT>(st, L, nseg, nb_tail, lane);
       stage_compute(st, L, slabs[wave], acc);
     }
   } else {
-    stream_segments<NS, MT, D>(L, sg0, sg1, 0, slabs[wave], acc, lane);
+    stream_segments<1, MT, D, false, XL>(L, sg0, sg1, 0, slabs[wave], acc, lane);
   }
-  wg_reduce<NS, MT, W>(acc, red, wave, lane);
+  wg_reduce<1, MT, W>(acc, red, wave, lane);
   if (wave != 0) return;
+  const int g = lane >> 4, n = n0 + 4 * (GATED ? g & 1 : g);
+  const auto cols = epi.template columns<4>(n);
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     const int t = t0 + mt * 16 + (lane & 15);
-    if (t >= T) continue;
-    float v[NS][4];
+    float v[4];
 #pragma unroll
-    for (int i = 0; i < NS; ++i)
+    for (int j = 0; j < 4; ++j) v[j] = acc[mt][0][j];
+    if constexpr (GATED) {
+      float u[4];  // rows 8 and up of the tile: the lanes 32 on
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = acc[mt][i][j];
-    const int n = n0 + 4 * (lane >> 4);
-    const auto cols = epi.template columns<4>(n);
-    if constexpr (GATED)
-      epi.template store<4>(t, n, v[0], v[1], cols);
-    else
-      epi.template store<4>(t, n, v[0], cols, epi.template fetch<4>(t, n));
+      for (int j = 0; j < 4; ++j) u[j] = __shfl_xor(v[j], 32, 64);
+      if (t < T && g < 2) epi.template store<4>(t, n, v, u, cols);
+    } else {
+      if (t < T) epi.template store<4>(t, n, v, cols, epi.template fetch<4>(t, n));
+    }
   }
 }
 
@@ -451,32 +475,34 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
                           const typename EpilogueOf<GATED>::type& epi, void* workspace, int T, int K, int rows,
                           hipStream_t stream) {
   if (T <= STREAM_MAX_T || K < FWD_KB) {
-    const int items = (rows + SUB_ROWS - 1) / SUB_ROWS, nseg = K / SEG_K;
+    const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
+    const int items = (rows + cols - 1) / cols, nseg = K / SEG_K;
     int W = 1;
     while (W < 8 && 2 * W <= nseg && items * W < 2048) W *= 2;
-    if (T > 16 && GATED) W = std::min(W, 4);
+    const bool sbyte = K % SEG_K != 0, xl = T <= 16 && !sbyte && (int64_t)T * K <= STREAM_XL;
     const dim3 grid(items * ((T + STREAM_MAX_T - 1) / STREAM_MAX_T)), block(W * 64);
-#define MX_STREAM(WW, M, SB) \
-  hipLaunchKernelGGL((stream_kernel<WW, M, GATED, SB>), grid, block, 0, stream, x, w, s, epi, T, K, rows)
-#define MX_STREAM_W(WW)         \
-  if (K % SEG_K == 0) {         \
-    if (T > 16)                 \
-      MX_STREAM(WW, 2, false);  \
-    else                        \
-      MX_STREAM(WW, 1, false);  \
-  } else if (T > 16) {          \
-    MX_STREAM(WW, 2, true);     \
-  } else {                      \
-    MX_STREAM(WW, 1, true);     \
-  }
+    const unsigned xl_bytes = xl ? (unsigned)(T * K * 2) : 0u;
+#define MX_STREAM(WW, M, SB, XX) \
+  hipLaunchKernelGGL((stream_kernel<WW, M, GATED, SB, XX>), grid, block, xl_bytes, stream, x, w, s, epi, T, K, rows)
+#define MX_STREAM_W(WW)               \
+  if (xl)                             \
+    MX_STREAM(WW, 1, false, true);    \
+  else if (!sbyte && T <= 16)         \
+    MX_STREAM(WW, 1, false, false);   \
+  else if (!sbyte)                    \
+    MX_STREAM(WW, 2, false, false);   \
+  else if (T <= 16)                   \
+    MX_STREAM(WW, 1, true, false);    \
+  else                                \
+    MX_STREAM(WW, 2, true, false)
     if (W == 1) {
-      MX_STREAM_W(1)
+      MX_STREAM_W(1);
     } else if (W == 2) {
-      MX_STREAM_W(2)
+      MX_STREAM_W(2);
     } else if (W == 4) {
-      MX_STREAM_W(4)
+      MX_STREAM_W(4);
     } else {
-      MX_STREAM_W(8)
+      MX_STREAM_W(8);
     }
 #undef MX_STREAM_W
 #undef MX_STREAM
