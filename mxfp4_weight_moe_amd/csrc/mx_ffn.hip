@@ -458,12 +458,12 @@ TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated) {
     }
     split = std::min<int64_t>(GPU_CUS / p.ntiles, stages / 4);
   } else {
-    p.mt = T > 1024 ? 4 : T > 64 ? 2 : 1;
+    p.mt = T <= 64 ? 1 : tile_choice(T, rows * (gated ? 2 : 1), FORWARD_ROUND_256, FORWARD_ROUND_128);
     p.nt = p.mt == 4 ? 4 : 2;
     const int bm = 64 * p.mt, cols = (gated ? 32 : 64) * p.nt;
     p.mtiles = (int)((T + bm - 1) / bm);
     p.ntiles = (int)((rows + cols - 1) / cols);
-    split = std::min<int64_t>(GPU_CUS / std::max<int64_t>(1, (int64_t)p.mtiles * p.ntiles), stages / 2);
+    split = tile_split((int64_t)p.mtiles * p.ntiles, stages, p.mt == 2 && stages >= 32);
   }
   p.nsplit = (int)std::max<int64_t>(1, split);
   if (p.nsplit > 1) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows) * (gated ? 2 : 1) * 4;
@@ -531,8 +531,6 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
     MX_TILE(2, 2, 3);
   else if (p.mt == 2)
     MX_TILE(2, 2, 2);
-  else if (deep)
-    MX_TILE(1, 2, 6);
   else
     MX_TILE(1, 2, 2);
 #undef MX_TILE

@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(256) dz_kernel(Slope f, uint16_t* __restrict__
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int n = blockIdx.x * DZ_COLS + cx * 8;
   const int64_t t0 = (int64_t)blockIdx.y * strip_rows, t1 = min(t0 + strip_rows, T);
-  const bool wide = n + 8 <= N && (N & 7) == 0;
+  const bool wide = n + 8 <= N;
   const int left = N - n;
   float sum[8] = {};
   if (n < (dz ? ldz : N)) {  // columns N .. ldz read as 0
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(256) dz_gated_kernel(const uint16_t* __restric
   const int cx = threadIdx.x & 31, ry = threadIdx.x >> 5;
   const int n = blockIdx.x * DZ_COLS + cx * 8;
   const int64_t t0 = (int64_t)blockIdx.y * strip_rows, t1 = min(t0 + strip_rows, T);
-  const bool wide = n + 8 <= I && (I & 7) == 0;
+  const bool wide = n + 8 <= I;
   const int left = I - n;
   float sg[8] = {}, su[8] = {};
   if (n < I) {
@@ -233,20 +233,21 @@ __global__ void __launch_bounds__(256) dx_combine_kernel(const float* __restrict
 
 TilePlan backward_plan(int64_t T, int64_t K, int64_t N) {
   TilePlan p{};
-  p.mt = T > 1024 ? 4 : T > 64 ? 2 : 1;
+  p.mt = T <= 64 ? 1 : tile_choice(T, K, BACKWARD_ROUND_256, BACKWARD_ROUND_128);
   p.nt = p.mt == 4 ? 4 : 2;
   const int bm = 64 * p.mt, bn = 64 * p.nt;
   p.mtiles = (int)((T + bm - 1) / bm);
   p.ntiles = (int)((K + bn - 1) / bn);
-  const int64_t tiles = (int64_t)p.mtiles * p.ntiles, stages = (N + BWD_KB - 1) / BWD_KB;
-  int64_t split = tiles >= GPU_CUS ? 1 : GPU_CUS / tiles;
-  p.nsplit = (int)std::max<int64_t>(1, std::min(split, stages / 4));
+  const int64_t stages = (N + BWD_KB - 1) / BWD_KB;
+  p.nsplit = (int)tile_split((int64_t)p.mtiles * p.ntiles, stages / 2, p.mt == 2 && stages >= 64);
   if (p.nsplit > 1) p.bytes = (size_t)p.nsplit * T * K * 4;
   return p;
 }
 
-// Rows per strip of the dz launch: enough workgroups for the chip, whole groups of 8 rows.
+// Rows per strip of the dz launch: enough workgroups for the chip, whole groups of 8 rows.  Up
+// to 64 rows one strip, which writes the bias gradient itself and saves a launch.
 int dz_strip_rows(int64_t T, int64_t cols) {
+  if (T <= 64) return 64;
   const int64_t ctiles = (cols + DZ_COLS - 1) / DZ_COLS;
   const int64_t want = std::max<int64_t>(1, 4 * GPU_CUS / ctiles);
   int64_t rows = (T + want - 1) / want;
@@ -266,7 +267,7 @@ BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, b
     return at;
   };
   if (need_dz && dx) b.dz = take((size_t)T * b.ldz * 2);
-  if (dbias) b.bias_parts = take((size_t)b.strips * N * 4);
+  if (dbias && b.strips > 1) b.bias_parts = take((size_t)b.strips * N * 4);
   if (dx) {
     b.tile = backward_plan(T, K, N);
     b.parts = take(b.tile.bytes);
@@ -311,14 +312,14 @@ int launch_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const ui
   const BackwardPlan b = backward_workspace(T, K, N, N, !direct, dx != nullptr, dbias != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* dz = (dx && !direct) ? reinterpret_cast<uint16_t*>(ws + b.dz) : nullptr;
-  float* bp = dbias ? reinterpret_cast<float*>(ws + b.bias_parts) : nullptr;
+  float* bp = !dbias ? nullptr : b.strips > 1 ? reinterpret_cast<float*>(ws + b.bias_parts) : dbias;
   if (dz || bp) {
     const dim3 grid((b.ldz + DZ_COLS - 1) / DZ_COLS, b.strips);
     hipLaunchKernelGGL((dz_kernel<LinearSlope>), grid, dim3(256), 0, stream, LinearSlope{dy, z, N, act, scale}, dz,
                        b.ldz, bp, (int64_t)T, b.strip_rows);
     if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
   }
-  if (bp) {
+  if (bp && b.strips > 1) {
     const int st = launch_strip_sum(bp, b.strips, N, 1, &dbias, stream);
     if (st != MX_OK) return st;
   }
@@ -332,11 +333,11 @@ int launch_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t
   const BackwardPlan b = backward_workspace(T, H, 2 * (int64_t)I, I, true, dx != nullptr, dbias != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* dz = dx ? reinterpret_cast<uint16_t*>(ws + b.dz) : nullptr;
-  float* bp = dbias ? reinterpret_cast<float*>(ws + b.bias_parts) : nullptr;
+  float* bp = !dbias ? nullptr : b.strips > 1 ? reinterpret_cast<float*>(ws + b.bias_parts) : dbias;
   const dim3 grid((I + DZ_COLS - 1) / DZ_COLS, b.strips);
   hipLaunchKernelGGL(dz_gated_kernel, grid, dim3(256), 0, stream, dh, z, I, act, dz, b.ldz, bp, (int64_t)T, b.strip_rows);
   if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
-  if (bp) {
+  if (bp && b.strips > 1) {
     const int st = launch_strip_sum(bp, b.strips, 2 * I, 1, &dbias, stream);
     if (st != MX_OK) return st;
   }

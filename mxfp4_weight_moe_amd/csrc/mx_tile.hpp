@@ -144,6 +144,30 @@ __device__ __forceinline__ void tile_zero(f32x16 (&acc)[MT][NT]) {
       for (int j = 0; j < 16; ++j) acc[m][i][j] = 0.f;
 }
 
+// ------------------------------------------------------------------ which tiles
+
+// Tiles of 256 x 256 (one a CU) or 128 x 128 (two a CU)?  The large ones take less time for the
+// same work, the small ones leave fewer CUs idle in the last round.  What a round of each takes
+// (of 256 and of 512 tiles; microseconds at a reduction of 7168 forward and 4096 backward):
+//   forward   174 and 106     gate_up of 1536 to 4096 tokens, H = 7168, I = 2048
+//   backward  110 and 82      7168 <- 4096, 1024 to 2048 tokens
+// e.g. gate_up at 2048 tokens takes 107 with the small tiles and 113 with the large ones, at
+// 3000 tokens 175 and 141.
+constexpr int FORWARD_ROUND_256 = 174, FORWARD_ROUND_128 = 106;
+constexpr int BACKWARD_ROUND_256 = 110, BACKWARD_ROUND_128 = 82;
+inline int tile_choice(int64_t T, int64_t cols, int64_t round_256, int64_t round_128) {
+  const int64_t large = ((T + 255) / 256) * ((cols + 255) / 256), small = ((T + 127) / 128) * ((cols + 127) / 128);
+  return (large + GPU_CUS - 1) / GPU_CUS * round_256 <= (small + 2 * GPU_CUS - 1) / (2 * GPU_CUS) * round_128 ? 4 : 2;
+}
+// Over how many workgroups the reduction of a tile is split, each with two stages or more: as
+// many as there are CUs for, and two (fill_second) where tiles of 128 x 128 then take the second
+// place on each CU and the reduction is long (gate_up, H = 7168: 768 tokens 65 -> 57 us; not
+// 2048 -> 7168, 31 -> 45).
+inline int64_t tile_split(int64_t tiles, int64_t stages, bool fill_second) {
+  const int64_t split = std::max<int64_t>(GPU_CUS / tiles, fill_second && tiles <= GPU_CUS ? 2 : 1);
+  return std::max<int64_t>(1, std::min(split, stages / 2));
+}
+
 // ------------------------------------------------------------------ matrix instructions
 
 // acc += a x b in place: lane (r = lane & 31, g = lane >> 5) gives values 8g .. 8g + 7 of row r
