@@ -408,7 +408,7 @@ MX_API int moe_mxfp4_forward_persistent(const uint16_t* x, const float* router_l
  */
 enum mx_act {
   MX_ACT_NONE = 0,      /* z */
-  MX_ACT_RELU = 1,      /* max(z, 0); its slope at 0 is 0 */
+  MX_ACT_RELU = 1,      /* max(z, 0), NaN for NaN; its slope at 0 is 0 */
   MX_ACT_SILU = 2,      /* z / (1 + exp(-z)) */
   MX_ACT_GELU = 3,      /* z/2 (1 + erf(z / sqrt 2)) */
   MX_ACT_GELU_TANH = 4, /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
@@ -527,7 +527,8 @@ MX_API int mx_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, co
  * epilogue (b is then never rounded).
  *   x bf16 [T, H]; w_gate_up, s_gate_up, bias_gate_up, act as for mx_gate_up;
  *   w_down uint8 [H, I/2], s_down uint8 [H, I/32], bias_down optional, bf16 [H];
- *   w_pre, w_post, gate, gate_mode, scale, eps as for mx_norm_residual;  y bf16 [T, H] (written).
+ *   w_pre, w_post, gate, gate_mode, scale, eps as for mx_norm_residual;  y bf16 [T, H]
+ *   (written; may be x itself).
  *   H % 32 == 0 and I % 32 == 0; with a norm or gate also H <= MX_NORM_MAX_H.
  */
 MX_API size_t mx_ffn_block_workspace_size(int64_t T, int64_t H, int64_t I);

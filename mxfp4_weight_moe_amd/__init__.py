@@ -732,10 +732,12 @@ def mx_gate_up_backward(dh: torch.Tensor, z: torch.Tensor, W_gate_up: torch.Tens
 def _gate_mode(gate, T: int, H: int, dev) -> int:
     if gate is None:
         return _GATE_NONE
-    if not isinstance(gate, torch.Tensor) or tuple(gate.shape) not in ((T, 1), (H,), (T, H)):
+    shape = gate.shape if isinstance(gate, torch.Tensor) else None
+    mode = {(H,): _GATE_CHANNEL, (T, H): _GATE_FULL, (T, 1): _GATE_TOKEN}.get(shape)
+    if mode is None:
         raise ValueError(f"gate must be a tensor of shape [T, 1], [H] or [T, H] with T={T}, H={H}")
-    _check(gate, "gate", _BF16, None, dev)
-    return _GATE_CHANNEL if gate.dim() == 1 else _GATE_TOKEN if gate.shape[1] == 1 else _GATE_FULL
+    _tensor(gate, "gate", _BF16, shape, dev)
+    return mode
 
 
 def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
@@ -759,10 +761,10 @@ def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: tor
         _tensor(b, "b", _BF16, (T, H), dev)
         y = out
         if y is None:
-            y = torch.empty((T, H), dtype=_BF16, device=dev)
+            y = x.new_empty((T, H))
         else:
             _tensor(y, "out", _BF16, (T, H), dev)
-    xn = torch.empty((T, H), dtype=_BF16, device=dev) if w_pre is not None else None
+    xn = x.new_empty((T, H)) if w_pre is not None else None
     _call(_lib.mx_norm_residual, dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale, _opt(w_pre), eps,
           _opt(y), _opt(xn), T, H)
     return (x if y is None else y), xn
@@ -790,8 +792,8 @@ def mx_norm_residual_backward(dy: torch.Tensor | None, dxn: torch.Tensor | None,
         raise ValueError("w_pre, dxn and y go together")
     if b is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need b")
-    dx = torch.empty((T, H), dtype=_BF16, device=dev)
-    db = torch.empty((T, H), dtype=_BF16, device=dev) if b is not None else None
+    dx = first.new_empty((T, H))
+    db = first.new_empty((T, H)) if b is not None else None
     dgate = None
     if gate is not None:
         dgate = torch.empty(tuple(gate.shape), dtype=_BF16 if mode == _GATE_FULL else _F32, device=dev)
@@ -825,7 +827,7 @@ def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tens
     mode = _gate_mode(gate, T, H, dev)
     code = _act_code(act)
     if out is None:
-        out = torch.empty((T, H), dtype=_BF16, device=dev)
+        out = x.new_empty((T, H))
     else:
         _tensor(out, "out", _BF16, (T, H), dev)
     ws, wp, wn = _scratch(_lib.mx_ffn_block_workspace_size(T, H, I), dev, ws)

@@ -110,10 +110,13 @@ def value_error(z, ez, a):
 
 # ------------------------------------------------------------------ linear
 
-# streaming (T <= 32), then every tile height, odd rows and columns, K tails of 32, 64 and 96
+# streaming (T <= 32, K < 128), thin tiles (33 to 128 tokens), tiles of 64 (K % 128 != 0), 128 and
+# 256 rows, split and whole K, odd rows and columns, K tails of 32, 64 and 96
 LINEAR_SHAPES = [(1, 256, 64), (1, 32, 1), (2, 96, 7), (5, 512, 33), (16, 288, 16), (17, 2048, 40), (31, 256, 100),
                  (32, 160, 264), (33, 128, 8), (40, 32, 1), (64, 544, 130), (65, 256, 64), (77, 2048, 257),
-                 (129, 96, 300), (300, 512, 520), (1025, 192, 264), (1300, 256, 65), (1100, 32, 512)]
+                 (129, 96, 300), (300, 512, 520), (1025, 192, 264), (1300, 256, 65), (1100, 32, 512),
+                 (128, 2048, 33), (97, 1024, 6200), (50, 2080, 70), (120, 1056, 64), (200, 2048, 129), (200, 2080, 65),
+                 (130, 4096, 64), (4100, 544, 2100), (4200, 128, 2060), (4097, 1024, 2049)]
 
 
 def linear_inputs(T, K, N, seed):
@@ -196,7 +199,8 @@ def check_dx(dx, dz, edz, w, s, rounded, N):
 
 
 BWD_SHAPES = [(1, 32, 1), (1, 256, 64), (3, 96, 7), (33, 128, 16), (64, 288, 130), (65, 160, 257), (100, 512, 520),
-              (129, 544, 33), (700, 96, 72), (1025, 256, 264), (1100, 32, 100), (1030, 288, 65)]
+              (129, 544, 33), (700, 96, 72), (1025, 256, 264), (1100, 32, 100), (1030, 288, 65),
+              (4, 128, 1000), (70, 256, 1090), (200, 544, 4160), (4100, 2112, 200), (4130, 2080, 64), (4100, 2176, 1)]
 
 
 @pytest.mark.parametrize("T,K,N", BWD_SHAPES)
@@ -238,7 +242,8 @@ def test_backward_nan_and_neighbours(mx):
 # ------------------------------------------------------------------ gate_up
 
 GATED_SHAPES = [(1, 256, 64), (1, 32, 1), (3, 96, 7), (16, 288, 33), (17, 512, 16), (32, 160, 100), (33, 128, 8),
-                (64, 544, 65), (65, 1024, 130), (130, 96, 257), (1025, 192, 136), (1100, 256, 33), (1030, 32, 264)]
+                (64, 544, 65), (65, 1024, 130), (130, 96, 257), (1025, 192, 136), (1100, 256, 33), (1030, 32, 264),
+                (128, 2048, 72), (90, 1024, 3100), (200, 2048, 40), (4100, 288, 1050), (4097, 512, 1031)]
 
 
 @pytest.mark.parametrize("T,H,I", GATED_SHAPES)
@@ -569,6 +574,58 @@ def test_streams(mx):
     for g in got:
         for a, b in zip(g, want):
             assert torch.equal(a, b)
+
+
+def test_offsets_past_32_bits(mx):
+    """Outputs, activations and weights of more than 4 GB: the last rows against the definition."""
+    g = gen(6)
+    dg = torch.Generator(device=DEV)
+    dg.manual_seed(1)
+    say("long activations")
+    T, K, N = 70001, 128, 32800  # y has 4.6 GB
+    x, (w, s) = bf(T, K, g=g), weights(N, K, g)
+    xd, wd, sd = cuda(x, w, s)
+    y = mx.mx_linear_fused(xd, wd, sd)
+    rows = [0, 32769, 65536, T - 1]
+    z, ez = z_of(x[rows], w, s, None)
+    within(y[rows], z, (1 + B) * ez + B * z.abs(), "y")
+    dx = mx.mx_linear_fused_backward(y, wd, sd, need_dbias=False)[0]
+    dz = y[rows].double().cpu()
+    check_dx(dx[rows].cpu(), dz, torch.zeros_like(dz), w, s, False, N)
+    del y, dx
+    say("many weights")
+    T, K, N = 5, 2080, 1 << 22  # 4.4 GB of codes
+    wd = torch.randint(0, 256, (N, K // 2), generator=dg, device=DEV, dtype=torch.uint8)
+    sd = torch.full((N, K // 32), 118, dtype=torch.uint8, device=DEV)
+    x = bf(T, K, g=g)
+    for act_t in (T, 40):
+        xx = bf(act_t, K, g=g)
+        y = mx.mx_linear_fused(xx.to(DEV), wd, sd)
+        last = slice(N - 70, N)
+        z, ez = z_of(xx, wd[last].cpu(), sd[last].cpu(), None)
+        within(y[:, last], z, (1 + B) * ez + B * z.abs(), "y")
+    del wd, sd, y
+    say("long norms")
+    T, H = 300001, 8192
+    x = torch.randn((T, H), generator=dg, device=DEV, dtype=torch.bfloat16)
+    wi = torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    xn = mx.mx_norm_residual(x, w_pre=wi)[1]
+    rows = [0, 262144, T - 1]
+    v = x[rows].double().cpu()
+    want = v * rms(v)
+    within(xn[rows], want, ((1 + B) * (H + 16) * U + B) * want.abs(), "xn")
+
+
+def test_block_in_place(mx):
+    T, H, I = 40, 256, 96
+    x, wgu, sgu, wd, sd, wi, bgu, bd, wo, gate = block_inputs(T, H, I, 12)
+    say("block in place")
+    for post in (False, True):
+        more = dict(w_post=wo, gate=gate) if post else {}
+        want = mx.mx_ffn_block(x, wgu, sgu, wd, sd, wi, bgu, bd, **more)
+        y = x.clone()
+        mx.mx_ffn_block(y, wgu, sgu, wd, sd, wi, bgu, bd, out=y, **more)
+        assert torch.equal(y, want)
 
 
 def test_caller_workspace(mx):
