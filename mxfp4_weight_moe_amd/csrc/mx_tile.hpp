@@ -543,20 +543,26 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   // where this thread's columns go: LDS row 16 i + column_row(q & 15) of its wave column, chunk o
   const int qrow = column_row(q & 15);
   const uint32_t put = L::Rows::BYTES + (uint32_t)((q >> 4) * NT * 32 + qrow) * 128 + ((o ^ row_key<8>(qrow)) << 4);
-  uint32_t code[8], sb[8];  // of the stage after the current one
+  uint32_t code[8];  // of the stage after the current one, and its rows' scales
+  float scale[8];
+  uint32_t code2[8], scale2[8];  // of the stage after that, as loaded
   u32x4 frag[2][MT], wf[2][NT], column[2];
   // The first weight row of the stage that load_one loads from, moved on a stage at a time.
   const uint8_t* wstage = w + (size_t)st0 * BWD_KB * wld;
   const uint8_t* sstage = s + (size_t)st0 * BWD_KB * sld;
   auto load_one = [&](int i) {
     if constexpr (CPT == 8)
-      code[i] = *reinterpret_cast<const uint32_t*>(wstage + woff[i]);
+      code2[i] = *reinterpret_cast<const uint32_t*>(wstage + woff[i]);
     else
-      code[i] = *reinterpret_cast<const uint16_t*>(wstage + woff[i]);
+      code2[i] = *reinterpret_cast<const uint16_t*>(wstage + woff[i]);
     if constexpr (S4)
-      sb[i] = *reinterpret_cast<const uint32_t*>(sstage + soff[i]);
+      scale2[i] = *reinterpret_cast<const uint32_t*>(sstage + soff[i]);
     else
-      sb[i] = sstage[soff[i]];
+      scale2[i] = sstage[soff[i]];
+  };
+  auto take_one = [&](int i) {
+    code[i] = here(code2[i]);
+    scale[i] = __uint_as_float(here(__float_as_uint(e8m0_scale_operand(S4 ? (scale2[i] >> sshift) & 0xFFu : scale2[i]))));
   };
   auto move_on = [&](bool yes) {
     wstage += yes ? BWD_KB * wld : 0;
@@ -576,14 +582,13 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   auto clear_rows = [&]() {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (o * 8 + i >= left) code[i] = 0u, sb[i] = 127u << sshift;
+      if (o * 8 + i >= left) code[i] = 0u, scale[i] = 1.f;
   };
   // half of column pair b, row pair p2: rows 2 p2 and 2 p2 + 1
   auto decode_pair = [&](auto B, auto P2) __attribute__((always_inline)) {
     constexpr int b = B, p2 = P2;
-    auto scale = [&](int i) { return e8m0_scale_operand(S4 ? (sb[i] >> sshift) & 0xFFu : sb[i]); };
-    const uint32_t lo = decode2<b>(code[2 * p2], scale(2 * p2));
-    const uint32_t hi = decode2<b>(code[2 * p2 + 1], scale(2 * p2 + 1));
+    const uint32_t lo = decode2<b>(code[2 * p2], scale[2 * p2]);
+    const uint32_t hi = decode2<b>(code[2 * p2 + 1], scale[2 * p2 + 1]);
     column[0][p2] = __builtin_amdgcn_perm(hi, lo, 0x05040100u);  // low halves: column 2b
     column[1][p2] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
   };
@@ -603,6 +608,8 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
 #pragma unroll
   for (int i = 0; i < 8; ++i) load_one(i);
   rows.copy(lds, st0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) take_one(i);
   if (ragged && st0 == last_stage) clear_rows();
   unrolled<NT>([&](auto B) __attribute__((always_inline)) {
     unrolled<4>([&](auto P2) __attribute__((always_inline)) { decode_pair(B, P2); });
@@ -614,6 +621,8 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   if (ragged && second == last_stage) clamp_rows();
 #pragma unroll
   for (int i = 0; i < 8; ++i) load_one(i);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) take_one(i);
   wait_copies();
   __syncthreads();
 #pragma unroll
@@ -646,12 +655,15 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
           constexpr int e = k * per_read + E;
           if constexpr (e < READS) read_one(last ? nxt : cur, next, e);
         });
-        // copies of the next stage's dz rows: steps 0 and 1
-        constexpr int per_copy = (COPIES + 2 * SLOTS - 1) / (2 * SLOTS);
-        unrolled<per_copy>([&](auto E) __attribute__((always_inline)) {
-          constexpr int e = n * per_copy + E;
-          if constexpr (e < COPIES) rows.copy_one(nxt, cs, e);
-        });
+        // step 0: codes and scales of the stage after next, copies of the next stage's dz rows
+        if constexpr (u == 0) {
+          unrolled<8>([&](auto E) __attribute__((always_inline)) {
+            if constexpr (E * SLOTS / 8 == k) load_one(E);
+          });
+          unrolled<COPIES>([&](auto E) __attribute__((always_inline)) {
+            if constexpr ((2 * E + 1) * SLOTS / (2 * COPIES) == k) rows.copy_one(nxt, cs, E);
+          });
+        }
         // decoding the next stage: steps 1 and 2, a column pair's 4 row pairs, then its writes
         constexpr int units = 4 * NT, per_unit = (units + 2 * SLOTS - 1) / (2 * SLOTS);
         constexpr int every = per_unit > 1 ? 1 : 2 * SLOTS / units;
@@ -666,14 +678,11 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
               }
             }
           });
-        // the codes of the stage after next: step 3, used from the next stage's step 1 on
-        if constexpr (last) {
-          constexpr int per_load = (8 + SLOTS - 1) / SLOTS;
-          unrolled<per_load>([&](auto E) __attribute__((always_inline)) {
-            constexpr int e = k * per_load + E;
-            if constexpr (e < 8) load_one(e);
+        // step 3: what was loaded in step 0 is taken over
+        if constexpr (last)
+          unrolled<8>([&](auto E) __attribute__((always_inline)) {
+            if constexpr (E * SLOTS / 8 == k) take_one(E);
           });
-        }
         keep_order();
       });
     });
