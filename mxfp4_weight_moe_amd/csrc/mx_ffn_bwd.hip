@@ -2,8 +2,8 @@
 //   linear   dz = scale * dy * act'(z);  dx = dz W;  dbias = sum over tokens of dz
 //   gate_up  dz = [dh * u * act'(g) | dh * act(g)] with z = [g | u]; dx and dbias the same way
 // First launch: dz in bf16 (rounded here once, as the matrix instructions take bf16; the bias
-// sums use the unrounded fp32 values) and per-strip column sums; then the strips' sums; then
-// the product dz W in tiles (mx_tile.hpp).
+// sums use the unrounded fp32 values) and per-strip column sums; then
+// the product dz W in tiles (mx_tile.hpp), with the strips' sums beside it.
 #include "mx_epilogue.hpp"
 #include "mx_tile.hpp"
 
@@ -124,60 +124,94 @@ __global__ void __launch_bounds__(256) dz_gated_kernel(const uint16_t* __restric
 }
 
 // out[k][c] = sum over strips, in a fixed order, of parts[strip][k][c] for the k whose out is
-// set: a workgroup takes 64 columns of one k, each of its 16 waves a sixteenth of the strips,
-// 8 loads at a time (4 waves with one load at a time took 35 us for 512 strips of 3 x 7168).
+// set: a workgroup takes 64 columns of one k.  The strips are summed in 16 parts, a part a wave
+// or four, and then the parts, in the same order whatever the number of waves W; a wave has 8
+// or 16 loads in flight (with 4 parts and one load at a time 512 strips of 3 x 7168 took 35 us,
+// 16 waves with 8 take 5).
+constexpr int STRIP_PARTS = 16;
 struct StripOut {
   float* p[3];
 };
 
-__global__ void __launch_bounds__(1024) strip_sum_kernel(const float* __restrict__ parts, StripOut out, int strips,
-                                                         int cols, int arrays) {
-  __shared__ float red[16][64];
-  const int k = blockIdx.y;
+template <int W>
+__device__ __forceinline__ void strip_sum(float (&red)[STRIP_PARTS][64], const float* __restrict__ parts,
+                                          const StripOut& out, int strips, int cols, int arrays, int c0, int k) {
   if (!out.p[k]) return;
-  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  constexpr int PW = STRIP_PARTS / W, U = W == STRIP_PARTS ? 8 : 4;  // parts of a wave, loads of each
+  const int lane = threadIdx.x & 63, q = threadIdx.x >> 6, c = c0 + lane;
   const float* p = parts + (size_t)k * cols + min(c, cols - 1);
   const size_t step = (size_t)arrays * cols;
-  const int i1 = strips * (q + 1) / 16;
-  float a = 0.f;
-  for (int i = strips * q / 16; i < i1; i += 8) {
-    float v[8];
+  float a[PW] = {};
+  int i0[PW], i1[PW];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = p[min(i + u, i1 - 1) * step];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) a += i + u < i1 ? v[u] : 0.f;
+  for (int j = 0; j < PW; ++j) {
+    i0[j] = strips * (q * PW + j) / STRIP_PARTS;
+    i1[j] = strips * (q * PW + j + 1) / STRIP_PARTS;
   }
-  red[q][lane] = a;
+  for (int i = 0; i < (strips + STRIP_PARTS - 1) / STRIP_PARTS; i += U) {
+    float v[PW][U];
+#pragma unroll
+    for (int j = 0; j < PW; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u) v[j][u] = p[min(i0[j] + i + u, strips - 1) * step];
+#pragma unroll
+    for (int j = 0; j < PW; ++j)
+#pragma unroll
+      for (int u = 0; u < U; ++u) a[j] += i0[j] + i + u < i1[j] ? v[j][u] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < PW; ++j) red[q * PW + j][lane] = a[j];
   __syncthreads();
   if (q == 0 && c < cols) {
     float s = red[0][lane];
 #pragma unroll
-    for (int w = 1; w < 16; ++w) s += red[w][lane];
+    for (int w = 1; w < STRIP_PARTS; ++w) s += red[w][lane];
     out.p[k][c] = s;
   }
+}
+
+__global__ void __launch_bounds__(STRIP_PARTS * 64) strip_sum_kernel(const float* __restrict__ parts, StripOut out,
+                                                                     int strips, int cols, int arrays) {
+  __shared__ float red[STRIP_PARTS][64];
+  strip_sum<STRIP_PARTS>(red, parts, out, strips, cols, arrays, blockIdx.x * 64, blockIdx.y);
 }
 
 int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float* const* out, hipStream_t stream) {
   StripOut o{};
   for (int k = 0; k < arrays; ++k) o.p[k] = out[k];
-  hipLaunchKernelGGL(strip_sum_kernel, dim3((cols + 63) / 64, arrays), dim3(1024), 0, stream, parts, o, strips, cols,
-                     arrays);
+  hipLaunchKernelGGL(strip_sum_kernel, dim3((cols + 63) / 64, arrays), dim3(STRIP_PARTS * 64), 0, stream, parts, o,
+                     strips, cols, arrays);
   return hip_status(hipGetLastError());
 }
 
 // ------------------------------------------------------------------ dx = alpha * dz W
 
-template <int MT, int NT, bool S4>
+// The bias gradient's strips that the same launch sums.
+struct BiasStrips {
+  const float* parts;
+  float* dbias;
+  int strips, cols;
+};
+
+// Workgroups past the tiles sum the bias gradient's strips, 64 columns each, on CUs that the
+// last round of tiles leaves idle (a launch of its own took 5 us).
+template <int MT, int NT>
 __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
     backward_kernel(const uint16_t* __restrict__ dz, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                     uint16_t* __restrict__ dx, float* __restrict__ parts, float alpha, int T, int K, int N, int ldz,
-                    int mtiles, int ntiles, int nsplit) {
+                    int mtiles, int ntiles, int nsplit, BiasStrips bias) {
   constexpr int BM = 2 * MT * 32, BN = 2 * NT * 32;
   typedef BackwardLds<MT, NT> L;
   __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
+  const int tiles = mtiles * ntiles * nsplit;
+  if ((int)blockIdx.x >= tiles) {
+    strip_sum<4>(*reinterpret_cast<float(*)[STRIP_PARTS][64]>(lds), bias.parts, StripOut{{bias.dbias}}, bias.strips, bias.cols, 1,
+                 ((int)blockIdx.x - tiles) * 64, 0);
+    return;
+  }
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int wm = wave >> 1, wn = wave & 1;
-  const int tile = xcd_tile(blockIdx.x, mtiles * ntiles * nsplit);
+  const int tile = xcd_tile(blockIdx.x, tiles);
   const int split = tile % nsplit, nt = tile / nsplit % ntiles, mt0 = tile / nsplit / ntiles;
   const int m0 = mt0 * BM, k0 = nt * BN;
   const int stages = (N + BWD_KB - 1) / BWD_KB;
@@ -186,7 +220,7 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
   zs.init(dz, m0, T, ldz, wave, lane);
   f32x16 acc[MT][NT];
   tile_zero(acc);
-  backward_tile<MT, NT, S4>(zs, w, s, N, K, k0, st0, st1, lds, wm, wn, lane, acc);
+  backward_tile<MT, NT>(zs, w, s, N, K, k0, st0, st1, lds, wm, wn, lane, acc);
   const int r = lane & 31, g = lane >> 5;
   constexpr int CPT = ColumnStage<NT>::CPT;
 #pragma unroll
@@ -276,26 +310,20 @@ BackwardPlan backward_workspace(int64_t T, int64_t K, int64_t N, int64_t cols, b
   return b;
 }
 
+// dx, and the sums of the bias gradient's strips if there are any.
 static int launch_dx(const uint16_t* dz, int ldz, const uint8_t* w, const uint8_t* s, uint16_t* dx, float alpha,
-                     const TilePlan& p, float* parts, int T, int K, int N, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-  const bool s4 = K % 128 == 0 && aligned(s, 4);
-#define MX_TILE1(MT, NT, S4)                                                                                       \
-  hipLaunchKernelGGL((backward_kernel<MT, NT, S4>), grid, dim3(256), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, \
-                     ldz, p.mtiles, p.ntiles, p.nsplit)
-#define MX_TILE(MT, NT)        \
-  if (s4)                      \
-    MX_TILE1(MT, NT, true);    \
-  else                         \
-    MX_TILE1(MT, NT, false)
-  if (p.mt == 4) {
+                     const TilePlan& p, float* parts, int T, int K, int N, const BiasStrips& bias, hipStream_t stream) {
+  const int sums = bias.strips > 1 ? (bias.cols + 63) / 64 : 0;
+  const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit + sums));
+#define MX_TILE(MT, NT)                                                                                        \
+  hipLaunchKernelGGL((backward_kernel<MT, NT>), grid, dim3(256), 0, stream, dz, w, s, dx, parts, alpha, T, K, N, \
+                     ldz, p.mtiles, p.ntiles, p.nsplit, bias)
+  if (p.mt == 4)
     MX_TILE(4, 4);
-  } else if (p.mt == 2) {
+  else if (p.mt == 2)
     MX_TILE(2, 2);
-  } else {
+  else
     MX_TILE(1, 2);
-  }
-#undef MX_TILE1
 #undef MX_TILE
   if (p.nsplit > 1) {
     const int64_t pieces = (int64_t)T * (K / 8);
@@ -319,13 +347,9 @@ int launch_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const ui
                        b.ldz, bp, (int64_t)T, b.strip_rows);
     if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
   }
-  if (bp && b.strips > 1) {
-    const int st = launch_strip_sum(bp, b.strips, N, 1, &dbias, stream);
-    if (st != MX_OK) return st;
-  }
-  if (!dx) return MX_OK;
+  if (!dx) return b.strips > 1 ? launch_strip_sum(bp, b.strips, N, 1, &dbias, stream) : MX_OK;
   return launch_dx(direct ? dy : dz, direct ? N : b.ldz, w, s, dx, direct ? scale : 1.f, b.tile,
-                   reinterpret_cast<float*>(ws + b.parts), T, K, N, stream);
+                   reinterpret_cast<float*>(ws + b.parts), T, K, N, BiasStrips{bp, dbias, bp ? b.strips : 0, N}, stream);
 }
 
 int launch_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t* w, const uint8_t* s, int act,
@@ -337,12 +361,9 @@ int launch_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t
   const dim3 grid((I + DZ_COLS - 1) / DZ_COLS, b.strips);
   hipLaunchKernelGGL(dz_gated_kernel, grid, dim3(256), 0, stream, dh, z, I, act, dz, b.ldz, bp, (int64_t)T, b.strip_rows);
   if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
-  if (bp && b.strips > 1) {
-    const int st = launch_strip_sum(bp, b.strips, 2 * I, 1, &dbias, stream);
-    if (st != MX_OK) return st;
-  }
-  if (!dx) return MX_OK;
-  return launch_dx(dz, b.ldz, w, s, dx, 1.f, b.tile, reinterpret_cast<float*>(ws + b.parts), T, H, 2 * I, stream);
+  if (!dx) return b.strips > 1 ? launch_strip_sum(bp, b.strips, 2 * I, 1, &dbias, stream) : MX_OK;
+  return launch_dx(dz, b.ldz, w, s, dx, 1.f, b.tile, reinterpret_cast<float*>(ws + b.parts), T, H, 2 * I,
+                   BiasStrips{bp, dbias, bp ? b.strips : 0, 2 * I}, stream);
 }
 
 }  // namespace mx

@@ -509,13 +509,16 @@ struct BackwardLds {
 
 // acc[m][i] += W columns (as the MFMA's rows) x dz rows (its columns) over the stages
 // [st0, st1) of weight rows, for a workgroup of 2 x 2 waves.  dz has a multiple of 64 columns,
-// those past N zero.  As in forward_tile, what prepares the next step and the next stage goes
-// between the matrix instructions: reads of both operands' fragments, decoding the weights of
-// the next stage, whose codes were loaded a stage before, and copies of its dz rows.
-// S4: K % 128 == 0 and s is 4-byte aligned; a row's scale then comes with the 4 bytes around
-// it.  (A loaded byte is widened where the loop begins, long before its use, and the wave
-// waits for it there.)
-template <int MT, int NT, bool S4>
+// those past N zero.  A stage is 4 steps, and as in forward_tile what prepares later ones goes
+// between the matrix instructions.  Both operands' fragments come from the LDS here (192 KB of
+// its traffic a stage of 256 x 256, three quarters of the time of the products), so they are
+// read two steps ahead, one every other slot, and the barrier stands in the middle of the
+// stage: from step 2 on the next stage's fragments are read, and the buffer of the current one
+// is filled again, dz rows by copies, weights by decoding codes that were loaded nearly a stage
+// before.  The gate_up backward of 4096 tokens (H = 7168, I = 2048) takes 220 us with the work
+// spread like this, 221 with all reads in the first half of a step and decoding in two of the
+// four, and 225 with the codes loaded 30 products before their use as well.
+template <int MT, int NT>
 __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>::Rows& rows,
                                               const uint8_t* __restrict__ w, const uint8_t* __restrict__ s, int N,
                                               int K, int k0, int st0, int st1, uint8_t* lds, int wm, int wn, int lane,
@@ -526,13 +529,12 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   const int r = lane & 31, g = lane >> 5, o = threadIdx.x >> 5, q = threadIdx.x & 31;
   const int wld = K >> 1, sld = K >> 5;
   const int col = min(k0 + CPT * q, K - CPT);  // columns past K: the last ones again, never stored
-  const int block = col >> 5, sshift = S4 ? 8 * (block & 3) : 0, sfirst = S4 ? block & ~3 : block;
   // byte offsets of this thread's 8 rows from the stage's first
   uint32_t woff[8], soff[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     woff[i] = (uint32_t)((o * 8 + i) * wld + (col >> 1));
-    soff[i] = (uint32_t)((o * 8 + i) * sld + sfirst);
+    soff[i] = (uint32_t)((o * 8 + i) * sld + (col >> 5));
   }
   uint32_t at[4], wat[4];  // LDS byte offsets of this lane's chunks at step u, first tile
 #pragma unroll
@@ -546,7 +548,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   uint32_t code[8];  // of the stage after the current one, and its rows' scales
   float scale[8];
   uint32_t code2[8], scale2[8];  // of the stage after that, as loaded
-  u32x4 frag[2][MT], wf[2][NT], column[2];
+  u32x4 frag[STEPS][MT], wf[STEPS][NT], column[2];
   // The first weight row of the stage that load_one loads from, moved on a stage at a time.
   const uint8_t* wstage = w + (size_t)st0 * BWD_KB * wld;
   const uint8_t* sstage = s + (size_t)st0 * BWD_KB * sld;
@@ -555,14 +557,11 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
       code2[i] = *reinterpret_cast<const uint32_t*>(wstage + woff[i]);
     else
       code2[i] = *reinterpret_cast<const uint16_t*>(wstage + woff[i]);
-    if constexpr (S4)
-      scale2[i] = *reinterpret_cast<const uint32_t*>(sstage + soff[i]);
-    else
-      scale2[i] = sstage[soff[i]];
+    scale2[i] = sstage[soff[i]];
   };
   auto take_one = [&](int i) {
     code[i] = here(code2[i]);
-    scale[i] = __uint_as_float(here(__float_as_uint(e8m0_scale_operand(S4 ? (scale2[i] >> sshift) & 0xFFu : scale2[i]))));
+    scale[i] = __uint_as_float(here(__float_as_uint(e8m0_scale_operand(scale2[i]))));
   };
   auto move_on = [&](bool yes) {
     wstage += yes ? BWD_KB * wld : 0;
@@ -576,7 +575,7 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
     for (int i = 0; i < 8; ++i) {
       const int row = min(o * 8 + i, left - 1);
       woff[i] = (uint32_t)(row * wld + (col >> 1));
-      soff[i] = (uint32_t)(row * sld + sfirst);
+      soff[i] = (uint32_t)(row * sld + (col >> 5));
     }
   };
   auto clear_rows = [&]() {
@@ -597,91 +596,95 @@ __device__ __forceinline__ void backward_tile(const typename BackwardLds<MT, NT>
   };
   auto read_one = [&](const uint8_t* buf, int u, int e) {  // operand e of step u
     if (e < MT)
-      frag[u & 1][e] = ld16(buf + at[u] + e * 4096);
+      frag[u][e] = ld16(buf + at[u] + e * 4096);
     else
-      wf[u & 1][e - MT] = ld16(buf + wat[u] + (e - MT) * 4096);
+      wf[u][e - MT] = ld16(buf + wat[u] + (e - MT) * 4096);
+  };
+  // Decoding takes the slots of steps 2, 3 and the next 0: unit e of UNITS is a row pair of a
+  // column pair, whose columns are written after its last.
+  constexpr int UNITS = 4 * NT;
+  auto unit = [&](uint8_t* buf, auto E) __attribute__((always_inline)) {
+    constexpr int e = E;
+    decode_pair(std::integral_constant<int, e / 4>{}, std::integral_constant<int, e % 4>{});
+    if constexpr (e % 4 == 3) {
+      put_column(buf, e / 4, 0);
+      put_column(buf, e / 4, 1);
+    }
   };
 
-  // the first stage's operands and the second's codes
+  // the first stage, the second as far as a step 3 leaves it, and the third's codes
   const bool ragged = left < BWD_KB;
-  if (ragged && st0 == last_stage) clamp_rows();
+  uint8_t* cur = lds;
+  uint8_t* nxt = lds + L::ONE;
+  const int second = min(st0 + 1, st1 - 1), third = min(st0 + 2, st1 - 1);
+  auto load_stage = [&](int st) {
+    if (ragged && st == last_stage) clamp_rows();
 #pragma unroll
-  for (int i = 0; i < 8; ++i) load_one(i);
-  rows.copy(lds, st0);
+    for (int i = 0; i < 8; ++i) load_one(i);
+  };
+  auto take_stage = [&](int st) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) take_one(i);
-  if (ragged && st0 == last_stage) clear_rows();
-  unrolled<NT>([&](auto B) __attribute__((always_inline)) {
-    unrolled<4>([&](auto P2) __attribute__((always_inline)) { decode_pair(B, P2); });
-    put_column(lds, B, 0);
-    put_column(lds, B, 1);
-  });
-  const int second = min(st0 + 1, st1 - 1);
+    for (int i = 0; i < 8; ++i) take_one(i);
+    if (ragged && st == last_stage) clear_rows();
+  };
+  load_stage(st0);
+  rows.copy(cur, st0);
+  rows.copy(nxt, second);
+  take_stage(st0);
   move_on(second > st0);
-  if (ragged && second == last_stage) clamp_rows();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) load_one(i);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) take_one(i);
+  load_stage(second);
+  unrolled<UNITS>([&](auto E) __attribute__((always_inline)) { unit(cur, E); });
+  take_stage(second);
+  move_on(third > second);
+  load_stage(third);
+  unrolled<UNITS>([&](auto E) __attribute__((always_inline)) {
+    if constexpr (3 * E < 2 * UNITS) unit(nxt, E);
+  });
   wait_copies();
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < READS; ++e) read_one(lds, 0, e);
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int e = 0; e < READS; ++e) read_one(cur, u, e);
   settle_mfma(acc);  // the accumulators have been cleared
 
-  uint8_t* cur = lds;
-  uint8_t* nxt = lds + L::ONE;
   for (int st = st0; st < st1; ++st) {
-    // the stages that are decoded and copied, and loaded, meanwhile; past the last one that one
-    // again, which nothing uses
-    const int cs = min(st + 1, st1 - 1), ls = min(st + 2, st1 - 1);
-    move_on(ls > cs);
-    if (ragged) {
-      if (cs == last_stage) clear_rows();
-      if (ls == last_stage) clamp_rows();
-    }
+    // the stages that are decoded and copied, and loaded, from step 2 on; past the last one that
+    // one again, which nothing uses
+    const int cs = min(st + 2, st1 - 1), ls = min(st + 3, st1 - 1);
     unrolled<STEPS>([&](auto U) __attribute__((always_inline)) {
-      constexpr int u = U, next = (u + 1) % STEPS;
-      constexpr bool last = u == STEPS - 1;
-      if constexpr (last) {
+      constexpr int u = U;
+      if constexpr (u == 2) {
+        if (ragged) {
+          if (cs == last_stage) clear_rows();
+          if (ls == last_stage) clamp_rows();
+        }
+        move_on(ls > cs);
         wait_copies();
-        __syncthreads();  // the next stage is whole, and no wave reads `cur` any more
+        __syncthreads();  // the next stage is whole, and every wave has read the last of `cur`
       }
       unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
-        constexpr int k = S, m = k / NT, i = k % NT, n = u * SLOTS + k;
-        mfma_in_place(acc[m][i], wf[u & 1][i], frag[u & 1][m]);
-        constexpr int per_read = (READS + SLOTS - 1) / SLOTS;
-        unrolled<per_read>([&](auto E) __attribute__((always_inline)) {
-          constexpr int e = k * per_read + E;
-          if constexpr (e < READS) read_one(last ? nxt : cur, next, e);
+        constexpr int k = S, m = k / NT, i = k % NT;
+        mfma_in_place(acc[m][i], wf[u][i], frag[u][m]);
+        // of n items E stands in slot E * slots / n, the reads half a distance later
+        unrolled<READS>([&](auto E) __attribute__((always_inline)) {
+          if constexpr ((2 * E + 1) * SLOTS / (2 * READS) == k) read_one(u < 2 ? cur : nxt, (u + 2) % STEPS, E);
         });
-        // step 0: codes and scales of the stage after next, copies of the next stage's dz rows
-        if constexpr (u == 0) {
-          unrolled<8>([&](auto E) __attribute__((always_inline)) {
-            if constexpr (E * SLOTS / 8 == k) load_one(E);
-          });
+        constexpr int d = (u + 2) % STEPS * SLOTS + k;  // slot of the decoding
+        unrolled<UNITS>([&](auto E) __attribute__((always_inline)) {
+          if constexpr (E * (3 * SLOTS) / UNITS == d) unit(u == 0 ? nxt : cur, E);
+        });
+        // step 1: what was loaded in step 3 is taken over; step 2: copies of dz rows; step 3:
+        // loads of codes and scales
+        unrolled<8>([&](auto E) __attribute__((always_inline)) {
+          if constexpr (E * SLOTS / 8 == k) {
+            if constexpr (u == 1) take_one(E);
+            if constexpr (u == 3) load_one(E);
+          }
+        });
+        if constexpr (u == 2)
           unrolled<COPIES>([&](auto E) __attribute__((always_inline)) {
-            if constexpr ((2 * E + 1) * SLOTS / (2 * COPIES) == k) rows.copy_one(nxt, cs, E);
-          });
-        }
-        // decoding the next stage: steps 1 and 2, a column pair's 4 row pairs, then its writes
-        constexpr int units = 4 * NT, per_unit = (units + 2 * SLOTS - 1) / (2 * SLOTS);
-        constexpr int every = per_unit > 1 ? 1 : 2 * SLOTS / units;
-        if constexpr (u > 0 && !last && n % every == 0)
-          unrolled<per_unit>([&](auto E) __attribute__((always_inline)) {
-            constexpr int e = (n - SLOTS) / every * per_unit + E;
-            if constexpr (e < units) {
-              decode_pair(std::integral_constant<int, e / 4>{}, std::integral_constant<int, e % 4>{});
-              if constexpr (e % 4 == 3) {
-                put_column(nxt, e / 4, 0);
-                put_column(nxt, e / 4, 1);
-              }
-            }
-          });
-        // step 3: what was loaded in step 0 is taken over
-        if constexpr (last)
-          unrolled<8>([&](auto E) __attribute__((always_inline)) {
-            if constexpr (E * SLOTS / 8 == k) take_one(E);
+            if constexpr (E * SLOTS / COPIES == k) rows.copy_one(cur, cs, E);
           });
         keep_order();
       });
