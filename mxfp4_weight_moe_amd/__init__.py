@@ -570,6 +570,7 @@ def _act_code(act: str) -> int:
 # building a Stream object (2 us of the 12 that a call took).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _tensor(t, name: str, dtype, shape, dev):
@@ -600,7 +601,7 @@ def _call(fn, dev, *args):
     """The C call `fn` on dev's current stream, which is its last argument."""
     index = dev.index
     stream = _raw_stream(index)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         st = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
@@ -644,7 +645,7 @@ def mx_linear_fused(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tens
         _tensor(residual, "residual", _BF16, (T, N), dev)
     code = _act_code(act)
     if out is None:
-        out = x.new_empty((T, N))
+        out = x.new_empty((T, N)) if residual is None else torch.empty_like(residual)
     else:
         _tensor(out, "out", _BF16, (T, N), dev)
     z = torch.empty((T, N), dtype=_BF16, device=dev) if save_z else None
@@ -761,10 +762,10 @@ def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: tor
         _tensor(b, "b", _BF16, (T, H), dev)
         y = out
         if y is None:
-            y = x.new_empty((T, H))
+            y = torch.empty_like(x)
         else:
             _tensor(y, "out", _BF16, (T, H), dev)
-    xn = x.new_empty((T, H)) if w_pre is not None else None
+    xn = torch.empty_like(x) if w_pre is not None else None
     _call(_lib.mx_norm_residual, dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale, _opt(w_pre), eps,
           _opt(y), _opt(xn), T, H)
     return (x if y is None else y), xn
@@ -792,8 +793,8 @@ def mx_norm_residual_backward(dy: torch.Tensor | None, dxn: torch.Tensor | None,
         raise ValueError("w_pre, dxn and y go together")
     if b is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need b")
-    dx = first.new_empty((T, H))
-    db = first.new_empty((T, H)) if b is not None else None
+    dx = torch.empty_like(first)
+    db = torch.empty_like(first) if b is not None else None
     dgate = None
     if gate is not None:
         dgate = torch.empty(tuple(gate.shape), dtype=_BF16 if mode == _GATE_FULL else _F32, device=dev)
@@ -827,7 +828,7 @@ def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tens
     mode = _gate_mode(gate, T, H, dev)
     code = _act_code(act)
     if out is None:
-        out = x.new_empty((T, H))
+        out = torch.empty_like(x)
     else:
         _tensor(out, "out", _BF16, (T, H), dev)
     ws, wp, wn = _scratch(_lib.mx_ffn_block_workspace_size(T, H, I), dev, ws)

@@ -98,7 +98,9 @@ __device__ __forceinline__ void act_values_slopes(int act, const float (&z)[V], 
       for (int i = 0; i < V; ++i) {
         const float p = logistic(gelu_tanh_arg(z[i]));
         a[i] = z[i] * p;
-        d[i] = __builtin_fmaf(a[i] * (1.f - p), 1.5957691216057308f * __builtin_fmaf(0.134145f * z[i], z[i], 1.f), p);
+        // z^2 held below overflow: the factor before it is 0 from |z| = 10 on
+        const float z2 = fminf(z[i] * z[i], 1e30f);
+        d[i] = __builtin_fmaf(a[i] * (1.f - p), 1.5957691216057308f * __builtin_fmaf(0.134145f, z2, 1.f), p);
       }
       break;
     case MX_ACT_SIGMOID:
@@ -127,7 +129,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // V consecutive bf16 values from p (V = 4 or 8), as one piece where all V exist (`wide`), else
 // one by one up to `n` values (the rest read as 0).  A piece need not be aligned beyond its
 // values: rows of an odd length stay whole accesses (global memory takes them at any address;
-// value by value a gate_up of 4096 tokens with I = 1466 took 65 us instead of 49).
+// value by value a gate_up of 3332 tokens with H = 2240, I = 1466 took 65 us instead of 62).
 template <int V>
 struct Piece {
   uint32_t q[V / 2];

@@ -222,6 +222,22 @@ def test_linear_backward(mx, T, K, N):
         assert again[1] is None and torch.equal(again[0], dx)
 
 
+@pytest.mark.parametrize("kind", ["relu", "silu", "gelu", "gelu_tanh", "sigmoid"])
+def test_far_values(mx, kind):
+    """Where squares and cubes of z overflow, activations and slopes are their limits."""
+    z = torch.tensor([[1e15, -1e15, 1e20, -1e20, 1e30, -1e30, 3e38, -3e38]]).bfloat16()
+    N, K = 8, 32
+    w = torch.zeros(N, K // 2, dtype=torch.uint8)
+    s = torch.full((N, 1), 127, dtype=torch.uint8)
+    dy = torch.arange(1.0, 9.0).reshape(1, N).bfloat16()
+    pos = (z > 0).double()
+    say("far values", kind)
+    y = mx.mx_linear_fused(*cuda(torch.zeros(1, K, dtype=torch.bfloat16), w, s), bias=z[0].to(DEV), act=kind)
+    assert torch.equal(y.double().cpu(), pos if kind == "sigmoid" else pos * z.double())
+    db = mx.mx_linear_fused_backward(*cuda(dy, w, s, z), 1.0, kind, need_dx=False)[1]
+    assert torch.equal(db.double().cpu(), (dy.double() * pos * (kind != "sigmoid"))[0])
+
+
 def test_backward_nan_and_neighbours(mx):
     for T in (2, 70, 1030):
         g = gen(T)
