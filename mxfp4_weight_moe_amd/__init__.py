@@ -1,5 +1,6 @@
-"""Python binding of the mxmoe C ABI (include/mxmoe.h): MXFP4 weight-streaming MoE layer
-and dense MXFP4 linear layer for MI355X (gfx950).
+"""Python binding of the mxmoe C ABI (include/mxmoe.h): MXFP4 weight-streaming MoE layer,
+dense MXFP4 linear layer and dense feed-forward operators with their gradients for MI355X
+(gfx950).
 
 Argument marshalling only: every step of the computation runs in the HIP kernels of
 libmxmoe.so.  PyTorch provides device memory and the current stream.  If the library is

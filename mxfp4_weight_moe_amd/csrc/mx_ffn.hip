@@ -31,8 +31,10 @@ struct EpilogueOf<true> {
 };
 
 // A workgroup has one MFMA tile of 16 weight rows: 16 rows of a linear layer, or 8 gate rows and
-// the 8 up rows of the same columns (a tile of each would leave half the CUs idle at I = 2048:
-// 9.9 us at T = 8 with H = 7168).
+// the 8 up rows of the same columns (a tile of each would leave half the CUs idle at I = 2048).
+// Bound by the latency of a workgroup's few serial steps: 7168 -> 4096 with 4 tokens takes
+// 6.8 us (2.3 TB/s of weights), gate_up of 8 tokens, H = 7168, I = 2048, 7.5 us (9.9 with a tile
+// of each).
 // SBYTE: scale rows whose length is no multiple of 8 bytes (K % 256 != 0) go byte by byte.
 // XL: the workgroup first copies x to LDS (dynamic, T * K bf16); read from memory, only T of
 // every 16 lanes of a fragment load are active.
@@ -125,6 +127,11 @@ __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restri
 // linear layer), rounded up so that a lane's 8 consecutive values always fit.
 __host__ __device__ static inline int part_cols(int rows) { return (rows + 7) / 8 * 8; }
 
+// Bound by the matrix units at the clock that the power limit leaves (79% busy at 1.8 GHz):
+// 4096 tokens, 7168 -> 4096 with gelu, bias and residual 191 us, 1.26 PFLOP/s; gate_up of the same
+// size with z kept 173 us.  The epilogue of a 256 x 256 tile (26 and 10 us of these) has nothing
+// to overlap with: its accumulators fill the registers.
+//
 // rows: output columns (N, or I for gate_up).  nsplit > 1: part z of K goes to parts[z] as
 // fp32 [T][part columns (x 2)].  A wave's NT MFMA tiles are 32 consecutive weight rows each;
 // for gate_up the first half of them gate rows, the second half the up rows of the same columns.
@@ -256,9 +263,12 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
 // A workgroup takes 32 NT weight rows (gate_up: half of them gate rows, half the up rows of the
 // same columns) and a wave each 32 tokens.  A wave loads everything it needs by itself, its
 // activation rows and its own copy of the codes and scales, into a ring of its own in the LDS:
-// no barriers.  With N >= 6144 or so and NT = 1 there is no split of K either, whose second
-// launch costs 3 to 4 us at these sizes; with fewer rows NT = 2 halves the activations that a
-// CU reads beside the same weights, and K is split.
+// no barriers.  Where 32 rows a workgroup give three quarters of the CUs one, there is no split
+// of K either, whose second launch costs 3 to 4 us at these sizes; with fewer rows NT = 2 halves
+// the activations that a CU reads beside the same weights, and K is split (gate_up of 128 tokens,
+// H = 7168, I = 2048: 20.2 us, with NT = 1 and 128 workgroups 21.4).  Bound by what a CU reads
+// through its L2, 0.7 MB there; 77 tokens, 2048 -> 7168: 10 us.  Tiles of 128 x 128 with
+// barriers took 17 and 25 us.
 constexpr int THIN_MAX_T = 128;
 template <int NT>
 struct ThinStage {
@@ -452,7 +462,7 @@ TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated) {
     p.mtiles = 1;
     p.thin = 1;
     p.ntiles = (int)((rows + (gated ? 15 : 31)) / (gated ? 16 : 32));
-    if (4 * p.ntiles < 3 * GPU_CUS) {  // measured: H = 7168, I = 2048, T = 128
+    if (4 * p.ntiles < 3 * GPU_CUS) {  // see thin_kernel
       p.thin = 2;
       p.ntiles = (p.ntiles + 1) / 2;
     }
@@ -511,8 +521,8 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   const TilePlan p = forward_plan(T, K, rows, GATED);
   float* parts = static_cast<float*>(workspace);
   const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-  // One tile a CU and K in whole stages: more stages in the LDS.  Measured at T = 128 with
-  // H = 7168, I = 2048 (7 stages a workgroup); see forward_tile.
+  // One tile a CU and K in whole stages: more stages in the LDS (gate_up of 128 tokens, H = 7168,
+  // I = 2048, with tiles of 128 x 128: 25 us, 27 with two stages).
   const bool deep = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS && K % FWD_KB == 0 &&
                     (int64_t)rows * (K >> 5) < ((int64_t)1 << 31);
 #define MX_TILE(MT, NT, D)                                                                                           \

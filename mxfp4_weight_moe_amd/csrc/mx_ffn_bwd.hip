@@ -11,7 +11,9 @@ namespace mx {
 
 // ------------------------------------------------------------------ dz and the bias gradient
 
-// A workgroup takes 256 columns (32 threads of 8) and a strip of rows, 8 at a time.
+// A workgroup takes 256 columns (32 threads of 8) and a strip of rows, 8 at a time.  Bound by
+// memory: 2048 x 4096 with z 50 MB in 12 us, 4.1 TB/s; gated, 4096 x 2048, 84 MB in 14 us (inputs
+// partly from the last-level cache).
 constexpr int DZ_COLS = 256;
 
 struct LinearSlope {
@@ -69,7 +71,7 @@ __global__ void __launch_bounds__(256) dz_kernel(Slope f, uint16_t* __restrict__
   }
 }
 
-// gate_up: 8 columns of both halves a thread.
+// gate_up: 8 columns of both halves a thread, see above.
 __global__ void __launch_bounds__(256) dz_gated_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ z,
                                                        int I, int act, uint16_t* __restrict__ dz, int ldz,
                                                        float* __restrict__ parts, int64_t T, int strip_rows) {
