@@ -230,12 +230,13 @@ struct LinearEpilogue {
       for (int i = 0; i < V; ++i) v[i] += b[i];
     if (z) store_bf16<V>(z + at, v, wide<V>(n), N - n);
     act_values(act, v);
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= scale;
     unpack(res, r);
     if (residual)
 #pragma unroll
-      for (int i = 0; i < V; ++i) v[i] += r[i];
+      for (int i = 0; i < V; ++i) v[i] = __builtin_fmaf(scale, v[i], r[i]);
+    else
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] *= scale;
     store_bf16<V>(y + at, v, wide<V>(n), N - n);
   }
 };

@@ -150,11 +150,11 @@ __device__ __forceinline__ void tile_zero(f32x16 (&acc)[MT][NT]) {
 // same work, the small ones leave fewer CUs idle in the last round.  What a round of each takes
 // (of 256 and of 512 tiles; microseconds at a reduction of 7168 forward and 4096 backward):
 //   forward   174 and 106     gate_up of 1536 to 4096 tokens, H = 7168, I = 2048
-//   backward  110 and 82      7168 <- 4096, 1024 to 2048 tokens
-// e.g. gate_up at 2048 tokens takes 107 with the small tiles and 113 with the large ones, at
-// 3000 tokens 175 and 141.
+//   backward   99 and 80      7168 <- 4096, 2048 and 1024 tokens
+// e.g. gate_up at 2048 tokens takes 108 with the small tiles and 111 with the large ones, at
+// 3000 tokens 174 and 143; the backward of 4096 tokens 270 and 200.
 constexpr int FORWARD_ROUND_256 = 174, FORWARD_ROUND_128 = 106;
-constexpr int BACKWARD_ROUND_256 = 110, BACKWARD_ROUND_128 = 82;
+constexpr int BACKWARD_ROUND_256 = 99, BACKWARD_ROUND_128 = 80;
 inline int tile_choice(int64_t T, int64_t cols, int64_t round_256, int64_t round_128) {
   const int64_t large = ((T + 255) / 256) * ((cols + 255) / 256), small = ((T + 127) / 128) * ((cols + 127) / 128);
   return (large + GPU_CUS - 1) / GPU_CUS * round_256 <= (small + 2 * GPU_CUS - 1) / (2 * GPU_CUS) * round_128 ? 4 : 2;
