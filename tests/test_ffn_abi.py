@@ -114,6 +114,15 @@ def test_alignment(call, names):
         assert call(gate=P((1 << 20) + 1), mode=1) == ALIGN
 
 
+@pytest.mark.parametrize("call,K", [(linear, "K"), (gate_up, "H")])
+def test_scale_alignment(call, K):
+    """8 bytes where K % 256 == 0, 4 where K % 128 == 0, else any: what passes is refused for its workspace."""
+    for k, off, want in ((2048, 4, ALIGN), (2048, 8, WORKSPACE), (2176, 2, ALIGN), (2176, 4, WORKSPACE),
+                         (2080, 1, WORKSPACE)):
+        assert call(**{K: k}, s=P((1 << 20) + off), ws=None) == want, (k, off)
+    assert linear_bwd(s=P((1 << 20) + 1), K=2048, ws=None) == WORKSPACE
+
+
 def test_workspaces():
     L = m.raw()
     need = L.mx_linear_fused_workspace_size(64, 2048, 64)

@@ -632,6 +632,71 @@ def test_offsets_past_32_bits(mx):
     within(xn[rows], want, ((1 + B) * (H + 16) * U + B) * want.abs(), "xn")
 
 
+def test_most_tokens(mx):
+    """T = 2^24, the limit: sampled rows against the definition, the bias gradient whole."""
+    T, N = 1 << 24, 3
+    rows = [0, 1 << 22, 3 << 22, T - 2, T - 1]
+    for K in (32, 128):
+        g = gen(K)
+        dg = torch.Generator(device=DEV)
+        dg.manual_seed(K)
+        say("most tokens", K)
+        x = torch.randn((T, K), generator=dg, device=DEV, dtype=torch.bfloat16)
+        w, s = weights(2 * N, K, g)
+        wd, sd = cuda(w, s)
+        y = mx.mx_linear_fused(x, wd[:N], sd[:N].clone())
+        xr = x[rows].cpu()
+        z, ez = z_of(xr, w[:N], s[:N], None)
+        within(y[rows], z, (1 + B) * ez + B * z.abs(), "y")
+        h, zg = mx.mx_gate_up(x, wd, sd, act="relu", save_z=True)
+        z, ez = z_of(xr, w, s, None)
+        want, u = z[:, :N].clamp(min=0), z[:, N:]
+        err = ez[:, :N] * u.abs() + ez[:, N:] * want + ez[:, :N] * ez[:, N:] + U * (want * u).abs()
+        within(h[rows], want * u, (1 + B) * err + B * (want * u).abs(), "h")
+        del x
+        dx, db = mx.mx_linear_fused_backward(y, wd[:N], sd[:N].clone())
+        dz = y[rows].double().cpu()
+        check_dx(dx[rows].cpu(), dz, torch.zeros_like(dz), w[:N], s[:N], False, N)
+        # 1024 strips of 2^14 rows: 2^11 + 8 + 1024 additions in a row at most
+        yd = y.double()
+        within(db, yd.sum(0).cpu(), (2 ** 12) * U * yd.abs().sum(0).cpu(), "dbias")
+        del yd, dx
+        dx, db = mx.mx_gate_up_backward(h, zg, wd, sd, act="relu")
+        hr, zr = h[rows].double().cpu(), zg[rows].double().cpu()
+        dz = torch.cat((hr * zr[:, N:] * (zr[:, :N] > 0), hr * zr[:, :N].clamp(min=0)), 1)
+        check_dx(dx[rows].cpu(), dz, 4 * U * dz.abs(), w, s, True, 2 * N)
+        del dx, db, y, h, zg
+    say("most tokens, norm")
+    x = torch.randn((T, 8), generator=dg, device=DEV, dtype=torch.bfloat16)
+    one = torch.ones(8, dtype=torch.bfloat16, device=DEV)
+    xn = mx.mx_norm_residual(x, w_pre=one)[1]
+    v = x[rows].double().cpu()
+    want = v * rms(v)
+    within(xn[rows], want, ((1 + B) * 24 * U + B) * want.abs(), "xn")
+
+
+@pytest.mark.parametrize("T", [3, 40, 200])
+def test_longest_reduction(mx, T):
+    """K = 2^20 forward, and N = 2^20 weight rows in the backward product."""
+    K, N = 1 << 20, 33
+    g = gen(T)
+    x, (w, s) = bf(T, K, g=g), weights(N, K, g)
+    say("longest reduction", T)
+    y = mx.mx_linear_fused(*cuda(x, w, s))
+    z, ez = z_of(x, w, s, None)
+    within(y, z, (1 + B) * ez + B * z.abs(), "y")
+    dy = bf(T, N, g=g)
+    dx, db = mx.mx_linear_fused_backward(*cuda(dy, w, s))
+    dz = dy.double()
+    check_dx(dx, dz, torch.zeros_like(dz), w, s, False, N)
+    within(db, dz.sum(0), (T + 8) * U * dz.abs().sum(0), "dbias")
+    dy, (w, s) = bf(T, K, g=g), weights(K, 32, g)
+    dx, db = mx.mx_linear_fused_backward(*cuda(dy, w, s))
+    dz = dy.double()
+    check_dx(dx, dz, torch.zeros_like(dz), w, s, False, K)
+    within(db, dz.sum(0), (T + 8) * U * dz.abs().sum(0), "dbias")
+
+
 def test_block_in_place(mx):
     T, H, I = 40, 256, 96
     x, wgu, sgu, wd, sd, wi, bgu, bd, wo, gate = block_inputs(T, H, I, 12)
