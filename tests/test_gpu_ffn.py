@@ -376,8 +376,11 @@ def norm_grads(dy, dxn, y, b, w_post, gate, scale, w_pre, mode):
 
 
 # every kernel width (one wave up to 1024 threads), rows that fill it and odd ones
+# rows of a quarter and half a wave, of 1 to 16 waves, and more than one piece a thread; several
+# rows a workgroup
 NORM_SHAPES = [(1, 8), (3, 64), (5, 512), (2, 520), (33, 1000), (7, 2048), (4, 2056), (9, 4096), (600, 72), (3, 7168),
-               (5, 8200), (2, 16384), (1030, 264), (2100, 40)]
+               (5, 8200), (2, 16384), (1030, 264), (2100, 40), (2050, 128), (701, 136), (1031, 256), (300, 1024),
+               (260, 8704)]
 NORM_KINDS = [("full", True, True), ("none", True, True), ("channel", True, True), ("token", True, False),
               ("token", False, True), ("channel", False, False), ("none", False, True), (None, False, True)]
 
