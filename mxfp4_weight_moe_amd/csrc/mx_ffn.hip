@@ -5,8 +5,8 @@
 // product, scale and residual are applied to the fp32 sums, and each output is rounded once.
 //
 // Three kernels, by the number of tokens:
-//   * up to STREAM_MAX_T (and for K < 128) a workgroup owns 16 weight rows, its waves split K,
-//     and every weight byte is read once (stream_kernel);
+//   * few (up to 8 or 16, to 32 for odd K; any for K < 128): a workgroup owns 16 weight rows, its
+//     waves split K, and every weight byte is read once (stream_kernel);
 //   * up to THIN_MAX_T a wave takes 32 tokens and 32 or 64 weight rows (thin_kernel);
 //   * beyond, tiles of tokens x rows (mx_tile.hpp), where the matrix instructions set the time
 //     (forward_kernel).
@@ -277,7 +277,8 @@ struct ThinStage {
   static constexpr int LOADS = 8 + 2 * NT + 1;  // a stage's copies to LDS
 };
 
-template <int NT, bool GATED>
+// KS: waves to the same 32 tokens, among which K is split; their sums meet in the LDS.
+template <int NT, bool GATED, int KS>
 __global__ void __launch_bounds__(256, 1)
     thin_kernel(const uint16_t* __restrict__ x, const uint8_t* __restrict__ w, const uint8_t* __restrict__ s,
                 typename EpilogueOf<GATED>::type epi, float* __restrict__ parts, int T, int K, int rows, int ntiles,
@@ -287,9 +288,9 @@ __global__ void __launch_bounds__(256, 1)
   constexpr int COLS = GATED ? 16 * NT : 32 * NT;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int tile = xcd_tile(blockIdx.x, ntiles * nsplit);
-  const int split = tile % nsplit, n0 = tile / nsplit * COLS, m0 = wave * 32;
-  const int stages = K / FWD_KB;
-  const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
+  const int split = tile % nsplit, n0 = tile / nsplit * COLS, m0 = wave / KS * 32;
+  const int stages = K / FWD_KB, part = split * KS + wave % KS, of = nsplit * KS;
+  const int st0 = (int)((int64_t)stages * part / of), st1 = (int)((int64_t)stages * (part + 1) / of);
   uint8_t* ring = lds + wave * (L::D * L::BYTES);
 
   // Rows that do not exist lie past the end of their buffers and read as zero.
@@ -345,10 +346,13 @@ __global__ void __launch_bounds__(256, 1)
   uint8_t* nxt = ring + L::BYTES;
   uint8_t* fill = ring + 2 * L::BYTES;
   static_assert(L::D == 3, "three buffers");
-  load(st0, cur);
-  load(min(st0 + 1, st1 - 1), nxt);
-  wait_copies<L::LOADS>();
-  Operands o = read(cur);
+  Operands o{};
+  if (KS == 1 || st0 < st1) {  // K may have fewer stages than parts
+    load(st0, cur);
+    load(min(st0 + 1, st1 - 1), nxt);
+    wait_copies<L::LOADS>();
+    o = read(cur);
+  }
   for (int st = st0; st < st1; ++st) {
     load(min(st + 2, st1 - 1), fill);  // its last content was used two stages ago
     wait_copies<L::LOADS>();           // the next stage has landed
@@ -376,14 +380,22 @@ __global__ void __launch_bounds__(256, 1)
   constexpr int PIECES = COLS / 8, ROWS = 64 / PIECES;
   const int p = lane % PIECES, n = n0 + p * 8;
   const auto cols = epi.template columns<8>(n);
+  // each of the KS waves sums its share of the rows
+  constexpr int SHARE = 32 / KS, ITERS = (SHARE + ROWS - 1) / ROWS;
+  const uint8_t* first = lds + wave / KS * KS * (L::D * L::BYTES);
+  if constexpr (KS > 1) __syncthreads();
 #pragma unroll
-  for (int it = 0; it < 32 / ROWS; ++it) {
-    const int row = it * ROWS + lane / PIECES, t = m0 + row;
-    if (t >= T || n >= rows) continue;
+  for (int it = 0; it < ITERS; ++it) {
+    const int row = it * ROWS + lane / PIECES + wave % KS * SHARE, t = m0 + row;
+    if (t >= T || n >= rows || (ROWS > SHARE && lane / PIECES >= SHARE)) continue;
     f32x4 q[GATED ? 4 : 2];
 #pragma unroll
-    for (int j = 0; j < (GATED ? 4 : 2); ++j)
-      q[j] = *reinterpret_cast<const f32x4*>(ring + out_at<NT>(row, 2 * p + (j & 1) + (j >> 1) * (4 * NT)));
+    for (int j = 0; j < (GATED ? 4 : 2); ++j) {
+      const uint32_t at = out_at<NT>(row, 2 * p + (j & 1) + (j >> 1) * (4 * NT));
+      q[j] = *reinterpret_cast<const f32x4*>(first + at);
+#pragma unroll
+      for (int k = 1; k < KS; ++k) q[j] += *reinterpret_cast<const f32x4*>(first + k * (L::D * L::BYTES) + at);
+    }
     if (nsplit > 1) {
       float* o2 = parts + ((size_t)split * T + t) * ((GATED ? 2 : 1) * (size_t)pc) + n;
 #pragma unroll
@@ -451,22 +463,47 @@ __global__ void __launch_bounds__(64) combine_kernel(const float* __restrict__ p
 
 // ------------------------------------------------------------------ launch plans
 
+// Whether the up rows' scales lie within 32-bit offsets of the gate rows'.
+static bool scales_in_reach(int64_t K, int64_t rows, bool gated) {
+  return !gated || rows * (K >> 5) < ((int64_t)1 << 31);
+}
+// Thin tiles from 9 tokens on, or from 17 where one round of workgroups streams the weights with
+// the activations in the LDS (4096 -> 4096, 16 tokens: 6.5 us against 6.9; 4096 -> 7168, two
+// rounds: 11.3 against 7.5; at 8 tokens 6.7 and 6.9; 4096 -> 4096 at 32 tokens: 11.4 and 7.0).
+static bool takes_thin(int64_t T, int64_t K, int64_t rows, bool gated) {
+  if (T <= 8 || T > THIN_MAX_T || K % FWD_KB != 0 || !scales_in_reach(K, rows, gated)) return false;
+  return T > 16 || K % SEG_K != 0 || T * K > STREAM_XL || rows > GPU_CUS * (gated ? SUB_ROWS / 2 : SUB_ROWS);
+}
+static bool takes_stream(int64_t T, int64_t K, int64_t rows, bool gated) {
+  return K < FWD_KB || (T <= STREAM_MAX_T && !takes_thin(T, K, rows, gated));
+}
+
 // Which tile and how many parts of K.  Both depend on the sizes alone, so that the workspace a
 // call needs does too.
 TilePlan forward_plan(int64_t T, int64_t K, int64_t rows, bool gated) {
   TilePlan p{};
-  if (T <= STREAM_MAX_T || K < FWD_KB) return p;
+  if (takes_stream(T, K, rows, gated)) return p;
   const int64_t stages = (K + FWD_KB - 1) / FWD_KB;
   int64_t split;
-  if (T <= THIN_MAX_T && K % FWD_KB == 0 && rows * (K >> 5) < ((int64_t)1 << 31)) {
+  if (takes_thin(T, K, rows, gated)) {
+    // Waves of a workgroup that 32-token groups leave split K; over workgroups it is split where
+    // that saves a wave 12 stages or more, 4 left at least: with fewer the second launch costs
+    // more (up to 32 tokens 8192 -> 1000: 9.8 us whole, 8.5 in 4 parts; gate_up with H = 4096,
+    // I = 500: 7.1 and 8.9 in 2).
     p.mtiles = 1;
     p.thin = 1;
+    p.ks = T <= 32 ? 4 : T <= 64 ? 2 : 1;
     p.ntiles = (int)((rows + (gated ? 15 : 31)) / (gated ? 16 : 32));
-    if (4 * p.ntiles < 3 * GPU_CUS) {  // see thin_kernel
+    const int64_t per_wave = stages / p.ks;
+    const int pairs = (p.ntiles + 1) / 2;
+    const bool wide = p.ks == 1 && 4 * p.ntiles < 3 * GPU_CUS;  // see thin_kernel
+    split = std::max<int64_t>(1, std::min<int64_t>(GPU_CUS / (wide ? pairs : p.ntiles), per_wave / 4));
+    if (per_wave - per_wave / split < 12) {
+      split = 1;
+    } else if (wide) {
       p.thin = 2;
-      p.ntiles = (p.ntiles + 1) / 2;
+      p.ntiles = pairs;
     }
-    split = std::min<int64_t>(GPU_CUS / p.ntiles, stages / 4);
   } else {
     p.mt = T <= 64 ? 1 : tile_choice(T, rows * (gated ? 2 : 1), FORWARD_ROUND_256, FORWARD_ROUND_128);
     p.nt = p.mt == 4 ? 4 : 2;
@@ -484,12 +521,14 @@ template <bool GATED>
 static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
                           const typename EpilogueOf<GATED>::type& epi, void* workspace, int T, int K, int rows,
                           hipStream_t stream) {
-  if (T <= STREAM_MAX_T || K < FWD_KB) {
+  if (takes_stream(T, K, rows, GATED)) {
     const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
     const int items = (rows + cols - 1) / cols, nseg = K / SEG_K;
     int W = 1;
-    while (W < 8 && 2 * W <= nseg && items * W < 2048) W *= 2;
-    const bool sbyte = K % SEG_K != 0, xl = T <= 16 && !sbyte && (int64_t)T * K <= STREAM_XL;
+    while (W < 8 && 2 * W <= nseg && 2 * W * items <= 2048) W *= 2;
+    // up to 16 tokens in whole segments, up to 32 byte by byte; K % 256 == 0 with more than 16 is
+    // left for gate_up alone, where its scales are too far apart for the thin tiles
+    const bool sbyte = K % SEG_K != 0 || T > 16, xl = T <= 16 && !sbyte && (int64_t)T * K <= STREAM_XL;
     const dim3 grid(items * ((T + STREAM_MAX_T - 1) / STREAM_MAX_T)), block(W * 64);
     const unsigned xl_bytes = xl ? (unsigned)(T * K * 2) : 0u;
 #define MX_STREAM(WW, M, SB, XX) \
@@ -497,10 +536,8 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
 #define MX_STREAM_W(WW)               \
   if (xl)                             \
     MX_STREAM(WW, 1, false, true);    \
-  else if (!sbyte && T <= 16)         \
-    MX_STREAM(WW, 1, false, false);   \
   else if (!sbyte)                    \
-    MX_STREAM(WW, 2, false, false);   \
+    MX_STREAM(WW, 1, false, false);   \
   else if (T <= 16)                   \
     MX_STREAM(WW, 1, true, false);    \
   else                                \
@@ -524,17 +561,21 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   // One tile a CU and K in whole stages: more stages in the LDS (gate_up with H = 7168,
   // I = 2048: 256 tokens 30.6 us, 31.4 with two stages; 500 tokens 42.8 and 44.8).
   const bool deep = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS && K % FWD_KB == 0 &&
-                    (int64_t)rows * (K >> 5) < ((int64_t)1 << 31);
+                    scales_in_reach(K, rows, GATED);
 #define MX_TILE(MT, NT, D)                                                                                           \
   hipLaunchKernelGGL((forward_kernel<MT, NT, 2, 2, D, GATED>), grid, dim3(256), 0, stream, x, w, s, epi, parts, T, K, \
                      rows, p.mtiles, p.ntiles, p.nsplit)
-#define MX_THIN(NT)                                                                                                     \
-  hipLaunchKernelGGL((thin_kernel<NT, GATED>), grid, dim3(64 * ((T + 31) / 32)), 0, stream, x, w, s, epi, parts, T, K, rows, \
-                     p.ntiles, p.nsplit)
-  if (p.thin == 1)
-    MX_THIN(1);
-  else if (p.thin == 2)
-    MX_THIN(2);
+#define MX_THIN(NT, KS)                                                                                                 \
+  hipLaunchKernelGGL((thin_kernel<NT, GATED, KS>), grid, dim3(64 * KS * ((T + 31) / 32)), 0, stream, x, w, s, epi, parts, \
+                     T, K, rows, p.ntiles, p.nsplit)
+  if (p.thin == 2)
+    MX_THIN(2, 1);
+  else if (p.thin && p.ks == 4)
+    MX_THIN(1, 4);
+  else if (p.thin && p.ks == 2)
+    MX_THIN(1, 2);
+  else if (p.thin)
+    MX_THIN(1, 1);
   else if (p.mt == 4)
     MX_TILE(4, 4, 2);
   else if (p.mt == 2 && deep)

@@ -117,18 +117,18 @@ def test_alignment(call, names):
 @pytest.mark.parametrize("call,K", [(linear, "K"), (gate_up, "H")])
 def test_scale_alignment(call, K):
     """8 bytes where K % 256 == 0, 4 where K % 128 == 0, else any: what passes is refused for its workspace."""
-    for k, off, want in ((2048, 4, ALIGN), (2048, 8, WORKSPACE), (2176, 2, ALIGN), (2176, 4, WORKSPACE),
-                         (2080, 1, WORKSPACE)):
+    for k, off, want in ((8192, 4, ALIGN), (8192, 8, WORKSPACE), (8320, 2, ALIGN), (8320, 4, WORKSPACE),
+                         (8224, 1, WORKSPACE)):
         assert call(**{K: k}, s=P((1 << 20) + off), ws=None) == want, (k, off)
     assert linear_bwd(s=P((1 << 20) + 1), K=2048, ws=None) == WORKSPACE
 
 
 def test_workspaces():
     L = m.raw()
-    need = L.mx_linear_fused_workspace_size(64, 2048, 64)
-    assert need > 0 and linear(K=2048, wb=need - 1) == WORKSPACE
-    assert linear(K=2048, ws=None, wb=need) == WORKSPACE
-    assert linear(K=2048, ws=P((1 << 20) + 128), wb=need) == WORKSPACE
+    need = L.mx_linear_fused_workspace_size(64, 8192, 64)
+    assert need > 0 and linear(K=8192, wb=need - 1) == WORKSPACE
+    assert linear(K=8192, ws=None, wb=need) == WORKSPACE
+    assert linear(K=8192, ws=P((1 << 20) + 128), wb=need) == WORKSPACE
     for call, size in ((linear_bwd, L.mx_linear_fused_backward_workspace_size(64, 256, 64)),
                        (gate_up_bwd, L.mx_gate_up_backward_workspace_size(64, 256, 64)),
                        (norm_bwd, L.mx_norm_residual_backward_workspace_size(4, 64)),
@@ -137,8 +137,8 @@ def test_workspaces():
         assert call(wb=size - 1) == WORKSPACE
         assert call(ws=None) == WORKSPACE
         assert call(ws=P((1 << 20) + 16)) == WORKSPACE
-    need = L.mx_gate_up_workspace_size(64, 2048, 64)
-    assert need > 0 and gate_up(H=2048, wb=need - 1) == WORKSPACE
+    need = L.mx_gate_up_workspace_size(64, 8192, 64)
+    assert need > 0 and gate_up(H=8192, wb=need - 1) == WORKSPACE
     # a decode step streams the weights and needs none
     assert L.mx_linear_fused_workspace_size(4, 7168, 4096) == 0
     assert L.mx_gate_up_workspace_size(4, 7168, 2048) == 0

@@ -110,13 +110,17 @@ def value_error(z, ez, a):
 
 # ------------------------------------------------------------------ linear
 
-# streaming (T <= 32, K < 128), thin tiles (33 to 128 tokens), tiles of 64 (K % 128 != 0), 128 and
+# streaming (few tokens, K < 128), thin tiles (9 to 128 tokens, 1, 2 and 4 parts of K in a
+# workgroup, fewer stages than parts, over several workgroups), tiles of 64 (K % 128 != 0), 128 and
 # 256 rows, split and whole K, odd rows and columns, K tails of 32, 64 and 96
 LINEAR_SHAPES = [(1, 256, 64), (1, 32, 1), (2, 96, 7), (5, 512, 33), (16, 288, 16), (17, 2048, 40), (31, 256, 100),
                  (32, 160, 264), (33, 128, 8), (40, 32, 1), (64, 544, 130), (65, 256, 64), (77, 2048, 257),
                  (129, 96, 300), (300, 512, 520), (1025, 192, 264), (1300, 256, 65), (1100, 32, 512),
                  (128, 2048, 33), (97, 1024, 6200), (50, 2080, 70), (120, 1056, 64), (200, 2048, 129), (200, 2080, 65),
-                 (130, 4096, 64), (4100, 544, 2100), (4200, 128, 2060), (4097, 1024, 2049)]
+                 (130, 4096, 64), (4100, 544, 2100), (4200, 128, 2060), (4097, 1024, 2049),
+                 (12, 384, 40), (16, 8192, 40), (9, 128, 4300), (13, 512, 4200), (24, 128, 300), (25, 16384, 70),
+                 (48, 384, 33), (59, 8192, 100), (64, 128, 65), (90, 4096, 100), (3, 256, 4200), (3, 160, 9000),
+                 (8, 16384, 24)]
 
 
 def linear_inputs(T, K, N, seed):
@@ -259,7 +263,9 @@ def test_backward_nan_and_neighbours(mx):
 
 GATED_SHAPES = [(1, 256, 64), (1, 32, 1), (3, 96, 7), (16, 288, 33), (17, 512, 16), (32, 160, 100), (33, 128, 8),
                 (64, 544, 65), (65, 1024, 130), (130, 96, 257), (1025, 192, 136), (1100, 256, 33), (1030, 32, 264),
-                (128, 2048, 72), (90, 1024, 3100), (200, 2048, 40), (4100, 288, 1050), (4097, 512, 1031)]
+                (128, 2048, 72), (90, 1024, 3100), (200, 2048, 40), (4100, 288, 1050), (4097, 512, 1031),
+                (12, 640, 24), (10, 256, 2100), (32, 16384, 20), (20, 128, 9), (60, 8192, 33), (41, 256, 100),
+                (90, 4096, 60), (3, 256, 2100), (5, 16384, 17)]
 
 
 @pytest.mark.parametrize("T,H,I", GATED_SHAPES)
@@ -714,9 +720,10 @@ def test_block_in_place(mx):
 
 def test_caller_workspace(mx):
     """A caller's workspace with any content, one byte short refused."""
-    T, K, N = 40, 2048, 64
+    T, K, N = 40, 8192, 64
     x, w, s, bias, res = cuda(*linear_inputs(T, K, N, 2))
     need = mx.raw().mx_linear_fused_workspace_size(T, K, N)
+    assert need > 0
     ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)
     say("workspace", need)
     assert torch.equal(mx.mx_linear_fused(x, w, s, bias, ws=ws), mx.mx_linear_fused(x, w, s, bias))
