@@ -5,7 +5,7 @@
 // product, scale and residual are applied to the fp32 sums, and each output is rounded once.
 //
 // Three kernels, by the number of tokens:
-//   * few (up to 8 or 16, to 32 for odd K; any for K < 128): a workgroup owns 16 weight rows, its
+//   * few (up to 8, some sizes to 16, odd K to 32; any for K < 128): a workgroup owns 16 weight rows, its
 //     waves split K, and every weight byte is read once (stream_kernel);
 //   * up to THIN_MAX_T a wave takes 32 tokens and 32 or 64 weight rows (thin_kernel);
 //   * beyond, tiles of tokens x rows (mx_tile.hpp), where the matrix instructions set the time
@@ -258,14 +258,15 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
   }
 }
 
-// ------------------------------------------------------------------ 33 to 128 tokens: thin tiles
+// ------------------------------------------------------------------ up to 128 tokens: thin tiles
 
 // A workgroup takes 32 NT weight rows (gate_up: half of them gate rows, half the up rows of the
 // same columns) and a wave each 32 tokens.  A wave loads everything it needs by itself, its
 // activation rows and its own copy of the codes and scales, into a ring of its own in the LDS:
-// no barriers.  Where 32 rows a workgroup give three quarters of the CUs one, there is no split
-// of K either, whose second launch costs 3 to 4 us at these sizes; with fewer rows NT = 2 halves
-// the activations that a CU reads beside the same weights, and K is split (gate_up of 128 tokens,
+// no barriers in the loop.  Up to 64 tokens the waves that are left over split K.  Where 32 rows
+// a workgroup give three quarters of the CUs one, K is not split over workgroups, whose second
+// launch costs 3 to 4 us at these sizes; with fewer rows and more than 64 tokens NT = 2 halves the
+// activations that a CU reads beside the same weights, and K is split (gate_up of 128 tokens,
 // H = 7168, I = 2048: 20.2 us, with NT = 1 and 128 workgroups 21.4).  Bound by what a CU reads
 // through its L2, 0.7 MB there; 77 tokens, 2048 -> 7168: 10 us.  Tiles of 128 x 128 with
 // barriers took 17 and 25 us.
@@ -467,11 +468,12 @@ __global__ void __launch_bounds__(64) combine_kernel(const float* __restrict__ p
 static bool scales_in_reach(int64_t K, int64_t rows, bool gated) {
   return !gated || rows * (K >> 5) < ((int64_t)1 << 31);
 }
-// Thin tiles from 9 tokens on, or from 17 where one round of workgroups streams the weights with
+// Thin tiles from 9 tokens on (5, see below), or from 17 where one round of workgroups streams the weights with
 // the activations in the LDS (4096 -> 4096, 16 tokens: 6.5 us against 6.9; 4096 -> 7168, two
 // rounds: 11.3 against 7.5; at 8 tokens 6.7 and 6.9; 4096 -> 4096 at 32 tokens: 11.4 and 7.0).
+// Streaming scales byte by byte (K % 256 != 0) ends earlier: 4224 -> 5000, 8 tokens, 9.9 and 6.9.
 static bool takes_thin(int64_t T, int64_t K, int64_t rows, bool gated) {
-  if (T <= 8 || T > THIN_MAX_T || K % FWD_KB != 0 || !scales_in_reach(K, rows, gated)) return false;
+  if (T <= (K % SEG_K == 0 ? 8 : 4) || T > THIN_MAX_T || K % FWD_KB != 0 || !scales_in_reach(K, rows, gated)) return false;
   return T > 16 || K % SEG_K != 0 || T * K > STREAM_XL || rows > GPU_CUS * (gated ? SUB_ROWS / 2 : SUB_ROWS);
 }
 static bool takes_stream(int64_t T, int64_t K, int64_t rows, bool gated) {
@@ -525,6 +527,8 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
     const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
     const int items = (rows + cols - 1) / cols, nseg = K / SEG_K;
     int W = 1;
+    // as many waves as the CUs hold at once: at more than 256 workgroups of 8 a second round begins
+    // (4096 -> 7168, one token: 7.3 us with 8 waves, 5.4 with 4)
     while (W < 8 && 2 * W <= nseg && 2 * W * items <= 2048) W *= 2;
     // up to 16 tokens in whole segments, up to 32 byte by byte; K % 256 == 0 with more than 16 is
     // left for gate_up alone, where its scales are too far apart for the thin tiles

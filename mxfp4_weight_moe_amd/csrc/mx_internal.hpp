@@ -146,7 +146,7 @@ constexpr int GPU_CUS = 256;  // gfx950; launch plans use it, so that workspaces
 // A tiled product: the MFMA tiles of each of a workgroup's 2 x 2 waves (mt x nt of 32 x 32), the
 // workgroup tiles, and over how many workgroups the reduction is split (bytes: their fp32 parts).
 struct TilePlan {
-  int thin, ks;  // 9 to 128 tokens: the thin kernel's NT and KS (mt and nt unused), else 0
+  int thin, ks;  // up to 128 tokens: the thin kernel's NT and KS (mt and nt unused), else 0
   int mt, nt, mtiles, ntiles, nsplit;
   size_t bytes;
 };

@@ -120,7 +120,7 @@ LINEAR_SHAPES = [(1, 256, 64), (1, 32, 1), (2, 96, 7), (5, 512, 33), (16, 288, 1
                  (130, 4096, 64), (4100, 544, 2100), (4200, 128, 2060), (4097, 1024, 2049),
                  (12, 384, 40), (16, 8192, 40), (9, 128, 4300), (13, 512, 4200), (24, 128, 300), (25, 16384, 70),
                  (48, 384, 33), (59, 8192, 100), (64, 128, 65), (90, 4096, 100), (3, 256, 4200), (3, 160, 9000),
-                 (8, 16384, 24)]
+                 (8, 16384, 24), (5, 384, 40), (7, 4224, 70)]
 
 
 def linear_inputs(T, K, N, seed):
