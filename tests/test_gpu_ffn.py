@@ -641,6 +641,32 @@ def test_offsets_past_32_bits(mx):
     within(xn[rows], want, ((1 + B) * (H + 16) * U + B) * want.abs(), "xn")
 
 
+def test_gate_up_scales_past_32_bits(mx):
+    """Up rows whose scales begin 2 GB after the gate rows' (68 GB of codes)."""
+    I, K = 1 << 21, 1 << 15
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("needs 90 GB of GPU memory")
+    g = gen(8)
+    wd = torch.zeros((2 * I, K // 2), dtype=torch.uint8, device=DEV)
+    sd = torch.full((2 * I, K // 32), 118, dtype=torch.uint8, device=DEV)
+    n = 70
+    cols = torch.cat((torch.arange(I - n, I), torch.arange(n)))
+    for r in (cols, I + cols):
+        w, s = weights(len(cols), K, g)
+        wd[r.to(DEV)], sd[r.to(DEV)] = cuda(w, s)
+    both = torch.cat((cols, I + cols)).to(DEV)
+    w, s = wd[both].cpu(), sd[both].cpu()
+    for T in (3, 20, 40, 130):
+        say("gate_up scales far apart", T)
+        x = bf(T, K, g=g)
+        h = mx.mx_gate_up(x.to(DEV), wd, sd, act="relu")[:, cols.to(DEV)]
+        z, ez = z_of(x, w, s, None)
+        m = len(cols)
+        a, u = z[:, :m].clamp(min=0), z[:, m:]
+        err = ez[:, :m] * u.abs() + ez[:, m:] * a + ez[:, :m] * ez[:, m:] + U * (a * u).abs()
+        within(h, a * u, (1 + B) * err + B * (a * u).abs(), "h")
+
+
 def test_most_tokens(mx):
     """T = 2^24, the limit: sampled rows against the definition, the bias gradient whole."""
     T, N = 1 << 24, 3
