@@ -177,12 +177,14 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
 #pragma unroll
     for (int q = 0; q < L::Scales::COPIES; ++q) {
       const int i = 2 * q + (lane >> 5);
-      ss.off[q] = ((uint32_t)row_of((wn * NT + i) * 32 + (lane & 31)) + (i >= HALF ? (uint32_t)rows : 0u)) * (uint32_t)(K >> 5);
+      const uint32_t row = (uint32_t)row_of((wn * NT + i) * 32 + (lane & 31));
+      ss.off[q] = (row + (i >= HALF ? (uint32_t)rows : 0u)) * (uint32_t)(K >> 5);
     }
   }
   f32x16 acc[MT][NT];
   tile_zero(acc);
-  forward_tile<MT, NT, WM, WN, D>(xs, cs, ss, sbase, (uint32_t)(min(WN * WCOLS, rows - n0) * (K >> 5)), soff, K, st0, st1, lds, wm, wn, lane, acc);
+  forward_tile<MT, NT, WM, WN, D>(xs, cs, ss, sbase, (uint32_t)(min(WN * WCOLS, rows - n0) * (K >> 5)), soff, K, st0,
+                                  st1, lds, wm, wn, lane, acc);
 
   const int pc = part_cols(rows);
   // MB rows of MFMA tiles at a time through the LDS; then row by row, PIECES lanes a row with 8
