@@ -1,9 +1,10 @@
 // Backward of the dense feed-forward operators (frozen MXFP4 weights):
 //   linear   dz = scale * dy * act'(z);  dx = dz W;  dbias = sum over tokens of dz
 //   gate_up  dz = [dh * u * act'(g) | dh * act(g)] with z = [g | u]; dx and dbias the same way
-// First launch: dz in bf16 (rounded here once, as the matrix instructions take bf16; the bias
-// sums use the unrounded fp32 values) and per-strip column sums; then
-// the product dz W in tiles (mx_tile.hpp), with the strips' sums beside it.
+// First launch: dz in bf16 (rounded here once where there is an activation, as the matrix
+// instructions take bf16; without one dy itself, and the scale after the product; the bias sums
+// use the unrounded fp32 values) and per-strip column sums; then the product dz W in tiles
+// (mx_tile.hpp), with the strips' sums beside it.
 #include "mx_epilogue.hpp"
 #include "mx_tile.hpp"
 
@@ -22,7 +23,8 @@ struct LinearSlope {
   int N, act;
   float scale;
   __device__ __forceinline__ int cols() const { return N; }
-  __device__ __forceinline__ void dz(int64_t t, int n, float (&v)[8], bool wide, int left) const {
+  // dy * act'(z), before the scale
+  __device__ __forceinline__ void unscaled(int64_t t, int n, float (&v)[8], bool wide, int left) const {
     load_bf16<8>(dy + (size_t)t * N + n, v, wide, left);
     if (z) {
       float zv[8], a[8], d[8];
@@ -31,13 +33,14 @@ struct LinearSlope {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= d[i];
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] *= scale;
   }
+  // What the product multiplies its sums with.  Without an activation it reads dy, exact in bf16,
+  // and the scale comes after it; scale * dy would be rounded once more.
+  __device__ __host__ __forceinline__ float alpha() const { return z ? 1.f : scale; }
 };
 
-// dz (bf16 [T][ldz], zeros in columns N .. ldz) and, if parts is set, the fp32 column sums of
-// this strip in parts[strip][cols].
+// dz / alpha (bf16 [T][ldz], zeros in columns N .. ldz) and, if parts is set, the fp32 column sums
+// of dz in this strip in parts[strip][cols].
 template <class Slope>
 __global__ void __launch_bounds__(256) dz_kernel(Slope f, uint16_t* __restrict__ dz, int ldz, float* __restrict__ parts,
                                                  int64_t T, int strip_rows) {
@@ -52,8 +55,11 @@ __global__ void __launch_bounds__(256) dz_kernel(Slope f, uint16_t* __restrict__
   if (n < (dz ? ldz : N)) {  // columns N .. ldz read as 0
     for (int64_t t = t0 + ry; t < t1; t += 8) {
       float v[8];
-      f.dz(t, n, v, wide, left);
-      if (dz) store_bf16<8>(dz + (size_t)t * ldz + n, v, true, 8);
+      f.unscaled(t, n, v, wide, left);
+      if (dz && !f.z) store_bf16<8>(dz + (size_t)t * ldz + n, v, true, 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= f.scale;
+      if (dz && f.z) store_bf16<8>(dz + (size_t)t * ldz + n, v, true, 8);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum[i] += v[i];
     }
@@ -337,19 +343,20 @@ static int launch_dx(const uint16_t* dz, int ldz, const uint8_t* w, const uint8_
 int launch_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const uint8_t* w, const uint8_t* s, float scale,
                                  int act, uint16_t* dx, float* dbias, int T, int K, int N, void* workspace,
                                  hipStream_t stream) {
-  const bool direct = !z && N % BWD_KB == 0;  // dz = scale * dy: the product reads dy itself
+  const LinearSlope slope{dy, z, N, act, scale};
+  const bool direct = !z && N % BWD_KB == 0;  // dz / alpha is dy itself
   const BackwardPlan b = backward_workspace(T, K, N, N, !direct, dx != nullptr, dbias != nullptr);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* dz = (dx && !direct) ? reinterpret_cast<uint16_t*>(ws + b.dz) : nullptr;
   float* bp = !dbias ? nullptr : b.strips > 1 ? reinterpret_cast<float*>(ws + b.bias_parts) : dbias;
   if (dz || bp) {
     const dim3 grid((b.ldz + DZ_COLS - 1) / DZ_COLS, b.strips);
-    hipLaunchKernelGGL((dz_kernel<LinearSlope>), grid, dim3(256), 0, stream, LinearSlope{dy, z, N, act, scale}, dz,
-                       b.ldz, bp, (int64_t)T, b.strip_rows);
+    hipLaunchKernelGGL((dz_kernel<LinearSlope>), grid, dim3(256), 0, stream, slope, dz, b.ldz, bp, (int64_t)T,
+                       b.strip_rows);
     if (hipGetLastError() != hipSuccess) return MX_ERR_HIP;
   }
   if (!dx) return b.strips > 1 ? launch_strip_sum(bp, b.strips, N, 1, &dbias, stream) : MX_OK;
-  return launch_dx(direct ? dy : dz, direct ? N : b.ldz, w, s, dx, direct ? scale : 1.f, b.tile,
+  return launch_dx(direct ? dy : dz, direct ? N : b.ldz, w, s, dx, slope.alpha(), b.tile,
                    reinterpret_cast<float*>(ws + b.parts), T, K, N, BiasStrips{bp, dbias, bp ? b.strips : 0, N}, stream);
 }
 

@@ -780,3 +780,22 @@ def test_refusals(mx):
     for bad in ((x, x, x), (x, None, None, None, one), (x, x, None, None, None, None, 1.0, one)):
         with pytest.raises((ValueError, TypeError)):
             mx.mx_norm_residual_backward(*bad)
+
+
+# ------------------------------------------------------------------ what a call may do beside the cases above
+
+@pytest.mark.parametrize("T,K,N", [(1, 32, 1), (3, 96, 7), (4, 128, 1000), (40, 64, 64), (70, 256, 1090), (130, 160, 65),
+                                   (129, 96, 128), (4130, 2080, 70)])
+def test_linear_backward_scales_without_activation(mx, T, K, N):
+    """Without an activation dy goes into the product as it is, whatever N: the only rounding of dx
+    is its own, also with a scale that is no power of two."""
+    g = gen(T + N)
+    w, s = weights(N, K, g)
+    dy = bf(T, N, g=g)
+    for scale in (float(np.float32(1 / 3)), float(np.float32(-1.4142))):
+        say("scale without activation", T, K, N, scale)
+        dx, db = mx.mx_linear_fused_backward(*cuda(dy, w, s), None, scale, "none")
+        dz = scale * dy.double()
+        edz = 4 * U * dz.abs()
+        say("   worst", check_dx(dx, dz, edz, w, s, False, N))
+        within(db, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbias")
