@@ -106,8 +106,10 @@ __device__ __forceinline__ void act_values_slopes(int act, const float (&z)[V], 
     case MX_ACT_SIGMOID:
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        a[i] = logistic(z[i]);
-        d[i] = a[i] * (1.f - a[i]);
+        // a (1 - a) from e = exp(-|z|) <= 1: of 1 - a as a difference no digit is left at z = 17
+        const float e = __expf(-__builtin_fabsf(z[i])), r = __builtin_amdgcn_rcpf(1.f + e);
+        a[i] = z[i] < 0.f ? e * r : r;
+        d[i] = e * r * r;
       }
       break;
     default:

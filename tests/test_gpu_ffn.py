@@ -799,3 +799,49 @@ def test_linear_backward_scales_without_activation(mx, T, K, N):
         edz = 4 * U * dz.abs()
         say("   worst", check_dx(dx, dz, edz, w, s, False, N))
         within(db, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbias")
+
+
+def tail_errors(z, kind):
+    """Bounds of the kernels' act(z) and act'(z) in fp32, relative in the tails: an exponential of a
+    is off by |a| u for its rounded argument and 0.3 |a| u for the constant that makes it a power of
+    two, beside a few u of its own; what lies below the smallest normal value may be 0."""
+    z = z.double()
+    a, d = act(z, kind)
+    floor = 2.0 ** -126 * (1 + z.abs())
+    if kind == "gelu":
+        pdf = torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+        tail = 0.5 * torch.erfc(z.abs() / math.sqrt(2))
+        et = tail * (1.3 * z * z / 2 + 0.7 * z * z / 2 + 16) * U + (z > 0) * U  # z^2 / 2 itself is rounded
+        return z.abs() * et + U * a.abs() + floor, et + z.abs() * pdf * (z * z + 8) * U + U * d.abs() + floor
+    if kind == "gelu_tanh":  # a logistic of A, whose six roundings count as its argument's
+        k = 2 * math.sqrt(2 / math.pi)
+        A, D, per = k * (z + 0.044715 * z ** 3), k * (1 + 3 * 0.044715 * z * z), 7.3
+    else:
+        A, D, per = z, torch.ones_like(z), 1.3
+    p, q = torch.sigmoid(A), torch.sigmoid(-A)
+    ep = q * (per * A.abs() + 3) * U + 4 * U  # of p, relative
+    if kind == "sigmoid":
+        return ep * p + floor, p * q * (2 * per * A.abs() + 12) * U + floor
+    # the slope p + z p (1 - p) D, with 1 - p formed from p
+    ed = ep * p + z.abs() * p * D * (q * (ep + 8 * U) + p * ep + U) + U * d.abs() + floor * (1 + D)
+    return z.abs() * p * (ep + U) + floor, ed
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu", "gelu_tanh", "sigmoid"])
+def test_activation_tails(mx, kind):
+    """Every bf16 pre-activation up to |z| = 13, given through the bias: the stored activation is
+    exact to its rounding also where it is tiny, and so is the slope, which the bias gradient of one
+    token gives in fp32."""
+    z = torch.arange(0, 1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    z = z[(z.abs() <= 13) & (z.abs() >= 2.0 ** -10)]
+    N, K = z.numel(), 32
+    w = torch.zeros(N, K // 2, dtype=torch.uint8)
+    s = torch.full((N, 1), 127, dtype=torch.uint8)
+    say("tails", kind, N)
+    ea, ed = tail_errors(z, kind)
+    a, d = act(z.double(), kind)
+    y = mx.mx_linear_fused(*cuda(torch.zeros(1, K, dtype=torch.bfloat16), w, s), bias=z.to(DEV), act=kind)
+    say("   worst", within(y[0], a, (1 + B) * ea + B * a.abs(), "activation"))
+    one = torch.ones(1, N, dtype=torch.bfloat16)
+    db = mx.mx_linear_fused_backward(*cuda(one, w, s, z[None]), 1.0, kind, need_dx=False)[1]
+    say("   worst", within(db, d, ed, "slope"))
