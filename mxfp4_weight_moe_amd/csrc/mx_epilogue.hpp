@@ -7,9 +7,12 @@
 
 namespace mx {
 
-// p = 1 / (1 + e^-z).  e^-z overflows to Inf below z = -88, where p = 0 is right to fp32's
-// smallest normal value; 1 ulp reciprocal and exponential, so p is within 2e-7 of exact
-// relative to p for |z| <= 16.
+// Error bounds below count u = 2^-24, half a step of fp32.  exp(a) is 2^(a log2 e) with the
+// argument and the constant rounded, so it is off by 1.3 |a| u beside its own 2 u, and 0 below
+// fp32's smallest normal value.
+//
+// p = 1 / (1 + e^-z), off by at most (1.3 |z| (1 - p) + 6) u relative to p; 0 below z = -87.3,
+// where p is less than 2^-126.
 __device__ __forceinline__ float logistic(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
 
 // gelu_tanh(z) = z/2 (1 + tanh v) with v = sqrt(2/pi) (z + 0.044715 z^3); (1 + tanh v) / 2 is
@@ -21,8 +24,10 @@ __device__ __forceinline__ float gelu_tanh_arg(float z) {
 // The normal distribution function, Phi(z) = erfc(-z / sqrt 2) / 2.  With a = |z| / sqrt 2 and
 // t = 1 / (1 + 0.4 a), erfc(a) e^(a^2) = t P(t); P is a degree-8 least-squares fit of ours with
 // the weights moved until the relative error was level, 6e-8 on 0 <= a <= 9.6 (beyond, the
-// exponential is 0).  In fp32 the result is within 5e-7 relative of exact, tails included, for
-// 13 instructions; the library's erff with its two branches took 30 us of a 240 us product.
+// exponential is 0).  In fp32 the exponential's argument sets the error: the tail is within
+// (z^2 + 16) u of exact, relative (1e-6 at z = -1, 2e-6 at -4, 7e-6 at -10), what is stored in
+// bf16 is rounded by 65536 u.  13 instructions; the library's erff with its two branches took
+// 30 us of a 240 us product.
 __device__ __forceinline__ float normal_cdf(float z) {
   const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.282842712f, __builtin_fabsf(z), 1.f));
   float p = 2.023664985e-02f;
