@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
         if constexpr (POST) repack(cur.b[i]);
       }
       r = rsqrtf(s1[0] * inv_h + a.eps);
-      rc = r * r * s1[1] * inv_h;
+      rc = r * (r * s1[1] * inv_h);  // r * r leaves fp32 for the smallest eps
       q = rsqrtf(s1[2] * inv_h + a.eps);
     }
     float tok = a.scale;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
       }
       if (a.gate_mode == MX_GATE_TOKEN && a.dgate && threadIdx.x % L == 0 && threadIdx.x < 64)
         static_cast<float*>(a.dgate)[t] = s2[1];
-      const float qc = q * q * s2[0] * inv_h;
+      const float qc = q * (q * s2[0] * inv_h);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if constexpr (POST) {

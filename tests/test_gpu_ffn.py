@@ -845,3 +845,24 @@ def test_activation_tails(mx, kind):
     one = torch.ones(1, N, dtype=torch.bfloat16)
     db = mx.mx_linear_fused_backward(*cuda(one, w, s, z[None]), 1.0, kind, need_dx=False)[1]
     say("   worst", within(db, d, ed, "slope"))
+
+
+@pytest.mark.parametrize("H", [64, 512, 7168, 8704])
+def test_norm_smallest_eps(mx, H):
+    """An eps whose root's reciprocal has no square in fp32: rows of zeros keep finite gradients."""
+    T, eps = 3, float(np.float32(1e-40))
+    x, b, wo, gate, wi, dy, dxn = norm_inputs(T, H, "channel", True, True, H)
+    x[:], b[:] = 0, 0
+    say("smallest eps", H)
+    xd, bd, wod, gd, wid, dyd, dxnd = cuda(x, b, wo, gate, wi, dy, dxn)
+    y, xn = mx.mx_norm_residual(xd, bd, wod, gd, 1.0, wid, eps)
+    assert not bool(y.any()) and not bool(xn.any())
+    got = mx.mx_norm_residual_backward(dyd, dxnd, xd, bd, wod, gd, 1.0, wid, eps)
+    r = 1 / math.sqrt(eps)
+    D = dbl(dy) + r * dbl(dxn) * dbl(wi)
+    within(got["dx"], D, B * D.abs() + 16 * U * D.abs(), "dx")
+    big = r * D * dbl(gate) * dbl(wo)  # of the order of 1e40, beyond bf16
+    db = got["db"].double().cpu()
+    assert not bool(db.isnan().any()) and torch.equal(torch.sign(db), torch.sign(big))
+    for name in ("dgate", "dw_post", "dw_pre"):
+        assert not bool(got[name].any()), name
