@@ -13,11 +13,10 @@
 // In the last two K is split over several workgroups while there are fewer tiles than CUs; the
 // fp32 parts are then summed in a fixed order by a second launch (combine_kernel).
 #include "mx_epilogue.hpp"
+#include "mx_grid.hpp"
 #include "mx_tile.hpp"
 
 namespace mx {
-
-constexpr int STREAM_MAX_T = 32;
 
 // ------------------------------------------------------------------ few tokens: weight streaming
 
@@ -47,9 +46,11 @@ __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restri
   __shared__ __attribute__((aligned(16))) uint8_t slabs[W][SLAB_BYTES];
   __shared__ f32x4 red[(W > 1) ? W * MT * 64 : 1];
   extern __shared__ u32x4 xdyn[];
+  static_assert(MT <= 2 && STREAM_MAX_T == 32, "a workgroup's tokens");
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int items = (rows + COLS - 1) / COLS;
-  const int n0 = blockIdx.x % items * COLS, t0 = blockIdx.x / items * (MT * 16);
+  // one tile of 16 tokens is all of them
+  const int n0 = blockIdx.x * COLS, t0 = MT == 1 ? 0 : (blockIdx.z * gridDim.y + blockIdx.y) * STREAM_MAX_T;
+  if (MT > 1 && t0 >= T) return;
   const size_t kb = (size_t)(K >> 1), ks = (size_t)(K >> 5);
   // weight row of MFMA row r; past the last row the last one again
   auto weight_row = [&](int r) {
@@ -528,7 +529,8 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
                           hipStream_t stream) {
   if (takes_stream(T, K, rows, GATED)) {
     const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
-    const int items = (rows + cols - 1) / cols, nseg = K / SEG_K;
+    const StreamGrid sg = stream_grid(T, rows, cols);
+    const int items = (int)sg.items, nseg = K / SEG_K;
     int W = 1;
     // as many waves as the CUs hold at once: at more than 256 workgroups of 8 a second round begins
     // (4096 -> 7168, one token: 7.3 us with 8 waves, 5.4 with 4)
@@ -536,7 +538,7 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
     // up to 16 tokens in whole segments, up to 32 byte by byte; K % 256 == 0 with more than 16 is
     // left for gate_up alone, where its scales are too far apart for the thin tiles
     const bool sbyte = K % SEG_K != 0 || T > 16, xl = T <= 16 && !sbyte && (int64_t)T * K <= STREAM_XL;
-    const dim3 grid(items * ((T + STREAM_MAX_T - 1) / STREAM_MAX_T)), block(W * 64);
+    const dim3 grid(sg.items, sg.y, sg.z), block(W * 64);
     const unsigned xl_bytes = xl ? (unsigned)(T * K * 2) : 0u;
 #define MX_STREAM(WW, M, SB, XX) \
   hipLaunchKernelGGL((stream_kernel<WW, M, GATED, SB, XX>), grid, block, xl_bytes, stream, x, w, s, epi, T, K, rows)

@@ -1,6 +1,8 @@
 """Refusals of the dense feed-forward operators: every call here fails a host-side check, so
 nothing is enqueued and no pointer is followed."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 import torch
@@ -176,3 +178,27 @@ def test_binding_refuses_host_tensors_and_wrong_types():
         m.mx_gate_up(None, w, s)
     with pytest.raises(TypeError):
         m.mx_norm_residual_backward(None, None, None)
+
+
+def test_stream_grid_at_the_limits(tmp_path):
+    """The streaming launch within the grid limits of HIP (fewer than 2^32 threads along x, 65535
+    workgroups along y and z) wherever the calls' sizes are allowed, and over every token."""
+    src = tmp_path / "grid.cpp"
+    csrc = os.path.join(os.path.dirname(m.__file__), "csrc")
+    src.write_text(f'#include "{csrc}/mx_grid.hpp"\nextern "C" void grid(int64_t T, int64_t rows, int64_t cols, uint32_t* o) '
+                   "{ const auto g = mx::stream_grid(T, rows, cols); o[0] = g.items, o[1] = g.y, o[2] = g.z; }\n")
+    so = tmp_path / "grid.so"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", str(src), "-o", str(so)], check=True)
+    grid = ctypes.CDLL(str(so)).grid
+    grid.argtypes = [ctypes.c_int64] * 3 + [ctypes.POINTER(ctypes.c_uint32)]
+    out = (ctypes.c_uint32 * 3)()
+    tokens = sorted({min(max(t + d, 1), 1 << 24) for e in range(25) for t in (1 << e, 3 << max(e - 1, 0)) for d in (-1, 0, 1)})
+    for cols, most in ((16, 1 << 22), (8, 1 << 21)):  # a linear layer's rows, one half of gate_up's
+        for rows in (1, cols - 1, cols, cols + 1, 1024, 2056, most - 1, most):
+            for T in tokens:
+                grid(T, rows, cols, out)
+                x, y, z = out
+                assert x == -(-rows // cols) and 1 <= y <= 65535 and 1 <= z <= 65535, (T, rows, cols)
+                # more than one group of tokens has one wave a workgroup (K < 128), one group up to 8
+                assert x * (64 if T > 32 else 512) < 1 << 32
+                assert (y * z - y) * 32 < T <= y * z * 32 < 1 << 31, (T, y, z)

@@ -866,3 +866,35 @@ def test_norm_smallest_eps(mx, H):
     assert not bool(db.isnan().any()) and torch.equal(torch.sign(db), torch.sign(big))
     for name in ("dgate", "dw_post", "dw_pre"):
         assert not bool(got[name].any()), name
+
+
+@pytest.mark.parametrize("call", ["linear", "gate_up"])
+def test_short_reduction_most_workgroups(mx, call):
+    """K = 32 with so many tokens and rows that one axis of a grid could not hold the threads: sampled
+    rows against the definition, the first and last columns."""
+    T, K, N = 1 << 24, 32, (2056 if call == "linear" else 1032)
+    if torch.cuda.mem_get_info()[0] < 4.2 * T * N:
+        pytest.skip("needs 145 GB (linear) or 73 GB (gate_up) of GPU memory")
+    g = gen(N)
+    dg = torch.Generator(device=DEV)
+    dg.manual_seed(N)
+    say("most workgroups", call)
+    x = torch.randn((T, K), generator=dg, device=DEV, dtype=torch.bfloat16)
+    rows = [0, 31, 32, (1 << 20) - 1, 1 << 20, (1 << 23) + 5, T - 33, T - 1]
+    xr = x[rows].cpu()
+    if call == "linear":
+        w, s = weights(N, K, g)
+        y = torch.full((T, N), math.nan, dtype=torch.bfloat16, device=DEV)
+        mx.mx_linear_fused(x, *cuda(w, s), out=y)
+        z, ez = z_of(xr, w, s, None)
+        within(y[rows], z, (1 + B) * ez + B * z.abs(), "y")
+    else:
+        w, s = weights(2 * N, K, g)
+        y = torch.full((T, N), math.nan, dtype=torch.bfloat16, device=DEV)
+        mx.mx_gate_up(x, *cuda(w, s), act="relu", out=y)
+        z, ez = z_of(xr, w, s, None)
+        a, u = z[:, :N].clamp(min=0), z[:, N:]
+        err = ez[:, :N] * u.abs() + ez[:, N:] * a + ez[:, :N] * ez[:, N:] + U * (a * u).abs()
+        within(y[rows], a * u, (1 + B) * err + B * (a * u).abs(), "h")
+    for t0 in range(0, T, 1 << 21):  # no row was left out
+        assert not bool(y[t0:t0 + (1 << 21), ::257].isnan().any()), t0
