@@ -776,10 +776,12 @@ def mx_norm_residual_backward(dy: torch.Tensor | None, dxn: torch.Tensor | None,
                               b: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
                               gate: torch.Tensor | None = None, scale: float = 1.0,
                               w_pre: torch.Tensor | None = None, eps: float = 1e-6,
-                              ws: torch.Tensor | None = None) -> dict:
-    """All gradients of mx_norm_residual from those of y and xn: a dict of dx, db (bf16 [T, H]),
+                              ws: torch.Tensor | None = None, *, need_db: bool = True, need_dgate: bool = True,
+                              need_dw_post: bool = True, need_dw_pre: bool = True) -> dict:
+    """The gradients of mx_norm_residual from those of y and xn: a dict of dx, db (bf16 [T, H]),
     dgate (fp32 [T, 1] or [H], bf16 [T, H]), dw_post and dw_pre (fp32 [H]), None for what the
-    forward did not have.  y is the forward's y (its x without b); dy may be None with w_pre."""
+    forward did not have or is not asked for.  y is the forward's y (its x without b); dy may be
+    None with w_pre."""
     first = dy if dy is not None else dxn
     T, H = _bf16_rows(first, "dy" if dy is not None else "dxn")
     dev = first.device
@@ -795,12 +797,12 @@ def mx_norm_residual_backward(dy: torch.Tensor | None, dxn: torch.Tensor | None,
     if b is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need b")
     dx = torch.empty_like(first)
-    db = torch.empty_like(first) if b is not None else None
+    db = torch.empty_like(first) if b is not None and need_db else None
     dgate = None
-    if gate is not None:
+    if gate is not None and need_dgate:
         dgate = torch.empty(tuple(gate.shape), dtype=_BF16 if mode == _GATE_FULL else _F32, device=dev)
-    dw_post = torch.empty(H, dtype=_F32, device=dev) if w_post is not None else None
-    dw_pre = torch.empty(H, dtype=_F32, device=dev) if w_pre is not None else None
+    dw_post = torch.empty(H, dtype=_F32, device=dev) if w_post is not None and need_dw_post else None
+    dw_pre = torch.empty(H, dtype=_F32, device=dev) if w_pre is not None and need_dw_pre else None
     ws, wp, wn = _scratch(_lib.mx_norm_residual_backward_workspace_size(T, H), dev, ws)
     _call(_lib.mx_norm_residual_backward, dev, _opt(dy), _opt(dxn), _opt(y), _opt(b), _opt(w_post), _opt(gate), mode,
           scale, _opt(w_pre), eps, dx.data_ptr(), _opt(db), _opt(dgate), _opt(dw_post), _opt(dw_pre), T, H, wp, wn)

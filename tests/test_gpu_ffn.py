@@ -898,3 +898,18 @@ def test_short_reduction_most_workgroups(mx, call):
         within(y[rows], a * u, (1 + B) * err + B * (a * u).abs(), "h")
     for t0 in range(0, T, 1 << 21):  # no row was left out
         assert not bool(y[t0:t0 + (1 << 21), ::257].isnan().any()), t0
+
+
+@pytest.mark.parametrize("T,H", [(5, 264), (40, 8704)])
+@pytest.mark.parametrize("kind", ["channel", "token", "full"])
+def test_norm_backward_leaves_out(mx, T, H, kind):
+    """Every gradient beside dx can be left out; the others keep their bits."""
+    y, b, wo, gate, wi, dy, dxn = cuda(*norm_inputs(T, H, kind, True, True, T + H))
+    args = (dy, dxn, y, b, wo, gate, 0.7, wi, EPS)
+    say("left out", T, H, kind)
+    want = mx.mx_norm_residual_backward(*args)
+    names = ("db", "dgate", "dw_post", "dw_pre")
+    for off in [(n,) for n in names] + [names[:2], names[1:], names]:
+        got = mx.mx_norm_residual_backward(*args, **{f"need_{n}": False for n in off})
+        for n, v in want.items():
+            assert got[n] is None if n in off else torch.equal(got[n], v), (off, n)
