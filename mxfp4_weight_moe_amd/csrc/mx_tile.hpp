@@ -246,10 +246,6 @@ struct CodeStage {
   __device__ __forceinline__ void copy_one(uint8_t* buf, int stage, int q) const {
     copy16_to_lds(buf_[q], off[q], (uint32_t)stage * 64, buf + (q * NW + wave) * 1024);
   }
-  __device__ __forceinline__ void copy(uint8_t* buf, int stage) const {
-#pragma unroll
-    for (int q = 0; q < COPIES; ++q) copy_one(buf, stage, q);
-  }
   // The last, partial stage: `valid` (< 4) blocks of each row, zero codes beyond.
   __device__ __forceinline__ void copy_tail(uint8_t* buf, int stage, int valid) const {
 #pragma unroll
