@@ -913,3 +913,44 @@ def test_norm_backward_leaves_out(mx, T, H, kind):
         got = mx.mx_norm_residual_backward(*args, **{f"need_{n}": False for n in off})
         for n, v in want.items():
             assert got[n] is None if n in off else torch.equal(got[n], v), (off, n)
+
+
+def test_training_step_every_gradient(mx):
+    """The backward of norm -> gate_up -> down -> norm, every call's gradients against the definition on
+    the values that the call before gave: bias and norm-weight gradients, the gate's, and gate_up's
+    input gradient from the saved pre-activations, whose halves the forward laid out."""
+    T, H, I = 70, 256, 96
+    x, wgu, sgu, wd, sd, wi, bgu, bd, wo, gate = block_inputs(T, H, I, 9)
+    dy = bf(T, H, g=gen(1)).to(DEV)
+    say("training step, every gradient")
+    _, xn = mx.mx_norm_residual(x, w_pre=wi)
+    h, z = mx.mx_gate_up(xn, wgu, sgu, bgu, "silu", save_z=True)
+    b = mx.mx_linear_fused(h, wd, sd, bd)
+    post = mx.mx_norm_residual_backward(dy, None, None, b, wo, gate, 0.5)
+    dh, dbd = mx.mx_linear_fused_backward(post["db"], wd, sd)
+    dxn, dbgu = mx.mx_gate_up_backward(dh, z, wgu, sgu, "silu")
+    pre = mx.mx_norm_residual_backward(post["dx"], dxn, x, w_pre=wi)
+    d, over_t = (2 * H + 64) * U, (T + 16) * U
+
+    def check(got, want, names):
+        for name in names:
+            v, size = want[name]
+            rounded = B if got[name].dtype == torch.bfloat16 else 0.0
+            within(got[name], v, (1 + rounded) * (d + over_t) * size + rounded * v.abs(), name)
+
+    c = [dbl(t.cpu()) for t in (dy, b, wo, gate)]
+    check(post, norm_grads(c[0], None, c[0], c[1], c[2], c[3], 0.5, None, "token"), ("dx", "db", "dgate", "dw_post"))
+    db = dbl(post["db"].cpu())
+    within(dbd, db.sum(0), (T + 8) * U * db.abs().sum(0), "dbd")
+    # the saved pre-activations are the forward's, gate half first
+    zw, ez = z_of(xn.cpu(), wgu.cpu(), sgu.cpu(), bgu.cpu())
+    within(z, zw, (1 + B) * ez + B * zw.abs(), "z")
+    dhc, zc = dbl(dh.cpu()), dbl(z.cpu())
+    a, slope = act(zc[:, :I], "silu")
+    dz = torch.cat((dhc * zc[:, I:] * slope, dhc * a), 1)
+    e = ACT_ERR * (1 + zc[:, :I].abs())
+    edz = torch.cat((dhc.abs() * zc[:, I:].abs() * e, dhc.abs() * e), 1) + 4 * U * dz.abs()
+    check_dx(dxn.cpu(), dz, edz, wgu.cpu(), sgu.cpu(), True, 2 * I)
+    within(dbgu, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbgu")
+    want = norm_grads(dbl(post["dx"].cpu()), dbl(dxn.cpu()), dbl(x.cpu()), None, None, None, 1.0, dbl(wi.cpu()), "none")
+    check(pre, want, ("dx", "dw_pre"))
