@@ -954,3 +954,20 @@ def test_training_step_every_gradient(mx):
     within(dbgu, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbgu")
     want = norm_grads(dbl(post["dx"].cpu()), dbl(dxn.cpu()), dbl(x.cpu()), None, None, None, 1.0, dbl(wi.cpu()), "none")
     check(pre, want, ("dx", "dw_pre"))
+
+
+@pytest.mark.parametrize("T,H,I", [(4100, 2112, 70), (4130, 2080, 33), (4097, 2176, 64)])
+def test_gate_up_backward_wide_tiles(mx, T, H, I):
+    """Sizes whose product takes tiles of 256 x 256, ragged in tokens, columns and weight rows."""
+    g = gen(T + H + I)
+    w, s = weights(2 * I, H, g)
+    dh, z = bf(T, I, g=g), bf(T, 2 * I, g=g, std=1.5)
+    say("gate_up backward, wide tiles", T, H, I)
+    dx, db = mx.mx_gate_up_backward(*cuda(dh, z, w, s), "silu")
+    gt, up, d = z[:, :I].double(), z[:, I:].double(), dh.double()
+    a, slope = act(gt, "silu")
+    dz = torch.cat((d * up * slope, d * a), 1)
+    e = ACT_ERR * (1 + gt.abs())
+    edz = torch.cat((d.abs() * up.abs() * e, d.abs() * e), 1) + 4 * U * dz.abs()
+    say("   worst", check_dx(dx, dz, edz, w, s, True, 2 * I))
+    within(db, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbias")
