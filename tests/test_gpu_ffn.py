@@ -971,3 +971,88 @@ def test_gate_up_backward_wide_tiles(mx, T, H, I):
     edz = torch.cat((d.abs() * up.abs() * e, d.abs() * e), 1) + 4 * U * dz.abs()
     say("   worst", check_dx(dx, dz, edz, w, s, True, 2 * I))
     within(db, dz.sum(0), edz.sum(0) + (T + 8) * U * dz.abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("T,H,I", [(2, 256, 64), (40, 288, 96), (300, 512, 160)])
+def test_block_options(mx, T, H, I):
+    """Every combination of the block's norms, gate and biases against the separate calls, into the first
+    rows of a longer output."""
+    x, wgu, sgu, wd, sd, wi, bgu, bd, wo, _ = block_inputs(T, H, I, T + H + 1)
+    g = gen(H)
+    gates = {None: None, "token": bf(T, 1, g=g), "channel": bf(H, g=g), "full": bf(T, H, g=g)}
+    say("block options", T, H, I)
+    for pre in (None, wi):
+        for post in (None, wo):
+            for kind, gate in gates.items():
+                gate = None if gate is None else gate.to(DEV)
+                for b1, b2 in ((None, None), (bgu, bd)):
+                    xn = x if pre is None else mx.mx_norm_residual(x, w_pre=pre, eps=1e-5)[1]
+                    h = mx.mx_gate_up(xn, wgu, sgu, b1, "relu")
+                    if post is None and gate is None:
+                        want = mx.mx_linear_fused(h, wd, sd, b2, x, -0.7)
+                    else:
+                        want, _ = mx.mx_norm_residual(x, mx.mx_linear_fused(h, wd, sd, b2), post, gate, -0.7, eps=1e-5)
+                    buf = torch.full((T + 2, H), 7.0, dtype=torch.bfloat16, device=DEV)
+                    y = mx.mx_ffn_block(x, wgu, sgu, wd, sd, pre, b1, b2, "relu", post, gate, -0.7, 1e-5, out=buf[:T])
+                    what = (pre is not None, post is not None, kind, b1 is not None)
+                    assert torch.equal(y, want) and bool((buf[T:] == 7).all()), what
+
+
+@pytest.mark.parametrize("T,K,N", [(1, 32, 1), (3, 96, 33), (20, 8192, 40), (70, 4096, 130), (200, 2048, 64),
+                                   (1030, 288, 257), (4100, 2112, 66)])
+def test_workspaces_are_large_enough(mx, T, K, N):
+    """Every call with a workspace of exactly the size it asks for, inside a larger buffer: the bytes
+    behind it stay as they were, and so do the results."""
+    L, g = mx.raw(), gen(T + K + N)
+    x, (w, s), dy = bf(T, K, g=g), weights(N, K, g), bf(T, N, g=g)
+    w2, s2 = weights(2 * N, K, g)
+    wd, sd = weights(K, 32, g)
+    wgu, sgu = weights(64, K, g)
+    x, w, s, dy, w2, s2, wd, sd, wgu, sgu = cuda(x, w, s, dy, w2, s2, wd, sd, wgu, sgu)
+    z2 = bf(T, 2 * N, g=g).to(DEV)
+    one = torch.ones(K, dtype=torch.bfloat16, device=DEV)
+    calls = [(L.mx_linear_fused_workspace_size(T, K, N), lambda ws: [mx.mx_linear_fused(x, w, s, ws=ws)]),
+             (L.mx_linear_fused_backward_workspace_size(T, K, N),
+              lambda ws: list(mx.mx_linear_fused_backward(dy, w, s, dy, 0.3, "silu", ws=ws))),
+             (L.mx_linear_fused_backward_workspace_size(T, K, N),
+              lambda ws: list(mx.mx_linear_fused_backward(dy, w, s, None, 0.3, ws=ws))),
+             (L.mx_gate_up_workspace_size(T, K, N), lambda ws: [mx.mx_gate_up(x, w2, s2, ws=ws)]),
+             (L.mx_gate_up_backward_workspace_size(T, K, N), lambda ws: list(mx.mx_gate_up_backward(dy, z2, w2, s2, ws=ws))),
+             (L.mx_norm_residual_backward_workspace_size(T, K),
+              lambda ws: list(mx.mx_norm_residual_backward(x, x, x, x, one, one, 1.0, one, ws=ws).values())),
+             (L.mx_ffn_block_workspace_size(T, K, 32), lambda ws: [mx.mx_ffn_block(x, wgu, sgu, wd, sd, one, w_post=one, ws=ws)])]
+    for i, (need, call) in enumerate(calls):
+        say("workspace", i, T, K, N, need)
+        buf = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+        for a, b in zip(call(buf[:need]), call(None)):
+            assert torch.equal(a, b), i
+        assert bool((buf[need:] == 0x5A).all()), i
+
+
+def test_two_threads_at_once(mx):
+    """Two host threads, a stream each, the same tensors."""
+    import threading
+    run = every_call(mx, 45, 256, 96, 4)
+    want = [t.clone() for t in run()]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = run()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    say("two threads")
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for o in got:
+        for a, b in zip(o, want):
+            assert torch.equal(a, b)
