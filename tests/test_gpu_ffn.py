@@ -1056,3 +1056,45 @@ def test_two_threads_at_once(mx):
     for o in got:
         for a, b in zip(o, want):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,K,N", [(2, 256, 40), (3, 288, 33), (20, 160, 40), (12, 512, 40), (40, 256, 40), (100, 640, 70),
+                                   (50, 288, 33), (200, 288, 129), (200, 512, 130), (1100, 288, 520)])
+def test_subnormal_weights_and_activations(mx, T, K, N):
+    """Weights below bf16's and fp32's smallest normal value (scale bytes 0 to 3) with large
+    activations, and subnormal activations with large scales, forward and backward."""
+    for lo, hi, top in ((0, 4, 2.0 ** 100), (245, 250, 2.0 ** -130)):
+        g = gen(T + K + N + lo)
+        w, s = weights(N, K, g, lo, hi)
+        x, dy = (bf(T, K, g=g).double() * top).bfloat16(), (bf(T, N, g=g).double() * top).bfloat16()
+        say("subnormal", T, K, N, lo)
+        y = mx.mx_linear_fused(*cuda(x, w, s))
+        z, ez = z_of(x, w, s, None)
+        say("   worst", within(y, z, (1 + B) * ez + B * z.abs(), "y"))
+        dx, db = mx.mx_linear_fused_backward(*cuda(dy, w, s))
+        dz = dy.double()
+        say("   worst", check_dx(dx, dz, torch.zeros_like(dz), w, s, False, N))
+        within(db, dz.sum(0), (T + 8) * U * dz.abs().sum(0), "dbias")
+
+
+@pytest.mark.parametrize("T,H", [(7, 8), (9, 40), (6, 128), (5, 136), (3, 256), (6, 1024), (5, 8200)])
+def test_norm_rows_do_not_mix(mx, T, H):
+    """Rows with NaN and Inf leave every other row's outputs and gradients as they are, bit for bit, also
+    where several rows share a wave."""
+    y, b, wo, gate, wi, dy, dxn = norm_inputs(T, H, "token", True, True, T + H)
+    say("rows", T, H)
+
+    def run(y, b, gate, dy, dxn):
+        y, b, gate, dy, dxn, o, i = cuda(y, b, gate, dy, dxn, wo, wi)
+        f = mx.mx_norm_residual(y, b, o, gate, 0.7, i, EPS)
+        r = mx.mx_norm_residual_backward(dy, dxn, y, b, o, gate, 0.7, i, EPS)
+        return [t.cpu() for t in (*f, r["dx"], r["db"], r["dgate"])]
+
+    want = run(y, b, gate, dy, dxn)
+    bad = [T // 2, T - 1]
+    y2, b2, g2, dy2 = y.clone(), b.clone(), gate.clone(), dy.clone()
+    y2[bad[0], 0], b2[bad[0], H - 1], g2[bad[1]], dy2[bad[1], H // 2] = math.nan, math.inf, math.nan, -math.inf
+    keep = [t for t in range(T) if t not in bad]
+    for a, c in zip(run(y2, b2, g2, dy2, dxn), want):
+        assert torch.equal(a[keep], c[keep])
+        assert not bool(a[bad].isfinite().all(1).any())
