@@ -204,12 +204,15 @@ __device__ __forceinline__ void add_to(f32x4* s, const float (&v)[8]) {
 // Bound by memory: at T = 4096, H = 7168 with both norms and a gate per channel 352 MB move in
 // 79 us, 4.5 TB/s, as fast as a plain copy; with two pieces a thread, lane sums through the LDS
 // and no row ahead it was 119.
+// With both norms and 16 waves the compiler spills 8 of 128 registers (36 bytes of scratch a thread).
 // Beyond H = 8192 (V = 4, 8 waves) there are no registers for that, nor for all sums of parameter
 // gradients: those of w_post and the gate then stay in the LDS, each thread's in places of its
-// own, and the weights are loaded for each row.  Then bound by the vector unit and the wait at
-// each row: 8704 x 4096 with both norms and a gate per channel 204 us, 2.1 TB/s (16 waves of two
-// pieces: 315, and 562 with all sums in registers, which spill; the next row's lines brought to
-// the L2 ahead: 263).
+// own, and the weights are loaded for each row.  Both norms' instance still spills 41 of 256
+// registers (168 bytes of scratch a thread, 25 stores and 44 loads of it in the code), the others
+// none.  8704 x 4096 with both norms and a gate per channel 206 us, 2.1 TB/s; how much of that is
+// the spills and how much the wait at each row has not been told apart (16 waves of two pieces: 315,
+// and 562 with all sums in registers, which spill more; the next row's lines brought to the L2
+// ahead: 263).
 template <int NT, int V, int L, bool BLK, bool POST, bool PRE>
 __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
   static_assert(L == 64 || NT == 64, "short rows have no barriers");
