@@ -271,9 +271,11 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
 // a workgroup give three quarters of the CUs one, K is not split over workgroups, whose second
 // launch costs 3 to 4 us at these sizes; with fewer rows and more than 64 tokens NT = 2 halves the
 // activations that a CU reads beside the same weights, and K is split (gate_up of 128 tokens,
-// H = 7168, I = 2048: 20.2 us, with NT = 1 and 128 workgroups 21.4).  Bound by what a CU reads
-// through its L2, 0.7 MB there; 77 tokens, 2048 -> 7168: 10 us.  Tiles of 128 x 128 with
-// barriers took 17 and 25 us.
+// H = 7168, I = 2048: 20.2 us, with NT = 1 and 128 workgroups 21.4).  A CU then reads 0.70 MB
+// through its L2: 0.46 MB of activations, and its 57 KB of codes and 4 KB of scales four times, once
+// for each wave, which each decodes; about 20 bytes a cycle over the launch's 15 to 17 us.  That the
+// read path is what bounds it has not been shown.  77 tokens, 2048 -> 7168: 10 us.  Tiles of
+// 128 x 128 with barriers took 17 and 25 us.
 constexpr int THIN_MAX_T = 128;
 template <int NT>
 struct ThinStage {
