@@ -552,6 +552,10 @@ def moe_mxfp4_forward(x: torch.Tensor, router_logits: torch.Tensor, top_k: int, 
 
 
 # ------------------------------------------------------------------ dense feed-forward operators
+#
+# Autograd does not record these calls: their results have no history, also where an input
+# requires grad.  The gradients come from the *_backward calls, e.g. inside a
+# torch.autograd.Function.
 
 _ACTS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4, "sigmoid": 5}
 _GATE_NONE, _GATE_TOKEN, _GATE_CHANNEL, _GATE_FULL = 0, 1, 2, 3
@@ -636,7 +640,8 @@ def mx_linear_fused(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tens
                     save_z: bool = False, out: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """y[T,N] = residual + scale * act(x W^T + bias), all in fp32, rounded once to bf16.
     act: none, relu, silu, gelu, gelu_tanh or sigmoid.  out may be the residual itself.
-    save_z=True: (y, z), z = x W^T + bias in bf16 for mx_linear_fused_backward."""
+    save_z=True: (y, z), z = x W^T + bias in bf16 for mx_linear_fused_backward.  Autograd
+    records nothing: the gradients are that call's."""
     T, K = _bf16_rows(x, "x")
     dev = x.device
     N = _weights(w_codes, w_scales, "weight", None, K, dev)
@@ -687,7 +692,8 @@ def mx_gate_up(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor
                ws: torch.Tensor | None = None):
     """h[T,I] = act(x Wg^T + bg) * (x Wu^T + bu) with W_gate_up [2I, H/2] (gate rows, then up
     rows), all in fp32, rounded once to bf16.  save_z=True: (h, z), z bf16 [T, 2I] the two
-    pre-activations for mx_gate_up_backward."""
+    pre-activations for mx_gate_up_backward.  Autograd records nothing: the gradients are that
+    call's."""
     T, H = _bf16_rows(x, "x")
     dev = x.device
     two_i = _weights(W_gate_up, S_gate_up, "W_gate_up", None, H, dev)
@@ -748,7 +754,8 @@ def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: tor
     """(y, xn): y = x + scale * gate * rms_norm(b) * w_post, the residual stream after a block
     with output b, and xn = rms_norm(y) * w_pre, the next block's input; each norm where its
     weight is given, xn None without w_pre.  gate: [T, 1] per token, [H] per channel or [T, H].
-    Without b: (x, rms_norm(x) * w_pre).  out, for y, may be x itself."""
+    Without b: (x, rms_norm(x) * w_pre).  out, for y, may be x itself.  Autograd records nothing:
+    the gradients are mx_norm_residual_backward's."""
     T, H = _bf16_rows(x, "x")
     dev = x.device
     for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
@@ -816,7 +823,8 @@ def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tens
                  out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """A dense feed-forward block of a transformer: y = x + scale * gate * rms_norm(b) * w_post
     with b = mx_gate_up(rms_norm(x) * w_pre) W_down^T + bias_down; each norm where its weight is
-    given, gate as for mx_norm_residual."""
+    given, gate as for mx_norm_residual.  out may be x itself.  For inference: it saves nothing for
+    a backward pass and autograd records nothing; a training step makes the separate calls."""
     T, H = _bf16_rows(x, "x")
     dev = x.device
     two_i = _weights(W_gate_up, S_gate_up, "W_gate_up", None, H, dev)
