@@ -423,6 +423,8 @@ enum mx_act {
  *   residual  optional, bf16 [T, N]; may be y itself
  *   scale     finite;  act: an mx_act
  *   y bf16 [T, N] (written);  z  optional, bf16 [T, N] (written): what the backward call takes
+ * One or two tokens through a narrow layer without an epilogue are faster in mx_linear, which
+ * gives each weight row a wave of its own (2048 -> 2048, one token: 3.1 us, here 3.7).
  */
 MX_API size_t mx_linear_fused_workspace_size(int64_t T, int64_t K, int64_t N);
 MX_API int mx_linear_fused(const uint16_t* x, const uint8_t* w_codes, const uint8_t* w_scales, const uint16_t* bias,
