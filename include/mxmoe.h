@@ -438,7 +438,8 @@ MX_API int mx_linear_fused(const uint16_t* x, const uint8_t* w_codes, const uint
  *   dx     optional, bf16 [T, K] (written);  dbias  optional, fp32 [N] (written); one is needed
  *   w_codes, w_scales  as for mx_linear_fused; may be NULL without dx
  * For dx, dz is rounded to bf16 where there is an activation (the matrix instructions take
- * bf16): each product is off by at most 2^-8 of itself.  dbias sums the fp32 values.
+ * bf16): each product is off by at most 2^-8 of itself.  Without one dx = scale * (dy W), dy as
+ * it is.  dbias sums the fp32 values.
  */
 MX_API size_t mx_linear_fused_backward_workspace_size(int64_t T, int64_t K, int64_t N);
 MX_API int mx_linear_fused_backward(const uint16_t* dy, const uint16_t* z, const uint8_t* w_codes,
@@ -464,7 +465,7 @@ MX_API int mx_gate_up(const uint16_t* x, const uint8_t* w_gate_up, const uint8_t
  * Its backward, from dh [T, I] bf16 and z [T, 2I] as mx_gate_up wrote it:
  *   dz = [ dh * u * act'(g) | dh * act(g) ],  dx = dz W,  dbias[n] = sum_t dz[t,n]
  *   dx  optional, bf16 [T, H] (written);  dbias  optional, fp32 [2I] (written); one is needed.
- * dz is rounded to bf16 for dx, as in mx_linear_fused_backward.
+ * dz is rounded to bf16 for dx, whatever the activation (it is a product of two or three values).
  */
 MX_API size_t mx_gate_up_backward_workspace_size(int64_t T, int64_t H, int64_t I);
 MX_API int mx_gate_up_backward(const uint16_t* dh, const uint16_t* z, const uint8_t* w_gate_up,
