@@ -1,10 +1,11 @@
 // Backward of the dense feed-forward operators (frozen MXFP4 weights):
 //   linear   dz = scale * dy * act'(z);  dx = dz W;  dbias = sum over tokens of dz
 //   gate_up  dz = [dh * u * act'(g) | dh * act(g)] with z = [g | u]; dx and dbias the same way
-// First launch: dz in bf16 (rounded here once where there is an activation, as the matrix
-// instructions take bf16; without one dy itself, and the scale after the product; the bias sums
-// use the unrounded fp32 values) and per-strip column sums; then the product dz W in tiles
-// (mx_tile.hpp), with the strips' sums beside it.
+// First launch: dz in bf16 and per-strip column sums, which use the unrounded fp32 values.  Where
+// there is an activation dz is rounded here, once, as the matrix instructions take bf16: dx is then
+// 0.0024 from exact instead of 0.0017 (root mean square), and dz in two bf16 parts would double the
+// product.  Without one it is dy itself, and the scale follows the product.  Then the product dz W
+// in tiles (mx_tile.hpp), with the strips' sums beside it.
 #include "mx_epilogue.hpp"
 #include "mx_tile.hpp"
 
