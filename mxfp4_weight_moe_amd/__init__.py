@@ -623,6 +623,14 @@ def _bf16_rows(t, name: str):
     return t.shape
 
 
+def _apart(out, t, name: str, itself: bool = False):
+    """Refuses an output over an input that other workgroups still read while it is written;
+    `itself`: over exactly the same elements it is fine, each is read before it is written."""
+    o, i = out.data_ptr(), t.data_ptr()
+    if o < i + 2 * t.numel() and i < o + 2 * out.numel() and not (itself and o == i):
+        raise ValueError(f"out must not overlap {name}" + (" except as the same tensor" if itself else ""))
+
+
 def _weights(codes, scales, name: str, rows: int | None, K: int, dev) -> int:
     if rows is None:
         if not isinstance(codes, torch.Tensor) or codes.dim() != 2:
@@ -639,8 +647,8 @@ def mx_linear_fused(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tens
                     residual: torch.Tensor | None = None, scale: float = 1.0, act: str = "none",
                     save_z: bool = False, out: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """y[T,N] = residual + scale * act(x W^T + bias), all in fp32, rounded once to bf16.
-    act: none, relu, silu, gelu, gelu_tanh or sigmoid.  out may be the residual itself.
-    save_z=True: (y, z), z = x W^T + bias in bf16 for mx_linear_fused_backward.  Autograd
+    act: none, relu, silu, gelu, gelu_tanh or sigmoid.  out may be the residual itself,
+    not x.  save_z=True: (y, z), z = x W^T + bias in bf16 for mx_linear_fused_backward.  Autograd
     records nothing: the gradients are that call's."""
     T, K = _bf16_rows(x, "x")
     dev = x.device
@@ -654,6 +662,9 @@ def mx_linear_fused(x: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tens
         out = x.new_empty((T, N)) if residual is None else torch.empty_like(residual)
     else:
         _tensor(out, "out", _BF16, (T, N), dev)
+        _apart(out, x, "x")
+        if residual is not None:
+            _apart(out, residual, "residual", itself=True)
     z = torch.empty((T, N), dtype=_BF16, device=dev) if save_z else None
     ws, wp, wn = _scratch(_lib.mx_linear_fused_workspace_size(T, K, N), dev, ws)
     _call(_lib.mx_linear_fused, dev, x.data_ptr(), w_codes.data_ptr(), w_scales.data_ptr(), _opt(bias), _opt(residual),
@@ -707,6 +718,7 @@ def mx_gate_up(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor
         out = x.new_empty((T, I))
     else:
         _tensor(out, "out", _BF16, (T, I), dev)
+        _apart(out, x, "x")
     z = torch.empty((T, two_i), dtype=_BF16, device=dev) if save_z else None
     ws, wp, wn = _scratch(_lib.mx_gate_up_workspace_size(T, H, I), dev, ws)
     _call(_lib.mx_gate_up, dev, x.data_ptr(), W_gate_up.data_ptr(), S_gate_up.data_ptr(), _opt(bias), code, out.data_ptr(),
@@ -773,6 +785,8 @@ def mx_norm_residual(x: torch.Tensor, b: torch.Tensor | None = None, w_post: tor
             y = torch.empty_like(x)
         else:
             _tensor(y, "out", _BF16, (T, H), dev)
+            _apart(y, x, "x", itself=True)
+            _apart(y, b, "b", itself=True)
     xn = torch.empty_like(x) if w_pre is not None else None
     _call(_lib.mx_norm_residual, dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale, _opt(w_pre), eps,
           _opt(y), _opt(xn), T, H)
@@ -842,6 +856,7 @@ def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tens
         out = torch.empty_like(x)
     else:
         _tensor(out, "out", _BF16, (T, H), dev)
+        _apart(out, x, "x", itself=True)
     ws, wp, wn = _scratch(_lib.mx_ffn_block_workspace_size(T, H, I), dev, ws)
     _call(_lib.mx_ffn_block, dev, x.data_ptr(), _opt(w_pre), W_gate_up.data_ptr(), S_gate_up.data_ptr(),
           _opt(bias_gate_up), code, W_down.data_ptr(), S_down.data_ptr(), _opt(bias_down), _opt(w_post), _opt(gate), mode,

@@ -1098,3 +1098,29 @@ def test_norm_rows_do_not_mix(mx, T, H):
     for a, c in zip(run(y2, b2, g2, dy2, dxn), want):
         assert torch.equal(a[keep], c[keep])
         assert not bool(a[bad].isfinite().all(1).any())
+
+
+def test_refuse_outputs_over_inputs(mx):
+    """out over x, whole or in part, also where x is the residual too, and over part of what it may
+    stand on as a whole: refused before anything runs."""
+    T, K = 40, 64
+    g = gen(1)
+    w, s, w2, s2 = cuda(*weights(K, K, g), *weights(2 * K, K, g))
+    buf = bf(2 * T, K, g=g).to(DEV)
+    keep = buf.clone()
+    x, shifted, beside = buf[:T], buf[1:T + 1], buf[T:]
+    other = bf(T, K, g=g).to(DEV)
+    say("out over x")
+    for out in (x, shifted):
+        with pytest.raises(ValueError, match="overlap"):
+            mx.mx_linear_fused(x, w, s, residual=x, out=out)
+        with pytest.raises(ValueError, match="overlap"):
+            mx.mx_gate_up(x, w2, s2, out=out)
+    for call in (lambda: mx.mx_linear_fused(other, w, s, residual=x, out=shifted),
+                 lambda: mx.mx_norm_residual(x, other, out=shifted), lambda: mx.mx_norm_residual(other, x, out=shifted),
+                 lambda: mx.mx_ffn_block(x, w2, s2, w, s, out=shifted)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    assert torch.equal(buf, keep)
+    want = mx.mx_gate_up(x, w2, s2)
+    assert torch.equal(mx.mx_gate_up(x, w2, s2, out=beside), want)  # beside it is fine
