@@ -1124,3 +1124,19 @@ def test_refuse_outputs_over_inputs(mx):
     assert torch.equal(buf, keep)
     want = mx.mx_gate_up(x, w2, s2)
     assert torch.equal(mx.mx_gate_up(x, w2, s2, out=beside), want)  # beside it is fine
+
+
+@pytest.mark.parametrize("T,H", [(3, 72), (40, 2048), (5, 8704)])
+def test_plain_residual(mx, T, H):
+    """No norm and no gate: y = x + scale * b, and its gradients."""
+    x, b, _, _, _, dy, _ = norm_inputs(T, H, "none", False, False, H)
+    scale = float(np.float32(0.3))
+    say("plain residual", T, H)
+    y, xn = mx.mx_norm_residual(*cuda(x, b), scale=scale)
+    want = x.double() + scale * b.double()
+    assert xn is None
+    within(y, want, (1 + B) * U * want.abs() + B * want.abs(), "y")
+    got = mx.mx_norm_residual_backward(dy.to(DEV), None, None, b.to(DEV), scale=scale)
+    assert {k for k, v in got.items() if v is not None} == {"dx", "db"} and torch.equal(got["dx"].cpu(), dy)
+    want = scale * dy.double()
+    within(got["db"], want, (1 + B) * U * want.abs() + B * want.abs(), "db")
