@@ -250,6 +250,7 @@ struct LinearEpilogue {
 
 // h = act(g + bg) * (u + bu); optionally the biased g and u.
 struct GatedEpilogue {
+  static constexpr bool WHOLE_BLOCKS = false;  // takes any piece of a row, not blocks of 32 alone
   const uint16_t* bias;  // [2I] or null
   uint16_t* h;           // [T, I]
   uint16_t* z;           // [T, 2I] or null
@@ -273,9 +274,9 @@ struct GatedEpilogue {
     }
     return c;
   }
+  // g becomes h; z is stored
   template <int V>
-  __device__ __forceinline__ void store(int t, int n, float (&g)[V], float (&u)[V], const Columns<V>& c) const {
-    if (n >= I) return;
+  __device__ __forceinline__ void product(int t, int n, float (&g)[V], float (&u)[V], const Columns<V>& c) const {
     const bool w = wide<V>(n);
     const int left = I - n;
     if (bias) {
@@ -294,7 +295,12 @@ struct GatedEpilogue {
     act_values(act, g);
 #pragma unroll
     for (int i = 0; i < V; ++i) g[i] *= u[i];
-    store_bf16<V>(h + (size_t)t * I + n, g, w, left);
+  }
+  template <int V>
+  __device__ __forceinline__ void store(int t, int n, float (&g)[V], float (&u)[V], const Columns<V>& c) const {
+    if (n >= I) return;
+    product<V>(t, n, g, u, c);
+    store_bf16<V>(h + (size_t)t * I + n, g, wide<V>(n), I - n);
   }
 };
 

@@ -14,7 +14,7 @@
 // fp32 parts are then summed in a fixed order by a second launch (combine_kernel).
 #include "mx_epilogue.hpp"
 #include "mx_grid.hpp"
-#include "mx_tile.hpp"
+#include "mx_tile_out.hpp"
 
 namespace mx {
 
@@ -124,10 +124,6 @@ __global__ void __launch_bounds__(W * 64) stream_kernel(const uint16_t* __restri
 
 // ------------------------------------------------------------------ many tokens: tiles
 
-// Columns per row of the fp32 parts of a split K (each half of gate_up, or all rows of a
-// linear layer), rounded up so that a lane's 8 consecutive values always fit.
-__host__ __device__ static inline int part_cols(int rows) { return (rows + 7) / 8 * 8; }
-
 // Bound by the matrix units and the power limit: with products alone the clock falls to 1.7 GHz,
 // here they are busy for 68% of a launch's cycles (gate_up, epilogue included) at 1.85 GHz.
 // 4096 tokens, 7168 -> 4096 with gelu, bias and residual 191 us, 1.26 PFLOP/s; gate_up of the same
@@ -187,79 +183,7 @@ __global__ void __launch_bounds__(WM * WN * 64, MT == 4 || D > 2 ? 1 : 2)
   forward_tile<MT, NT, WM, WN, D>(xs, cs, ss, sbase, (uint32_t)(min(WN * WCOLS, rows - n0) * (K >> 5)), soff, K, st0,
                                   st1, lds, wm, wn, lane, acc);
 
-  const int pc = part_cols(rows);
-  // MB rows of MFMA tiles at a time through the LDS; then row by row, PIECES lanes a row with 8
-  // columns each, so a lane has the same columns in all its rows.  U rows of a lane go
-  // together, and what the next ones read (the residual) is fetched meanwhile.
-  constexpr int MB = MT < 2 ? 1 : 2;
-  static_assert(WM * WN * MB * NT * 4096 <= L::BYTES, "results of all waves in the stages' LDS");
-  uint8_t* mine = lds + wave * (MB * NT * 4096);
-  constexpr int PIECES = WCOLS / 8, ROWS = 64 / PIECES, ITERS = MB * 32 / ROWS, U = ITERS < 4 ? ITERS : 4;
-  const int p = lane % PIECES, n = n0 + wn * WCOLS + p * 8;
-  const int t0 = m0 + wm * MT * 32 + lane / PIECES;
-  const auto cols = epi.template columns<8>(n);
-  struct Ahead {
-    Piece<8> r[U];
-  };
-  auto fetch = [&](int it) {  // row t0 + it * ROWS and the U - 1 after it
-    Ahead f{};
-    if constexpr (!GATED) {
-      if (nsplit == 1)
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-          const int t = t0 + (it + k) * ROWS;
-          if (t < T) f.r[k] = epi.template fetch<8>(t, n);
-        }
-    }
-    return f;
-  };
-  Ahead next = fetch(0);
-  __syncthreads();  // every wave has read its last fragments
-#pragma unroll
-  for (int b = 0; b < MT / MB; ++b) {
-#pragma unroll
-    for (int m = 0; m < MB; ++m) tile_to_lds<NT>(mine + m * NT * 4096, acc[b * MB + m], lane);
-#pragma unroll 1
-    for (int it = 0; it < ITERS; it += U) {
-      const Ahead now = next;
-      if (b * ITERS + it + U < MT / MB * ITERS) next = fetch(b * ITERS + it + U);
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int row = (it + k) * ROWS + lane / PIECES;
-        const int t = t0 + (b * ITERS + it + k) * ROWS;
-        if (t >= T || n >= rows) continue;
-        f32x4 q[GATED ? 4 : 2];
-        q[0] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 2 * p));
-        q[1] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 2 * p + 1));
-        if constexpr (GATED) {
-          q[2] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 4 * NT + 2 * p));
-          q[3] = *reinterpret_cast<const f32x4*>(mine + out_at<NT>(row, 4 * NT + 2 * p + 1));
-        }
-        if (nsplit > 1) {
-          f32x4* o = reinterpret_cast<f32x4*>(parts + ((size_t)split * T + t) * ((GATED ? 2 : 1) * (size_t)pc) + n);
-          o[0] = q[0];
-          o[1] = q[1];
-          if constexpr (GATED) {
-            o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(o) + pc);
-            o[0] = q[2];
-            o[1] = q[3];
-          }
-        } else {
-          float v[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = q[j >> 2][j & 3];
-          if constexpr (GATED) {
-            float u[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) u[j] = q[2 + (j >> 2)][j & 3];
-            epi.template store<8>(t, n, v, u, cols);
-          } else {
-            epi.template store<8>(t, n, v, cols, now.r[k]);
-          }
-        }
-      }
-    }
-  }
+  tile_output<MT, NT, WM, WN, GATED, L::BYTES>(acc, epi, parts, lds, T, rows, m0, n0, split, nsplit, wave, lane);
 }
 
 // ------------------------------------------------------------------ up to 128 tokens: thin tiles
@@ -423,51 +347,6 @@ __global__ void __launch_bounds__(256, 1)
   }
 }
 
-// Sums the parts of a split K in ascending order and applies the epilogue: 8 columns a thread.
-template <bool GATED>
-__global__ void __launch_bounds__(64) combine_kernel(const float* __restrict__ parts,
-                                                      typename EpilogueOf<GATED>::type epi, int T, int pc, int nsplit) {
-  const int per_row = pc / 8;
-  const int64_t id = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (id >= (int64_t)T * per_row) return;
-  const int t = (int)(id / per_row), n = (int)(id % per_row) * 8;
-  const size_t ld = GATED ? 2 * (size_t)pc : (size_t)pc;
-  const float* p = parts + (size_t)t * ld + n;
-  const size_t step = (size_t)T * ld;
-  f32x4 a[2] = {}, b[2] = {};
-  for (int z0 = 0; z0 < nsplit; z0 += 4) {  // four parts' loads at a time
-    f32x4 q[4][GATED ? 4 : 2];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float* r = p + min(z0 + k, nsplit - 1) * step;
-      q[k][0] = *reinterpret_cast<const f32x4*>(r);
-      q[k][1] = *reinterpret_cast<const f32x4*>(r + 4);
-      if constexpr (GATED) {
-        q[k][2] = *reinterpret_cast<const f32x4*>(r + pc);
-        q[k][3] = *reinterpret_cast<const f32x4*>(r + pc + 4);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (z0 + k >= nsplit) break;
-      a[0] += q[k][0];
-      a[1] += q[k][1];
-      if constexpr (GATED) {
-        b[0] += q[k][2];
-        b[1] += q[k][3];
-      }
-    }
-  }
-  float v[8], u[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = a[j >> 2][j & 3], u[j] = b[j >> 2][j & 3];
-  const auto cols = epi.template columns<8>(n);
-  if constexpr (GATED)
-    epi.template store<8>(t, n, v, u, cols);
-  else
-    epi.template store<8>(t, n, v, cols, epi.template fetch<8>(t, n));
-}
-
 // ------------------------------------------------------------------ launch plans
 
 // Whether the up rows' scales lie within 32-bit offsets of the gate rows'.
@@ -600,7 +479,7 @@ static int launch_forward(const uint16_t* x, const uint8_t* w, const uint8_t* s,
   if (p.nsplit > 1) {
     const int pc = part_cols(rows);
     const int64_t pieces = (int64_t)T * (pc / 8);
-    hipLaunchKernelGGL((combine_kernel<GATED>), dim3((unsigned)((pieces + 63) / 64)), dim3(64), 0, stream, parts,
+    hipLaunchKernelGGL((combine_kernel<GATED, typename EpilogueOf<GATED>::type>), dim3((unsigned)((pieces + 63) / 64)), dim3(64), 0, stream, parts,
                        epi, T, pc, p.nsplit);
   }
   return hip_status(hipGetLastError());
