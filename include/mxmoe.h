@@ -541,6 +541,142 @@ MX_API int mx_ffn_block(const uint16_t* x, const uint16_t* w_pre, const uint8_t*
                         float scale, float eps, uint16_t* y, int64_t T, int64_t H, int64_t I, void* workspace,
                         size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Microscaled activations: what a block hands on is quantized once, by the call that computes
+ * it, and multiplied as it is stored, by the scaled matrix instructions.  For decode steps as for
+ * prompts and training batches (1 <= T <= 2^24).  Conventions, limits and workspaces as for the dense
+ * feed-forward operators above; the additional tensors are
+ *   codes   MXFP8: uint8 [T, K], one E4M3 element a byte.  MXFP4: uint8 [T, K/2], element 2i in the
+ *           low nibble of byte i.  16-byte aligned
+ *   scales  uint8 [T, K/32], one E8M0 byte per 32 consecutive values of a row; any address, 16-byte
+ *           aligned where K % 512 == 0 (for a product's operands)
+ * as mx_quantize gives them:  per block of 32 the scale is 2^(floor(log2 amax) - 8) for MXFP8 and
+ * 2^(floor(log2 amax) - 2) for MXFP4, at least 2^-127, and each value divided by it is rounded to the
+ * nearest element (ties to the even code), saturating at +-448 or +-6.  An all-zero block gets scale
+ * byte 0; a block with an Inf or NaN gets scale byte 0xFF, which makes all its values NaN.
+ *
+ * Gradients are straight-through: mx_norm_residual_backward, mx_linear_fused_backward and
+ * mx_gate_up_backward take these calls' y and z as they take those of their own forward calls.
+ */
+enum mx_format {
+  MX_FORMAT_MXFP8 = 0, /* E4M3 elements */
+  MX_FORMAT_MXFP4 = 1  /* E2M1 elements */
+};
+enum mx_type {
+  MX_TYPE_BF16 = 0,
+  MX_TYPE_F32 = 1
+};
+
+/*
+ * The quantizer alone (bit-exact).
+ *   x       x_type [rows, K] (16-byte aligned);  codes, scales  (written)
+ *   values  optional, bf16 [rows, K] (written): the values that the codes stand for (what a
+ *           quantization-aware forward pass goes on with); exact, but for MXFP8 elements below
+ *           2^-124, which bf16's last step of 2^-133 rounds
+ *   rows >= 1, K >= 32, K % 32 == 0, rows * K <= 2^38.
+ */
+MX_API int mx_quantize(const void* x, int x_type, int format, uint8_t* codes, uint8_t* scales, uint16_t* values,
+                       int64_t rows, int64_t K, void* stream);
+
+/*
+ * mx_norm_residual whose xn leaves quantized, from its fp32 value:
+ *   y = x + scale * gate * n  (bf16),  codes and scales of  rms_norm(y) * w_pre
+ *   xn  optional, bf16 [T, H] (written): rms_norm(y) * w_pre rounded to bf16, for a consumer that reads
+ *       it unquantized (a router)
+ *   w_pre is required, H % 32 == 0; without b the call is the norm before a block alone.  Other
+ *   arguments as for mx_norm_residual.
+ */
+MX_API int mx_norm_residual_quantize(const uint16_t* x, const uint16_t* b, const uint16_t* w_post,
+                                     const uint16_t* gate, int gate_mode, float scale, const uint16_t* w_pre, float eps,
+                                     uint16_t* y, uint16_t* xn, int format, uint8_t* codes, uint8_t* scales, int64_t T,
+                                     int64_t H, void* stream);
+
+/*
+ * mx_linear_fused for quantized activations:
+ *   z[t,n] = sum_k a[t,k] w[n,k] + bias[n],   y[t,n] = residual[t,n] + scale * act(z[t,n])
+ *   a_codes, a_scales  the activations in `format`, [T, K];  other arguments as for mx_linear_fused
+ * The products are exact; the scaled matrix instructions sum them in fp32 but drop, within groups of 8,
+ * bits more than about 14 binades below the group's largest product, so |z - exact| stays below about
+ * 2^-10 of sum_k |a w| (2^-8 |z| more where it is stored in bf16).
+ */
+MX_API size_t mx_linear_quantized_workspace_size(int64_t T, int64_t K, int64_t N);
+MX_API int mx_linear_quantized(const uint8_t* a_codes, const uint8_t* a_scales, int format, const uint8_t* w_codes,
+                               const uint8_t* w_scales, const uint16_t* bias, const uint16_t* residual, float scale,
+                               int act, uint16_t* y, uint16_t* z, int64_t T, int64_t K, int64_t N, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
+/*
+ * mx_gate_up for quantized activations; h leaves as bf16 or quantized, from its fp32 value:
+ *   h        bf16 [T, I] (written), or NULL;
+ *   h_codes, h_scales  (written), exactly where h is NULL: h in h_format, I % 32 == 0 (MX_ERR_SHAPE)
+ *   z  optional, bf16 [T, 2I] (written);  other arguments as for mx_gate_up and mx_linear_quantized
+ */
+MX_API size_t mx_gate_up_quantized_workspace_size(int64_t T, int64_t H, int64_t I);
+MX_API int mx_gate_up_quantized(const uint8_t* a_codes, const uint8_t* a_scales, int format, const uint8_t* w_gate_up,
+                                const uint8_t* s_gate_up, const uint16_t* bias, int act, uint16_t* h, int h_format,
+                                uint8_t* h_codes, uint8_t* h_scales, uint16_t* z, int64_t T, int64_t H, int64_t I,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------------
+ * Routing by scores, for decode steps as for training batches (1 <= T <= 2^24).  moe_route_topk takes a
+ * softmax over the chosen logits; these calls have what the routers of current mixture-of-experts models
+ * add to that: scores over all experts (softmax or sigmoid), a bias that balances the experts' load
+ * without entering the gates, a choice of expert groups ahead of the experts', and renormalised,
+ * scaled gates.
+ *   p[e]   = softmax(logits[t,:])[e] or 1 / (1 + exp(-logits[t,e]))
+ *   key[e] = p[e] + bias[e]
+ *   groups: E / n_group consecutive experts each; a group's value is the sum of its two largest keys
+ *           (MX_GROUP_TOP2; its one key where it has one) or its largest (MX_GROUP_MAX); the
+ *           topk_group groups of largest value stay (ties to the lower group)
+ *   ids    = the top_k largest keys among them in descending order (ties to the lower id); without a
+ *           bias the order is that of the logits
+ *   gates[t,j] = scale * p[ids[j]], divided by sum_i p[ids[i]] with renormalize
+ * Keys and group values are compared in 64 bits, gates rounded once to fp32.  NaN logits sort below all
+ * others, and their row's gates are NaN (softmax) or NaN where chosen (sigmoid); an expert masked
+ * with -Inf has score 0; a row of nothing but -Inf, or whose chosen scores sum to 0, has gates 0.
+ *   logits  logits_type [T, E];  bias  optional, fp32 [E];  ids int32 [T, top_k], gates fp32
+ *   [T, top_k] (written)
+ *   E <= MX_MAX_EXPERTS, top_k <= MX_MAX_TOPK, n_group <= MX_MAX_GROUPS and divides E,
+ *   1 <= topk_group <= n_group, top_k <= topk_group * E / n_group; scale finite.
+ */
+enum mx_score {
+  MX_SCORE_SOFTMAX = 0,
+  MX_SCORE_SIGMOID = 1
+};
+enum mx_group_score {
+  MX_GROUP_TOP2 = 0,
+  MX_GROUP_MAX = 1
+};
+#define MX_MAX_GROUPS 64
+MX_API int moe_route_scored(const void* logits, int logits_type, const float* bias, int score, int64_t n_group,
+                            int64_t topk_group, int group_score, int renormalize, float scale, int32_t* ids,
+                            float* gates, int64_t T, int64_t E, int64_t top_k, void* stream);
+
+/*
+ * Its gradient into the logits (the choice itself, and with it the bias, has none):
+ *   c[j] = scale * dgates[t,j];  dp[ids[j]] = c[j], with renormalize (c[j] - sum_i c[i] p[ids[i]] / S) / S,
+ *   S = sum_i p[ids[i]];  dlogits = dp p (1 - p) (sigmoid), p (dp - sum_e dp[e] p[e]) (softmax), dp = 0
+ *   where an expert is not chosen
+ *   dgates  fp32 [T, top_k];  logits, score, renormalize, scale as in the forward call, ids its ids (each
+ *   row distinct; ids outside [0, E) are skipped);  dlogits  logits_type [T, E] (written)
+ * Rows of the forward's gates 0 have gradient 0.
+ */
+MX_API int moe_route_scored_backward(const float* dgates, const void* logits, int logits_type, const int32_t* ids,
+                                     int score, int renormalize, float scale, void* dlogits, int64_t T, int64_t E,
+                                     int64_t top_k, void* stream);
+
+/*
+ * moe_mxfp4_forward from a routing that the caller has (moe_route_scored's): the layer without its
+ * first stage.
+ *   ids int32 [T, top_k], each row top_k distinct ids in [0, E);  gates fp32 [T, top_k]
+ *   act8  nonzero: MXFP8 activations, as moe_mxfp4_forward_a8
+ * Other arguments, workspace and limits as for moe_mxfp4_forward (T <= MX_MAX_TOKENS).
+ */
+MX_API int moe_mxfp4_forward_routed(const uint16_t* x, const int32_t* ids, const float* gates, int64_t top_k,
+                                    const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,
+                                    const uint8_t* s_down, int act8, uint16_t* y, int64_t T, int64_t H, int64_t I,
+                                    int64_t E, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * HBM reference kernels (measurement utilities, not steps of the layer).  "Zyphra
  * Inference Wave 2" (footnote 6 of its roofline discussion) measures MI355X's HBM with a

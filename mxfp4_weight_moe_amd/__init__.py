@@ -1,6 +1,6 @@
 """Python binding of the mxmoe C ABI (include/mxmoe.h): MXFP4 weight-streaming MoE layer,
-dense MXFP4 linear layer and dense feed-forward operators with their gradients for MI355X
-(gfx950).
+dense MXFP4 linear layer, dense feed-forward operators with their gradients, microscaled
+activations and routing by scores for MI355X (gfx950).
 
 Argument marshalling only: every step of the computation runs in the HIP kernels of
 libmxmoe.so.  PyTorch provides device memory and the current stream.  If the library is
@@ -83,6 +83,21 @@ for _n in _FFN_SIZES:
     getattr(_lib, _n).argtypes = [_I64] * (2 if "norm" in _n else 3)
 for _n in _FFN_CALLS:
     getattr(_lib, _n).restype = ctypes.c_int
+_lib.mx_quantize.argtypes = [_P, _INT, _INT, _P, _P, _P, _I64, _I64, _P]
+_lib.mx_norm_residual_quantize.argtypes = [_P, _P, _P, _P, _INT, _F, _P, _F, _P, _P, _INT, _P, _P, _I64, _I64, _P]
+_lib.mx_linear_quantized.argtypes = [_P, _P, _INT, _P, _P, _P, _P, _F, _INT, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
+_lib.mx_gate_up_quantized.argtypes = [_P, _P, _INT, _P, _P, _P, _INT, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P]
+_lib.moe_route_scored.argtypes = [_P, _INT, _P, _INT, _I64, _I64, _INT, _INT, _F, _P, _P, _I64, _I64, _I64, _P]
+_lib.moe_route_scored_backward.argtypes = [_P, _P, _INT, _P, _INT, _INT, _F, _P, _I64, _I64, _I64, _P]
+_lib.moe_mxfp4_forward_routed.argtypes = [_P, _P, _P, _I64, _P, _P, _P, _P, _INT, _P, _I64, _I64, _I64, _I64, _P, _SZ, _P]
+_Q_SIZES = ("mx_linear_quantized_workspace_size", "mx_gate_up_quantized_workspace_size")
+_Q_CALLS = ("mx_quantize", "mx_norm_residual_quantize", "mx_linear_quantized", "mx_gate_up_quantized",
+            "moe_route_scored", "moe_route_scored_backward", "moe_mxfp4_forward_routed")
+for _n in _Q_SIZES:
+    getattr(_lib, _n).restype = _SZ
+    getattr(_lib, _n).argtypes = [_I64] * 3
+for _n in _Q_CALLS:
+    getattr(_lib, _n).restype = ctypes.c_int
 for _n in ("mx_linear", "mxfp4_dequantize", "moe_route_topk", "moe_sort_by_expert", "moe_route_sort",
            "moe_gate_up_swiglu", "moe_down_combine", "moe_mxfp4_forward", "moe_mxfp4_forward_persistent",
            "moe_mxfp4_forward_shared", "moe_mxfp4_forward_a8", "mx_linear_a8", "mxfp8_quantize", "mx_hbm_read",
@@ -95,7 +110,7 @@ EXPORTED = ("mx_version", "mx_status_string", "mx_linear", "mxfp4_dequantize", "
             "moe_mxfp4_workspace_size", "moe_mxfp4_forward", "moe_mxfp4_forward_persistent",
             "moe_mxfp4_forward_shared", "moe_mxfp4_forward_a8", "mx_linear_a8", "mxfp8_quantize", "mx_hbm_read",
             "mx_hbm_copy", "moe_mxfp4_forward_noalloc", "moe_gate_up_swiglu_from_ids", "moe_expert_gemms_from_ids",
-            "moe_combine") + _FFN_CALLS + _FFN_SIZES
+            "moe_combine") + _FFN_CALLS + _FFN_SIZES + _Q_CALLS + _Q_SIZES
 MX_ERR_SCRATCH = -6
 MX_NOALLOC_SCRATCH_BYTES = 40 << 20
 
@@ -861,4 +876,272 @@ def mx_ffn_block(x: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tens
     _call(_lib.mx_ffn_block, dev, x.data_ptr(), _opt(w_pre), W_gate_up.data_ptr(), S_gate_up.data_ptr(),
           _opt(bias_gate_up), code, W_down.data_ptr(), S_down.data_ptr(), _opt(bias_down), _opt(w_post), _opt(gate), mode,
           scale, eps, out.data_ptr(), T, H, I, wp, wn)
+    return out
+
+
+# ------------------------------------------------------------------ microscaled activations
+#
+# Straight-through gradients: mx_norm_residual_backward, mx_linear_fused_backward and
+# mx_gate_up_backward take these calls' y and z as they take their own forward calls'.
+
+_FORMATS = {"mxfp8": 0, "mxfp4": 1}
+
+
+def _format_code(fmt: str) -> int:
+    code = _FORMATS.get(fmt)
+    if code is None:
+        raise ValueError(f"fmt must be one of {', '.join(_FORMATS)}, got {fmt!r}")
+    return code
+
+
+def _code_bytes(K: int, fmt: int) -> int:
+    return K // 2 if fmt else K
+
+
+def mx_quantize(x: torch.Tensor, fmt: str = "mxfp8", save_values: bool = False):
+    """(codes, scales) of bf16 or fp32 rows [..., K] in MXFP8 (codes uint8 [..., K]) or MXFP4
+    ([..., K/2], element 2i in the low nibble), scales uint8 [..., K/32].  save_values=True:
+    (codes, scales, values), values bf16 [..., K] what the codes stand for."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in (_BF16, _F32):
+        _check(x, "x", _BF16)  # names what is wrong
+    _check(x, "x", x.dtype)
+    if x.dim() < 1 or x.numel() == 0:
+        raise ValueError(f"x is empty: {list(x.shape)}")
+    code = _format_code(fmt)
+    dev, lead, K = x.device, x.shape[:-1], x.shape[-1]
+    if K % 32:
+        raise ValueError(f"the last dimension {K} must be a multiple of 32")
+    codes = torch.empty((*lead, _code_bytes(K, code)), dtype=_U8, device=dev)
+    scales = torch.empty((*lead, K // 32), dtype=_U8, device=dev)
+    values = torch.empty(x.shape, dtype=_BF16, device=dev) if save_values else None
+    _call(_lib.mx_quantize, dev, x.data_ptr(), 1 if x.dtype is _F32 else 0, code, codes.data_ptr(), scales.data_ptr(),
+          _opt(values), x.numel() // K, K)
+    return (codes, scales, values) if save_values else (codes, scales)
+
+
+def mx_norm_residual_quantize(x: torch.Tensor, b: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
+                              gate: torch.Tensor | None = None, scale: float = 1.0,
+                              w_pre: torch.Tensor | None = None, eps: float = 1e-6, fmt: str = "mxfp8",
+                              save_xn: bool = False, out: torch.Tensor | None = None):
+    """(y, codes, scales, xn): mx_norm_residual whose xn = rms_norm(y) * w_pre leaves in MXFP8 or
+    MXFP4, quantized from its fp32 value; save_xn=True: xn in bf16 too (else None).  w_pre is
+    required.  Without b: y is x, the norm before a block alone.  out, for y, may be x itself."""
+    T, H = _bf16_rows(x, "x")
+    dev = x.device
+    if w_pre is None:
+        raise ValueError("w_pre is required: what is quantized is rms_norm(y) * w_pre")
+    for t, n in ((w_post, "w_post"), (w_pre, "w_pre")):
+        if t is not None:
+            _tensor(t, n, _BF16, (H,), dev)
+    mode, code = _gate_mode(gate, T, H, dev), _format_code(fmt)
+    if H % 32:
+        raise ValueError(f"H = {H} must be a multiple of 32")
+    y = None
+    if b is None:
+        if w_post is not None or gate is not None or out is not None:
+            raise ValueError("without b the call takes w_pre alone")
+    else:
+        _tensor(b, "b", _BF16, (T, H), dev)
+        y = out
+        if y is None:
+            y = torch.empty_like(x)
+        else:
+            _tensor(y, "out", _BF16, (T, H), dev)
+            _apart(y, x, "x", itself=True)
+            _apart(y, b, "b", itself=True)
+    codes = torch.empty((T, _code_bytes(H, code)), dtype=_U8, device=dev)
+    scales = torch.empty((T, H // 32), dtype=_U8, device=dev)
+    xn = torch.empty_like(x) if save_xn else None
+    _call(_lib.mx_norm_residual_quantize, dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale,
+          w_pre.data_ptr(), eps, _opt(y), _opt(xn), code, codes.data_ptr(), scales.data_ptr(), T, H)
+    return (x if y is None else y), codes, scales, xn
+
+
+def _quantized(codes, scales, K: int):
+    """(T, format) of activations in MXFP8 or MXFP4, told apart by the length of their code rows."""
+    if not (isinstance(codes, torch.Tensor) and codes.dtype is _U8 and codes.is_cuda and codes.dim() == 2
+            and codes.is_contiguous()):
+        _check(codes, "codes", _U8, 2)
+    if codes.numel() == 0:
+        raise ValueError(f"codes are empty: {list(codes.shape)}")
+    T, n = codes.shape
+    if n != K and 2 * n != K:
+        raise ValueError(f"codes have {n} bytes a row, expected {K} (MXFP8) or {K // 2} (MXFP4)")
+    if K % 32:
+        raise ValueError(f"the reduction length {K} must be a multiple of 32")
+    _tensor(scales, "scales", _U8, (T, K // 32), codes.device)
+    return T, int(n != K)
+
+
+def _two_d(t, name: str):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-d tensor")
+    return t
+
+
+def mx_linear_quantized(codes: torch.Tensor, scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+                        bias: torch.Tensor | None = None, residual: torch.Tensor | None = None, scale: float = 1.0,
+                        act: str = "none", save_z: bool = False, out: torch.Tensor | None = None,
+                        ws: torch.Tensor | None = None):
+    """mx_linear_fused for activations in MXFP8 (codes [T, K]) or MXFP4 ([T, K/2]), scales
+    [T, K/32]: y[T,N] = residual + scale * act(a W^T + bias), fp32 sums, rounded once to bf16.
+    save_z=True: (y, z) for mx_linear_fused_backward.  Autograd records nothing."""
+    K = _two_d(w_codes, "weight codes").shape[1] * 2
+    T, fmt = _quantized(codes, scales, K)
+    dev = codes.device
+    N = _weights(w_codes, w_scales, "weight", None, K, dev)
+    if bias is not None:
+        _tensor(bias, "bias", _BF16, (N,), dev)
+    if residual is not None:
+        _tensor(residual, "residual", _BF16, (T, N), dev)
+    code = _act_code(act)
+    if out is None:
+        out = torch.empty((T, N), dtype=_BF16, device=dev)
+    else:
+        _tensor(out, "out", _BF16, (T, N), dev)
+        if residual is not None:
+            _apart(out, residual, "residual", itself=True)
+    z = torch.empty((T, N), dtype=_BF16, device=dev) if save_z else None
+    ws, wp, wn = _scratch(_lib.mx_linear_quantized_workspace_size(T, K, N), dev, ws)
+    _call(_lib.mx_linear_quantized, dev, codes.data_ptr(), scales.data_ptr(), fmt, w_codes.data_ptr(),
+          w_scales.data_ptr(), _opt(bias), _opt(residual), scale, code, out.data_ptr(), _opt(z), T, K, N, wp, wn)
+    return (out, z) if save_z else out
+
+
+def mx_gate_up_quantized(codes: torch.Tensor, scales: torch.Tensor, W_gate_up: torch.Tensor, S_gate_up: torch.Tensor,
+                         bias: torch.Tensor | None = None, act: str = "silu", fmt: str | None = None,
+                         save_z: bool = False, ws: torch.Tensor | None = None):
+    """mx_gate_up for activations in MXFP8 or MXFP4.  fmt None: h bf16 [T, I]; "mxfp8" or "mxfp4":
+    (h_codes, h_scales), quantized from the fp32 value (I % 32 == 0), ready for
+    mx_linear_quantized.  save_z=True: z bf16 [T, 2I] comes last, for mx_gate_up_backward.
+    Autograd records nothing."""
+    H = _two_d(W_gate_up, "W_gate_up codes").shape[1] * 2
+    T, a_fmt = _quantized(codes, scales, H)
+    dev = codes.device
+    two_i = _weights(W_gate_up, S_gate_up, "W_gate_up", None, H, dev)
+    if two_i % 2:
+        raise ValueError("W_gate_up must have an even number of rows")
+    I = two_i // 2
+    if bias is not None:
+        _tensor(bias, "bias", _BF16, (two_i,), dev)
+    code, h, hc, hs, h_fmt = _act_code(act), None, None, None, 0
+    if fmt is None:
+        h = torch.empty((T, I), dtype=_BF16, device=dev)
+    else:
+        h_fmt = _format_code(fmt)
+        if I % 32:
+            raise ValueError(f"I = {I} must be a multiple of 32 for a quantized h")
+        hc = torch.empty((T, _code_bytes(I, h_fmt)), dtype=_U8, device=dev)
+        hs = torch.empty((T, I // 32), dtype=_U8, device=dev)
+    z = torch.empty((T, two_i), dtype=_BF16, device=dev) if save_z else None
+    ws, wp, wn = _scratch(_lib.mx_gate_up_quantized_workspace_size(T, H, I), dev, ws)
+    _call(_lib.mx_gate_up_quantized, dev, codes.data_ptr(), scales.data_ptr(), a_fmt, W_gate_up.data_ptr(),
+          S_gate_up.data_ptr(), _opt(bias), code, _opt(h), h_fmt, _opt(hc), _opt(hs), _opt(z), T, H, I, wp, wn)
+    res = (h,) if fmt is None else (hc, hs)
+    if save_z:
+        res += (z,)
+    return res[0] if len(res) == 1 else res
+
+
+# ------------------------------------------------------------------ routing by scores
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"top2": 0, "max": 1}
+MX_MAX_GROUPS = 64
+
+
+def _choice(table: dict, key, name: str) -> int:
+    code = table.get(key) if isinstance(key, str) else None
+    if code is None:
+        raise ValueError(f"{name} must be one of {', '.join(table)}, got {key!r}")
+    return code
+
+
+def _logits(logits):
+    if not isinstance(logits, torch.Tensor) or logits.dtype not in (_BF16, _F32):
+        _check(logits, "router_logits", _F32, 2)  # names what is wrong
+    _check(logits, "router_logits", logits.dtype, 2)
+    if logits.numel() == 0:
+        raise ValueError(f"router_logits is empty: {list(logits.shape)}")
+    return (*logits.shape, 1 if logits.dtype is _F32 else 0)
+
+
+def moe_route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                     n_group: int = 1, topk_group: int = 1, group_score: str = "top2", renormalize: bool = False,
+                     scale: float = 1.0, ids: torch.Tensor | None = None, gates: torch.Tensor | None = None):
+    """(ids int32 [T,k], gates fp32 [T,k]) from logits [T,E] in fp32 or bf16: scores p = softmax
+    or sigmoid over all experts; the top_k experts by p + bias (fp32 [E]; it enters the choice,
+    not the gates) among the topk_group best of n_group groups of consecutive experts (by the
+    sum of their two best or their best); gates = scale * p, divided by their sum with
+    renormalize.  Descending order, ties to the lower id, compared in 64 bits.  Autograd records
+    nothing: the gradient is moe_route_scored_backward's."""
+    T, E, kind = _logits(logits)
+    dev = logits.device
+    if bias is not None:
+        _tensor(bias, "bias", _F32, (E,), dev)
+    sc, gs = _choice(_SCORES, score, "score"), _choice(_GROUP_SCORES, group_score, "group_score")
+    if ids is None:
+        ids = torch.empty((T, max(0, top_k)), dtype=torch.int32, device=dev)
+    else:
+        _tensor(ids, "ids", torch.int32, (T, top_k), dev)
+    if gates is None:
+        gates = torch.empty((T, max(0, top_k)), dtype=_F32, device=dev)
+    else:
+        _tensor(gates, "gates", _F32, (T, top_k), dev)
+    if top_k < 1:
+        raise ValueError(f"top_k must be at least 1, got {top_k}")
+    _call(_lib.moe_route_scored, dev, logits.data_ptr(), kind, _opt(bias), sc, n_group, topk_group, gs,
+          1 if renormalize else 0, scale, ids.data_ptr(), gates.data_ptr(), T, E, top_k)
+    return ids, gates
+
+
+def moe_route_scored_backward(dgates: torch.Tensor, logits: torch.Tensor, ids: torch.Tensor, score: str = "softmax",
+                              renormalize: bool = False, scale: float = 1.0) -> torch.Tensor:
+    """dlogits [T,E] (of the logits' type) of moe_route_scored from dgates fp32 [T,k] and the ids
+    that it chose (each row distinct; ids outside [0, E) are skipped).  The bias has no gradient."""
+    T, E, kind = _logits(logits)
+    dev = logits.device
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-d tensor")
+    k = ids.shape[1]
+    _tensor(ids, "ids", torch.int32, (T, k), dev)
+    _tensor(dgates, "dgates", _F32, (T, k), dev)
+    sc = _choice(_SCORES, score, "score")
+    dlogits = torch.empty_like(logits)
+    _call(_lib.moe_route_scored_backward, dev, dgates.data_ptr(), logits.data_ptr(), kind, ids.data_ptr(), sc,
+          1 if renormalize else 0, scale, dlogits.data_ptr(), T, E, k)
+    return dlogits
+
+
+def moe_mxfp4_forward_routed(x: torch.Tensor, ids: torch.Tensor, gates: torch.Tensor, W_gate_up: torch.Tensor,
+                             S_gate_up: torch.Tensor, W_down: torch.Tensor, S_down: torch.Tensor,
+                             out: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                             act8: bool = False) -> torch.Tensor:
+    """moe_mxfp4_forward from a routing that the caller has (moe_route_scored's ids int32 [T,k],
+    each row distinct and in [0, E), and gates fp32 [T,k]).  act8=True: MXFP8 activations."""
+    _check(x, "x", _BF16, 2)
+    dev = x.device
+    T, H = x.shape
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a 2-d tensor")
+    k = ids.shape[1]
+    _tensor(ids, "ids", torch.int32, (T, k), dev)
+    _tensor(gates, "gates", _F32, (T, k), dev)
+    for t, n in ((W_gate_up, "W_gate_up"), (S_gate_up, "S_gate_up"), (W_down, "W_down"), (S_down, "S_down")):
+        _check(t, n, _U8, 3, dev)
+    E, I = W_down.shape[0], W_down.shape[2] * 2
+    if (W_gate_up.shape != (E, 2 * I, H // 2) or S_gate_up.shape != (E, 2 * I, H // 32)
+            or W_down.shape != (E, H, I // 2) or S_down.shape != (E, H, I // 32)):
+        raise ValueError("expert weight shapes do not match [E, 2I, H/2], [E, 2I, H/32], [E, H, I/2], [E, H, I/32]")
+    if out is None:
+        out = torch.empty((T, H), dtype=_BF16, device=dev)
+    else:
+        _tensor(out, "out", _BF16, (T, H), dev)
+        _apart(out, x, "x")
+    if ws is None:
+        ws = workspace(T, H, I, E, k, dev)
+    _check(ws, "workspace", _U8, 1, dev)
+    _call(_lib.moe_mxfp4_forward_routed, dev, x.data_ptr(), ids.data_ptr(), gates.data_ptr(), k, W_gate_up.data_ptr(),
+          S_gate_up.data_ptr(), W_down.data_ptr(), S_down.data_ptr(), 1 if act8 else 0, out.data_ptr(), T, H, I, E,
+          ws.data_ptr(), ws.numel())
     return out

@@ -419,6 +419,43 @@ int moe_mxfp4_forward_a8(const uint16_t* x, const float* router_logits, int64_t 
                           workspace, workspace_bytes, true, stream);
 }
 
+int moe_mxfp4_forward_routed(const uint16_t* x, const int32_t* ids, const float* gates, int64_t top_k,
+                             const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,
+                             const uint8_t* s_down, int act8, uint16_t* y, int64_t T, int64_t H, int64_t I, int64_t E,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+  if (!ids) return MX_ERR_NULL;
+  int st = moe_forward_args(x, gates, top_k, 0, w_gate_up, s_gate_up, w_down, s_down, y, T, H, I, E);
+  if (st != MX_OK) return st;
+  if (!aligned(ids, 4)) return MX_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256)) return MX_ERR_WORKSPACE;
+  const MoeWorkspace ws = moe_workspace_carve(workspace, T, H, I, E, top_k);
+  if (workspace_bytes < ws.bytes) return MX_ERR_WORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int t = (int)T, h = (int)H, i = (int)I, e = (int)E, k = (int)top_k;
+  const bool a8 = act8 != 0;
+  const SortView sv{ws.counts, ws.offsets, ws.sorted_slots, ws.active, ws.num_active};
+  // the launches of moe_mxfp4_forward behind its routing
+  if (experts_sorted_fits(t, e, k, h, i) && experts_sorted_pays(t, e, k, i)) {
+    if ((st = launch_fill_ones(ws.h, (size_t)t * k * i * 2, s)) != MX_OK) return st;
+    if ((st = launch_experts_sorted(x, ids, w_gate_up, s_gate_up, w_down, s_down, ws.h, ws.dpart, ws.ctl, t, h, i, e, k,
+                                    a8, s)) != MX_OK)
+      return st;
+    return launch_combine(ws.dpart, gates, y, t, h, k, s);
+  }
+  if (gate_up_sorted_fits(t, e, k, h, i)) {
+    st = launch_gate_up_sorted(x, ids, w_gate_up, s_gate_up, ws.h, ws.counts, ws.offsets, ws.sorted_slots, ws.active,
+                               ws.num_active, ws.ctl, t, h, i, e, k, a8, s);
+  } else {
+    st = launch_sort(ids, t, k, e, ws.counts, ws.offsets, ws.sorted_slots, ws.active, ws.num_active, s);
+    if (st == MX_OK) st = launch_gate_up(x, w_gate_up, s_gate_up, sv, ws.h, ws.ctl, t, h, i, e, k, a8, s);
+  }
+  if (st != MX_OK) return st;
+  bool combined = false;
+  if ((st = launch_down(ws.h, gates, w_down, s_down, sv, ws.dpart, y, &combined, ws.ctl, t, h, i, e, k, a8, s)) != MX_OK)
+    return st;
+  return combined ? MX_OK : launch_combine(ws.dpart, gates, y, t, h, k, s);
+}
+
 int moe_mxfp4_forward_persistent(const uint16_t* x, const float* router_logits, int64_t top_k,
                                  const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,
                                  const uint8_t* s_down, uint16_t* y, int64_t T, int64_t H, int64_t I, int64_t E,

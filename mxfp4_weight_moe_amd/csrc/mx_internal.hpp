@@ -179,10 +179,42 @@ int launch_strip_sum(const float* parts, int strips, int cols, int arrays, float
 int launch_norm_residual(const uint16_t* x, const uint16_t* b, const uint16_t* w_post, const uint16_t* gate,
                          int gate_mode, float scale, const uint16_t* w_pre, float eps, uint16_t* y, uint16_t* xn, int T,
                          int H, hipStream_t stream);
+int launch_norm_residual_quantize(const uint16_t* x, const uint16_t* b, const uint16_t* w_post, const uint16_t* gate,
+                                  int gate_mode, float scale, const uint16_t* w_pre, float eps, uint16_t* y,
+                                  uint16_t* xn, int format, uint8_t* codes, uint8_t* scales, int T, int H,
+                                  hipStream_t stream);
 int norm_backward_groups(int64_t T, int64_t H);
 int launch_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const uint16_t* y, const uint16_t* b,
                                   const uint16_t* w_post, const uint16_t* gate, int gate_mode, float scale,
                                   const uint16_t* w_pre, float eps, uint16_t* dx, uint16_t* db, void* dgate,
                                   float* dw_post, float* dw_pre, int T, int H, float* parts, hipStream_t stream);
+
+// ------------------------------------------------------------------ microscaled activations
+
+int launch_quantize(const void* x, bool f32, int format, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
+                    uint16_t* values, hipStream_t stream);
+// quantized: gate_up's output is
+TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool quantized);
+int launch_linear_quantized(const uint8_t* a, const uint8_t* as, int format, const uint8_t* w, const uint8_t* s,
+                            const uint16_t* bias, const uint16_t* residual, float scale, int act, uint16_t* y,
+                            uint16_t* z, int T, int K, int N, void* workspace, hipStream_t stream);
+// h_codes: h leaves quantized (h null), else as bf16
+int launch_gate_up_quantized(const uint8_t* a, const uint8_t* as, int format, const uint8_t* w, const uint8_t* s,
+                             const uint16_t* bias, int act, uint16_t* h, int out_format, uint8_t* h_codes,
+                             uint8_t* h_scales, uint16_t* z, int T, int H, int I, void* workspace, hipStream_t stream);
+
+// ------------------------------------------------------------------ scored routing
+
+struct RouteScored {
+  const void* logits;  // [T, E] fp32 or bf16
+  const float* bias;   // [E] or null
+  bool bf16, sigmoid, top2, renormalize;
+  int E, k, groups, kept;
+  int64_t T;
+  float scale;
+};
+int launch_route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStream_t stream);
+int launch_route_scored_backward(const RouteScored& a, const float* dgates, const int32_t* ids, void* dlogits,
+                                 hipStream_t stream);
 
 }  // namespace mx

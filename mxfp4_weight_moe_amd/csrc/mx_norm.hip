@@ -13,6 +13,7 @@
 // workgroup's rows and are summed over the workgroups in a fixed order by a second launch.
 #include "mx_epilogue.hpp"
 #include "mx_internal.hpp"
+#include "mx_quant.hpp"
 
 namespace mx {
 
@@ -26,6 +27,8 @@ struct NormArgs {
   const uint16_t* dxn;
   uint16_t* y;             // forward: y; backward: dx
   uint16_t* xn;            // forward: xn; backward: db
+  uint8_t* codes;          // xn in MXFP8 or MXFP4 (then xn itself is optional)
+  uint8_t* scales;
   void* dgate;             // token: fp32 [T]; full: bf16 [T, H]
   float* parts;            // [workgroups][arrays][H]
   int gate_mode;
@@ -97,9 +100,12 @@ constexpr u32x4 ZERO4 = {0u, 0u, 0u, 0u};
 // Bound by memory: 8192 x 7168 with both norms and a gate per channel, 470 MB, in 80 to 89 us,
 // 5.3 TB/s or more; 32 rows take 4 us, launch and latency.
 // L: lanes of a row.  Less than a wave, for short rows, and a wave has 64 / L rows at a time.
-template <int NT, int V, int L, bool BLK, bool POST, bool PRE>
+// FMT: xn leaves as MXFP8 (8) or MXFP4 (4) codes and scales, quantized from its fp32 value; H % 32 == 0
+// then, so that a block is a quad of lanes of one row.
+template <int NT, int V, int L, bool BLK, bool POST, bool PRE, int FMT = 0>
 __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
   static_assert(L == 64 || NT == 64, "short rows have no barriers");
+  static_assert(FMT == 0 || PRE, "what is quantized is xn");
   __shared__ float red[2][NT / 64];
   const int vecs = a.H / 8;
   u32x4 wpost[V], wpre[V], gch[V];
@@ -177,7 +183,14 @@ __global__ void __launch_bounds__(NT) norm_kernel(NormArgs a) {
         unpack8(wpre[i], w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = v[j] * q * w[j];
-        if (ok[i]) *reinterpret_cast<u32x4*>(a.xn + row + at[i] * 8) = pack8(v);
+        if constexpr (FMT == 0) {
+          if (ok[i]) *reinterpret_cast<u32x4*>(a.xn + row + at[i] * 8) = pack8(v);
+        } else if (ok[i]) {
+          uint32_t c[FMT / 4], byte;
+          quantize8<FMT>(v, c, byte);
+          store_codes8<FMT>(a.codes, a.scales, row / 8 + at[i], c, byte);
+          if (a.xn) *reinterpret_cast<u32x4*>(a.xn + row + at[i] * 8) = pack8(v);
+        }
       }
     }
     if constexpr (NT > 64) __syncthreads();  // the sums are read before the next row's are written
@@ -457,11 +470,11 @@ __global__ void __launch_bounds__(NT) norm_backward_kernel(NormArgs a) {
 // Rows of a workgroup at a time.
 static int norm_rows(int64_t H) { return H <= 128 ? 4 : H <= 256 ? 2 : 1; }
 
-template <bool BLK, bool POST, bool PRE>
+template <bool BLK, bool POST, bool PRE, int FMT = 0>
 static void norm_forward(const NormArgs& a, hipStream_t stream) {
   const int rows = norm_rows(a.H);
   const dim3 grid((unsigned)std::min((a.T + rows - 1) / rows, 8 * GPU_CUS));
-#define MX_CALL(NT, V, L) hipLaunchKernelGGL((norm_kernel<NT, V, L, BLK, POST, PRE>), grid, dim3(NT), 0, stream, a)
+#define MX_CALL(NT, V, L) hipLaunchKernelGGL((norm_kernel<NT, V, L, BLK, POST, PRE, FMT>), grid, dim3(NT), 0, stream, a)
   MX_NORM_SIZES(MX_CALL);
 #undef MX_CALL
 }
@@ -487,6 +500,28 @@ int launch_norm_residual(const uint16_t* x, const uint16_t* b, const uint16_t* w
     w_pre ? norm_forward<true, true, true>(a, stream) : norm_forward<true, true, false>(a, stream);
   else
     w_pre ? norm_forward<true, false, true>(a, stream) : norm_forward<true, false, false>(a, stream);
+  return hip_status(hipGetLastError());
+}
+
+template <int FMT>
+static void norm_forward_quantized(const NormArgs& a, hipStream_t stream) {
+  if (!a.b)
+    norm_forward<false, false, true, FMT>(a, stream);
+  else if (a.w_post)
+    norm_forward<true, true, true, FMT>(a, stream);
+  else
+    norm_forward<true, false, true, FMT>(a, stream);
+}
+
+int launch_norm_residual_quantize(const uint16_t* x, const uint16_t* b, const uint16_t* w_post, const uint16_t* gate,
+                                  int gate_mode, float scale, const uint16_t* w_pre, float eps, uint16_t* y,
+                                  uint16_t* xn, int format, uint8_t* codes, uint8_t* scales, int T, int H,
+                                  hipStream_t stream) {
+  NormArgs a{};
+  a.x = x, a.b = b, a.w_post = w_post, a.w_pre = w_pre, a.gate = gate;
+  a.y = y, a.xn = xn, a.gate_mode = gate_mode, a.T = T, a.H = H, a.scale = scale, a.eps = eps;
+  a.codes = codes, a.scales = scales;
+  format == MX_FORMAT_MXFP8 ? norm_forward_quantized<8>(a, stream) : norm_forward_quantized<4>(a, stream);
   return hip_status(hipGetLastError());
 }
 

@@ -1,0 +1,393 @@
+// Dense feed-forward operators whose activations are microscaled already:
+//   linear   y = residual + scale * act(a W^T + bias)
+//   gate_up  h = act(a Wg^T + bg) * (a Wu^T + bu)     (gate rows [0, I), up rows [I, 2I) of W)
+// a in MXFP8 or MXFP4, W in MXFP4, fp32 sums; h in bf16, or quantized again from its fp32 value.
+//
+// Two kernels, by the number of tokens: up to STREAM_Q_MAX_T the weights are streamed once, a
+// workgroup to 16 weight rows (stream_q_kernel); beyond, tiles (mx_tile_q.hpp).
+#include "mx_grid.hpp"
+#include "mx_tile_out.hpp"
+#include "mx_tile_q.hpp"
+
+namespace mx {
+
+// h leaves as codes and scales.  I % 32 == 0: the 8 columns of each of 4 lanes are a block.
+template <int FMT>
+struct GatedQuantEpilogue : GatedEpilogue {
+  static constexpr bool WHOLE_BLOCKS = true;
+  uint8_t* codes;   // [T, I] or [T, I / 2]
+  uint8_t* scales;  // [T, I / 32]
+  template <int V>
+  __device__ __forceinline__ void store(int t, int n, float (&g)[V], float (&u)[V], const Columns<V>& c) const {
+    static_assert(V == 8, "a quad of lanes is a block");
+    if (n >= I) return;
+    product<V>(t, n, g, u, c);
+    uint32_t q[FMT / 4], byte;
+    quantize8<FMT>(g, q, byte);
+    store_codes8<FMT>(codes, scales, ((size_t)t * I + n) / 8, q, byte);
+  }
+};
+
+// What a product reads.
+struct QOperands {
+  const uint8_t* a;   // [T, K] (MXFP8) or [T, K / 2]
+  const uint8_t* as;  // [T, K / 32]
+  const uint8_t* w;   // [rows (x 2), K / 2]
+  const uint8_t* ws;  // [rows (x 2), K / 32]
+};
+
+// ------------------------------------------------------------------ few tokens: weight streaming
+
+constexpr int STREAM_Q_MAX_T = 32;
+
+// v_mfma_scale_f32_16x16x128_f8f6f4: lane (r = lane & 15, g = lane >> 4) gives E2M1 block g of row r, or
+// E4M3 values 16 g .. + 15 of both halves of the 128.
+template <int FMT>
+__device__ __forceinline__ f32x4 mfma_stream_q(const u32x4& w, const QFragment<FMT>& a, f32x4 c, int sw, int sa) {
+  const i32x8 wo = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wo, q_operand(a), c, 4, FMT == 8 ? 0 : 4, 0, sw, 0, sa);
+}
+
+// A workgroup has 16 weight rows (gate_up: 8 gate rows and the 8 up rows of the same columns), its W
+// waves split K.  A lane loads its operands straight from memory: 16 code bytes of a weight row and 32
+// (16) of a token a step of 128 values.
+template <int FMT, int W, int MT, bool GATED, class Epilogue>
+__global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T,
+                                                          int K, int rows) {
+  constexpr int COLS = GATED ? SUB_ROWS / 2 : SUB_ROWS, D = 4;
+  __shared__ f32x4 red[(W > 1) ? W * MT * 64 : 1];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * COLS;
+  const size_t kb = (size_t)(K >> 1), ks = (size_t)(K >> 5), ka = (size_t)K * FMT / 8;
+  // past the last row or token the last one again; what it gives is not stored
+  const size_t row = GATED ? (size_t)min(n0 + (r & 7), rows - 1) + (r >= 8 ? (size_t)rows : 0) : (size_t)min(n0 + r, rows - 1);
+  const uint8_t* wp = o.w + row * kb + 16 * g;
+  const uint8_t* sp = o.ws + row * ks + g;
+  const uint8_t* ap[MT];
+  const uint8_t* asp[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const size_t t = (size_t)min(m * 16 + r, T - 1);
+    ap[m] = o.a + t * ka + 16 * g;
+    asp[m] = o.as + t * ks + g;
+  }
+  const int blocks = K >> 5, steps = (blocks + 3) >> 2;
+  const int s0 = (int)((int64_t)steps * wave / W), s1 = (int)((int64_t)steps * (wave + 1) / W);
+  struct Step {
+    u32x4 w;
+    QFragment<FMT> a[MT];
+    uint32_t sw, sa[MT];
+  };
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  auto load = [&](int j) {
+    Step s;
+    const int left = blocks - 4 * j;  // blocks of this step
+    const bool ok = g < left;
+    s.w = ok ? ld_stream16(wp + (size_t)j * 64) : zero;
+    s.sw = ok ? sp[j * 4] : 0u;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      s.sa[m] = ok ? asp[m][j * 4] : 0u;
+      if constexpr (FMT == 8) {
+        s.a[m].v[0] = (g >> 1) < left ? ld16(ap[m] + (size_t)j * 128) : zero;
+        s.a[m].v[1] = 2 + (g >> 1) < left ? ld16(ap[m] + (size_t)j * 128 + 64) : zero;
+      } else {
+        s.a[m].v[0] = ok ? ld16(ap[m] + (size_t)j * 64) : zero;
+      }
+    }
+    return s;
+  };
+  f32x4 acc[MT][1];
+  acc_zero(acc);
+  Step q[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (s0 + d < s1) q[d] = load(s0 + d);
+  for (int j = s0; j < s1; j += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      if (j + d >= s1) break;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m][0] = mfma_stream_q<FMT>(q[d].w, q[d].a[m], acc[m][0], (int)q[d].sw, (int)q[d].sa[m]);
+      if (j + d + D < s1) q[d] = load(j + d + D);
+    }
+  }
+  wg_reduce<1, MT, W>(acc, red, wave, lane);
+  if (wave != 0) return;
+  const int n = n0 + 4 * (GATED ? g & 1 : g);
+  const int pc = part_cols(rows);
+  const auto cols = epi.template columns<4>(n);
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int t = m * 16 + r;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = acc[m][0][j];
+    if (parts) {  // n + 4 <= pc
+      if (t < T && n < rows)
+        *reinterpret_cast<f32x4*>(parts + (size_t)t * ((GATED ? 2 : 1) * (size_t)pc) + (GATED && g >= 2 ? pc : 0) + n) = acc[m][0];
+      continue;
+    }
+    if constexpr (GATED) {
+      float u[4];  // rows 8 and up of the tile: the lanes 32 on
+#pragma unroll
+      for (int j = 0; j < 4; ++j) u[j] = __shfl_xor(v[j], 32, 64);
+      if constexpr (!Epilogue::WHOLE_BLOCKS)
+        if (t < T && g < 2) epi.template store<4>(t, n, v, u, cols);
+    } else {
+      if (t < T) epi.template store<4>(t, n, v, cols, epi.template fetch<4>(t, n));
+    }
+  }
+}
+
+// ------------------------------------------------------------------ tiles
+
+template <int FMT, int MT, int NT, int D, bool GATED, class Epilogue>
+__global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
+    tile_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T, int K, int rows, int mtiles, int ntiles,
+                  int nsplit) {
+  typedef QLds<FMT, MT, NT, D> L;
+  constexpr int WCOLS = NT * 32 / (GATED ? 2 : 1), HALF = GATED ? NT / 2 : NT, COLS = 2 * WCOLS;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wm = wave >> 1, wn = wave & 1;
+  const int tile = xcd_tile(blockIdx.x, mtiles * ntiles * nsplit);
+  const int split = tile % nsplit, nt = tile / nsplit % ntiles, mt0 = tile / nsplit / ntiles;
+  const int m0 = mt0 * L::BM, n0 = nt * COLS;
+  const int stages = (K + Q_KB - 1) / Q_KB, full = K / Q_KB, tail = (K >> 5) & 3;
+  const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
+
+  // Row lr of the workgroup's 64 NT: row r of MFMA tile lr >> 5, counted from the tile's first row in the
+  // gate or the up half; past the last row (or token) the last one again, never stored.
+  auto weight_half = [&](int lr) { return (size_t)n0 + ((lr >> 5) % NT >= HALF ? (size_t)rows : 0); };
+  auto weight_row = [&](int lr) { return min((lr >> 5) / NT * WCOLS + (lr >> 5) % HALF * 32 + (lr & 31), rows - 1 - n0); };
+  auto token_row = [&](int lr) { return min(lr, T - 1 - m0); };
+  typename L::Rows as;
+  as.init((int64_t)K * FMT / 8, min(L::BM, T - m0), wave, lane,
+          [&](int) { return o.a + (size_t)m0 * ((size_t)K * FMT / 8); }, token_row);
+  typename L::Codes cs;
+  cs.init(K >> 1, min(COLS, rows - n0), wave, lane, [&](int lr) { return o.w + weight_half(lr) * (size_t)(K >> 1); }, weight_row);
+  QScales<L::BM, L::BN> sc;
+  const size_t ks = (size_t)(K >> 5);
+  sc.init(K, K % (Q_KB * Q_GROUP) == 0, [&](int lr) {
+    return lr < L::BM ? o.as + (size_t)(m0 + token_row(lr)) * ks
+                      : o.ws + (weight_half(lr - L::BM) + weight_row(lr - L::BM)) * ks;
+  });
+
+  constexpr int XC = L::Rows::COPIES, LOADS = XC + L::Codes::COPIES, FIRST = LOADS / 2;
+  auto copy = [&](uint8_t* buf, int st, auto Q) __attribute__((always_inline)) {
+    constexpr int q = Q;
+    if constexpr (q < XC)
+      as.copy_one(buf, st, st < full ? 8 : tail * (FMT / 4), q);
+    else
+      cs.copy_one(buf + L::Rows::BYTES, st, st < full ? 8 : tail, q - XC);
+  };
+  const int r = lane & 31, g = lane >> 5;
+  constexpr int AF = FMT / 4;  // 16-byte pieces of a fragment
+  uint32_t at[2][AF], wat[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+#pragma unroll
+    for (int p = 0; p < AF; ++p) {
+      const int c = FMT == 8 ? 4 * u + 2 * p + g : 2 * u + g;
+      at[u][p] = (uint32_t)(wm * MT * 32 + r) * L::ARB + ((c ^ q_key<L::ARB>(r)) << 4);
+    }
+    wat[u] = L::Rows::BYTES + (uint32_t)(wn * NT * 32 + r) * L::WRB + (((2 * u + g) ^ q_key<L::WRB>(r)) << 4);
+  }
+  const uint32_t sat = L::SCALES_AT + (uint32_t)(wm * MT * 32 + r) * 16;
+  const uint32_t wsat = L::SCALES_AT + (uint32_t)(L::BM + wn * NT * 32 + r) * 16;
+  auto scales_of = [&](int group) { return lds + L::SCALES_AT + (group & 1) * L::SCALES; };
+
+  f32x16 acc[MT][NT];
+  tile_zero(acc);
+  QFragment<FMT> frag[2][MT];
+  u32x4 w[2][NT];
+  uint32_t raw_a[MT], raw_w[NT], sa[2][MT], sw[2][NT];  // a stage's 4 scale bytes; step u's in the low byte
+  auto read_scale = [&](int st, int e) {
+    const uint32_t o2 = (uint32_t)((st >> 2) & 1) * L::SCALES + (st & 3) * 4;
+    if (e < MT)
+      raw_a[e] = *reinterpret_cast<const uint32_t*>(lds + sat + o2 + e * 512);
+    else
+      raw_w[e - MT] = *reinterpret_cast<const uint32_t*>(lds + wsat + o2 + (e - MT) * 512);
+  };
+  auto take_scale = [&](int u, int e) {
+    if (e < MT)
+      sa[u][e] = raw_a[e] >> (16 * u + 8 * g);
+    else
+      sw[u][e - MT] = raw_w[e - MT] >> (16 * u + 8 * g);
+  };
+  auto read = [&](const uint8_t* buf, int u, int e) {  // piece e of a step's operands
+    if (e < NT)
+      w[u][e] = ld16(buf + wat[u] + e * (32 * L::WRB));
+    else
+      frag[u][(e - NT) / AF].v[(e - NT) % AF] = ld16(buf + at[u][(e - NT) % AF] + (e - NT) / AF * (32 * L::ARB));
+  };
+  constexpr int SLOTS = MT * NT, READS = NT + MT * AF, SCALES = MT + NT;
+  auto buffer_of = [&](int i) { return lds + i * L::ONE; };
+
+  // A part of K that starts inside a group of scales takes the next group along: the copies that
+  // follow a later load would be too few for the waits below to cover it.
+  const int group0 = st0 >> 2;
+  sc.load(group0, scales_of(group0));
+  sc.store(scales_of(group0));
+  if ((st0 & 3) != 0 && 4 * (group0 + 1) < st1) {
+    sc.load(group0 + 1, scales_of(group0 + 1));
+    sc.store(scales_of(group0 + 1));
+  }
+  unrolled<D - 1>([&](auto J) __attribute__((always_inline)) {
+    unrolled<LOADS>([&](auto Q) __attribute__((always_inline)) { copy(buffer_of(J), min(st0 + J, st1 - 1), Q); });
+  });
+  unrolled<FIRST>([&](auto Q) __attribute__((always_inline)) { copy(buffer_of(D - 1), min(st0 + D - 1, st1 - 1), Q); });
+  q_barrier<(D - 2) * LOADS + FIRST>();
+#pragma unroll
+  for (int e = 0; e < SCALES; ++e) read_scale(st0, e);
+#pragma unroll
+  for (int e = 0; e < READS; ++e) read(lds, 0, e);
+#pragma unroll
+  for (int e = 0; e < SCALES; ++e) take_scale(0, e);
+
+  int cur = 0, fill = D - 1;  // buffers of the current stage, and of the one D - 1 stages on
+  for (int st = st0; st < st1; ++st) {
+    const int nxt = cur + 1 == D ? 0 : cur + 1;
+    const int next_group = (st >> 2) + 1;
+    const bool more = 4 * next_group < st1 && (st & ~3) >= st0;
+    if (more && (st & 3) == 0) sc.load(next_group, scales_of(next_group));
+    const int c0 = min(st + D - 1, st1 - 1), c1 = min(st + D, st1 - 1);
+    unrolled<2>([&](auto U) __attribute__((always_inline)) {
+      constexpr int u = U;
+      if constexpr (u == 1) {
+        if (more && (st & 3) == 3) sc.store(scales_of(next_group));
+        // the next stage has landed for every wave, and no wave reads the current one any more
+        q_barrier<(D - 2) * LOADS>();
+      }
+      unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
+        constexpr int k = S, m = k / NT, i = k % NT;
+        mfma_q<FMT>(acc[m][i], w[u][i], frag[u][m], sw[u][i], sa[u][m]);
+        if constexpr (u == 1)
+          unrolled<SCALES>([&](auto E) __attribute__((always_inline)) {
+            if constexpr (E * SLOTS / (2 * SCALES) == k) read_scale(st + 1, E);
+          });
+        unrolled<READS>([&](auto E) __attribute__((always_inline)) {
+          if constexpr (E * SLOTS / READS == k) read(buffer_of(u == 0 ? cur : nxt), 1 - u, E);
+        });
+        unrolled<SCALES>([&](auto E) __attribute__((always_inline)) {
+          if constexpr (SLOTS / 2 + E * (SLOTS - SLOTS / 2) / SCALES == k) take_scale(1 - u, E);
+        });
+        unrolled<LOADS>([&](auto E) __attribute__((always_inline)) {
+          if constexpr (u == 1 && E < FIRST && E * SLOTS / FIRST == k) copy(buffer_of(cur), c1, E);
+          if constexpr (u == 0 && E >= FIRST && (E - FIRST) * SLOTS / (LOADS - FIRST) == k) copy(buffer_of(fill), c0, E);
+        });
+        keep_order();
+      });
+    });
+    fill = cur;
+    cur = nxt;
+  }
+  wait_copies();  // the repeated copies of the last stages: the LDS is used again
+  tile_output<MT, NT, 2, 2, GATED, L::BYTES>(acc, epi, parts, lds, T, rows, m0, n0, split, nsplit, wave, lane);
+}
+
+// ------------------------------------------------------------------ launch plans
+
+static bool takes_stream_q(int64_t T) { return T <= STREAM_Q_MAX_T; }
+
+// quantized: the product's output is, which a workgroup of the streaming kernel, with fewer columns
+// than a block, leaves to a second launch.
+TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool quantized) {
+  TilePlan p{};
+  p.nsplit = 1;
+  bool parts = quantized;
+  if (!takes_stream_q(T)) {
+    const int64_t cols_all = rows * (gated ? 2 : 1);
+    const int64_t large = ((T + 255) / 256) * ((cols_all + 255) / 256);
+    p.mt = T <= 64 ? 1 : large >= GPU_CUS / 2 ? 4 : 2;
+    p.nt = p.mt == 4 ? 4 : 2;
+    const int bm = 64 * p.mt, cols = (gated ? 32 : 64) * p.nt;
+    p.mtiles = (int)((T + bm - 1) / bm);
+    p.ntiles = (int)((rows + cols - 1) / cols);
+    const int64_t stages = (K + Q_KB - 1) / Q_KB;
+    p.nsplit = (int)tile_split((int64_t)p.mtiles * p.ntiles, stages, false);
+    parts = p.nsplit > 1;
+  }
+  if (parts) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows) * (gated ? 2 : 1) * 4;
+  return p;
+}
+
+template <int FMT, bool GATED, class Epilogue>
+static int launch_product_q(const QOperands& o, const Epilogue& epi, bool quantized, void* workspace, int T, int K,
+                            int rows, hipStream_t stream) {
+  const TilePlan p = quantized_plan(T, K, rows, GATED, quantized);
+  float* parts = p.bytes ? static_cast<float*>(workspace) : nullptr;
+  if (takes_stream_q(T)) {
+    const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
+    const int items = (rows + cols - 1) / cols, steps = (K + 127) / 128;
+    int W = 1;
+    while (W < 8 && 2 * W <= steps && 2 * W * items <= 2048) W *= 2;
+#define MX_STREAM_Q(WW, M) \
+  hipLaunchKernelGGL((stream_q_kernel<FMT, WW, M, GATED, Epilogue>), dim3(items), dim3(WW * 64), 0, stream, o, epi, parts, T, K, rows)
+#define MX_STREAM_Q_W(WW) \
+  if (T <= 16)            \
+    MX_STREAM_Q(WW, 1);   \
+  else                    \
+    MX_STREAM_Q(WW, 2)
+    if (W == 1) {
+      MX_STREAM_Q_W(1);
+    } else if (W == 2) {
+      MX_STREAM_Q_W(2);
+    } else if (W == 4) {
+      MX_STREAM_Q_W(4);
+    } else {
+      MX_STREAM_Q_W(8);
+    }
+#undef MX_STREAM_Q_W
+#undef MX_STREAM_Q
+  } else {
+    const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
+#define MX_TILE_Q(MT, NT)                                                                                        \
+  hipLaunchKernelGGL((tile_q_kernel<FMT, MT, NT, FMT == 8 ? 3 : 4, GATED, Epilogue>), grid, dim3(256), 0, stream, o, epi, \
+                     p.nsplit > 1 ? parts : nullptr, T, K, rows, p.mtiles, p.ntiles, p.nsplit)
+    if (p.mt == 4)
+      MX_TILE_Q(4, 4);
+    else if (p.mt == 2)
+      MX_TILE_Q(2, 2);
+    else
+      MX_TILE_Q(1, 2);
+#undef MX_TILE_Q
+  }
+  if (parts) {
+    const int pc = part_cols(rows);
+    const int64_t pieces = (int64_t)T * (pc / 8);
+    hipLaunchKernelGGL((combine_kernel<GATED, Epilogue>), dim3((unsigned)((pieces + 63) / 64)), dim3(64), 0, stream, parts,
+                       epi, T, pc, p.nsplit);
+  }
+  return hip_status(hipGetLastError());
+}
+
+int launch_linear_quantized(const uint8_t* a, const uint8_t* as, int format, const uint8_t* w, const uint8_t* s,
+                            const uint16_t* bias, const uint16_t* residual, float scale, int act, uint16_t* y,
+                            uint16_t* z, int T, int K, int N, void* workspace, hipStream_t stream) {
+  const QOperands o{a, as, w, s};
+  const LinearEpilogue epi{bias, residual, y, z, N, act, scale};
+  return format == MX_FORMAT_MXFP8 ? launch_product_q<8, false>(o, epi, false, workspace, T, K, N, stream)
+                                   : launch_product_q<4, false>(o, epi, false, workspace, T, K, N, stream);
+}
+
+template <int FMT>
+static int gate_up_q(const QOperands& o, const GatedEpilogue& epi, int out_format, uint8_t* codes, uint8_t* scales,
+                     void* workspace, int T, int H, int I, hipStream_t stream) {
+  if (!codes) return launch_product_q<FMT, true>(o, epi, false, workspace, T, H, I, stream);
+  if (out_format == MX_FORMAT_MXFP8)
+    return launch_product_q<FMT, true>(o, GatedQuantEpilogue<8>{epi, codes, scales}, true, workspace, T, H, I, stream);
+  return launch_product_q<FMT, true>(o, GatedQuantEpilogue<4>{epi, codes, scales}, true, workspace, T, H, I, stream);
+}
+
+int launch_gate_up_quantized(const uint8_t* a, const uint8_t* as, int format, const uint8_t* w, const uint8_t* s,
+                             const uint16_t* bias, int act, uint16_t* h, int out_format, uint8_t* h_codes,
+                             uint8_t* h_scales, uint16_t* z, int T, int H, int I, void* workspace, hipStream_t stream) {
+  const QOperands o{a, as, w, s};
+  const GatedEpilogue epi{bias, h, z, I, act};
+  return format == MX_FORMAT_MXFP8 ? gate_up_q<8>(o, epi, out_format, h_codes, h_scales, workspace, T, H, I, stream)
+                                   : gate_up_q<4>(o, epi, out_format, h_codes, h_scales, workspace, T, H, I, stream);
+}
+
+}  // namespace mx
