@@ -49,68 +49,93 @@ __device__ __forceinline__ f32x4 mfma_stream_q(const u32x4& w, const QFragment<F
 }
 
 // A workgroup has 16 weight rows (gate_up: 8 gate rows and the 8 up rows of the same columns), its W
-// waves split K.  A lane loads its operands straight from memory: 16 code bytes of a weight row and 32
-// (16) of a token a step of 128 values.
+// waves split K.  A lane loads its operands straight from memory, 256 values (Q_UNIT) at a time and 4 of
+// those ahead: two 16-byte pieces of a weight row, four (two) of a token, 8 scale bytes of each.
+constexpr int Q_UNIT = 256;
 template <int FMT, int W, int MT, bool GATED, class Epilogue>
 __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T,
                                                           int K, int rows) {
-  constexpr int COLS = GATED ? SUB_ROWS / 2 : SUB_ROWS, D = 4;
+  constexpr int COLS = GATED ? SUB_ROWS / 2 : SUB_ROWS, D = 4, AP = FMT / 4;
   __shared__ f32x4 red[(W > 1) ? W * MT * 64 : 1];
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
   const int n0 = blockIdx.x * COLS;
   const size_t kb = (size_t)(K >> 1), ks = (size_t)(K >> 5), ka = (size_t)K * FMT / 8;
   // past the last row or token the last one again; what it gives is not stored
   const size_t row = GATED ? (size_t)min(n0 + (r & 7), rows - 1) + (r >= 8 ? (size_t)rows : 0) : (size_t)min(n0 + r, rows - 1);
   const uint8_t* wp = o.w + row * kb + 16 * g;
-  const uint8_t* sp = o.ws + row * ks + g;
+  const uint8_t* sp = o.ws + row * ks;
   const uint8_t* ap[MT];
   const uint8_t* asp[MT];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const size_t t = (size_t)min(m * 16 + r, T - 1);
     ap[m] = o.a + t * ka + 16 * g;
-    asp[m] = o.as + t * ks + g;
+    asp[m] = o.as + t * ks;
   }
-  const int blocks = K >> 5, steps = (blocks + 3) >> 2;
-  const int s0 = (int)((int64_t)steps * wave / W), s1 = (int)((int64_t)steps * (wave + 1) / W);
-  struct Step {
-    u32x4 w;
-    QFragment<FMT> a[MT];
-    uint32_t sw, sa[MT];
+  typedef u32x2 scales_any __attribute__((aligned(1)));
+  struct Unit {
+    u32x4 w[2];
+    QFragment<FMT> a[MT][2];
+    u32x2 sw, sa[MT];
   };
-  const u32x4 zero = {0u, 0u, 0u, 0u};
-  auto load = [&](int j) {
-    Step s;
-    const int left = blocks - 4 * j;  // blocks of this step
-    const bool ok = g < left;
-    s.w = ok ? ld_stream16(wp + (size_t)j * 64) : zero;
-    s.sw = ok ? sp[j * 4] : 0u;
+  auto load = [&](Unit& u, int j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) u.w[h] = ld_stream16(wp + (size_t)j * (Q_UNIT / 2) + h * 64);
+    u.sw = *reinterpret_cast<const scales_any*>(sp + (size_t)j * (Q_UNIT / 32));
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      s.sa[m] = ok ? asp[m][j * 4] : 0u;
-      if constexpr (FMT == 8) {
-        s.a[m].v[0] = (g >> 1) < left ? ld16(ap[m] + (size_t)j * 128) : zero;
-        s.a[m].v[1] = 2 + (g >> 1) < left ? ld16(ap[m] + (size_t)j * 128 + 64) : zero;
-      } else {
-        s.a[m].v[0] = ok ? ld16(ap[m] + (size_t)j * 64) : zero;
-      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int p = 0; p < AP; ++p) u.a[m][h].v[p] = ld16(ap[m] + (size_t)j * (Q_UNIT * FMT / 8) + (h * AP + p) * 64);
+      u.sa[m] = *reinterpret_cast<const scales_any*>(asp[m] + (size_t)j * (Q_UNIT / 32));
     }
-    return s;
   };
   f32x4 acc[MT][1];
   acc_zero(acc);
-  Step q[D];
+  auto multiply = [&](const Unit& u) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+        acc[m][0] = mfma_stream_q<FMT>(u.w[h], u.a[m][h], acc[m][0], (int)(u.sw[h] >> (8 * g)), (int)(u.sa[m][h] >> (8 * g)));
+  };
+  const int units = K / Q_UNIT;
+  const int u0 = (int)((int64_t)units * wave / W), u1 = (int)((int64_t)units * (wave + 1) / W);
+  Unit q[D];
 #pragma unroll
   for (int d = 0; d < D; ++d)
-    if (s0 + d < s1) q[d] = load(s0 + d);
-  for (int j = s0; j < s1; j += D) {
+    if (u0 + d < u1) load(q[d], u0 + d);
+  for (int j = u0; j < u1; j += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      if (j + d >= s1) break;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) acc[m][0] = mfma_stream_q<FMT>(q[d].w, q[d].a[m], acc[m][0], (int)q[d].sw, (int)q[d].sa[m]);
-      if (j + d + D < s1) q[d] = load(j + d + D);
+      if (j + d < u1) {
+        multiply(q[d]);
+        if (j + d + D < u1) load(q[d], j + d + D);
+      }
     }
+  }
+  // What is left of K, fewer than 8 blocks: missing ones are zero codes with zero scales.
+  const int left = (K % Q_UNIT) >> 5;
+  if (left > 0 && wave == W - 1) {
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    Unit u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int have = left - 4 * h, b = 8 * units + 4 * h + g;  // this lane's block
+      u.w[h] = g < have ? ld16(wp + (size_t)units * (Q_UNIT / 2) + h * 64) : zero;
+      u.sw[h] = g < have ? (uint32_t)sp[b] << (8 * g) : 0u;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int p = 0; p < AP; ++p) {
+          const int piece = FMT == 8 ? 2 * p + (g >> 1) : g;  // its block of the four
+          u.a[m][h].v[p] = piece < have ? ld16(ap[m] + (size_t)units * (Q_UNIT * FMT / 8) + (h * AP + p) * 64) : zero;
+        }
+        u.sa[m][h] = g < have ? (uint32_t)asp[m][b] << (8 * g) : 0u;
+      }
+    }
+    multiply(u);
   }
   wg_reduce<1, MT, W>(acc, red, wave, lane);
   if (wave != 0) return;
@@ -142,22 +167,28 @@ __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue 
 
 // ------------------------------------------------------------------ tiles
 
-template <int FMT, int MT, int NT, int D, bool GATED, class Epilogue>
-__global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
+template <int FMT, int MT, int NT, int WM, int WN, int D, bool GATED, class Epilogue>
+__global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::PER_SIMD))
     tile_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T, int K, int rows, int mtiles, int ntiles,
                   int nsplit) {
-  typedef QLds<FMT, MT, NT, D> L;
-  constexpr int WCOLS = NT * 32 / (GATED ? 2 : 1), HALF = GATED ? NT / 2 : NT, COLS = 2 * WCOLS;
+  typedef QLds<FMT, MT, NT, WM, WN, D> L;
+  constexpr int WCOLS = NT * 32 / (GATED ? 2 : 1), HALF = GATED ? NT / 2 : NT, COLS = WN * WCOLS;
   __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WN, wn = wave % WN;
   const int tile = xcd_tile(blockIdx.x, mtiles * ntiles * nsplit);
-  const int split = tile % nsplit, nt = tile / nsplit % ntiles, mt0 = tile / nsplit / ntiles;
+  // Four rows of tiles together, column by column: the 32 tiles that an XCD has at once then read fewer
+  // rows of both operands than two whole rows of 16 would.
+  const int split = tile % nsplit, id = tile / nsplit, band = id / (4 * ntiles), high = min(4, mtiles - 4 * band);
+  const int mt0 = 4 * band + (id - 4 * band * ntiles) % high, nt = (id - 4 * band * ntiles) / high;
   const int m0 = mt0 * L::BM, n0 = nt * COLS;
   const int stages = (K + Q_KB - 1) / Q_KB, full = K / Q_KB, tail = (K >> 5) & 3;
-  const int st0 = (int)((int64_t)stages * split / nsplit), st1 = (int)((int64_t)stages * (split + 1) / nsplit);
+  // K is split at whole groups of scales
+  const int groups = (stages + Q_GROUP - 1) / Q_GROUP;
+  const int g0 = (int)((int64_t)groups * split / nsplit), g1 = (int)((int64_t)groups * (split + 1) / nsplit);
+  const int st0 = g0 * Q_GROUP, st1 = min(g1 * Q_GROUP, stages);
 
-  // Row lr of the workgroup's 64 NT: row r of MFMA tile lr >> 5, counted from the tile's first row in the
+  // Row lr of the workgroup's weight rows: row r of MFMA tile lr >> 5, counted from the tile's first row in the
   // gate or the up half; past the last row (or token) the last one again, never stored.
   auto weight_half = [&](int lr) { return (size_t)n0 + ((lr >> 5) % NT >= HALF ? (size_t)rows : 0); };
   auto weight_row = [&](int lr) { return min((lr >> 5) / NT * WCOLS + (lr >> 5) % HALF * 32 + (lr & 31), rows - 1 - n0); };
@@ -167,7 +198,7 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
           [&](int) { return o.a + (size_t)m0 * ((size_t)K * FMT / 8); }, token_row);
   typename L::Codes cs;
   cs.init(K >> 1, min(COLS, rows - n0), wave, lane, [&](int lr) { return o.w + weight_half(lr) * (size_t)(K >> 1); }, weight_row);
-  QScales<L::BM, L::BN> sc;
+  QScales<L::BM, L::BN, 64 * WM * WN> sc;
   const size_t ks = (size_t)(K >> 5);
   sc.init(K, K % (Q_KB * Q_GROUP) == 0, [&](int lr) {
     return lr < L::BM ? o.as + (size_t)(m0 + token_row(lr)) * ks
@@ -178,10 +209,25 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
   auto copy = [&](uint8_t* buf, int st, auto Q) __attribute__((always_inline)) {
     constexpr int q = Q;
     if constexpr (q < XC)
-      as.copy_one(buf, st, st < full ? 8 : tail * (FMT / 4), q);
+      as.copy_one(buf, st, q);
     else
-      cs.copy_one(buf + L::Rows::BYTES, st, st < full ? 8 : tail, q - XC);
+      cs.copy_one(buf + L::Rows::BYTES, st, q - XC);
   };
+  // ahead of copies [FROM, FROM + N) of stage st, which is the last to come where it is partial
+  auto prepare = [&](int st, auto FROM, auto N) __attribute__((always_inline)) {
+    if (st != full) return;
+    unrolled<decltype(N)::value>([&](auto Q) __attribute__((always_inline)) {
+      constexpr int q = FROM + Q;
+      if constexpr (q < XC)
+        as.only(tail * (FMT / 4), q);
+      else
+        cs.only(tail, q - XC);
+    });
+  };
+  typedef std::integral_constant<int, 0> FromFirst;
+  typedef std::integral_constant<int, FIRST> FirstOnes;
+  typedef std::integral_constant<int, LOADS - FIRST> OtherOnes;
+  typedef std::integral_constant<int, LOADS> AllOnes;
   const int r = lane & 31, g = lane >> 5;
   constexpr int AF = FMT / 4;  // 16-byte pieces of a fragment
   uint32_t at[2][AF], wat[2];
@@ -202,19 +248,24 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
   tile_zero(acc);
   QFragment<FMT> frag[2][MT];
   u32x4 w[2][NT];
-  uint32_t raw_a[MT], raw_w[NT], sa[2][MT], sw[2][NT];  // a stage's 4 scale bytes; step u's in the low byte
-  auto read_scale = [&](int st, int e) {
-    const uint32_t o2 = (uint32_t)((st >> 2) & 1) * L::SCALES + (st & 3) * 4;
-    if (e < MT)
-      raw_a[e] = *reinterpret_cast<const uint32_t*>(lds + sat + o2 + e * 512);
-    else
-      raw_w[e - MT] = *reinterpret_cast<const uint32_t*>(lds + wsat + o2 + (e - MT) * 512);
+  // A group's scales, a dword a stage; shifted right by 8 g ahead of its stage, so that byte 0 is this
+  // lane's in step 0 and byte 2 in step 1.
+  uint32_t sa[MT][Q_GROUP], sw[NT][Q_GROUP];
+  auto scale_at = [&](int group, int e) {
+    return lds + (group & 1) * L::SCALES + (e < MT ? sat + e * 512 : wsat + (e - MT) * 512);
   };
-  auto take_scale = [&](int u, int e) {
-    if (e < MT)
-      sa[u][e] = raw_a[e] >> (16 * u + 8 * g);
-    else
-      sw[u][e - MT] = raw_w[e - MT] >> (16 * u + 8 * g);
+  auto read_scales = [&](int group, int e) {  // of the first three stages
+    typedef unsigned u32x3 __attribute__((ext_vector_type(3), aligned(16)));
+    const u32x3 v = *reinterpret_cast<const u32x3*>(scale_at(group, e));
+#pragma unroll
+    for (int j = 0; j < 3; ++j) (e < MT ? sa[e][j] : sw[e - MT][j]) = v[j];
+  };
+  auto read_last_scale = [&](int group, int e) {  // whose register the products still read meanwhile
+    (e < MT ? sa[e][3] : sw[e - MT][3]) = *reinterpret_cast<const uint32_t*>(scale_at(group, e) + 12);
+  };
+  auto shift_scale = [&](int stage, int e) {
+    uint32_t& s = e < MT ? sa[e][stage] : sw[e - MT][stage];
+    s >>= 8 * g;
   };
   auto read = [&](const uint8_t* buf, int u, int e) {  // piece e of a step's operands
     if (e < NT)
@@ -225,66 +276,84 @@ __global__ void __launch_bounds__(256, MT == 4 ? 1 : 2)
   constexpr int SLOTS = MT * NT, READS = NT + MT * AF, SCALES = MT + NT;
   auto buffer_of = [&](int i) { return lds + i * L::ONE; };
 
-  // A part of K that starts inside a group of scales takes the next group along: the copies that
-  // follow a later load would be too few for the waits below to cover it.
-  const int group0 = st0 >> 2;
-  sc.load(group0, scales_of(group0));
-  sc.store(scales_of(group0));
-  if ((st0 & 3) != 0 && 4 * (group0 + 1) < st1) {
-    sc.load(group0 + 1, scales_of(group0 + 1));
-    sc.store(scales_of(group0 + 1));
-  }
+  sc.load(g0, scales_of(g0));
+  sc.store(scales_of(g0));
   unrolled<D - 1>([&](auto J) __attribute__((always_inline)) {
-    unrolled<LOADS>([&](auto Q) __attribute__((always_inline)) { copy(buffer_of(J), min(st0 + J, st1 - 1), Q); });
+    const int st = min(st0 + J, st1 - 1);
+    prepare(st, FromFirst{}, AllOnes{});
+    unrolled<LOADS>([&](auto Q) __attribute__((always_inline)) { copy(buffer_of(J), st, Q); });
   });
+  prepare(min(st0 + D - 1, st1 - 1), FromFirst{}, FirstOnes{});
   unrolled<FIRST>([&](auto Q) __attribute__((always_inline)) { copy(buffer_of(D - 1), min(st0 + D - 1, st1 - 1), Q); });
   q_barrier<(D - 2) * LOADS + FIRST>();
 #pragma unroll
-  for (int e = 0; e < SCALES; ++e) read_scale(st0, e);
+  for (int e = 0; e < SCALES; ++e) read_scales(g0, e);
 #pragma unroll
   for (int e = 0; e < READS; ++e) read(lds, 0, e);
 #pragma unroll
-  for (int e = 0; e < SCALES; ++e) take_scale(0, e);
+  for (int e = 0; e < SCALES; ++e) shift_scale(0, e);
+  scales_ready(sa, 0);
+  scales_ready(sw, 0);
+  settle_mfma(acc);  // the accumulators have been cleared
 
   int cur = 0, fill = D - 1;  // buffers of the current stage, and of the one D - 1 stages on
-  for (int st = st0; st < st1; ++st) {
-    const int nxt = cur + 1 == D ? 0 : cur + 1;
-    const int next_group = (st >> 2) + 1;
-    const bool more = 4 * next_group < st1 && (st & ~3) >= st0;
-    if (more && (st & 3) == 0) sc.load(next_group, scales_of(next_group));
-    const int c0 = min(st + D - 1, st1 - 1), c1 = min(st + D, st1 - 1);
-    unrolled<2>([&](auto U) __attribute__((always_inline)) {
-      constexpr int u = U;
-      if constexpr (u == 1) {
-        if (more && (st & 3) == 3) sc.store(scales_of(next_group));
-        // the next stage has landed for every wave, and no wave reads the current one any more
-        q_barrier<(D - 2) * LOADS>();
-      }
-      unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
-        constexpr int k = S, m = k / NT, i = k % NT;
-        mfma_q<FMT>(acc[m][i], w[u][i], frag[u][m], sw[u][i], sa[u][m]);
-        if constexpr (u == 1)
-          unrolled<SCALES>([&](auto E) __attribute__((always_inline)) {
-            if constexpr (E * SLOTS / (2 * SCALES) == k) read_scale(st + 1, E);
+  for (int group = g0; group < g1; ++group) {
+    const bool more = group + 1 < g1;
+    unrolled<Q_GROUP>([&](auto G) __attribute__((always_inline)) {
+      constexpr int stage = G;
+      const int st = group * Q_GROUP + stage;
+      if (st >= st1) return;
+      if (stage == 0 && more) sc.load(group + 1, scales_of(group + 1));
+      const int nxt = cur + 1 == D ? 0 : cur + 1;
+      const int c0 = min(st + D - 1, st1 - 1), c1 = min(st + D, st1 - 1);
+      unrolled<2>([&](auto U) __attribute__((always_inline)) {
+        constexpr int u = U;
+        if constexpr (u == 0) {
+          prepare(c0, FirstOnes{}, OtherOnes{});
+        } else {
+          if (stage == Q_GROUP - 1 && more) sc.store(scales_of(group + 1));
+          // the next stage has landed for every wave (and, at a group's end, the next one's scales, which
+          // three and a half stages of copies follow), and no wave reads the current one any more
+          constexpr int LATER = (D - 2) * LOADS, SINCE = 4 * LOADS - FIRST;
+          q_barrier<(stage == Q_GROUP - 1 && SINCE < LATER ? SINCE : LATER)>();
+          prepare(c1, FromFirst{}, FirstOnes{});
+        }
+        unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
+          constexpr int k = S, m = k / NT, i = k % NT;
+          mfma_q<u>(acc[m][i], w[u][i], frag[u][m], sw[i][stage], sa[m][stage]);
+          // the next step's operands, in the first half
+          constexpr bool first_three = u == 1 && stage == Q_GROUP - 1, last = u == 0 && stage == 0;
+          constexpr int RS = first_three || last ? SCALES : 0, HALF_SLOTS = (SLOTS + 1) / 2;
+          unrolled<RS + READS>([&](auto E) __attribute__((always_inline)) {
+            if constexpr (E * HALF_SLOTS / (RS + READS) == k) {
+              if constexpr (E < READS)
+                read(buffer_of(u == 0 ? cur : nxt), 1 - u, E);
+              else if constexpr (first_three)
+                read_scales(group + 1, E - READS);
+              else
+                read_last_scale(group, E - READS);
+            }
           });
-        unrolled<READS>([&](auto E) __attribute__((always_inline)) {
-          if constexpr (E * SLOTS / READS == k) read(buffer_of(u == 0 ? cur : nxt), 1 - u, E);
+          if constexpr (u == 1 && k == SLOTS - 1)
+            unrolled<SCALES>([&](auto E) __attribute__((always_inline)) { shift_scale((stage + 1) % Q_GROUP, E); });
+          unrolled<LOADS>([&](auto E) __attribute__((always_inline)) {
+            if constexpr (u == 1 && E < FIRST && E * SLOTS / FIRST == k) copy(buffer_of(cur), c1, E);
+            if constexpr (u == 0 && E >= FIRST && (E - FIRST) * SLOTS / (LOADS - FIRST) == k) copy(buffer_of(fill), c0, E);
+          });
+          keep_order();
         });
-        unrolled<SCALES>([&](auto E) __attribute__((always_inline)) {
-          if constexpr (SLOTS / 2 + E * (SLOTS - SLOTS / 2) / SCALES == k) take_scale(1 - u, E);
-        });
-        unrolled<LOADS>([&](auto E) __attribute__((always_inline)) {
-          if constexpr (u == 1 && E < FIRST && E * SLOTS / FIRST == k) copy(buffer_of(cur), c1, E);
-          if constexpr (u == 0 && E >= FIRST && (E - FIRST) * SLOTS / (LOADS - FIRST) == k) copy(buffer_of(fill), c0, E);
-        });
-        keep_order();
+        if constexpr (u == 1) {
+          scales_ready(sa, (stage + 1) % Q_GROUP);
+          scales_ready(sw, (stage + 1) % Q_GROUP);
+        }
       });
+      fill = cur;
+      cur = nxt;
     });
-    fill = cur;
-    cur = nxt;
   }
+  settle_mfma(acc);
   wait_copies();  // the repeated copies of the last stages: the LDS is used again
-  tile_output<MT, NT, 2, 2, GATED, L::BYTES>(acc, epi, parts, lds, T, rows, m0, n0, split, nsplit, wave, lane);
+  tile_output<MT, NT, WM, WN, GATED, L::BYTES, (WM * WN > 4 ? 1 : 0)>(acc, epi, parts, lds, T, rows, m0, n0, split, nsplit, wave, lane);
 }
 
 // ------------------------------------------------------------------ launch plans
@@ -306,7 +375,8 @@ TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool qua
     p.mtiles = (int)((T + bm - 1) / bm);
     p.ntiles = (int)((rows + cols - 1) / cols);
     const int64_t stages = (K + Q_KB - 1) / Q_KB;
-    p.nsplit = (int)tile_split((int64_t)p.mtiles * p.ntiles, stages, false);
+    const int64_t groups = (stages + Q_GROUP - 1) / Q_GROUP;
+    p.nsplit = (int)std::max<int64_t>(1, std::min(GPU_CUS / ((int64_t)p.mtiles * p.ntiles), groups));
     parts = p.nsplit > 1;
   }
   if (parts) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows) * (gated ? 2 : 1) * 4;
@@ -320,9 +390,9 @@ static int launch_product_q(const QOperands& o, const Epilogue& epi, bool quanti
   float* parts = p.bytes ? static_cast<float*>(workspace) : nullptr;
   if (takes_stream_q(T)) {
     const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
-    const int items = (rows + cols - 1) / cols, steps = (K + 127) / 128;
+    const int items = (rows + cols - 1) / cols, units = K / Q_UNIT;
     int W = 1;
-    while (W < 8 && 2 * W <= steps && 2 * W * items <= 2048) W *= 2;
+    while (W < 8 && 2 * W <= units && 2 * W * items <= 2048) W *= 2;
 #define MX_STREAM_Q(WW, M) \
   hipLaunchKernelGGL((stream_q_kernel<FMT, WW, M, GATED, Epilogue>), dim3(items), dim3(WW * 64), 0, stream, o, epi, parts, T, K, rows)
 #define MX_STREAM_Q_W(WW) \
@@ -343,15 +413,18 @@ static int launch_product_q(const QOperands& o, const Epilogue& epi, bool quanti
 #undef MX_STREAM_Q
   } else {
     const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE_Q(MT, NT)                                                                                        \
-  hipLaunchKernelGGL((tile_q_kernel<FMT, MT, NT, FMT == 8 ? 3 : 4, GATED, Epilogue>), grid, dim3(256), 0, stream, o, epi, \
+#define MX_TILE_Q(MT, NT, WM, WN, D)                                                                                   \
+  hipLaunchKernelGGL((tile_q_kernel<FMT, MT, NT, WM, WN, D, GATED, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, o, epi,     \
                      p.nsplit > 1 ? parts : nullptr, T, K, rows, p.mtiles, p.ntiles, p.nsplit)
+    const bool alone = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS;  // a workgroup has its CU's LDS
     if (p.mt == 4)
-      MX_TILE_Q(4, 4);
+      MX_TILE_Q(2, 4, 4, 2, (FMT == 8 ? 3 : 4));
+    else if (p.mt == 2 && alone)
+      MX_TILE_Q(1, 2, 4, 2, (FMT == 8 ? 6 : 8));
     else if (p.mt == 2)
-      MX_TILE_Q(2, 2);
+      MX_TILE_Q(2, 2, 2, 2, (FMT == 8 ? 3 : 4));
     else
-      MX_TILE_Q(1, 2);
+      MX_TILE_Q(1, 2, 2, 2, (FMT == 8 ? 6 : 8));
 #undef MX_TILE_Q
   }
   if (parts) {

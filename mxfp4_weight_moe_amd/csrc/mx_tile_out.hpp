@@ -14,8 +14,9 @@ __host__ __device__ static inline int part_cols(int rows) { return (rows + 7) / 
 // by 32 weight rows each; for gate_up the first half of them gate rows, the second half the up rows
 // of the same columns.  m0, n0: the workgroup's first token and output column.  nsplit > 1: part
 // `split` of the reduction goes to parts[split] as fp32 [T][part columns (x 2)].  LDS_BYTES of `lds`
-// are free once every wave is here.
-template <int MT, int NT, int WM, int WN, bool GATED, int LDS_BYTES, class Epilogue>
+// are free once every wave is here.  ROWS_AT_ONCE: rows of MFMA tiles through the LDS at a time (0: two,
+// or the one there is).
+template <int MT, int NT, int WM, int WN, bool GATED, int LDS_BYTES, int ROWS_AT_ONCE = 0, class Epilogue>
 __device__ __forceinline__ void tile_output(const f32x16 (&acc)[MT][NT], const Epilogue& epi, float* __restrict__ parts,
                                             uint8_t* lds, int T, int rows, int m0, int n0, int split, int nsplit,
                                             int wave, int lane) {
@@ -25,7 +26,7 @@ __device__ __forceinline__ void tile_output(const f32x16 (&acc)[MT][NT], const E
   // MB rows of MFMA tiles at a time through the LDS; then row by row, PIECES lanes a row with 8
   // columns each, so a lane has the same columns in all its rows.  U rows of a lane go
   // together, and what the next ones read (the residual) is fetched meanwhile.
-  constexpr int MB = MT < 2 ? 1 : 2;
+  constexpr int MB = ROWS_AT_ONCE ? ROWS_AT_ONCE : MT < 2 ? 1 : 2;
   static_assert(WM * WN * MB * NT * 4096 <= LDS_BYTES, "results of all waves in the stages' LDS");
   uint8_t* mine = lds + wave * (MB * NT * 4096);
   constexpr int PIECES = WCOLS / 8, ROWS = 64 / PIECES, ITERS = MB * 32 / ROWS, U = ITERS < 4 ? ITERS : 4;

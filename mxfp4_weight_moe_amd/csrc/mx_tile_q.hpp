@@ -2,7 +2,7 @@
 // neither side is decoded, both go from memory to the LDS by buffer loads and from there into the
 // operand registers as they are stored.
 //
-// A workgroup of 2 x 2 waves owns 64 MT tokens by 64 NT weight rows; a wave holds MT x NT tiles of
+// A workgroup of WM x WN waves owns 32 WM MT tokens by 32 WN NT weight rows; a wave holds MT x NT tiles of
 // v_mfma_scale_f32_32x32x64_f8f6f4 (weights are its rows, tokens its columns).  Lane (r = lane & 31,
 // g = lane >> 5) of an instruction over 64 values (two blocks) gives
 //   E2M1: the 32 values of block g, 16 bytes;
@@ -59,22 +59,26 @@ struct QStage {
       off[q] = (uint32_t)row_of(first + lane / C) * (uint32_t)row_bytes + chunk * 16;
     }
   }
-  // chunks: how many of a row's chunks exist in this stage; the others become zeros
-  __device__ __forceinline__ void copy_one(uint8_t* lds, int stage, int chunks, int q) const {
-    copy16_to_lds(buf_[q], chunk < chunks ? off[q] : Q_NOWHERE, (uint32_t)stage * RB, lds + (q * NW + wave) * 1024);
+  __device__ __forceinline__ void copy_one(uint8_t* lds, int stage, int q) const {
+    copy16_to_lds(buf_[q], off[q], (uint32_t)stage * RB, lds + (q * NW + wave) * 1024);
+  }
+  // Before the copies of the last, partial stage: `chunks` of a row's exist there, the others become zeros.
+  __device__ __forceinline__ void only(int chunks, int q) {
+    if (chunk >= chunks) off[q] = Q_NOWHERE;
   }
 };
 
 // D: stages in the LDS.
-template <int FMT, int MT, int NT, int D>
+template <int FMT, int MT, int NT, int WM, int WN, int D>
 struct QLds {
-  static constexpr int NW = 4, BM = 64 * MT, BN = 64 * NT;
+  static constexpr int NW = WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
   static constexpr int ARB = Q_KB * FMT / 8, WRB = Q_KB / 2;  // bytes of a stage of a row
   typedef QStage<BM, ARB, NW> Rows;
   typedef QStage<BN, WRB, NW> Codes;
   static constexpr int ONE = Rows::BYTES + Codes::BYTES;
   static constexpr int SCALES_AT = D * ONE, SCALES = (BM + BN) * 16;
   static constexpr int BYTES = SCALES_AT + 2 * SCALES;
+  static constexpr int PER_SIMD = NW / 4 * (BYTES > 81920 ? 1 : 2);  // waves
 };
 
 template <int FMT>
@@ -88,18 +92,38 @@ __device__ __forceinline__ i32x8 q_operand(const QFragment<4>& f) {
   return i32x8{(int)f.v[0][0], (int)f.v[0][1], (int)f.v[0][2], (int)f.v[0][3], 0, 0, 0, 0};
 }
 
-// acc += w x a over 64 values; the scales are the low bytes of sw and sa.
-template <int FMT>
-__device__ __forceinline__ void mfma_q(f32x16& acc, const u32x4& w, const QFragment<FMT>& a, uint32_t sw, uint32_t sa) {
-  const i32x8 wo = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-  acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wo, q_operand(a), acc, 4, FMT == 8 ? 0 : 4, 0, (int)sw, 0, (int)sa);
+// acc += w x a over 64 values in place; the scales are byte 2 U of sw and sa.  As an instruction of our own:
+// the compiler moves products that it knows past the barrier, away from the reads and copies that they
+// should run beside.  It keeps no distances for it either: see settle_mfma, and scales_ready for the scales,
+// which vector instructions write (the codes come from the LDS, for which the compiler waits).
+template <int U>
+__device__ __forceinline__ void mfma_q(f32x16& acc, const u32x4& w, const QFragment<8>& a, uint32_t sw, uint32_t sa) {
+  const i32x8 v = __builtin_bit_cast(i32x8, __builtin_shufflevector(a.v[0], a.v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+  asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[%5,%5,0] cbsz:4"
+               : "+a"(acc) : "v"(w), "v"(v), "v"(sw), "v"(sa), "n"(U));
+}
+template <int U>
+__device__ __forceinline__ void mfma_q(f32x16& acc, const u32x4& w, const QFragment<4>& a, uint32_t sw, uint32_t sa) {
+  asm volatile("v_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 op_sel_hi:[%5,%5,0] cbsz:4 blgp:4"
+               : "+a"(acc) : "v"(w), "v"(a.v[0]), "v"(sw), "v"(sa), "n"(U));
+}
+// Two wait states between the last of these scales' shifts and a product.
+template <int N, int M>
+__device__ __forceinline__ void scales_ready(uint32_t (&s)[N][M], int m) {
+  static_assert(N == 1 || N == 2 || N == 4, "tiles of a wave");
+  if constexpr (N == 1)
+    asm volatile("s_nop 1" : "+v"(s[0][m]));
+  else if constexpr (N == 2)
+    asm volatile("s_nop 1" : "+v"(s[0][m]), "+v"(s[1][m]));
+  else
+    asm volatile("s_nop 1" : "+v"(s[0][m]), "+v"(s[1][m]), "+v"(s[2][m]), "+v"(s[3][m]));
 }
 
 // Scales of 512 values of a workgroup's BM + BN rows, 16 bytes each, into the LDS.  Rows that start at
 // multiples of 16 bytes go there directly, others through registers.
-template <int BM, int BN>
+template <int BM, int BN, int THREADS>
 struct QScales {
-  static constexpr int ROWS = BM + BN, EACH = (ROWS + 255) / 256;
+  static constexpr int ROWS = BM + BN, EACH = (ROWS + THREADS - 1) / THREADS;
   const uint8_t* row[EACH];  // this thread's rows
   u32x4 held[EACH];
   int bytes;                 // of a row
@@ -109,7 +133,7 @@ struct QScales {
   __device__ __forceinline__ void init(int K, bool direct_, F row_of) {
     bytes = K >> 5, direct = direct_;
 #pragma unroll
-    for (int i = 0; i < EACH; ++i) row[i] = row_of(min((int)threadIdx.x + 256 * i, ROWS - 1));
+    for (int i = 0; i < EACH; ++i) row[i] = row_of(min((int)threadIdx.x + THREADS * i, ROWS - 1));
   }
   // Starts group `g`; past the end of a row zeros (2^-127; the codes there are zero too).
   __device__ __forceinline__ void load(int g, uint8_t* lds) {
@@ -118,9 +142,9 @@ struct QScales {
       const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 #pragma unroll
       for (int i = 0; i < EACH; ++i)
-        if (256 * i + wave * 64 < ROWS)
+        if (THREADS * i + wave * 64 < ROWS)
           __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(row[i] + at),
-                                           (lds_ptr)(lds + (256 * i + wave * 64) * 16), 16, 0, 0);
+                                           (lds_ptr)(lds + (THREADS * i + wave * 64) * 16), 16, 0, 0);
       return;
     }
 #pragma unroll
@@ -145,7 +169,7 @@ struct QScales {
     if (direct) return;
 #pragma unroll
     for (int i = 0; i < EACH; ++i)
-      if ((int)threadIdx.x + 256 * i < ROWS) *reinterpret_cast<u32x4*>(lds + (threadIdx.x + 256 * i) * 16) = held[i];
+      if ((int)threadIdx.x + THREADS * i < ROWS) *reinterpret_cast<u32x4*>(lds + (threadIdx.x + THREADS * i) * 16) = held[i];
   }
 };
 
