@@ -198,6 +198,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&v)[V], boo
 // y = residual + scale * act(z + bias); optionally the biased z itself.  y may be the
 // residual: each element is read before it is written, by the same lane.
 struct LinearEpilogue {
+  static constexpr bool WHOLE_BLOCKS = false;
   const uint16_t* bias;      // [N] or null
   const uint16_t* residual;  // [T, N] or null
   uint16_t* y;               // [T, N]

@@ -194,7 +194,7 @@ int launch_norm_residual_backward(const uint16_t* dy, const uint16_t* dxn, const
 int launch_quantize(const void* x, bool f32, int format, int64_t rows, int64_t K, uint8_t* codes, uint8_t* scales,
                     uint16_t* values, hipStream_t stream);
 // quantized: gate_up's output is
-TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool quantized);
+TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool quantized, int format);
 int launch_linear_quantized(const uint8_t* a, const uint8_t* as, int format, const uint8_t* w, const uint8_t* s,
                             const uint16_t* bias, const uint16_t* residual, float scale, int act, uint16_t* y,
                             uint16_t* z, int T, int K, int N, void* workspace, hipStream_t stream);

@@ -3,8 +3,9 @@
 //   gate_up  h = act(a Wg^T + bg) * (a Wu^T + bu)     (gate rows [0, I), up rows [I, 2I) of W)
 // a in MXFP8 or MXFP4, W in MXFP4, fp32 sums; h in bf16, or quantized again from its fp32 value.
 //
-// Two kernels, by the number of tokens: up to STREAM_Q_MAX_T the weights are streamed once, a
-// workgroup to 16 weight rows (stream_q_kernel); beyond, tiles (mx_tile_q.hpp).
+// Three kernels, by the number of tokens: up to 16 (32 where thin tiles do not apply) the weights are
+// streamed once, a workgroup to 16 weight rows (stream_q_kernel); up to 64 a workgroup has all tokens and 32 or
+// 64 weight rows, its waves splitting K (thin_q_kernel); beyond, tiles (mx_tile_q.hpp).
 #include "mx_grid.hpp"
 #include "mx_tile_out.hpp"
 #include "mx_tile_q.hpp"
@@ -356,27 +357,194 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   tile_output<MT, NT, WM, WN, GATED, L::BYTES, (WM * WN > 4 ? 1 : 0)>(acc, epi, parts, lds, T, rows, m0, n0, split, nsplit, wave, lane);
 }
 
+// ------------------------------------------------------------------ up to 64 tokens: thin tiles
+
+// A workgroup takes 32 NT weight rows (gate_up: half of them gate rows, half the up rows of the same
+// columns) and all tokens; a wave 32 tokens and one of KS parts of K.  A wave copies what it needs into a ring
+// of its own in the LDS, no barriers in the loop; the parts' sums meet in the LDS.
+constexpr int THIN_Q_MAX_T = 64;
+template <int FMT, int NT>
+struct ThinQStage {
+  static constexpr int ARB = Q_KB * FMT / 8, A = 32 * ARB, CODES = 32 * NT * (Q_KB / 2);
+  static constexpr int SCALES_A = A + CODES, SCALES_W = SCALES_A + 256, BYTES = SCALES_W + 256;
+  static constexpr int D = 163840 / 8 / BYTES < 4 ? 163840 / 8 / BYTES : 4;  // stages in the ring of each of 8 waves
+  static constexpr int LOADS = A / 1024 + CODES / 1024 + 2;
+  static_assert(D >= 2 && D * BYTES >= NT * 4096 && (D - 1) * LOADS < 64, "a ring, also of a wave's sums");
+};
+
+template <int FMT, int NT, bool GATED, int KS, class Epilogue>
+__global__ void __launch_bounds__(512, 2) thin_q_kernel(QOperands o, Epilogue epi, int T, int K, int rows) {
+  typedef ThinQStage<FMT, NT> L;
+  constexpr int COLS = GATED ? 16 * NT : 32 * NT, D = L::D;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[8 * D * L::BYTES];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int n0 = blockIdx.x * COLS, m0 = wave / KS * 32;
+  const int stages = K / Q_KB, st0 = stages * (wave % KS) / KS, st1 = stages * (wave % KS + 1) / KS;
+  uint8_t* ring = lds + wave * (D * L::BYTES);
+
+  // Tokens and rows past the last: the last one again.
+  const int ka = K * FMT / 8;
+  constexpr int AC = L::ARB / 16, APER = 64 / AC, ACOPIES = 32 / APER, WCOPIES = 2 * NT;
+  const buffer abuf = make_buffer(o.a + (size_t)m0 * ka, (uint64_t)min(32, T - m0) * (uint64_t)ka);
+  const buffer asbuf = make_buffer(o.as + (size_t)m0 * (K >> 5), (uint64_t)min(32, T - m0) * (uint64_t)(K >> 5));
+  uint32_t aoff[ACOPIES];
+#pragma unroll
+  for (int q = 0; q < ACOPIES; ++q) {
+    const int r = q * APER + lane / AC;
+    aoff[q] = (uint32_t)min(r, T - 1 - m0) * (uint32_t)ka + (((lane % AC) ^ q_key<L::ARB>(r)) << 4);
+  }
+  const uint32_t asoff = (uint32_t)min(lane & 31, T - 1 - m0) * (uint32_t)(K >> 5);
+  // Row lr of the 32 NT: weight row n0 + lr, or column n0 + lr % COLS of half lr / COLS.
+  auto half_of = [&](int lr) { return (size_t)n0 + (GATED && lr >= COLS ? (size_t)rows : 0); };
+  auto row_of = [&](int lr) { return min(lr % COLS, rows - 1 - n0); };
+  const int have = min(COLS, rows - n0);
+  buffer wbuf[WCOPIES];
+  uint32_t woff[WCOPIES];
+#pragma unroll
+  for (int q = 0; q < WCOPIES; ++q) {
+    const int r = q * 16 + (lane >> 2);
+    wbuf[q] = make_buffer(o.w + half_of(q * 16) * (size_t)(K >> 1), (uint64_t)have * (uint64_t)(K >> 1));
+    woff[q] = (uint32_t)row_of(r) * (uint32_t)(K >> 1) + (((lane & 3) ^ q_key<64>(r)) << 4);
+  }
+  const uint8_t* wscale = o.ws + (half_of(lane & (32 * NT - 1)) + row_of(lane & (32 * NT - 1))) * (size_t)(K >> 5);
+  auto load = [&](int st, uint8_t* buf) {
+#pragma unroll
+    for (int q = 0; q < ACOPIES; ++q) copy16_to_lds(abuf, aoff[q], (uint32_t)st * L::ARB, buf + q * 1024);
+#pragma unroll
+    for (int q = 0; q < WCOPIES; ++q) copy16_to_lds(wbuf[q], woff[q], (uint32_t)st * 64, buf + L::A + q * 1024);
+    copy4_to_lds(asbuf, asoff, (uint32_t)st * 4, buf + L::SCALES_A);
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(wscale + st * 4),
+                                     (lds_ptr)(buf + L::SCALES_W), 4, 0, 0);
+  };
+  const int r = lane & 31, g = lane >> 5;
+  f32x16 acc[NT] = {};
+  int at = 0;
+#pragma unroll
+  for (int d = 0; d < D; ++d)
+    if (st0 + d < st1) load(st0 + d, ring + d * L::BYTES);
+  for (int st = st0; st < st1; ++st) {
+    // this stage has landed; up to D - 1 later ones are under way
+    const int later = st1 - 1 - st;
+    if (later >= D - 1)
+      wait_copies<(D - 1) * L::LOADS>();
+    else if (D > 2 && later == D - 2)
+      wait_copies<(D - 2) * L::LOADS>();
+    else if (D > 3 && later == D - 3)
+      wait_copies<(D - 3) * L::LOADS>();
+    else
+      wait_copies();
+    uint8_t* buf = ring + at * L::BYTES;
+    QFragment<FMT> a[2];
+    u32x4 w[2][NT];
+    uint32_t sw[NT];
+    const uint32_t sa = *reinterpret_cast<const uint32_t*>(buf + L::SCALES_A + r * 4) >> (8 * g);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sw[i] = *reinterpret_cast<const uint32_t*>(buf + L::SCALES_W + (i * 32 + r) * 4) >> (8 * g);
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+      for (int p = 0; p < FMT / 4; ++p) {
+        const int c = FMT == 8 ? 4 * u + 2 * p + g : 2 * u + g;
+        a[u].v[p] = ld16(buf + r * L::ARB + ((c ^ q_key<L::ARB>(r)) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < NT; ++i) w[u][i] = ld16(buf + L::A + (i * 32 + r) * 64 + (((2 * u + g) ^ q_key<64>(r)) << 4));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read: the buffer may be filled again
+    if (st + D < st1) load(st + D, buf);
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      const i32x8 w0 = {(int)w[0][i][0], (int)w[0][i][1], (int)w[0][i][2], (int)w[0][i][3], 0, 0, 0, 0};
+      const i32x8 w1 = {(int)w[1][i][0], (int)w[1][i][1], (int)w[1][i][2], (int)w[1][i][3], 0, 0, 0, 0};
+      acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w0, q_operand(a[0]), acc[i], 4, FMT == 8 ? 0 : 4, 0, (int)sw[i], 0, (int)sa);
+      acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w1, q_operand(a[1]), acc[i], 4, FMT == 8 ? 0 : 4, 2, (int)sw[i], 2, (int)sa);
+    }
+    at = at + 1 == D ? 0 : at + 1;
+  }
+  wait_copies();
+  tile_to_lds<NT>(ring, acc, lane);
+  // each of the KS waves sums its share of the rows
+  constexpr int PIECES = COLS / 8, ROWS = 64 / PIECES, SHARE = 32 / KS, ITERS = (SHARE + ROWS - 1) / ROWS;
+  const int p = lane % PIECES, n = n0 + p * 8;
+  const auto cols = epi.template columns<8>(n);
+  const uint8_t* first = lds + wave / KS * KS * (D * L::BYTES);
+  __syncthreads();
+#pragma unroll
+  for (int it = 0; it < ITERS; ++it) {
+    const int row = it * ROWS + lane / PIECES + wave % KS * SHARE, t = m0 + row;
+    if (t >= T || n >= rows || (ROWS > SHARE && lane / PIECES >= SHARE)) continue;
+    f32x4 q[GATED ? 4 : 2];
+#pragma unroll
+    for (int j = 0; j < (GATED ? 4 : 2); ++j) {
+      const uint32_t from = out_at<NT>(row, 2 * p + (j & 1) + (j >> 1) * (4 * NT));
+      q[j] = *reinterpret_cast<const f32x4*>(first + from);
+#pragma unroll
+      for (int k = 1; k < KS; ++k) q[j] += *reinterpret_cast<const f32x4*>(first + k * (D * L::BYTES) + from);
+    }
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = q[j >> 2][j & 3];
+    if constexpr (GATED) {
+      float u[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) u[j] = q[2 + (j >> 2)][j & 3];
+      epi.template store<8>(t, n, v, u, cols);
+    } else {
+      epi.template store<8>(t, n, v, cols, epi.template fetch<8>(t, n));
+    }
+  }
+}
+
 // ------------------------------------------------------------------ launch plans
 
-static bool takes_stream_q(int64_t T) { return T <= STREAM_Q_MAX_T; }
+// Thin tiles copy a stage's scales as dwords: whole groups of them, whose rows are aligned.  From 33 tokens
+// on they read the weights twice and a long reduction goes to tiles (64 tokens in MXFP8: 2048 -> 7168 6.8 us,
+// with tiles 14.4; 7168 -> 4096 16.4 and 13.2).
+static bool takes_thin_q(int64_t T, int64_t K) {
+  return T > 16 && T <= (K <= 4096 ? THIN_Q_MAX_T : 32) && K % (Q_KB * Q_GROUP) == 0;
+}
+static bool takes_stream_q(int64_t T, int64_t K) { return T <= STREAM_Q_MAX_T && !takes_thin_q(T, K); }
+
+// What a round of tiles takes, of 256 x 256 (one a CU) and of 128 x 128 (two a CU), in microseconds at a
+// reduction of 7168: MXFP8 92 and 58, MXFP4 70 and 50 (4096 and 2048 tokens, 7168 -> 4096).  E.g. 2048
+// tokens take 69 and 58 with the large tiles for 58 and 50 with the small ones, 4096 tokens 92 and 70 for 114
+// and 96.
+constexpr int Q8_ROUND_256 = 92, Q8_ROUND_128 = 58, Q4_ROUND_256 = 70, Q4_ROUND_128 = 50;
 
 // quantized: the product's output is, which a workgroup of the streaming kernel, with fewer columns
 // than a block, leaves to a second launch.
-TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool quantized) {
+TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool quantized, int format) {
   TilePlan p{};
   p.nsplit = 1;
+  if (takes_thin_q(T, K)) {
+    // 64 rows a workgroup where an output block needs them, or 32 would give more workgroups than CUs
+    const int64_t ones = (rows + (gated ? 15 : 31)) / (gated ? 16 : 32);
+    p.thin = quantized || ones > GPU_CUS ? 2 : 1;
+    p.ntiles = (int)((ones + p.thin - 1) / p.thin);
+    return p;
+  }
   bool parts = quantized;
-  if (!takes_stream_q(T)) {
-    const int64_t cols_all = rows * (gated ? 2 : 1);
-    const int64_t large = ((T + 255) / 256) * ((cols_all + 255) / 256);
-    p.mt = T <= 64 ? 1 : large >= GPU_CUS / 2 ? 4 : 2;
-    p.nt = p.mt == 4 ? 4 : 2;
-    const int bm = 64 * p.mt, cols = (gated ? 32 : 64) * p.nt;
+  if (!takes_stream_q(T, K)) {
+    const bool eight = format == MX_FORMAT_MXFP8;
+    p.mt = T <= 64 ? 1 : tile_choice(T, rows * (gated ? 2 : 1), eight ? Q8_ROUND_256 : Q4_ROUND_256, eight ? Q8_ROUND_128 : Q4_ROUND_128);
+    const int64_t bm = 64 * p.mt, all = rows * (gated ? 2 : 1), groups = (K + Q_KB * Q_GROUP - 1) / (Q_KB * Q_GROUP);
     p.mtiles = (int)((T + bm - 1) / bm);
-    p.ntiles = (int)((rows + cols - 1) / cols);
-    const int64_t stages = (K + Q_KB - 1) / Q_KB;
-    const int64_t groups = (stages + Q_GROUP - 1) / Q_GROUP;
-    p.nsplit = (int)std::max<int64_t>(1, std::min(GPU_CUS / ((int64_t)p.mtiles * p.ntiles), groups));
+    p.nt = p.mt == 4 ? 4 : 2;
+    auto tiles = [&](int64_t nt) { return (all + 64 * nt - 1) / (64 * nt) * p.mtiles; };
+    if (p.mt < 4 && tiles(2) <= GPU_CUS) {
+      // Fewer tiles than CUs: 128 or 64 weight rows a tile, K whole or in parts, by what a workgroup reads
+      // (a CU's read path gives some 50 kB a microsecond) and what parts cost (written at 3 and read at
+      // 4 MB a microsecond, 2.5 for the second launch).  7168 -> 4096 in MXFP8: 128 tokens 16.6 us with 64 rows in 4
+      // parts, 19.3 with 128 rows in 8; 2048 -> 7168, 128 tokens: 10.5 with 64 rows whole, 19.4 with 128 in 4.
+      double least = 0;
+      for (int nt = 2; nt >= 1; --nt)
+        for (int64_t split = 1; split <= groups && split * tiles(nt) <= GPU_CUS; ++split) {
+          const double read = (double)K * (bm * (eight ? 1.0 : 0.5) + 32.0 * nt) / (double)split / 50e3;
+          const double cost = read + (split > 1 ? 2.5 + 4.0 * (double)(split * T * all) * (1 / 3e6 + 1 / 4e6) : 0.0);
+          if (least == 0 || cost < least) least = cost, p.nt = nt, p.nsplit = (int)split;
+        }
+    }
+    p.ntiles = (int)(tiles(p.nt) / p.mtiles);
     parts = p.nsplit > 1;
   }
   if (parts) p.bytes = (size_t)p.nsplit * T * part_cols((int)rows) * (gated ? 2 : 1) * 4;
@@ -386,9 +554,23 @@ TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool qua
 template <int FMT, bool GATED, class Epilogue>
 static int launch_product_q(const QOperands& o, const Epilogue& epi, bool quantized, void* workspace, int T, int K,
                             int rows, hipStream_t stream) {
-  const TilePlan p = quantized_plan(T, K, rows, GATED, quantized);
+  const TilePlan p = quantized_plan(T, K, rows, GATED, quantized, FMT == 8 ? MX_FORMAT_MXFP8 : MX_FORMAT_MXFP4);
   float* parts = p.bytes ? static_cast<float*>(workspace) : nullptr;
-  if (takes_stream_q(T)) {
+  if (p.thin) {
+#define MX_THIN_Q(NT, KS) \
+  hipLaunchKernelGGL((thin_q_kernel<FMT, NT, GATED, KS, Epilogue>), dim3(p.ntiles), dim3(512), 0, stream, o, epi, T, K, rows)
+    if constexpr (!Epilogue::WHOLE_BLOCKS) {  // those have p.thin == 2
+      if (p.thin == 1 && T <= 32)
+        MX_THIN_Q(1, 8);
+      else if (p.thin == 1)
+        MX_THIN_Q(1, 4);
+    }
+    if (p.thin == 2 && T <= 32)
+      MX_THIN_Q(2, 8);
+    else if (p.thin == 2)
+      MX_THIN_Q(2, 4);
+#undef MX_THIN_Q
+  } else if (takes_stream_q(T, K)) {
     const int cols = GATED ? SUB_ROWS / 2 : SUB_ROWS;
     const int items = (rows + cols - 1) / cols, units = K / Q_UNIT;
     int W = 1;
@@ -413,16 +595,20 @@ static int launch_product_q(const QOperands& o, const Epilogue& epi, bool quanti
 #undef MX_STREAM_Q
   } else {
     const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE_Q(MT, NT, WM, WN, D)                                                                                   \
-  hipLaunchKernelGGL((tile_q_kernel<FMT, MT, NT, WM, WN, D, GATED, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, o, epi,     \
-                     p.nsplit > 1 ? parts : nullptr, T, K, rows, p.mtiles, p.ntiles, p.nsplit)
+#define MX_TILE_Q(MT, NT, WM, WN, D)                                                                                 \
+  hipLaunchKernelGGL((tile_q_kernel<FMT, MT, NT, WM, WN, D, GATED, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, o, \
+                     epi, p.nsplit > 1 ? parts : nullptr, T, K, rows, p.mtiles, p.ntiles, p.nsplit)
     const bool alone = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS;  // a workgroup has its CU's LDS
     if (p.mt == 4)
       MX_TILE_Q(2, 4, 4, 2, (FMT == 8 ? 3 : 4));
+    else if (p.mt == 2 && p.nt == 1)
+      MX_TILE_Q(1, 2, 4, 1, (FMT == 8 ? 6 : 8));
     else if (p.mt == 2 && alone)
       MX_TILE_Q(1, 2, 4, 2, (FMT == 8 ? 6 : 8));
     else if (p.mt == 2)
-      MX_TILE_Q(2, 2, 2, 2, (FMT == 8 ? 3 : 4));
+      MX_TILE_Q(1, 2, 4, 2, (FMT == 8 ? 3 : 4));
+    else if (p.nt == 1)
+      MX_TILE_Q(1, 2, 2, 1, (FMT == 8 ? 6 : 8));
     else
       MX_TILE_Q(1, 2, 2, 2, (FMT == 8 ? 6 : 8));
 #undef MX_TILE_Q

@@ -11,6 +11,12 @@ bool format_ok(int f) { return f == MX_FORMAT_MXFP8 || f == MX_FORMAT_MXFP4; }
 // Whole 16 bytes of scales go to the LDS at once where rows begin at multiples of them.
 bool q_scales_aligned(const uint8_t* s, int64_t K) { return K % 512 != 0 || aligned(s, 16); }
 
+// For either format: sizes alone say how large a workspace is.
+size_t linear_bytes(int64_t T, int64_t K, int64_t N) {
+  return std::max(quantized_plan(T, K, N, false, false, MX_FORMAT_MXFP8).bytes,
+                  quantized_plan(T, K, N, false, false, MX_FORMAT_MXFP4).bytes);
+}
+
 // What both routing calls share.
 int route_args(const void* logits, int logits_type, int score, float scale, int64_t T, int64_t E, int64_t k) {
   if (T < 1 || T > MAX_T || E < 1 || E > MX_MAX_EXPERTS || k < 1 || k > MX_MAX_TOPK || k > E) return MX_ERR_SHAPE;
@@ -51,7 +57,7 @@ int mx_norm_residual_quantize(const uint16_t* x, const uint16_t* b, const uint16
 }
 
 size_t mx_linear_quantized_workspace_size(int64_t T, int64_t K, int64_t N) {
-  return sizes_ok(T, K, N) ? quantized_plan(T, K, N, false, false).bytes : 0;
+  return sizes_ok(T, K, N) ? linear_bytes(T, K, N) : 0;
 }
 
 int mx_linear_quantized(const uint8_t* a_codes, const uint8_t* a_scales, int format, const uint8_t* w_codes,
@@ -65,14 +71,18 @@ int mx_linear_quantized(const uint8_t* a_codes, const uint8_t* a_scales, int for
       !opt_aligned(residual, 16) || !opt_aligned(z, 16) || !q_scales_aligned(a_scales, K) ||
       !q_scales_aligned(w_scales, K))
     return MX_ERR_ALIGN;
-  const int st = workspace_ok(workspace, workspace_bytes, quantized_plan(T, K, N, false, false).bytes);
+  const int st = workspace_ok(workspace, workspace_bytes, linear_bytes(T, K, N));
   if (st != MX_OK) return st;
   return launch_linear_quantized(a_codes, a_scales, format, w_codes, w_scales, bias, residual, scale, act, y, z, (int)T,
                                  (int)K, (int)N, workspace, static_cast<hipStream_t>(stream));
 }
 
 size_t mx_gate_up_quantized_workspace_size(int64_t T, int64_t H, int64_t I) {
-  return gated_ok(T, H, I) ? std::max(quantized_plan(T, H, I, true, true).bytes, quantized_plan(T, H, I, true, false).bytes) : 0;
+  if (!gated_ok(T, H, I)) return 0;
+  size_t most = 0;
+  for (int f : {MX_FORMAT_MXFP8, MX_FORMAT_MXFP4})
+    for (bool quantized : {false, true}) most = std::max(most, quantized_plan(T, H, I, true, quantized, f).bytes);
+  return most;
 }
 
 int mx_gate_up_quantized(const uint8_t* a_codes, const uint8_t* a_scales, int format, const uint8_t* w_gate_up,

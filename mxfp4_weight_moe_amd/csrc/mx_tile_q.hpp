@@ -78,7 +78,7 @@ struct QLds {
   static constexpr int ONE = Rows::BYTES + Codes::BYTES;
   static constexpr int SCALES_AT = D * ONE, SCALES = (BM + BN) * 16;
   static constexpr int BYTES = SCALES_AT + 2 * SCALES;
-  static constexpr int PER_SIMD = NW / 4 * (BYTES > 81920 ? 1 : 2);  // waves
+  static constexpr int PER_SIMD = NW < 4 ? 1 : NW / 4 * (BYTES > 81920 ? 1 : 2);  // waves
 };
 
 template <int FMT>

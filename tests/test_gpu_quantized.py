@@ -340,13 +340,17 @@ def value_error(z, ez):
     return ACT_LIP * ez + ACT_ERR * (1 + z.abs())
 
 
-# streaming (up to 32 tokens), tiles of 64, 128 and 256, K whole and split, tails of 32, 64 and 96, odd
-# rows; K from one block on; scales that go to the LDS directly (K % 512 == 0) or through registers
+# streaming (up to 16 tokens, 32 where K % 512 != 0), thin tiles (17 to 64 tokens, 32 and 64 rows, fewer
+# stages than waves), tiles of 64, 128 and 256 tokens by 64, 128 and 256 rows, K whole and split, tails of 32,
+# 64 and 96, odd rows; K from one block on; scales that go to the LDS directly (K % 512 == 0) or through
+# registers
 SHAPES = [(1, 32, 1), (1, 256, 64), (2, 96, 7), (5, 512, 33), (16, 288, 16), (17, 2048, 40), (31, 160, 100), (32, 7168, 24),
           (33, 128, 8), (33, 32, 1), (40, 2048, 130), (64, 544, 130), (64, 4096, 64), (65, 256, 64), (77, 2048, 257),
           (100, 64, 300), (128, 1024, 260), (129, 96, 300), (200, 4192, 65), (300, 512, 520), (300, 2048, 1000),
           (1025, 192, 264), (130, 4096, 64), (97, 1120, 200), (4100, 544, 2100), (4097, 1024, 2049), (4200, 32, 2060),
-          (4099, 640, 2080), (4200, 2560, 2300)]
+          (4099, 640, 2080), (4200, 2560, 2300), (24, 512, 33), (17, 1024, 9000), (50, 512, 8300), (64, 2048, 100),
+          (32, 16384, 33), (33, 4096, 70), (128, 2048, 7000), (100, 8192, 40), (40, 8192, 70), (60, 8192, 6000),
+          (256, 4096, 2000), (1000, 1536, 1000)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)
@@ -374,7 +378,9 @@ def test_linear(mx, T, K, N, fmt):
 
 GATED_SHAPES = [(1, 32, 1), (1, 256, 64), (3, 96, 32), (16, 288, 33), (17, 512, 160), (32, 2048, 96), (33, 128, 8),
                 (64, 544, 96), (65, 1024, 130), (77, 7168, 64), (130, 96, 257), (300, 2048, 512), (1025, 192, 136),
-                (4100, 288, 1056), (4097, 512, 1031), (4100, 2048, 1088), (4200, 32, 1056)]
+                (4100, 288, 1056), (4097, 512, 1031), (4100, 2048, 1088), (4200, 32, 1056),
+                (24, 512, 32), (17, 2048, 100), (32, 7168, 64), (20, 512, 4160), (50, 1024, 96), (64, 4096, 33), (45, 512, 4128),
+                (100, 2048, 2080), (50, 8192, 64), (128, 7168, 40)]
 
 
 @pytest.mark.parametrize("fmt", FORMATS)

@@ -64,7 +64,7 @@ def test_product_sizes(call, K, N):
                 {N: -1}, {N: (1 << 22) + 32}, {"T": 1 << 24, N: 1 << 18}, {"T": 1 << 24, K: 1 << 18}, {N: 1 << 62}):
         assert call(**bad) == SHAPE, bad
     assert gate_up_out(I=48) == SHAPE
-    assert gate_up(I=48, ws=None, T=64, H=8192) == WORKSPACE  # bf16 takes any I
+    assert gate_up(I=48, ws=None, T=100, H=8224) == WORKSPACE  # bf16 takes any I
 
 
 def test_other_sizes():
@@ -121,16 +121,16 @@ def test_type_and_scale_alignment():
     for call, K in ((linear, "K"), (gate_up, "H")):
         for n in ("sa", "s"):
             assert call(**{n: P((1 << 20) + 8), K: 8192}) == ALIGN
-            assert call(**{n: MIS, K: 8224}, ws=None) == WORKSPACE
+            assert call(**{n: MIS, K: 8224}, T=100, ws=None) == WORKSPACE
     assert norm(gate=P((1 << 20) + 8), mode=2) == ALIGN and norm(gate=MIS, mode=1) == ALIGN
 
 
 def test_workspaces():
     L = m.raw()
-    need = L.mx_linear_quantized_workspace_size(64, 8192, 64)
+    need = L.mx_linear_quantized_workspace_size(100, 8192, 64)
     assert need > 0
     for bad in (dict(wb=need - 1), dict(ws=None), dict(ws=P((1 << 20) + 128))):
-        assert linear(K=8192, **bad) == WORKSPACE
+        assert linear(T=100, K=8192, **bad) == WORKSPACE
     need = L.mx_gate_up_quantized_workspace_size(4, 256, 64)
     assert need > 0 and gate_up_out(T=4, wb=need - 1) == WORKSPACE and gate_up_out(T=4, ws=None) == WORKSPACE
     assert L.mx_linear_quantized_workspace_size(4, 7168, 4096) == 0
