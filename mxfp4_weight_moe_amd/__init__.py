@@ -894,28 +894,25 @@ def _format_code(fmt: str) -> int:
     return code
 
 
-def _code_bytes(K: int, fmt: int) -> int:
-    return K // 2 if fmt else K
-
-
 def mx_quantize(x: torch.Tensor, fmt: str = "mxfp8", save_values: bool = False):
     """(codes, scales) of bf16 or fp32 rows [..., K] in MXFP8 (codes uint8 [..., K]) or MXFP4
     ([..., K/2], element 2i in the low nibble), scales uint8 [..., K/32].  save_values=True:
     (codes, scales, values), values bf16 [..., K] what the codes stand for."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in (_BF16, _F32):
-        _check(x, "x", _BF16)  # names what is wrong
-    _check(x, "x", x.dtype)
-    if x.dim() < 1 or x.numel() == 0:
-        raise ValueError(f"x is empty: {list(x.shape)}")
+    if not (isinstance(x, torch.Tensor) and (x.dtype is _BF16 or x.dtype is _F32) and x.is_cuda and x.is_contiguous()):
+        _check(x, "x", _BF16 if getattr(x, "dtype", None) is not _F32 else _F32)  # names what is wrong
     code = _format_code(fmt)
-    dev, lead, K = x.device, x.shape[:-1], x.shape[-1]
+    shape, n = x.shape, x.numel()
+    if n == 0 or not shape:
+        raise ValueError(f"x is empty: {list(shape)}")
+    K = shape[-1]
     if K % 32:
         raise ValueError(f"the last dimension {K} must be a multiple of 32")
-    codes = torch.empty((*lead, _code_bytes(K, code)), dtype=_U8, device=dev)
-    scales = torch.empty((*lead, K // 32), dtype=_U8, device=dev)
-    values = torch.empty(x.shape, dtype=_BF16, device=dev) if save_values else None
-    _call(_lib.mx_quantize, dev, x.data_ptr(), 1 if x.dtype is _F32 else 0, code, codes.data_ptr(), scales.data_ptr(),
-          _opt(values), x.numel() // K, K)
+    lead = shape[:-1]
+    codes = x.new_empty((*lead, K // 2 if code else K), dtype=_U8)
+    scales = x.new_empty((*lead, K // 32), dtype=_U8)
+    values = x.new_empty(shape, dtype=_BF16) if save_values else None
+    _call(_lib.mx_quantize, x.device, x.data_ptr(), 1 if x.dtype is _F32 else 0, code, codes.data_ptr(),
+          scales.data_ptr(), _opt(values), n // K, K)
     return (codes, scales, values) if save_values else (codes, scales)
 
 
@@ -949,8 +946,8 @@ def mx_norm_residual_quantize(x: torch.Tensor, b: torch.Tensor | None = None, w_
             _tensor(y, "out", _BF16, (T, H), dev)
             _apart(y, x, "x", itself=True)
             _apart(y, b, "b", itself=True)
-    codes = torch.empty((T, _code_bytes(H, code)), dtype=_U8, device=dev)
-    scales = torch.empty((T, H // 32), dtype=_U8, device=dev)
+    codes = x.new_empty((T, H // 2 if code else H), dtype=_U8)
+    scales = x.new_empty((T, H // 32), dtype=_U8)
     xn = torch.empty_like(x) if save_xn else None
     _call(_lib.mx_norm_residual_quantize, dev, x.data_ptr(), _opt(b), _opt(w_post), _opt(gate), mode, scale,
           w_pre.data_ptr(), eps, _opt(y), _opt(xn), code, codes.data_ptr(), scales.data_ptr(), T, H)
@@ -996,12 +993,12 @@ def mx_linear_quantized(codes: torch.Tensor, scales: torch.Tensor, w_codes: torc
         _tensor(residual, "residual", _BF16, (T, N), dev)
     code = _act_code(act)
     if out is None:
-        out = torch.empty((T, N), dtype=_BF16, device=dev)
+        out = codes.new_empty((T, N), dtype=_BF16)
     else:
         _tensor(out, "out", _BF16, (T, N), dev)
         if residual is not None:
             _apart(out, residual, "residual", itself=True)
-    z = torch.empty((T, N), dtype=_BF16, device=dev) if save_z else None
+    z = codes.new_empty((T, N), dtype=_BF16) if save_z else None
     ws, wp, wn = _scratch(_lib.mx_linear_quantized_workspace_size(T, K, N), dev, ws)
     _call(_lib.mx_linear_quantized, dev, codes.data_ptr(), scales.data_ptr(), fmt, w_codes.data_ptr(),
           w_scales.data_ptr(), _opt(bias), _opt(residual), scale, code, out.data_ptr(), _opt(z), T, K, N, wp, wn)
@@ -1026,14 +1023,14 @@ def mx_gate_up_quantized(codes: torch.Tensor, scales: torch.Tensor, W_gate_up: t
         _tensor(bias, "bias", _BF16, (two_i,), dev)
     code, h, hc, hs, h_fmt = _act_code(act), None, None, None, 0
     if fmt is None:
-        h = torch.empty((T, I), dtype=_BF16, device=dev)
+        h = codes.new_empty((T, I), dtype=_BF16)
     else:
         h_fmt = _format_code(fmt)
         if I % 32:
             raise ValueError(f"I = {I} must be a multiple of 32 for a quantized h")
-        hc = torch.empty((T, _code_bytes(I, h_fmt)), dtype=_U8, device=dev)
-        hs = torch.empty((T, I // 32), dtype=_U8, device=dev)
-    z = torch.empty((T, two_i), dtype=_BF16, device=dev) if save_z else None
+        hc = torch.empty_like(codes) if codes.shape[1] == I and not h_fmt else codes.new_empty((T, I // 2 if h_fmt else I))
+        hs = codes.new_empty((T, I // 32))
+    z = codes.new_empty((T, two_i), dtype=_BF16) if save_z else None
     ws, wp, wn = _scratch(_lib.mx_gate_up_quantized_workspace_size(T, H, I), dev, ws)
     _call(_lib.mx_gate_up_quantized, dev, codes.data_ptr(), scales.data_ptr(), a_fmt, W_gate_up.data_ptr(),
           S_gate_up.data_ptr(), _opt(bias), code, _opt(h), h_fmt, _opt(hc), _opt(hs), _opt(z), T, H, I, wp, wn)
@@ -1045,6 +1042,7 @@ def mx_gate_up_quantized(codes: torch.Tensor, scales: torch.Tensor, W_gate_up: t
 
 # ------------------------------------------------------------------ routing by scores
 
+_I32 = torch.int32
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"top2": 0, "max": 1}
 MX_MAX_GROUPS = 64
@@ -1058,12 +1056,13 @@ def _choice(table: dict, key, name: str) -> int:
 
 
 def _logits(logits):
-    if not isinstance(logits, torch.Tensor) or logits.dtype not in (_BF16, _F32):
-        _check(logits, "router_logits", _F32, 2)  # names what is wrong
-    _check(logits, "router_logits", logits.dtype, 2)
-    if logits.numel() == 0:
+    if not (isinstance(logits, torch.Tensor) and (logits.dtype is _F32 or logits.dtype is _BF16) and logits.is_cuda
+            and logits.dim() == 2 and logits.is_contiguous()):
+        _check(logits, "router_logits", _F32 if getattr(logits, "dtype", None) is not _BF16 else _BF16, 2)
+    T, E = logits.shape
+    if T == 0 or E == 0:
         raise ValueError(f"router_logits is empty: {list(logits.shape)}")
-    return (*logits.shape, 1 if logits.dtype is _F32 else 0)
+    return T, E, 1 if logits.dtype is _F32 else 0
 
 
 def moe_route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", bias: torch.Tensor | None = None,
@@ -1079,17 +1078,17 @@ def moe_route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", b
     dev = logits.device
     if bias is not None:
         _tensor(bias, "bias", _F32, (E,), dev)
-    sc, gs = _choice(_SCORES, score, "score"), _choice(_GROUP_SCORES, group_score, "group_score")
-    if ids is None:
-        ids = torch.empty((T, max(0, top_k)), dtype=torch.int32, device=dev)
-    else:
-        _tensor(ids, "ids", torch.int32, (T, top_k), dev)
-    if gates is None:
-        gates = torch.empty((T, max(0, top_k)), dtype=_F32, device=dev)
-    else:
-        _tensor(gates, "gates", _F32, (T, top_k), dev)
     if top_k < 1:
         raise ValueError(f"top_k must be at least 1, got {top_k}")
+    sc, gs = _choice(_SCORES, score, "score"), _choice(_GROUP_SCORES, group_score, "group_score")
+    if ids is None:
+        ids = logits.new_empty((T, top_k), dtype=_I32)
+    else:
+        _tensor(ids, "ids", _I32, (T, top_k), dev)
+    if gates is None:
+        gates = logits.new_empty((T, top_k), dtype=_F32)
+    else:
+        _tensor(gates, "gates", _F32, (T, top_k), dev)
     _call(_lib.moe_route_scored, dev, logits.data_ptr(), kind, _opt(bias), sc, n_group, topk_group, gs,
           1 if renormalize else 0, scale, ids.data_ptr(), gates.data_ptr(), T, E, top_k)
     return ids, gates
@@ -1104,7 +1103,7 @@ def moe_route_scored_backward(dgates: torch.Tensor, logits: torch.Tensor, ids: t
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a 2-d tensor")
     k = ids.shape[1]
-    _tensor(ids, "ids", torch.int32, (T, k), dev)
+    _tensor(ids, "ids", _I32, (T, k), dev)
     _tensor(dgates, "dgates", _F32, (T, k), dev)
     sc = _choice(_SCORES, score, "score")
     dlogits = torch.empty_like(logits)
@@ -1125,7 +1124,7 @@ def moe_mxfp4_forward_routed(x: torch.Tensor, ids: torch.Tensor, gates: torch.Te
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
         raise ValueError("ids must be a 2-d tensor")
     k = ids.shape[1]
-    _tensor(ids, "ids", torch.int32, (T, k), dev)
+    _tensor(ids, "ids", _I32, (T, k), dev)
     _tensor(gates, "gates", _F32, (T, k), dev)
     for t, n in ((W_gate_up, "W_gate_up"), (S_gate_up, "S_gate_up"), (W_down, "W_down"), (S_down, "S_down")):
         _check(t, n, _U8, 3, dev)

@@ -11,12 +11,14 @@
 // The order is that of 64-bit keys: which experts a token takes does not depend on how a kernel rounds.
 // A token has 16 lanes (four tokens a wave: what a step of the choice costs beside the lanes' own work is
 // paid once for four).  Its keys are made in fp32 (without a bias they are the logits, exact), cut to
-// 22 bits above the expert's number, and the k + 2 largest found one by one; those few are then put in order
+// 22 to 26 bits above the expert's number, and the k + 2 largest found one by one; those few are then put in order
 // by their 64-bit keys.  That is the answer unless the key of a chosen expert lies within the fp32 error
 // of those that were not looked at, or two candidates' softmax scores within that of each other; then
-// (and where equal keys fill the border) the row is done again entirely in 64 bits.
+// (and where equal keys fill the border) the row's choice is made again, in 64 bits and one by one.  The same
+// for the groups.  That costs a launch 10 us or so, whatever the number of such rows.
 #include "mx_internal.hpp"
 #include "moe_route.hpp"
+#include "mx_tile.hpp"
 
 namespace mx {
 
@@ -55,6 +57,34 @@ __device__ __forceinline__ float row16_sum(float v) {
   return row_add_step<DPP_ROW_MIRROR>(v);
 }
 
+// Of the lane N places on, within the row.
+template <int N>
+__device__ __forceinline__ uint32_t rotate16(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, false);  // row_ror
+}
+template <int N>
+__device__ __forceinline__ float rotate16(float v) {
+  return __uint_as_float(rotate16<N>(__float_as_uint(v)));
+}
+template <int N>
+__device__ __forceinline__ double rotate16(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)rotate16<N>((uint32_t)(b >> 32)) << 32 | rotate16<N>((uint32_t)b));
+}
+
+// The middle one.
+__device__ __forceinline__ uint32_t median(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("v_med3_u32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+// route_key for a key that is cut anyway: -0 lies right below +0 (what that may confuse is seen when the
+// candidates are put in order), NaN at -Inf.
+__device__ __forceinline__ uint32_t rough_key(float v) {
+  const uint32_t b = __float_as_uint(__builtin_fmaxf(v, -INFINITY));
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
 // a before b in the order of choice.
 __device__ __forceinline__ bool before(double ka, int a, double kb, int b) { return ka > kb || (ka == kb && a < b); }
 // NaN counts as the lowest.
@@ -75,82 +105,86 @@ struct Scores {
   __device__ __forceinline__ double order(int e) const { return bias ? key(e) : ordered(logit(e)); }
 };
 
-// A row in 64 bits throughout, one choice after the other: expert j's number and score go to lane
-// j % 16, place j / 16.
+// Between a row's writes to the LDS and its reads of them: its 16 lanes are of one wave, whose accesses keep
+// their order.
+__device__ __forceinline__ void row_written() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// The best (value, number) of a row's lanes, in each of them; numbers below 0 are none.
+__device__ __forceinline__ void row16_best(double& k, int& id) {
+#pragma unroll
+  for (int m = 1; m < ROUTE_LANES; m <<= 1) {
+    const double ok = __shfl_xor(k, m, ROUTE_LANES);
+    const int oid = __shfl_xor(id, m, ROUTE_LANES);
+    if (oid >= 0 && (id < 0 || before(ok, oid, k, id))) k = ok, id = oid;
+  }
+}
+
+// 16 / groups lanes to a group (a power of two, one at least).
+__device__ __forceinline__ int group_lanes(int groups) { return groups <= 2 ? 8 : groups <= 4 ? 4 : groups <= 8 ? 2 : 1; }
+
+// A row's keys in 64 bits, to its place in the LDS; softmax: s.sum becomes exact.
 template <bool BF16>
-__device__ __attribute__((noinline)) void route_exact(const RouteScored& a, int64_t t, int lane, int (&mine_id)[2],
-                                                      double (&mine)[2]) {
-  Scores<BF16> s{a.logits, a.bias, (size_t)t * a.E, a.sigmoid, 0.0, 1.0};
-  auto most = [](double x, double y) { return x > y ? x : (y == y ? y : x); };
-  auto plus = [](double x, double y) { return x + y; };
-  if (!a.sigmoid) {
-    double m = -INFINITY, sum = 0.0;
-    for (int e = lane; e < a.E; e += ROUTE_LANES) m = most(m, s.logit(e));
-    s.top = row16(m, most);
-    for (int e = lane; e < a.E; e += ROUTE_LANES) sum += exp(s.logit(e) - s.top);
-    s.sum = row16(sum, plus);
-    if (s.top == -INFINITY) s.top = 0.0, s.sum = 1.0;  // nothing but -Inf: every score is 0
+__device__ __forceinline__ void exact_keys(Scores<BF16>& s, int E, int lane, double* keys) {
+  row_written();  // what was there has been read
+  if (!s.sigmoid) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int e = lane; e < E; e += ROUTE_LANES) sum += exp(s.logit(e) - s.top);
+    s.sum = row16(sum, [](double x, double y) { return x + y; });
+    if (s.sum == 0.0) s.sum = 1.0;  // nothing but -Inf: every score is 0
   }
-  // the best of (value, number) pairs behind the last one taken
-  double last = 0.0;
-  int last_id = -1;
-  auto best = [&](double k, int id) {
-#pragma unroll
-    for (int m = 1; m < ROUTE_LANES; m <<= 1) {
-      const double ok = __shfl_xor(k, m, ROUTE_LANES);
-      const int oid = __shfl_xor(id, m, ROUTE_LANES);
-      if (oid >= 0 && (id < 0 || before(ok, oid, k, id))) k = ok, id = oid;
+#pragma unroll 4
+  for (int e = lane; e < E; e += ROUTE_LANES) keys[e] = s.key(e);
+  row_written();
+}
+
+// The groups that stay, from the keys in the LDS; vals: a place for the groups' values behind them.
+__device__ __forceinline__ uint64_t exact_groups(const RouteScored& a, int lane, const double* keys, double* vals) {
+  const int size = a.E / a.groups, share = group_lanes(a.groups);
+  for (int c = lane / share; c < a.groups; c += ROUTE_LANES / share) {
+    double one = -INFINITY, two = -INFINITY;
+    for (int e = c * size + lane % share; e < (c + 1) * size; e += share) {
+      const double v = keys[e];
+      two = v > one ? one : (v > two ? v : two);
+      one = v > one ? v : one;
     }
-    last = k, last_id = id;
-  };
-  uint64_t open = ~0ull;
-  const int size = a.E / a.groups;
-  if (a.groups > 1) {
-    open = 0;
-    for (int j = 0; j < a.kept; ++j) {
-      double k = 0.0;
-      int g = -1;
-      for (int c = lane; c < a.groups; c += ROUTE_LANES) {
-        double one = -INFINITY, two = -INFINITY;
-        for (int e = c * size; e < (c + 1) * size; ++e) {
-          const double v = s.key(e);
-          two = v > one ? one : (v > two ? v : two);
-          one = v > one ? v : one;
-        }
-        const double v = a.top2 && size > 1 ? one + two : one;
-        if ((j == 0 || before(last, last_id, v, c)) && (g < 0 || before(v, c, k, g))) k = v, g = c;
-      }
-      best(k, g);
-      open |= 1ull << last_id;
+    for (int m = 1; m < share; m <<= 1) {
+      const double o1 = __shfl_xor(one, m, ROUTE_LANES), o2 = __shfl_xor(two, m, ROUTE_LANES);
+      const double lesser = o1 > one ? one : o1;
+      two = o2 > two ? o2 : two;
+      two = lesser > two ? lesser : two;
+      one = o1 > one ? o1 : one;
     }
+    vals[c] = a.top2 && size > 1 ? one + two : one;
   }
-  for (int j = 0; j < a.k; ++j) {
-    double k = 0.0;
-    int id = -1;
-    for (int e = lane; e < a.E; e += ROUTE_LANES) {
-      if (!((open >> (e / size)) & 1)) continue;
-      const double v = s.order(e);
-      if ((j == 0 || before(last, last_id, v, e)) && (id < 0 || before(v, e, k, id))) k = v, id = e;
-    }
-    best(k, id);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (j == lane + ROUTE_LANES * h) mine_id[h] = last_id, mine[h] = s.score(last_id);
+  row_written();
+  uint64_t open = 0;
+  for (int c = lane; c < a.groups; c += ROUTE_LANES) {
+    const double v = vals[c];
+    int rank = 0;
+    for (int o = 0; o < a.groups; ++o) rank += before(vals[o], o, v, c);
+    if (rank < a.kept) open |= 1ull << c;
   }
+  auto either = [](uint32_t x, uint32_t y) { return x | y; };
+  return (uint64_t)row16((uint32_t)(open >> 32), either) << 32 | row16((uint32_t)open, either);
 }
 
 // What is added to k for the candidates that show where the border lies.
 constexpr int ROUTE_MORE = 2;
-// Bound of an fp32 key's distance from its 64-bit one, relative to 1 + |key|: a sigmoid score is off by
-// (1.3 |l| (1 - p) p + 6 p) u < 2^-20, a softmax score, its sum of E <= 1024 terms among it, by less than
-// (64 + 24) u p, and the addition of the bias by u |key|.
-constexpr double ROUTE_FP32 = 0x1p-17;
+// Bounds of an fp32 score's distance from its 64-bit one, u = 2^-24.  Sigmoid: the exponential is off by
+// (1.3 |l| + 2) u of itself, which p (1 - p) <= 1/4 and |l| p (1 - p) < 0.23 leave 0.8 u of, the sum and its
+// reciprocal by 1.5 u: 3 u.  Softmax: a sum of E <= 1024 terms, 64 a lane and 4 steps, the terms
+// off by (1.3 |x| + 2) u with a weighted mean |x| below 4.5, and the score's own exponential: 88 u of the
+// largest score.  Adding the bias
+// rounds by u |key|.
+constexpr float ROUTE_U = 0x1p-24f;
 
 // PER: logits of a lane, chunks of 4 consecutive ones, E <= 16 PER; C: candidates of a lane, k + 2 <= 16 C
 // (k at most 32 with C = 3).
-template <bool BF16, int PER, int C>
-__global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t* __restrict__ ids, float* __restrict__ gates) {
-  extern __shared__ float shared[];  // with groups: per row its keys [E], its groups' values [groups]
+// WHOLE of a lane's places hold an expert whatever E.
+template <bool BF16, int PER, int C, int WHOLE>
+__global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_scored_kernel(RouteScored a, int32_t* __restrict__ ids, float* __restrict__ gates) {
+  extern __shared__ double shared[];  // with a bias or groups: per row E + groups values
   const int lane = threadIdx.x % ROUTE_LANES, row = threadIdx.x / ROUTE_LANES;
   const int64_t t0 = (int64_t)blockIdx.x * ROUTE_ROWS + row, t = t0 < a.T ? t0 : a.T - 1;  // rows past the last: it again
   const size_t at = (size_t)t * a.E;
@@ -159,7 +193,7 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
 #pragma unroll
   for (int i = 0; i < PER; i += 4) {
     const int e = 4 * (lane + ROUTE_LANES * (i / 4));
-    if (e + 4 <= E) {
+    if (i < WHOLE || e + 4 <= E) {
       if constexpr (BF16) {
         const u32x2 q = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(a.logits) + at + e);
 #pragma unroll
@@ -175,9 +209,11 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
     }
   }
   auto number = [&](int i) { return 4 * (lane + ROUTE_LANES * (i / 4)) + i % 4; };
+  constexpr uint32_t LAST = PER <= 4 ? 63 : PER <= 8 ? 127 : PER <= 16 ? 255 : PER <= 32 ? 511 : 1023;  // number
 
   // softmax: the largest logit and the sum
   float top = 0.f, sum = 1.f;
+  double total = 0.0;  // the sum, for the candidates
   if (!a.sigmoid) {
     float m = -INFINITY;
 #pragma unroll
@@ -194,6 +230,13 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
 #pragma unroll
       for (int i = 0; i < PER; ++i) z += __expf(l[i] - top);
       sum = row16_sum(z);
+      total = (double)sum;
+      if (a.bias) {  // fewer candidates come too near to one another
+        total = 0.0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) total += (double)__expf(l[i] - top);
+        total = row16(total, [](double x, double y) { return x + y; });
+      }
     } else {
       float z = 0.f;  // a NaN reaches every gate of its row
 #pragma unroll
@@ -201,15 +244,20 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
       sum = row16_sum(z) + 1.f;
     }
   }
+  if (total == 0.0) total = (double)sum;
+  Scores<BF16> s{a.logits, a.bias, at, a.sigmoid, (double)top, total};
   const float inv = 1.f / sum;
   auto score32 = [&](float v) { return a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-v)) : __expf(v - top) * inv; };
   auto ordered32 = [](float v) { return v == v ? v : -INFINITY; };
 
-  bool again = false;  // in 64 bits
+  bool exact = false;          // 64-bit keys are in the LDS
+  double off = 0.0, near = 0;  // bounds of the error of an fp32 key, of a candidate's softmax score
+  double* const row_lds = shared + row * (E + a.groups);
   uint32_t comp[PER];
   const bool groups = a.groups > 1;
+  uint64_t open = 0;  // groups that stay
   if (a.bias || groups) {
-    float* keys = shared + row * (E + a.groups);
+    float* keys = reinterpret_cast<float*>(row_lds);
     float* vals = keys + E;
     const int size = E / a.groups;
     const uint32_t magic = ((1u << 20) + size - 1) / size;  // e / size = (e * magic) >> 20 for e, size <= 1024
@@ -223,14 +271,25 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
       if (groups && e < E) keys[e] = key[i];
       size_of = fmaxf(size_of, key[i] == -INFINITY ? 0.f : fabsf(key[i]));
     }
+    size_of = row16(size_of, [](float x, float y) { return fmaxf(x, y); });
+    off = (double)(ROUTE_U * ((a.sigmoid ? 3.f : 88.f * inv) + size_of));
+    // exponentials off by (1.3 |x| + 2) u, summed in 64 bits: of E <= 1024 the mean |x|, weighted, is below 4.5
+    near = (double)(ROUTE_U * 12.f * inv);
     if (groups) {
       __syncthreads();
-      for (int g = lane; g < a.groups; g += ROUTE_LANES) {
+      const int share = group_lanes(a.groups);
+      for (int g = lane / share; g < a.groups; g += ROUTE_LANES / share) {
         float one = -INFINITY, two = -INFINITY;
-        for (int e = g * size; e < (g + 1) * size; ++e) {
+#pragma unroll 4
+        for (int e = g * size + lane % share; e < (g + 1) * size; e += share) {
           const float v = keys[e];
           two = fmaxf(two, fminf(one, v));
           one = fmaxf(one, v);
+        }
+        for (int m = 1; m < share; m <<= 1) {
+          const float o1 = __shfl_xor(one, m, ROUTE_LANES), o2 = __shfl_xor(two, m, ROUTE_LANES);
+          two = fmaxf(fmaxf(two, o2), fminf(one, o1));
+          one = fmaxf(one, o1);
         }
         vals[g] = a.top2 && size > 1 ? one + two : one;
       }
@@ -251,83 +310,143 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
           next = fmaxf(next, v);
         }
       }
-      size_of = row16(size_of, [](float x, float y) { return fmaxf(x, y); });
       auto either = [](uint32_t x, uint32_t y) { return x | y; };
       lo = row16(lo, either), hi = row16(hi, either);
+      open = (uint64_t)hi << 32 | lo;
       worst = row16(worst, [](float x, float y) { return fminf(x, y); });
       next = row16(next, [](float x, float y) { return fmaxf(x, y); });
-      // two values of two keys each
-      again = !((double)worst - (double)next > 4.0 * ROUTE_FP32 * (1.0 + (double)size_of));
+      // two values of two keys each, their sums rounded
+      if (!((double)worst - (double)next > 8.0 * off)) {
+        exact_keys(s, E, lane, row_lds);
+        exact = true;
+        open = exact_groups(a, lane, row_lds, row_lds + E);
+        lo = (uint32_t)open, hi = (uint32_t)(open >> 32);
+      }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         const uint32_t g = ((uint32_t)number(i) * magic) >> 20;
-        const float v = a.bias ? key[i] : ordered32(l[i]);
-        comp[i] = ((g < 32 ? lo >> g : hi >> (g & 31)) & 1) ? route_key(v) : 0u;
+        comp[i] = ((g < 32 ? lo >> g : hi >> (g & 31)) & 1) ? rough_key(a.bias ? key[i] : l[i]) : 0u;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) comp[i] = route_key(key[i]);
+      for (int i = 0; i < PER; ++i) comp[i] = rough_key(key[i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) comp[i] = route_key(ordered32(l[i]));
+    for (int i = 0; i < PER; ++i) comp[i] = rough_key(l[i]);
   }
+  // LAST - e below the cut: e's bits are those of the lane and of the place, apart
+  const uint32_t lane_bits = (uint32_t)(~lane & 15) << 2;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = number(i);
-    comp[i] = e < E && comp[i] ? (comp[i] & ~1023u) | (uint32_t)(1023 - e) : 0u;
+    const uint32_t place_bits = ~(uint32_t)(64 * (i / 4) + i % 4) & (LAST & ~0x3Cu);
+    uint32_t c = (comp[i] & ~LAST) | (lane_bits | place_bits);
+    if (groups) c = comp[i] ? c : 0u;
+    comp[i] = i < WHOLE || number(i) < E ? c : 0u;
   }
 
-  // The largest one below w, again and again: x - w wraps to the top exactly for x < w.
   uint32_t cand[C] = {};
   uint32_t w = 0;
   bool left = true;  // unless every expert is a candidate already
   const int rounds = a.k + ROUTE_MORE;
-  for (int j = 0; j < rounds; ++j) {
-    uint32_t m = 0;
+  bool found = false;
+  if constexpr (C == 1 && PER > 4) {
+    // Each lane's four largest, in order; a round takes the row's largest and moves its lane on.  Where a
+    // lane is taken four times (3.5 of 100 tokens at 10 candidates) the rest of it is unknown: below, then.
+    uint32_t m[4] = {};
 #pragma unroll
-    for (int i = 0; i < PER; i += 2) m = max(m, max(comp[i] - w, comp[i + 1] - w));
-    w += row16_max(m);
-    left = left && w != 0;
+    for (int i = 0; i < PER; ++i) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-      if (j == lane + ROUTE_LANES * c) cand[c] = left ? w : 0u;
+      for (int d = 3; d > 0; --d) m[d] = median(m[d - 1], m[d], comp[i]);
+      m[0] = max(m[0], comp[i]);
+    }
+    for (int j = 0; j < rounds; ++j) {
+      w = row16_max(m[0]);
+      left = left && w != 0;
+      if (j == lane) cand[0] = w;
+      const bool mine = m[0] == w;
+#pragma unroll
+      for (int d = 0; d < 3; ++d) m[d] = mine ? m[d + 1] : m[d];
+      m[3] = mine ? 0u : m[3];
+    }
+    found = __ballot(m[0] == 0) == 0;
+  }
+  if (!found) {
+    // The largest one below w, again and again: x - w wraps to the top exactly for x < w.
+    w = 0, left = true;
+    for (int j = 0; j < rounds; ++j) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < PER; i += 2) m = max(m, max(comp[i] - w, comp[i + 1] - w));
+      w += row16_max(m);
+      left = left && w != 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (j == lane + ROUTE_LANES * c) cand[c] = left ? w : 0u;
+    }
   }
 
   // the candidates' 64-bit keys, their order, and whether it is certain
-  Scores<BF16> s{a.logits, a.bias, at, a.sigmoid, (double)top, (double)sum};
   int id[C], rank[C];
   float cl[C], cb[C];
-  double key[C];
+  double key[C], p[C];
+  const bool rough = a.bias && !a.sigmoid && !exact;  // the sum is of fp32 exponentials
+  bool again = false;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    id[c] = cand[c] ? 1023 - (int)(cand[c] & 1023u) : 1 << 20;
+    id[c] = cand[c] ? (int)(LAST - (cand[c] & LAST)) : 1 << 20;
     cl[c] = cand[c] ? logit_at<BF16>(a.logits, at + id[c]) : -INFINITY;
     cb[c] = a.bias && cand[c] ? a.bias[id[c]] : 0.f;
-    key[c] = a.bias ? ordered(s.score_of((double)cl[c]) + (double)cb[c]) : ordered((double)cl[c]);
+    p[c] = s.score_of((double)cl[c]);
+    key[c] = a.bias ? ordered(p[c] + (double)cb[c]) : ordered((double)cl[c]);
     if (!cand[c]) key[c] = -INFINITY;  // its number puts it behind all others
     rank[c] = 0;
   }
-  const bool rough = a.bias && !a.sigmoid;  // these scores have the fp32 sum
+  if (a.bias) {
+    auto compare = [&](double ok, int oid, float ol, float ob, int d) {
+      rank[d] += before(ok, oid, key[d], id[d]);
+      if (rough && oid != id[d] && !(fabs(ok - key[d]) > 2.0 * near) && !(ol == cl[d] && ob == cb[d]))
+        again = again || (cand[d] != 0 && oid < 1 << 20);
+    };
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int n = min(ROUTE_LANES, rounds - ROUTE_LANES * c);
-    for (int j = 0; j < n; ++j) {
-      const double ok = __shfl(key[c], j, ROUTE_LANES);
-      const int oid = __shfl(id[c], j, ROUTE_LANES);
-      const float ol = __shfl(cl[c], j, ROUTE_LANES), ob = __shfl(cb[c], j, ROUTE_LANES);
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-      for (int d = 0; d < C; ++d) {
-        rank[d] += before(ok, oid, key[d], id[d]);
-        if (rough && oid != id[d] && !(fabs(ok - key[d]) > 2.0 * ROUTE_FP32 * (1.0 + fabs(ok))) && !(ol == cl[d] && ob == cb[d]))
-          again = again || (cand[d] != 0 && oid < 1 << 20);
-      }
+      for (int d = 0; d < C; ++d)
+        if (c != d) compare(key[c], id[c], cl[c], cb[c], d);
+      unrolled<ROUTE_LANES - 1>([&](auto N) __attribute__((always_inline)) {
+        const double ok = rotate16<N + 1>(key[c]);
+        const int oid = (int)rotate16<N + 1>((uint32_t)id[c]);
+        float ol = 0.f, ob = 0.f;
+        if (rough) ol = rotate16<N + 1>(cl[c]), ob = rotate16<N + 1>(cb[c]);
+#pragma unroll
+        for (int d = 0; d < C; ++d) compare(ok, oid, ol, ob, d);
+      });
     }
+  } else {
+    // the logits' own bits above the expert's number say the same in one comparison
+    uint64_t whole[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      whole[c] = cand[c] ? (uint64_t)route_key(ordered32(cl[c])) << 32 | (uint32_t)(1023 - id[c]) : 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+#pragma unroll
+      for (int d = 0; d < C; ++d)
+        if (c != d) rank[d] += whole[c] > whole[d];
+      unrolled<ROUTE_LANES - 1>([&](auto N) __attribute__((always_inline)) {
+        const uint64_t o = (uint64_t)rotate16<N + 1>((uint32_t)(whole[c] >> 32)) << 32 | rotate16<N + 1>((uint32_t)whole[c]);
+#pragma unroll
+        for (int d = 0; d < C; ++d) rank[d] += o > whole[d];
+      });
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      if (!cand[c]) rank[c] = a.k;  // none
   }
   if (left) {
     // everything that was not a candidate has an fp32 key of at most this
-    const double most = (double)route_value(w | 1023u);
-    const double least = a.bias ? most + ROUTE_FP32 * (1.0 + fabs(most)) : most;
+    const double most = (double)route_value(w | LAST);
+    const double least = a.bias ? most + off : most;
 #pragma unroll
     for (int c = 0; c < C; ++c)
       if (rank[c] == a.k - 1) again = again || !(key[c] > least);
@@ -336,19 +455,47 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
   again = ((rows >> (threadIdx.x & 48)) & 0xFFFFu) != 0;
 
   int out[C], out_id[C];
-  double p[C];
 #pragma unroll
-  for (int c = 0; c < C; ++c) out[c] = rank[c], out_id[c] = id[c], p[c] = rank[c] < a.k ? s.score_of((double)cl[c]) : 0.0;
+  for (int c = 0; c < C; ++c) {
+    out[c] = rank[c], out_id[c] = id[c];
+    if (rank[c] >= a.k) p[c] = 0.0;
+  }
   if (again) {
-    int mine_id[2] = {};
-    double mine[2] = {};
-    route_exact<BF16>(a, t, lane, mine_id, mine);
+    if (a.bias && !exact) exact_keys(s, E, lane, row_lds);
+    double last = 0.0;
+    int last_id = -1;
+    auto shut = [&](int e) { return groups && !((open >> (e / (E / a.groups))) & 1); };
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      out[c] = c < 2 ? lane + ROUTE_LANES * c : a.k;
-      out_id[c] = c < 2 ? mine_id[c] : 0;
-      p[c] = c < 2 && out[c] < a.k ? mine[c] : 0.0;
+    for (int c = 0; c < C; ++c) out[c] = a.k;
+    for (int j = 0; j < a.k; ++j) {
+      double k = 0.0;
+      int best = -1;
+      if (a.bias) {
+        for (int e = lane; e < E; e += ROUTE_LANES) {
+          const double v = row_lds[e];
+          if (!shut(e) && (j == 0 || before(last, last_id, v, e)) && (best < 0 || before(v, e, k, best))) k = v, best = e;
+        }
+      } else {
+        uint32_t m = 0;  // all bits of the logits, 0 for what is taken, shut or not there
+        int at_i = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          const uint32_t v = comp[i] ? route_key(ordered32(l[i])) : 0u;
+          if (v > m) m = v, at_i = i;
+        }
+        if (m) k = (double)route_value(m), best = number(at_i);
+      }
+      row16_best(k, best);
+      last = k, last_id = best;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (number(i) == best) comp[i] = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        if (j == lane + ROUTE_LANES * c) out[c] = j, out_id[c] = best;
     }
+#pragma unroll
+    for (int c = 0; c < C; ++c) p[c] = out[c] < a.k ? s.score(out_id[c]) : 0.0;
   }
   if (a.renormalize) {
     double all = 0.0;
@@ -367,30 +514,33 @@ __global__ void __launch_bounds__(64) route_scored_kernel(RouteScored a, int32_t
     }
 }
 
-template <bool BF16, int PER>
-static void route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.T + ROUTE_ROWS - 1) / ROUTE_ROWS));
-  const unsigned lds = a.groups > 1 ? ROUTE_ROWS * (unsigned)(a.E + a.groups) * 4 : 0;
-  if (a.k + ROUTE_MORE <= ROUTE_LANES)
-    hipLaunchKernelGGL((route_scored_kernel<BF16, PER, 1>), grid, dim3(64), lds, stream, a, ids, gates);
-  else
-    hipLaunchKernelGGL((route_scored_kernel<BF16, PER, 3>), grid, dim3(64), lds, stream, a, ids, gates);
-}
-
 template <bool BF16>
 static void route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStream_t stream) {
-  if (a.E <= 64)
-    route_scored<BF16, 4>(a, ids, gates, stream);
-  else if (a.E <= 128)
-    route_scored<BF16, 8>(a, ids, gates, stream);
-  else if (a.E <= 256)
-    route_scored<BF16, 16>(a, ids, gates, stream);
-  else if (a.E <= 384)
-    route_scored<BF16, 24>(a, ids, gates, stream);
-  else if (a.E <= 512)
-    route_scored<BF16, 32>(a, ids, gates, stream);
-  else
-    route_scored<BF16, 64>(a, ids, gates, stream);
+  const dim3 grid((unsigned)((a.T + ROUTE_ROWS - 1) / ROUTE_ROWS));
+  const unsigned lds = a.groups > 1 || a.bias ? ROUTE_ROWS * (unsigned)(a.E + a.groups) * 8 : 0;
+#define MX_ROUTE(PER, C, WHOLE) \
+  hipLaunchKernelGGL((route_scored_kernel<BF16, PER, C, WHOLE>), grid, dim3(64), lds, stream, a, ids, gates)
+  if (a.k + ROUTE_MORE > ROUTE_LANES) {
+    if (a.E <= 256)
+      MX_ROUTE(16, 3, 0);
+    else if (a.E <= 512)
+      MX_ROUTE(32, 3, 16);
+    else
+      MX_ROUTE(64, 3, 32);
+  } else if (a.E <= 64) {
+    MX_ROUTE(4, 1, 0);
+  } else if (a.E <= 128) {
+    MX_ROUTE(8, 1, 4);
+  } else if (a.E <= 256) {
+    MX_ROUTE(16, 1, 8);
+  } else if (a.E <= 384) {
+    MX_ROUTE(24, 1, 16);
+  } else if (a.E <= 512) {
+    MX_ROUTE(32, 1, 24);
+  } else {
+    MX_ROUTE(64, 1, 32);
+  }
+#undef MX_ROUTE
 }
 
 int launch_route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStream_t stream) {
@@ -407,78 +557,157 @@ int launch_route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStr
 // The few chosen values are worked out in 64 bits (what is left of differences of nearly equal values),
 // the rest of a dense row in 32.
 
-// A row: one wave.  The row's dp (dense) or dl goes through the LDS, where ids place it.
-template <bool BF16>
+// A row has 16 lanes, as in the forward call; k of them (two values each where k > 16) hold the chosen ones.
+// They write their values over the row behind it: the same wave's stores to one address keep their order.
+template <bool BF16, int PER>
 __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a, const float* __restrict__ dgates,
                                                                    const int32_t* __restrict__ ids, void* __restrict__ dlogits) {
-  __shared__ float row[MX_MAX_EXPERTS];
-  const int lane = threadIdx.x;
-  const int64_t t = blockIdx.x;
+  const int lane = threadIdx.x % ROUTE_LANES;
+  const int64_t t = (int64_t)blockIdx.x * ROUTE_ROWS + threadIdx.x / ROUTE_LANES;
+  if (t >= a.T) return;
   const size_t at = (size_t)t * a.E;
+  const int E = a.E;
   const bool dense = !a.sigmoid && !a.renormalize;
-  auto wave = [](double v, auto f) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v = f(v, __shfl_xor(v, m, 64));
-    return v;
-  };
   auto plus = [](double x, double y) { return x + y; };
   auto most = [](double x, double y) { return x > y ? x : (y == y ? y : x); };
-  for (int e = lane; e < a.E; e += 64) row[e] = 0.f;
-  int id = -1;
-  double c = 0.0, l = -INFINITY;
-  if (lane < a.k) {
-    id = ids[t * a.k + lane];
-    c = (double)a.scale * (double)dgates[t * a.k + lane];
-    if (id < 0 || id >= a.E)
-      id = -1;
-    else
-      l = (double)logit_at<BF16>(a.logits, at + id);
+  int id[2] = {-1, -1};
+  double c[2] = {}, l[2] = {-INFINITY, -INFINITY}, p[2] = {}, d[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = lane + ROUTE_LANES * h;
+    if (j >= a.k) continue;
+    const int e = ids[t * a.k + j];
+    if (e < 0 || e >= E) continue;
+    id[h] = e;
+    c[h] = (double)a.scale * (double)dgates[t * a.k + j];
+    l[h] = (double)logit_at<BF16>(a.logits, at + e);
   }
-  double top = 0.0, sum = 1.0, p = 0.0, d = c;
-  if (a.sigmoid) {
-    if (id >= 0) p = 1.0 / (1.0 + exp(-l));
-    if (a.renormalize) {
-      const double s = wave(p, plus), cp = wave(id >= 0 ? c * p : 0.0, plus);
-      d = s == 0.0 ? 0.0 : (c - cp / s) / s;
+  float v[PER];  // of a dense row the logits, then -p cp
+  float top32 = 0.f;
+  if (dense) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < PER; i += 4) {
+      const int e = 4 * (lane + ROUTE_LANES * (i / 4));
+      if (e + 4 <= E) {
+        if constexpr (BF16) {
+          const u32x2 q = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(a.logits) + at + e);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) v[i + 2 * j] = __uint_as_float(q[j] << 16), v[i + 2 * j + 1] = __uint_as_float(q[j] & 0xFFFF0000u);
+        } else {
+          const u32x4 q = *reinterpret_cast<const u32x4_any*>(static_cast<const float*>(a.logits) + at + e);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i + j] = __uint_as_float(q[j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i + j] = e + j < E ? logit_at<BF16>(a.logits, at + e + j) : -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i + j]);
     }
-    d *= p / (1.0 + exp(l));  // p (1 - p)
+    top32 = route_value(row16_max(route_key(m)));
+  }
+  if (a.sigmoid) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (id[h] >= 0) p[h] = 1.0 / (1.0 + exp(-l[h]));
+    double s = 1.0, cp = 0.0;
+    if (a.renormalize) {
+      s = row16(p[0] + p[1], plus);
+      cp = row16(c[0] * p[0] + c[1] * p[1], plus);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      d[h] = s == 0.0 ? 0.0 : (c[h] - cp / s) / s;
+      d[h] *= p[h] / (1.0 + exp(l[h]));  // p (1 - p)
+    }
   } else {
-    double m = l;
-    if (dense)
-      for (int e = lane; e < a.E; e += 64) m = most(m, (double)logit_at<BF16>(a.logits, at + e));
-    top = wave(m, most);
-    double z = 0.0;
-    if (dense)
-      for (int e = lane; e < a.E; e += 64) z += (double)__expf(logit_at<BF16>(a.logits, at + e) - (float)top);
-    else if (id >= 0)
-      z = exp(l - top);
-    sum = wave(z, plus);
-    if (top == -INFINITY) top = 0.0, sum = 1.0;  // nothing but -Inf: every score is 0
-    if (id >= 0) p = exp(l - top) / sum;
-    const double cp = wave(id >= 0 ? c * p : 0.0, plus);
-    d = p * (c - cp);
-    if (dense)
-      for (int e = lane; e < a.E; e += 64)
-        row[e] = (float)(-cp) * (__expf(logit_at<BF16>(a.logits, at + e) - (float)top) / (float)sum);
+    double top = dense ? (double)top32 : row16(most(l[0], l[1]), most), sum;
+    if (dense) {
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        v[i] = __expf(v[i] - top32);
+        z += v[i];
+      }
+      z = row16_sum(z);
+      sum = (double)z;
+    } else {
+      sum = row16((id[0] >= 0 ? exp(l[0] - top) : 0.0) + (id[1] >= 0 ? exp(l[1] - top) : 0.0), plus);
+    }
+    const bool nothing = top == -INFINITY;  // but -Inf: every score is 0
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (id[h] >= 0 && !nothing) p[h] = exp(l[h] - top) / sum;
+    const double cp = row16(c[0] * p[0] + c[1] * p[1], plus);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) d[h] = p[h] * (c[h] - cp);
+    if (dense) {
+      const float f = (float)(-cp / sum);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = nothing ? 0.f : f * v[i];
+    }
   }
-  __syncthreads();
-  if (id >= 0) row[id] = (float)d;
-  __syncthreads();
-  for (int e = lane; e < a.E; e += 64) {
-    if constexpr (BF16)
-      static_cast<uint16_t*>(dlogits)[at + e] = f32_to_bf16_rne(row[e]);
-    else
-      static_cast<float*>(dlogits)[at + e] = row[e];
+#pragma unroll
+  for (int i = 0; i < PER; i += 4) {
+    const int e = 4 * (lane + ROUTE_LANES * (i / 4));
+    float o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = dense ? v[i + j] : 0.f;
+    if (e + 4 <= E) {
+      if constexpr (BF16)
+        *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(dlogits) + at + e) =
+            u32x2{(uint32_t)f32_to_bf16_rne(o[0]) | (uint32_t)f32_to_bf16_rne(o[1]) << 16,
+                  (uint32_t)f32_to_bf16_rne(o[2]) | (uint32_t)f32_to_bf16_rne(o[3]) << 16};
+      else
+        *reinterpret_cast<u32x4_any*>(static_cast<float*>(dlogits) + at + e) =
+            u32x4{__float_as_uint(o[0]), __float_as_uint(o[1]), __float_as_uint(o[2]), __float_as_uint(o[3])};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e + j < E) {
+          if constexpr (BF16)
+            static_cast<uint16_t*>(dlogits)[at + e + j] = f32_to_bf16_rne(o[j]);
+          else
+            static_cast<float*>(dlogits)[at + e + j] = o[j];
+        }
+    }
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    if (id[h] >= 0) {
+      if constexpr (BF16)
+        static_cast<uint16_t*>(dlogits)[at + id[h]] = f32_to_bf16_rne((float)d[h]);
+      else
+        static_cast<float*>(dlogits)[at + id[h]] = (float)d[h];
+    }
+}
+
+template <bool BF16>
+static void route_scored_backward(const RouteScored& a, const float* dgates, const int32_t* ids, void* dlogits,
+                                  hipStream_t stream) {
+  const dim3 grid((unsigned)((a.T + ROUTE_ROWS - 1) / ROUTE_ROWS));
+#define MX_ROUTE_BWD(PER) \
+  hipLaunchKernelGGL((route_scored_backward_kernel<BF16, PER>), grid, dim3(64), 0, stream, a, dgates, ids, dlogits)
+  if (a.E <= 64)
+    MX_ROUTE_BWD(4);
+  else if (a.E <= 128)
+    MX_ROUTE_BWD(8);
+  else if (a.E <= 256)
+    MX_ROUTE_BWD(16);
+  else if (a.E <= 512)
+    MX_ROUTE_BWD(32);
+  else
+    MX_ROUTE_BWD(64);
+#undef MX_ROUTE_BWD
 }
 
 int launch_route_scored_backward(const RouteScored& a, const float* dgates, const int32_t* ids, void* dlogits,
                                  hipStream_t stream) {
-  const dim3 grid((unsigned)a.T);
-  if (a.bf16)
-    hipLaunchKernelGGL(route_scored_backward_kernel<true>, grid, dim3(64), 0, stream, a, dgates, ids, dlogits);
-  else
-    hipLaunchKernelGGL(route_scored_backward_kernel<false>, grid, dim3(64), 0, stream, a, dgates, ids, dlogits);
+  a.bf16 ? route_scored_backward<true>(a, dgates, ids, dlogits, stream)
+         : route_scored_backward<false>(a, dgates, ids, dlogits, stream);
   return hip_status(hipGetLastError());
 }
 
