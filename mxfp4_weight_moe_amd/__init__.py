@@ -970,6 +970,15 @@ def _quantized(codes, scales, K: int):
     return T, int(n != K)
 
 
+def _clear_of(out, *ts):
+    """Refuses an output over a tensor that other workgroups still read while it is written."""
+    o, n = out.data_ptr(), out.numel() * out.element_size()
+    for t, name in ts:
+        i = t.data_ptr()
+        if o < i + t.numel() * t.element_size() and i < o + n:
+            raise ValueError(f"out must not overlap {name}")
+
+
 def _two_d(t, name: str):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name} must be a 2-d tensor")
@@ -996,6 +1005,7 @@ def mx_linear_quantized(codes: torch.Tensor, scales: torch.Tensor, w_codes: torc
         out = codes.new_empty((T, N), dtype=_BF16)
     else:
         _tensor(out, "out", _BF16, (T, N), dev)
+        _clear_of(out, (codes, "codes"), (scales, "scales"))
         if residual is not None:
             _apart(out, residual, "residual", itself=True)
     z = codes.new_empty((T, N), dtype=_BF16) if save_z else None
@@ -1078,8 +1088,8 @@ def moe_route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", b
     dev = logits.device
     if bias is not None:
         _tensor(bias, "bias", _F32, (E,), dev)
-    if top_k < 1:
-        raise ValueError(f"top_k must be at least 1, got {top_k}")
+    if not 1 <= top_k <= min(E, MX_MAX_TOPK):
+        raise ValueError(f"top_k must be 1 to {min(E, MX_MAX_TOPK)}, got {top_k}")
     sc, gs = _choice(_SCORES, score, "score"), _choice(_GROUP_SCORES, group_score, "group_score")
     if ids is None:
         ids = logits.new_empty((T, top_k), dtype=_I32)
@@ -1089,6 +1099,8 @@ def moe_route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", b
         gates = logits.new_empty((T, top_k), dtype=_F32)
     else:
         _tensor(gates, "gates", _F32, (T, top_k), dev)
+        _clear_of(gates, (logits, "router_logits"), (ids, "ids"))
+    _clear_of(ids, (logits, "router_logits"))
     _call(_lib.moe_route_scored, dev, logits.data_ptr(), kind, _opt(bias), sc, n_group, topk_group, gs,
           1 if renormalize else 0, scale, ids.data_ptr(), gates.data_ptr(), T, E, top_k)
     return ids, gates

@@ -482,6 +482,47 @@ def test_unaligned_scales(mx):
         assert torch.equal(one, mx.mx_linear_quantized(a, sa2, w, s2))
 
 
+def test_offsets_beyond_32_bits(mx):
+    """9 GB of activation codes, and 4.5 GB of weight codes: rows at the far end against the formula."""
+    g = gen(3)
+    K = 8192
+    w, s = weights(64, K, g)
+    T = (1 << 20) + 77
+    dg = torch.Generator(device=DEV)
+    dg.manual_seed(1)
+    a = torch.randint(0, 120, (T, K), generator=dg, dtype=torch.uint8, device=DEV)
+    sa = torch.randint(118, 124, (T, K // 32), generator=dg, dtype=torch.uint8, device=DEV)
+    say("far tokens")
+    y = mx.mx_linear_quantized(a, sa, *cuda(w, s))
+    for at in (0, T // 2, T - 40):
+        z, ez = z_of(a[at:at + 40], sa[at:at + 40], "mxfp8", w, s, None)
+        within(y[at:at + 40], z, (1 + B) * ez + B * z.abs(), f"tokens from {at}")
+    del a, sa, y
+    N = (1 << 20) + 131
+    w = torch.randint(0, 256, (N, K // 2), generator=dg, dtype=torch.uint8, device=DEV)
+    s = torch.randint(115, 122, (N, K // 32), generator=dg, dtype=torch.uint8, device=DEV)
+    for T in (3, 24, 70, 300):
+        a, sa = activations(T, K, "mxfp4", g)
+        say("far rows", T)
+        y = mx.mx_linear_quantized(*cuda(a, sa), w, s)
+        for at in (0, N // 2, N - 50):
+            z, ez = z_of(a, sa, "mxfp4", w[at:at + 50], s[at:at + 50], None)
+            within(y[:, at:at + 50], z, (1 + B) * ez + B * z.abs(), f"rows from {at}")
+
+
+def test_quantize_beyond_32_bits_of_threads(mx):
+    """More than 2^35 values: threads past 2^32, a launch's limit along x."""
+    K = 1 << 15
+    rows = (1 << 20) + 3
+    x = torch.ones(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[-1] = torch.arange(K, device=DEV).to(torch.bfloat16) - 7
+    codes, scales = mx.mx_quantize(x, "mxfp4")
+    for at in (0, rows // 2, rows - 2):
+        assert (codes[at] == 0x66).all() and (scales[at] == 125).all()  # 1 = 4 * 2^-2
+    code, byte = quantize_ref(x[-1:].double().cpu().numpy(), "mxfp4")
+    assert np.array_equal(codes[-1:].cpu().numpy(), pack(code, "mxfp4")) and np.array_equal(scales[-1:].cpu().numpy(), byte)
+
+
 def test_product_refusals(mx):
     g = gen(1)
     a, sa, (w, s) = *activations(4, 64, "mxfp8", g), weights(32, 64, g)
@@ -500,6 +541,8 @@ def test_product_refusals(mx):
             mx.mx_gate_up_quantized(a, sa, w, s, **bad)
     with pytest.raises(ValueError):  # I = 16
         mx.mx_gate_up_quantized(a, sa, w, s, fmt="mxfp8")
+    with pytest.raises(ValueError, match="overlap"):
+        mx.mx_linear_quantized(a, sa, w[:32].contiguous(), s[:32].contiguous(), out=a.view(torch.bfloat16))
     with pytest.raises(ValueError):
         mx.mx_gate_up_quantized(a, sa, w[:31].contiguous(), s[:31].contiguous())
 
