@@ -631,9 +631,10 @@ MX_API int mx_gate_up_quantized(const uint8_t* a_codes, const uint8_t* a_scales,
  *   ids    = the top_k largest keys among them in descending order (ties to the lower id); without a
  *           bias the order is that of the logits
  *   gates[t,j] = scale * p[ids[j]], divided by sum_i p[ids[i]] with renormalize
- * Keys and group values are compared in 64 bits, gates rounded once to fp32.  NaN logits sort below all
- * others, and their row's gates are NaN (softmax) or NaN where chosen (sigmoid); an expert masked
- * with -Inf has score 0; a row of nothing but -Inf, or whose chosen scores sum to 0, has gates 0.
+ * Keys and group values are compared in 64 bits, gates rounded once to fp32.  NaN logits (and NaN keys
+ * and group values, which biases of +Inf and -Inf make) sort below all others; a row with a NaN logit has
+ * gates NaN (softmax) or NaN where it is chosen (sigmoid); an expert masked with -Inf has score 0; a row
+ * of nothing but -Inf, or whose chosen scores sum to 0, has gates 0.
  *   logits  logits_type [T, E];  bias  optional, fp32 [E];  ids int32 [T, top_k], gates fp32
  *   [T, top_k] (written)
  *   E <= MX_MAX_EXPERTS, top_k <= MX_MAX_TOPK, n_group <= MX_MAX_GROUPS and divides E,

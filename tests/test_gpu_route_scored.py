@@ -52,7 +52,7 @@ def ref(l, k, kind, bias, groups, kept, by, renorm, scale):
     order = low(l) if bias is None else key
     if groups > 1:
         per = key.reshape(T, groups, -1).sort(dim=-1, descending=True)[0]
-        val = per[..., 0] if by == "max" or per.shape[-1] == 1 else per[..., 0] + per[..., 1]
+        val = per[..., 0] if by == "max" or per.shape[-1] == 1 else low(per[..., 0] + per[..., 1])
         rank = val.sort(dim=-1, descending=True, stable=True)[1].argsort(-1)
         shut = (rank >= kept).repeat_interleave(E // groups, 1)
         # shut experts after all others, whatever their keys
@@ -423,3 +423,23 @@ def test_router_of_a_moe_block(mx):
     h = mx.mx_gate_up_quantized(codes, scales, W[0][0], W[1][0], fmt="mxfp8")
     y = mx.mx_linear_quantized(*h, W[2][0], W[3][0], residual=routed)
     assert bool(y.isfinite().all()) and y.shape == (T, H)
+
+
+@pytest.mark.parametrize("kind", ["softmax", "sigmoid"])
+def test_infinite_biases(mx, kind):
+    """-Inf shuts an expert and +Inf forces it; a group with both sums to NaN and counts as the lowest."""
+    g = gen(21)
+    l = torch.randn(70, 64, generator=g)
+    bias = torch.randn(64, generator=g) * 0.1
+    shut = bias.clone()
+    shut[::3] = -math.inf
+    forced = bias.clone()
+    forced[[5, 40]] = math.inf
+    both = bias.clone()
+    both[8:16] = -math.inf
+    both[24:32] = -math.inf
+    both[[9, 30]] = math.inf
+    for name, b in (("shut", shut), ("forced", forced), ("both", both)):
+        for groups, kept, by in ((1, 1, "max"), (8, 3, "top2"), (8, 6, "top2"), (8, 7, "top2"), (8, 3, "max")):
+            say("infinite", kind, name, groups, kept, by)
+            check(mx, l, 8, kind, b, groups, kept, by, True, what=name)
