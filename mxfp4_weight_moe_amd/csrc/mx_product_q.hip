@@ -52,6 +52,8 @@ __device__ __forceinline__ f32x4 mfma_stream_q(const u32x4& w, const QFragment<F
 // A workgroup has 16 weight rows (gate_up: 8 gate rows and the 8 up rows of the same columns), its W
 // waves split K.  A lane loads its operands straight from memory, 256 values (Q_UNIT) at a time and 4 of
 // those ahead: two 16-byte pieces of a weight row, four (two) of a token, 8 scale bytes of each.
+// Bound by latency: 7168 -> 4096, 15.6 MB, takes 6.5 us in MXFP8 and 6.1 in MXFP4 for 1 token (2.5 TB/s), 9.0 and 7.6
+// for 16, of which a launch and a first load are about 3.  16 waves a workgroup or 2 units ahead are equal.
 constexpr int Q_UNIT = 256;
 template <int FMT, int W, int MT, bool GATED, class Epilogue>
 __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T,
@@ -168,6 +170,22 @@ __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue 
 
 // ------------------------------------------------------------------ tiles
 
+// In a step, half a stage, a wave reads the next step's operands between its products (in the first half of
+// them) and issues half of a later stage's copies.  The one barrier of a stage lies between its two steps: the
+// second one's operands are in registers then, so the stage's buffer is free for the one D stages on.
+//
+// 256 x 256 (4096 x 7168 x 4096 with gelu, bias and residual 77 to 80 us in MXFP4; gate_up, H 7168, I 2048,
+// 4096 tokens, from and to MXFP8 86 to 91): each of 8 waves has 64 x 128, two waves a SIMD, so that one's products run
+// beside the other's reads (4 waves of 128 x 128: 86 for 80 at the time).  What bounds it: the products alone take
+// 32 us (MXFP4) and 55 (MXFP8), at the 7.0 and 3.4 PFLOP/s that they reach on random data here; with reads, scales
+// and barriers 44 and 64; with the copies 59 and 81; the epilogue of the one round of tiles is 8 to 19 more.  The
+// copies bring 1.8 and 2.8 MB to each CU, 37 and 55 us at the 50 kB a microsecond that a CU gets elsewhere.
+// MFMA busy 35% and 61% of the cycles at 2.0 GHz; LDS conflicts 1 cycle in 10.  Equal or slower: waves of 128 x 64,
+// lines requested into L2 6 to 12 stages ahead (80 for 77), other places for the reads among the products, wave
+// priorities.
+//
+// D, stages in the LDS: what fits beside one more workgroup on the CU, or, where a workgroup is alone there,
+// twice that.
 template <int FMT, int MT, int NT, int WM, int WN, int D, bool GATED, class Epilogue>
 __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::PER_SIMD))
     tile_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T, int K, int rows, int mtiles, int ntiles,
@@ -362,6 +380,11 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
 // A workgroup takes 32 NT weight rows (gate_up: half of them gate rows, half the up rows of the same
 // columns) and all tokens; a wave 32 tokens and one of KS parts of K.  A wave copies what it needs into a ring
 // of its own in the LDS, no barriers in the loop; the parts' sums meet in the LDS.
+// Bound by what a CU reads (50 kB a microsecond): 7168 -> 4096, 32 tokens, 128 workgroups with 0.34 MB each, takes
+// 10.5 us in MXFP8, 10.2 in MXFP4; 2048 -> 7168, 64 tokens, 6.8 and 6.5.  gate_up whose output is quantized needs 64
+// rows a workgroup, a block of 32 columns: H 7168, I 2048, 24 tokens 13 us on 64 CUs.  (Parts of K over more CUs and
+// a second launch to sum them should save some 2 of these in a graph, by what quantized_plan counts, and cost
+// other callers a launch and a workspace, some 4.)
 constexpr int THIN_Q_MAX_T = 64;
 template <int FMT, int NT>
 struct ThinQStage {
@@ -499,7 +522,7 @@ __global__ void __launch_bounds__(512, 2) thin_q_kernel(QOperands o, Epilogue ep
 
 // Thin tiles copy a stage's scales as dwords: whole groups of them, whose rows are aligned.  From 33 tokens
 // on they read the weights twice and a long reduction goes to tiles (64 tokens in MXFP8: 2048 -> 7168 6.8 us,
-// with tiles 14.4; 7168 -> 4096 16.4 and 13.2).
+// with tiles 14.4; 7168 -> 4096 16.4 and 11.6).
 static bool takes_thin_q(int64_t T, int64_t K) {
   return T > 16 && T <= (K <= 4096 ? THIN_Q_MAX_T : 32) && K % (Q_KB * Q_GROUP) == 0;
 }
@@ -534,8 +557,8 @@ TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool qua
     if (p.mt < 4 && tiles(2) <= GPU_CUS) {
       // Fewer tiles than CUs: 128 or 64 weight rows a tile, K whole or in parts, by what a workgroup reads
       // (a CU's read path gives some 50 kB a microsecond) and what parts cost (written at 3 and read at
-      // 4 MB a microsecond, 2.5 for the second launch).  7168 -> 4096 in MXFP8: 128 tokens 16.6 us with 64 rows in 4
-      // parts, 19.3 with 128 rows in 8; 2048 -> 7168, 128 tokens: 10.5 with 64 rows whole, 19.4 with 128 in 4.
+      // 4 MB a microsecond, 2.5 for the second launch).  7168 -> 4096 in MXFP8: 128 tokens 14.3 us with 64 rows in 4
+      // parts, 19.3 with 128 rows in 8; 2048 -> 7168, 128 tokens: 10.7 with 64 rows whole, 19.4 with 128 in 4.
       double least = 0;
       for (int nt = 2; nt >= 1; --nt)
         for (int64_t split = 1; split <= groups && split * tiles(nt) <= GPU_CUS; ++split) {
