@@ -174,23 +174,26 @@ __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue 
 // them) and issues half of a later stage's copies.  The one barrier of a stage lies between its two steps: the
 // second one's operands are in registers then, so the stage's buffer is free for the one D stages on.
 //
-// 256 x 256 (4096 x 7168 x 4096 with gelu, bias and residual 77 to 80 us in MXFP4; gate_up, H 7168, I 2048,
+// 256 x 256 (4096 x 7168 x 4096 with gelu, bias and residual 74 us in MXFP4; gate_up, H 7168, I 2048,
 // 4096 tokens, from and to MXFP8 86 to 91): each of 8 waves has 64 x 128, two waves a SIMD, so that one's products run
 // beside the other's reads (4 waves of 128 x 128: 86 for 80 at the time).  What bounds it: the products alone take
 // 32 us (MXFP4) and 55 (MXFP8), at the 7.0 and 3.4 PFLOP/s that they reach on random data here; with reads, scales
-// and barriers 44 and 64; with the copies 59 and 81; the epilogue of the one round of tiles is 8 to 19 more.  The
-// copies bring 1.8 and 2.8 MB to each CU, 37 and 55 us at the 50 kB a microsecond that a CU gets elsewhere.
-// MFMA busy 35% and 61% of the cycles at 2.0 GHz; LDS conflicts 1 cycle in 10.  Equal or slower: waves of 128 x 64,
+// and barriers 44 and 64; with the copies 55 and 81; the epilogue of the one round of tiles is 8 to 19 more.  The
+// copies bring 1.8 and 2.8 MB to each CU, 24 and 42 us at what a CU reads with nothing else to do.
+// MFMA busy 61% of the cycles at 2.0 GHz in MXFP8; LDS conflicts 1 cycle in 10.  Equal or slower: waves of 128 x 64,
 // lines requested into L2 6 to 12 stages ahead (80 for 77), other places for the reads among the products, wave
 // priorities.
 //
-// D, stages in the LDS: what fits beside one more workgroup on the CU, or, where a workgroup is alone there,
-// twice that.
-template <int FMT, int MT, int NT, int WM, int WN, int D, bool GATED, class Epilogue>
-__global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::PER_SIMD))
+// KB: whole lines of either operand in MXFP4 (4096 tokens 75 us for 80, 2048 44 for 51), but not in tiles of few
+// waves, which wait for the larger stage (300 tokens 7168 -> 4096 20.5 for 17.7).  MXFP8 has no LDS for it.
+// D, stages in the LDS: all that it holds for 256 x 256, half of that where two workgroups share a CU, and where
+// one is alone 4 or 3 stages: more only lets the first stage wait behind the others (128 tokens
+// 7168 -> 4096 in MXFP8 with 768 values 14.5 us, 512 13.9, 384 14.2; 2048 -> 7168, 300 tokens, 12.1, 11.5 and 11.9).
+template <int FMT, int KB, int MT, int NT, int WM, int WN, int D, bool GATED, class Epilogue>
+__global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, KB, MT, NT, WM, WN, D>::PER_SIMD))
     tile_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T, int K, int rows, int mtiles, int ntiles,
                   int nsplit) {
-  typedef QLds<FMT, MT, NT, WM, WN, D> L;
+  typedef QLds<FMT, KB, MT, NT, WM, WN, D> L;
   constexpr int WCOLS = NT * 32 / (GATED ? 2 : 1), HALF = GATED ? NT / 2 : NT, COLS = WN * WCOLS;
   __shared__ __attribute__((aligned(16))) uint8_t lds[L::BYTES];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -201,11 +204,12 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   const int split = tile % nsplit, id = tile / nsplit, band = id / (4 * ntiles), high = min(4, mtiles - 4 * band);
   const int mt0 = 4 * band + (id - 4 * band * ntiles) % high, nt = (id - 4 * band * ntiles) / high;
   const int m0 = mt0 * L::BM, n0 = nt * COLS;
-  const int stages = (K + Q_KB - 1) / Q_KB, full = K / Q_KB, tail = (K >> 5) & 3;
+  constexpr int STEPS = L::STEPS, GROUP = L::GROUP;
+  const int stages = (K + KB - 1) / KB, full = K / KB, tail = K % KB >> 5;
   // K is split at whole groups of scales
-  const int groups = (stages + Q_GROUP - 1) / Q_GROUP;
+  const int groups = (K + Q_KG - 1) / Q_KG;
   const int g0 = (int)((int64_t)groups * split / nsplit), g1 = (int)((int64_t)groups * (split + 1) / nsplit);
-  const int st0 = g0 * Q_GROUP, st1 = min(g1 * Q_GROUP, stages);
+  const int st0 = g0 * GROUP, st1 = min(g1 * GROUP, stages);
 
   // Row lr of the workgroup's weight rows: row r of MFMA tile lr >> 5, counted from the tile's first row in the
   // gate or the up half; past the last row (or token) the last one again, never stored.
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   cs.init(K >> 1, min(COLS, rows - n0), wave, lane, [&](int lr) { return o.w + weight_half(lr) * (size_t)(K >> 1); }, weight_row);
   QScales<L::BM, L::BN, 64 * WM * WN> sc;
   const size_t ks = (size_t)(K >> 5);
-  sc.init(K, K % (Q_KB * Q_GROUP) == 0, [&](int lr) {
+  sc.init(K, K % Q_KG == 0, [&](int lr) {
     return lr < L::BM ? o.as + (size_t)(m0 + token_row(lr)) * ks
                       : o.ws + (weight_half(lr - L::BM) + weight_row(lr - L::BM)) * ks;
   });
@@ -249,9 +253,9 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   typedef std::integral_constant<int, LOADS> AllOnes;
   const int r = lane & 31, g = lane >> 5;
   constexpr int AF = FMT / 4;  // 16-byte pieces of a fragment
-  uint32_t at[2][AF], wat[2];
+  uint32_t at[STEPS][AF], wat[STEPS];
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
+  for (int u = 0; u < STEPS; ++u) {
 #pragma unroll
     for (int p = 0; p < AF; ++p) {
       const int c = FMT == 8 ? 4 * u + 2 * p + g : 2 * u + g;
@@ -267,13 +271,13 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   tile_zero(acc);
   QFragment<FMT> frag[2][MT];
   u32x4 w[2][NT];
-  // A group's scales, a dword a stage; shifted right by 8 g ahead of its stage, so that byte 0 is this
-  // lane's in step 0 and byte 2 in step 1.
-  uint32_t sa[MT][Q_GROUP], sw[NT][Q_GROUP];
+  // A group's scales, a dword for two steps; shifted right by 8 g ahead of them, so that byte 0 is this
+  // lane's in the first and byte 2 in the second.
+  uint32_t sa[MT][4], sw[NT][4];
   auto scale_at = [&](int group, int e) {
     return lds + (group & 1) * L::SCALES + (e < MT ? sat + e * 512 : wsat + (e - MT) * 512);
   };
-  auto read_scales = [&](int group, int e) {  // of the first three stages
+  auto read_scales = [&](int group, int e) {  // of all steps but the last two
     typedef unsigned u32x3 __attribute__((ext_vector_type(3), aligned(16)));
     const u32x3 v = *reinterpret_cast<const u32x3*>(scale_at(group, e));
 #pragma unroll
@@ -282,15 +286,15 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   auto read_last_scale = [&](int group, int e) {  // whose register the products still read meanwhile
     (e < MT ? sa[e][3] : sw[e - MT][3]) = *reinterpret_cast<const uint32_t*>(scale_at(group, e) + 12);
   };
-  auto shift_scale = [&](int stage, int e) {
-    uint32_t& s = e < MT ? sa[e][stage] : sw[e - MT][stage];
+  auto shift_scale = [&](int pair, int e) {
+    uint32_t& s = e < MT ? sa[e][pair] : sw[e - MT][pair];
     s >>= 8 * g;
   };
   auto read = [&](const uint8_t* buf, int u, int e) {  // piece e of a step's operands
     if (e < NT)
-      w[u][e] = ld16(buf + wat[u] + e * (32 * L::WRB));
+      w[u & 1][e] = ld16(buf + wat[u] + e * (32 * L::WRB));
     else
-      frag[u][(e - NT) / AF].v[(e - NT) % AF] = ld16(buf + at[u][(e - NT) % AF] + (e - NT) / AF * (32 * L::ARB));
+      frag[u & 1][(e - NT) / AF].v[(e - NT) % AF] = ld16(buf + at[u][(e - NT) % AF] + (e - NT) / AF * (32 * L::ARB));
   };
   constexpr int SLOTS = MT * NT, READS = NT + MT * AF, SCALES = MT + NT;
   auto buffer_of = [&](int i) { return lds + i * L::ONE; };
@@ -318,52 +322,52 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
   int cur = 0, fill = D - 1;  // buffers of the current stage, and of the one D - 1 stages on
   for (int group = g0; group < g1; ++group) {
     const bool more = group + 1 < g1;
-    unrolled<Q_GROUP>([&](auto G) __attribute__((always_inline)) {
+    unrolled<GROUP>([&](auto G) __attribute__((always_inline)) {
       constexpr int stage = G;
-      const int st = group * Q_GROUP + stage;
+      const int st = group * GROUP + stage;
       if (st >= st1) return;
       if (stage == 0 && more) sc.load(group + 1, scales_of(group + 1));
       const int nxt = cur + 1 == D ? 0 : cur + 1;
       const int c0 = min(st + D - 1, st1 - 1), c1 = min(st + D, st1 - 1);
-      unrolled<2>([&](auto U) __attribute__((always_inline)) {
-        constexpr int u = U;
-        if constexpr (u == 0) {
-          prepare(c0, FirstOnes{}, OtherOnes{});
-        } else {
-          if (stage == Q_GROUP - 1 && more) sc.store(scales_of(group + 1));
+      unrolled<STEPS>([&](auto U) __attribute__((always_inline)) {
+        constexpr int u = U, pair = (stage * STEPS + u) / 2;
+        constexpr bool last_step = u == STEPS - 1;
+        if constexpr (u == 0) prepare(c0, FirstOnes{}, OtherOnes{});
+        if constexpr (last_step) {
+          if (stage == GROUP - 1 && more) sc.store(scales_of(group + 1));
           // the next stage has landed for every wave (and, at a group's end, the next one's scales, which
-          // three and a half stages of copies follow), and no wave reads the current one any more
-          constexpr int LATER = (D - 2) * LOADS, SINCE = 4 * LOADS - FIRST;
-          q_barrier<(stage == Q_GROUP - 1 && SINCE < LATER ? SINCE : LATER)>();
+          // the copies of nearly a group follow), and no wave reads the current one any more
+          constexpr int LATER = (D - 2) * LOADS, SINCE = GROUP * LOADS - FIRST;
+          q_barrier<(stage == GROUP - 1 && SINCE < LATER ? SINCE : LATER)>();
           prepare(c1, FromFirst{}, FirstOnes{});
         }
         unrolled<SLOTS>([&](auto S) __attribute__((always_inline)) {
           constexpr int k = S, m = k / NT, i = k % NT;
-          mfma_q<u>(acc[m][i], w[u][i], frag[u][m], sw[i][stage], sa[m][stage]);
+          mfma_q<(u & 1)>(acc[m][i], w[u & 1][i], frag[u & 1][m], sw[i][pair], sa[m][pair]);
           // the next step's operands, in the first half
-          constexpr bool first_three = u == 1 && stage == Q_GROUP - 1, last = u == 0 && stage == 0;
+          constexpr bool first_three = last_step && stage == GROUP - 1, last = u == 0 && stage == 0;
           constexpr int RS = first_three || last ? SCALES : 0, HALF_SLOTS = (SLOTS + 1) / 2;
           unrolled<RS + READS>([&](auto E) __attribute__((always_inline)) {
             if constexpr (E * HALF_SLOTS / (RS + READS) == k) {
               if constexpr (E < READS)
-                read(buffer_of(u == 0 ? cur : nxt), 1 - u, E);
+                read(buffer_of(last_step ? nxt : cur), (u + 1) % STEPS, E);
               else if constexpr (first_three)
                 read_scales(group + 1, E - READS);
               else
                 read_last_scale(group, E - READS);
             }
           });
-          if constexpr (u == 1 && k == SLOTS - 1)
-            unrolled<SCALES>([&](auto E) __attribute__((always_inline)) { shift_scale((stage + 1) % Q_GROUP, E); });
+          if constexpr ((u & 1) && k == SLOTS - 1)
+            unrolled<SCALES>([&](auto E) __attribute__((always_inline)) { shift_scale((pair + 1) % 4, E); });
           unrolled<LOADS>([&](auto E) __attribute__((always_inline)) {
-            if constexpr (u == 1 && E < FIRST && E * SLOTS / FIRST == k) copy(buffer_of(cur), c1, E);
+            if constexpr (last_step && E < FIRST && E * SLOTS / FIRST == k) copy(buffer_of(cur), c1, E);
             if constexpr (u == 0 && E >= FIRST && (E - FIRST) * SLOTS / (LOADS - FIRST) == k) copy(buffer_of(fill), c0, E);
           });
           keep_order();
         });
-        if constexpr (u == 1) {
-          scales_ready(sa, (stage + 1) % Q_GROUP);
-          scales_ready(sw, (stage + 1) % Q_GROUP);
+        if constexpr (u & 1) {
+          scales_ready(sa, (pair + 1) % 4);
+          scales_ready(sw, (pair + 1) % 4);
         }
       });
       fill = cur;
@@ -386,6 +390,7 @@ __global__ void __launch_bounds__(64 * WM * WN, (QLds<FMT, MT, NT, WM, WN, D>::P
 // a second launch to sum them should save some 2 of these in a graph, by what quantized_plan counts, and cost
 // other callers a launch and a workspace, some 4.)
 constexpr int THIN_Q_MAX_T = 64;
+constexpr int Q_KB = 128;  // values of a stage
 template <int FMT, int NT>
 struct ThinQStage {
   static constexpr int ARB = Q_KB * FMT / 8, A = 32 * ARB, CODES = 32 * NT * (Q_KB / 2);
@@ -524,15 +529,14 @@ __global__ void __launch_bounds__(512, 2) thin_q_kernel(QOperands o, Epilogue ep
 // on they read the weights twice and a long reduction goes to tiles (64 tokens in MXFP8: 2048 -> 7168 6.8 us,
 // with tiles 14.4; 7168 -> 4096 16.4 and 11.6).
 static bool takes_thin_q(int64_t T, int64_t K) {
-  return T > 16 && T <= (K <= 4096 ? THIN_Q_MAX_T : 32) && K % (Q_KB * Q_GROUP) == 0;
+  return T > 16 && T <= (K <= 4096 ? THIN_Q_MAX_T : 32) && K % Q_KG == 0;
 }
 static bool takes_stream_q(int64_t T, int64_t K) { return T <= STREAM_Q_MAX_T && !takes_thin_q(T, K); }
 
 // What a round of tiles takes, of 256 x 256 (one a CU) and of 128 x 128 (two a CU), in microseconds at a
-// reduction of 7168: MXFP8 92 and 58, MXFP4 70 and 50 (4096 and 2048 tokens, 7168 -> 4096).  E.g. 2048
-// tokens take 69 and 58 with the large tiles for 58 and 50 with the small ones, 4096 tokens 92 and 70 for 114
-// and 96.
-constexpr int Q8_ROUND_256 = 92, Q8_ROUND_128 = 58, Q4_ROUND_256 = 70, Q4_ROUND_128 = 50;
+// reduction of 7168: MXFP8 92 and 58, MXFP4 66 and 44 (4096 and 2048 tokens, 7168 -> 4096).  E.g. in MXFP8 2048
+// tokens take 69 with the large tiles for 58 with the small ones, 4096 tokens 92 for 114.
+constexpr int Q8_ROUND_256 = 92, Q8_ROUND_128 = 58, Q4_ROUND_256 = 66, Q4_ROUND_128 = 44;
 
 // quantized: the product's output is, which a workgroup of the streaming kernel, with fewer columns
 // than a block, leaves to a second launch.
@@ -550,7 +554,7 @@ TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool qua
   if (!takes_stream_q(T, K)) {
     const bool eight = format == MX_FORMAT_MXFP8;
     p.mt = T <= 64 ? 1 : tile_choice(T, rows * (gated ? 2 : 1), eight ? Q8_ROUND_256 : Q4_ROUND_256, eight ? Q8_ROUND_128 : Q4_ROUND_128);
-    const int64_t bm = 64 * p.mt, all = rows * (gated ? 2 : 1), groups = (K + Q_KB * Q_GROUP - 1) / (Q_KB * Q_GROUP);
+    const int64_t bm = 64 * p.mt, all = rows * (gated ? 2 : 1), groups = (K + Q_KG - 1) / Q_KG;
     p.mtiles = (int)((T + bm - 1) / bm);
     p.nt = p.mt == 4 ? 4 : 2;
     auto tiles = [&](int64_t nt) { return (all + 64 * nt - 1) / (64 * nt) * p.mtiles; };
@@ -618,22 +622,23 @@ static int launch_product_q(const QOperands& o, const Epilogue& epi, bool quanti
 #undef MX_STREAM_Q
   } else {
     const dim3 grid((unsigned)(p.mtiles * p.ntiles * p.nsplit));
-#define MX_TILE_Q(MT, NT, WM, WN, D)                                                                                 \
-  hipLaunchKernelGGL((tile_q_kernel<FMT, MT, NT, WM, WN, D, GATED, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, o, \
-                     epi, p.nsplit > 1 ? parts : nullptr, T, K, rows, p.mtiles, p.ntiles, p.nsplit)
+#define MX_TILE_Q(KB, MT, NT, WM, WN, D)                                                                             \
+  hipLaunchKernelGGL((tile_q_kernel<FMT, KB, MT, NT, WM, WN, D, GATED, Epilogue>), grid, dim3(64 * WM * WN), 0, stream, \
+                     o, epi, p.nsplit > 1 ? parts : nullptr, T, K, rows, p.mtiles, p.ntiles, p.nsplit)
     const bool alone = (int64_t)p.mtiles * p.ntiles * p.nsplit <= GPU_CUS;  // a workgroup has its CU's LDS
+    constexpr int LINE = FMT == 8 ? 128 : 256;  // values of a line of activations
     if (p.mt == 4)
-      MX_TILE_Q(2, 4, 4, 2, (FMT == 8 ? 3 : 4));
+      MX_TILE_Q(LINE, 2, 4, 4, 2, (FMT == 8 ? 3 : 2));
     else if (p.mt == 2 && p.nt == 1)
-      MX_TILE_Q(1, 2, 4, 1, (FMT == 8 ? 6 : 8));
+      MX_TILE_Q(128, 1, 2, 4, 1, 4);
     else if (p.mt == 2 && alone)
-      MX_TILE_Q(1, 2, 4, 2, (FMT == 8 ? 6 : 8));
+      MX_TILE_Q(LINE, 1, 2, 4, 2, (FMT == 8 ? 4 : 3));
     else if (p.mt == 2)
-      MX_TILE_Q(1, 2, 4, 2, (FMT == 8 ? 3 : 4));
+      MX_TILE_Q(LINE, 1, 2, 4, 2, (FMT == 8 ? 3 : 2));
     else if (p.nt == 1)
-      MX_TILE_Q(1, 2, 2, 1, (FMT == 8 ? 6 : 8));
+      MX_TILE_Q(128, 1, 2, 2, 1, 4);
     else
-      MX_TILE_Q(1, 2, 2, 2, (FMT == 8 ? 6 : 8));
+      MX_TILE_Q(128, 1, 2, 2, 2, 4);
 #undef MX_TILE_Q
   }
   if (parts) {

@@ -10,17 +10,18 @@
 //   and in either case the scale byte of block g,
 // and holds rows 8 (j >> 2) + 4 g + (j & 3) of column r of the result.
 //
-// A stage is 128 values of the reduction: rows of 128 (E4M3) or 64 bytes, two steps of 64 values.
+// A stage is 128 or 256 values of the reduction, two or four steps of 64.  Rows of 128 bytes a stage are whole
+// lines of memory: a CU reads 75 kB a microsecond of those, 52 of halves (512 rows of 3584 bytes, copies to the LDS
+// and nothing else).
 // Scales stay in the LDS 512 values at a time: 16 bytes a row, so that a row's line is touched once
-// in four stages (a dword a stage would touch as many lines as the codes do).
+// for them (a dword each 128 would touch as many lines as the codes do).
 #pragma once
 #include "mx_quant.hpp"
 #include "mx_tile.hpp"
 
 namespace mx {
 
-constexpr int Q_KB = 128;              // reduction values per stage
-constexpr int Q_GROUP = 4;             // stages whose scales go together
+constexpr int Q_KG = 512;              // whose scales go together
 constexpr uint32_t Q_NOWHERE = 1u << 31;  // a lane offset past the end of every buffer here: reads as zero
 
 // This wave's copies but the last LATER have landed and its LDS accesses are done; then the barrier.
@@ -68,11 +69,12 @@ struct QStage {
   }
 };
 
-// D: stages in the LDS.
-template <int FMT, int MT, int NT, int WM, int WN, int D>
+// KB: values of a stage; D: stages in the LDS.
+template <int FMT, int KB, int MT, int NT, int WM, int WN, int D>
 struct QLds {
   static constexpr int NW = WM * WN, BM = 32 * WM * MT, BN = 32 * WN * NT;
-  static constexpr int ARB = Q_KB * FMT / 8, WRB = Q_KB / 2;  // bytes of a stage of a row
+  static constexpr int STEPS = KB / 64, GROUP = Q_KG / KB;  // of a stage, stages of a group
+  static constexpr int ARB = KB * FMT / 8, WRB = KB / 2;  // bytes of a stage of a row
   typedef QStage<BM, ARB, NW> Rows;
   typedef QStage<BN, WRB, NW> Codes;
   static constexpr int ONE = Rows::BYTES + Codes::BYTES;
