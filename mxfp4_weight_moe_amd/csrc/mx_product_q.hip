@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue 
 // them) and issues half of a later stage's copies.  The one barrier of a stage lies between its two steps: the
 // second one's operands are in registers then, so the stage's buffer is free for the one D stages on.
 //
-// 256 x 256 (4096 x 7168 x 4096 with gelu, bias and residual 74 us in MXFP4; gate_up, H 7168, I 2048,
+// 256 x 256 (4096 x 7168 x 4096 with gelu, bias and residual 73 to 74 us in MXFP4; gate_up, H 7168, I 2048,
 // 4096 tokens, from and to MXFP8 86 to 91): each of 8 waves has 64 x 128, two waves a SIMD, so that one's products run
 // beside the other's reads (4 waves of 128 x 128: 86 for 80 at the time).  What bounds it: the products alone take
 // 32 us (MXFP4) and 55 (MXFP8), at the 7.0 and 3.4 PFLOP/s that they reach on random data here; with reads, scales
@@ -562,7 +562,8 @@ TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool qua
       // Fewer tiles than CUs: 128 or 64 weight rows a tile, K whole or in parts, by what a workgroup reads
       // (a CU's read path gives some 50 kB a microsecond) and what parts cost (written at 3 and read at
       // 4 MB a microsecond, 2.5 for the second launch).  7168 -> 4096 in MXFP8: 128 tokens 14.3 us with 64 rows in 4
-      // parts, 19.3 with 128 rows in 8; 2048 -> 7168, 128 tokens: 10.7 with 64 rows whole, 19.4 with 128 in 4.
+      // parts, 19.3 with 128 rows in 8; 2048 -> 7168, 128 tokens: 10.7 with 64 rows whole, 19.4 with 128 in 4 (14.1 and
+      // 9.6 since, with fewer stages ahead).
       double least = 0;
       for (int nt = 2; nt >= 1; --nt)
         for (int64_t split = 1; split <= groups && split * tiles(nt) <= GPU_CUS; ++split) {
