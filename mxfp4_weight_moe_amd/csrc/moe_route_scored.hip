@@ -560,26 +560,67 @@ int launch_route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStr
 //   sigmoid:  dl[ids] = dp p (1 - p), 0 elsewhere
 //   softmax:  dl = p (dp - sum dp p): dense, but renormalised it is a softmax over the chosen logits,
 //             dl[ids] = q (c - sum c q), 0 elsewhere
-// The few chosen values are worked out in 64 bits (what is left of differences of nearly equal values),
-// the rest of a dense row in 32.
-// 8192 x 256 with k 8: 5.4 us, 17 MB for a dense row's reads and writes, 8 for the others, which write alone (5.2);
-// 32 tokens 3.6.  A wave a row took 10.2: most of its lanes had no chosen value.
+// Where one expert has nearly all of a row, c - sum c q is the difference of two nearly equal values, and
+// with S the gates' digits go too.  So it is never formed: with q the weights of the chosen experts (p, or p / S)
+// and `rest` what the others have (0 renormalised),
+//   c[i] - sum c q = sum over j of (c[i] - c[j]) q[j] + c[i] rest
+// in 64 bits.  The others' exponentials and their sum are fp32, which no difference is formed of; 87 below the row's
+// largest logit they begin to lose digits.
+// 8192 x 256 fp32 with k 8, other logits from call to call: 6.9 us dense, 17 MB read and written (6.2 with the
+// difference formed from an fp32 sum, which left no right digit where the best logit was 16 above the next), 5.2 for
+// the others, which write 8 MB alone; 32 tokens 3.9 and 3.1.  A wave a row took 10.2 where 16 lanes took 5.4: most
+// lanes had no chosen value.
+
+// exp(x) for x <= 0, off by some 3 u of itself however far x is: what the product with log2 e loses in its
+// rounding (1.3 |x| u of the result) is multiplied back in.
+__device__ __forceinline__ float exp_far(float x) {
+  const float t = x * 1.44269504f;
+  const float left = __builtin_fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;  // log2 e = 1.44269504f + that
+  const float e = __builtin_amdgcn_exp2f(t);
+  return x > -126.f ? __builtin_fmaf(e, left * 0.693147181f, e) : e;  // not for -Inf, whose left is NaN
+}
+
+// The same sum in each lane of a row: at every step two lanes add the same two values.
+__device__ __forceinline__ double row16_plus(double v) {
+  v += rotate16<8>(v);
+  v += rotate16<4>(v);
+  v += rotate16<2>(v);
+  return v + rotate16<1>(v);
+}
+// Of lane J of the row.
+template <int J>
+__device__ __forceinline__ double broadcast16(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)b, 0x150 + J, 0xF, 0xF, false);  // row_newbcast
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), 0x150 + J, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Adds the sum over the first n lanes' values j of (c - cj) qj for each of this lane's two c.
+__device__ __forceinline__ void row16_pairs(const double (&c)[2], double cj, double qj, int n, double (&sum)[2]) {
+  unrolled<ROUTE_LANES>([&](auto J) __attribute__((always_inline)) {
+    if (J >= n) return;
+    const double oc = broadcast16<J>(cj), oq = broadcast16<J>(qj);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) sum[i] += (c[i] - oc) * oq;
+  });
+}
 
 // A row has 16 lanes, as in the forward call; k of them (two values each where k > 16) hold the chosen ones.
 // They write their values over the row behind it: the same wave's stores to one address keep their order.
 template <bool BF16, int PER>
 __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a, const float* __restrict__ dgates,
                                                                    const int32_t* __restrict__ ids, void* __restrict__ dlogits) {
-  const int lane = threadIdx.x % ROUTE_LANES;
-  const int64_t t = (int64_t)blockIdx.x * ROUTE_ROWS + threadIdx.x / ROUTE_LANES;
+  constexpr int WORDS = PER > 32 ? 2 : 1;
+  __shared__ uint32_t chosen[ROUTE_ROWS * ROUTE_LANES * WORDS];  // of a lane's places
+  const int lane = threadIdx.x % ROUTE_LANES, row = threadIdx.x / ROUTE_LANES;
+  const int64_t t = (int64_t)blockIdx.x * ROUTE_ROWS + row;
   if (t >= a.T) return;
   const size_t at = (size_t)t * a.E;
   const int E = a.E;
   const bool dense = !a.sigmoid && !a.renormalize;
-  auto plus = [](double x, double y) { return x + y; };
   auto most = [](double x, double y) { return x > y ? x : (y == y ? y : x); };
   int id[2] = {-1, -1};
-  double c[2] = {}, l[2] = {-INFINITY, -INFINITY}, p[2] = {}, d[2];
+  double c[2] = {}, l[2] = {-INFINITY, -INFINITY}, q[2] = {}, d[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int j = lane + ROUTE_LANES * h;
@@ -590,9 +631,12 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
     c[h] = (double)a.scale * (double)dgates[t * a.k + j];
     l[h] = (double)logit_at<BF16>(a.logits, at + e);
   }
-  float v[PER];  // of a dense row the logits, then -p cp
-  float top32 = 0.f;
+  float v[PER];  // of a dense row the logits, their exponentials, then -p sum c p
+  float top32 = 0.f, z = 0.f;  // the largest logit; the sum of the exponentials that are not chosen
   if (dense) {
+    uint32_t* const mine = chosen + (row * ROUTE_LANES + lane) * WORDS;
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) mine[w] = 0;
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; i += 4) {
@@ -615,47 +659,61 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
       for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i + j]);
     }
     top32 = route_value(row16_max(route_key(m)));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = exp_far(v[i] - top32);
+    // where a lane's logits are chosen ones: its places' bits, from the lanes that have the ids
+    row_written();
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (id[h] >= 0) {
+        const int place = 4 * (id[h] >> 6) + (id[h] & 3);
+        atomicOr(&chosen[(row * ROUTE_LANES + ((id[h] >> 2) & 15)) * WORDS + (place >> 5)], 1u << (place & 31));
+      }
+    row_written();
+    uint32_t taken[WORDS];
+#pragma unroll
+    for (int w = 0; w < WORDS; ++w) taken[w] = mine[w];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) z += (taken[i / 32] >> (i & 31)) & 1 ? 0.f : v[i];
+    z = row16_sum(z);
   }
+  double rest = 0.0;
   if (a.sigmoid) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (id[h] >= 0) p[h] = 1.0 / (1.0 + exp(-l[h]));
-    double s = 1.0, cp = 0.0;
+      if (id[h] >= 0) q[h] = 1.0 / (1.0 + exp(-l[h]));
     if (a.renormalize) {
-      s = row16(p[0] + p[1], plus);
-      cp = row16(c[0] * p[0] + c[1] * p[1], plus);
-    }
+      const double s = row16_plus(q[0] + q[1]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      d[h] = s == 0.0 ? 0.0 : (c[h] - cp / s) / s;
-      d[h] *= p[h] / (1.0 + exp(l[h]));  // p (1 - p)
+      for (int h = 0; h < 2; ++h) q[h] = s == 0.0 ? 0.0 : q[h] / s;
     }
   } else {
-    double top = dense ? (double)top32 : row16(most(l[0], l[1]), most), sum;
-    if (dense) {
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        v[i] = __expf(v[i] - top32);
-        z += v[i];
-      }
-      z = row16_sum(z);
-      sum = (double)z;
-    } else {
-      sum = row16((id[0] >= 0 ? exp(l[0] - top) : 0.0) + (id[1] >= 0 ? exp(l[1] - top) : 0.0), plus);
-    }
+    const double top = dense ? (double)top32 : row16(most(l[0], l[1]), most);
     const bool nothing = top == -INFINITY;  // but -Inf: every score is 0
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (id[h] >= 0 && !nothing) p[h] = exp(l[h] - top) / sum;
-    const double cp = row16(c[0] * p[0] + c[1] * p[1], plus);
+      if (id[h] >= 0 && !nothing) q[h] = exp(l[h] - top);
+    const double inv = nothing ? 1.0 : 1.0 / (row16_plus(q[0] + q[1]) + (double)z);
+    rest = nothing ? 0.0 : (double)z * inv;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) d[h] = p[h] * (c[h] - cp);
+    for (int h = 0; h < 2; ++h) q[h] *= inv;
     if (dense) {
-      const float f = (float)(-cp / sum);
+      const float f = (float)(-row16_plus(c[0] * q[0] + c[1] * q[1]) * inv);
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = nothing ? 0.f : f * v[i];
     }
+  }
+  if (a.sigmoid && !a.renormalize) {
+    d[0] = c[0], d[1] = c[1];
+  } else {
+    d[0] = c[0] * rest, d[1] = c[1] * rest;
+    row16_pairs(c, c[0], q[0], a.k, d);
+    if (a.k > ROUTE_LANES) row16_pairs(c, c[1], q[1], a.k - ROUTE_LANES, d);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    d[h] *= q[h];
+    if (a.sigmoid && id[h] >= 0) d[h] /= 1.0 + exp(l[h]);  // p (1 - p)
   }
 #pragma unroll
   for (int i = 0; i < PER; i += 4) {

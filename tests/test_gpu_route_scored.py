@@ -443,3 +443,135 @@ def test_infinite_biases(mx, kind):
         for groups, kept, by in ((1, 1, "max"), (8, 3, "top2"), (8, 6, "top2"), (8, 7, "top2"), (8, 3, "max")):
             say("infinite", kind, name, groups, kept, by)
             check(mx, l, 8, kind, b, groups, kept, by, True, what=name)
+
+
+# ------------------------------------------------------------------ confident rows, NaN, scores that vanish
+
+def grad_pairs(dg, l, ids, kind, renorm, scale):
+    """(gradient of the chosen logits, the sizes that its error goes by, gradient of the others, their sizes):
+    the same gradient with no difference of nearly equal values in it.  With q the chosen gates' weights and
+    `rest` what the experts that are not chosen have, c_i - sum c_j q_j = sum (c_i - c_j) q_j + c_i rest."""
+    l, ids, c = l.double(), ids.long(), scale * dg.double()
+    mine = l.gather(1, ids)
+    others = torch.ones_like(l, dtype=torch.bool).scatter(1, ids, False)
+    slope, rest = torch.ones_like(mine), torch.zeros_like(c[:, :1])
+    e_other = torch.zeros_like(l)
+    if kind == "sigmoid":
+        q, slope = torch.sigmoid(mine), torch.sigmoid(-mine)
+        if not renorm:
+            return c * q * slope, (c * q * slope).abs(), e_other, e_other
+    else:
+        top = l.max(1, keepdim=True)[0]
+        e_other = torch.exp(l - top) * others
+        q, rest = torch.exp(mine - top), e_other.sum(1, keepdim=True)
+    total = q.sum(1, keepdim=True) if renorm else q.sum(1, keepdim=True) + rest
+    q, rest, e_other = q / total, 0 * rest if renorm else rest / total, 0 * e_other if renorm else e_other / total
+    diff = c[:, :, None] - c[:, None, :]
+    pairs, size = (diff * q[:, None, :]).sum(2) + c * rest, (diff.abs() * q[:, None, :]).sum(2) + c.abs() * rest
+    return (q * slope * pairs, q * slope * size, -e_other * (c * q).sum(1, keepdim=True),
+            e_other * (c * q).abs().sum(1, keepdim=True))
+
+
+def test_pairs_are_the_gradient():
+    """grad_pairs against the definition p (dp - sum dp p) with 90 digits, on confident rows."""
+    from decimal import Decimal, localcontext
+    g = gen(31)
+    E, k = 7, 3
+    l = torch.randn(4, E, generator=g)
+    l[1, 2] += 20
+    l[2, 2] += 30
+    l[2, 4] = l[2, 2]
+    l[3, 0] += 60
+    dg = torch.randn(4, k, generator=g)
+    dg[2] = 1.0
+    for kind in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            ids = ref(l, k, kind, None, 1, 1, "max", renorm, 1.0)[0]
+            got, size, other, other_size = grad_pairs(dg, l, ids, kind, renorm, 2.5)
+            with localcontext() as ctx:
+                ctx.prec = 90
+                for t in range(4):
+                    v = [Decimal(float(x)) for x in l[t]]
+                    p = [1 / (1 + (-x).exp()) for x in v] if kind == "sigmoid" else [x.exp() for x in v]
+                    if kind == "softmax":
+                        z = sum(p)
+                        p = [x / z for x in p]
+                    c = [Decimal(2.5) * Decimal(float(x)) for x in dg[t]]
+                    at = [int(i) for i in ids[t]]
+                    if renorm:
+                        s = sum(p[i] for i in at)
+                        cp = sum(x * p[i] for x, i in zip(c, at)) / s
+                        c = [(x - cp) / s for x in c]
+                    dp = [Decimal(0)] * E
+                    for x, i in zip(c, at):
+                        dp[i] = x
+                    if kind == "sigmoid":
+                        d = [x * y * (1 - y) for x, y in zip(dp, p)]
+                    else:
+                        m = sum(x * y for x, y in zip(dp, p))
+                        d = [y * (x - m) for x, y in zip(dp, p)]
+                    for j, i in enumerate(at):
+                        assert abs(Decimal(float(got[t, j])) - d[i]) <= Decimal(1e-12) * Decimal(float(size[t, j])) + Decimal(1e-80)
+                    for i in set(range(E)) - set(at):
+                        # renormalised, a logit that is not chosen has no gradient: 0 but for the 90 digits
+                        tol = Decimal(1e-12) * Decimal(float(other_size[t, i])) + Decimal(1e-80)
+                        assert abs(Decimal(float(other[t, i])) - d[i]) <= tol
+
+
+def check_pairs(got, dg, l, ids, kind, renorm, scale, what=""):
+    """Softmax over all experts: the others' exponentials are summed in fp32, r = (E / 16 + 24) u of their sum,
+    which `rest` carries twice and the weights once; another expert's own is off by (1.3 |x| + 2) u, x its
+    distance from the largest of them, and multiplied in fp32.  The rest is 64-bit.  And half a step of the
+    stored type, in bf16 after one of fp32."""
+    want, size, other, other_size = grad_pairs(dg, l, ids, kind, renorm, scale)
+    l, half = l.double(), 2.0 ** -8 if l.dtype == torch.bfloat16 else U
+    dense = kind == "softmax" and not renorm
+    r = (l.shape[1] / 16 + 24) * U if dense else 2.0 ** -40
+    got = got.double().cpu()
+    tol = 3 * r * size + half * 1.01 * want.abs() + 2.0 ** -133
+    worst = float(((got.gather(1, ids.long()) - want).abs() / tol).max())
+    assert worst <= 1, f"{what}: chosen, worst {worst:.3g}"
+    others = torch.ones_like(l, dtype=torch.bool).scatter(1, ids.long(), False)
+    if not dense:
+        assert (got[others] == 0).all(), what
+    elif others.any():
+        x = (torch.where(others, l, torch.full_like(l, -math.inf)).max(1, keepdim=True)[0] - l).clamp(min=0)
+        tol = ((1.3 * x + 6) * U + 2 * r) * other_size + half * 1.01 * other.abs() + 2.0 ** -133
+        worst = float(((got - other).abs() / tol)[others].max())
+        assert worst <= 1, f"{what}: others, worst {worst:.3g}"
+
+
+@pytest.mark.parametrize("kind,renorm", [("softmax", False), ("softmax", True), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("E,k", [(17, 5), (64, 1), (256, 8), (384, 8), (1000, 16), (1024, 32), (40, 32), (32, 32)])
+def test_backward_of_confident_rows(mx, E, k, kind, renorm):
+    """One expert, or two alike, 8 to 60 above all others: their gradients keep their digits, also where
+    dgates are equal and what is left is the others' share alone."""
+    for gap in (8, 12, 16, 20, 30, 60):
+        for bf16 in (False, True):
+            g = gen(E + k + gap)
+            T = 24
+            l = torch.randn(T, E, generator=g) * 0.5
+            if kind == "sigmoid":
+                l -= gap  # whose scores are next to 1 only for the best
+            best = torch.randint(0, E, (T,), generator=g)
+            l[torch.arange(T), best] = 1.0 if kind == "sigmoid" else gap + 2.0
+            two = torch.randint(0, E, (T,), generator=g)
+            l[torch.arange(T)[1::2], two[1::2]] = l[torch.arange(T)[1::2], best[1::2]]
+            l = l.to(torch.bfloat16 if bf16 else torch.float32)
+            dg = torch.randn(T, k, generator=g)
+            dg[T // 2:] = 0.75
+            ids = mx.moe_route_scored(l.to(DEV), k, kind, renormalize=renorm, scale=2.5)[0]
+            d = mx.moe_route_scored_backward(dg.to(DEV), l.to(DEV), ids, kind, renorm, 2.5)
+            check_pairs(d, dg, l, ids.cpu(), kind, renorm, 2.5, f"gap {gap} {bf16}")
+
+
+def test_backward_of_vanishing_sigmoid_scores(mx):
+    """Renormalised sigmoid scores near the end of 64 bits: 1 / sum p is near its other end, the gradient is not."""
+    g = gen(43)
+    l = -700 - 8 * torch.rand(20, 16, generator=g)
+    dg = torch.randn(20, 4, generator=g) * 1e6
+    ids, gates = mx.moe_route_scored(l.to(DEV), 4, "sigmoid", renormalize=True, scale=2.5)
+    assert bool((gates[:, 0] > 0).all())
+    d = mx.moe_route_scored_backward(dg.to(DEV), l.to(DEV), ids, "sigmoid", True, 2.5)
+    assert bool(d.isfinite().all())
+    check_pairs(d, dg, l, ids.cpu(), "sigmoid", True, 2.5)
