@@ -660,7 +660,8 @@ MX_API int moe_route_scored(const void* logits, int logits_type, const float* bi
  *   where an expert is not chosen
  *   dgates  fp32 [T, top_k];  logits, score, renormalize, scale as in the forward call, ids its ids (each
  *   row distinct; ids outside [0, E) are skipped);  dlogits  logits_type [T, E] (written)
- * Rows of the forward's gates 0 have gradient 0.
+ * Rows of the forward's gates 0 have gradient 0.  A softmax row with a NaN logit, chosen or not, has gradient
+ * NaN, as it has gates NaN; a sigmoid row has it where a chosen logit is NaN (renormalised: at all that are chosen).
  */
 MX_API int moe_route_scored_backward(const float* dgates, const void* logits, int logits_type, const int32_t* ids,
                                      int score, int renormalize, float scale, void* dlogits, int64_t T, int64_t E,

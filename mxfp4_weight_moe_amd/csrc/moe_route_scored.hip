@@ -566,10 +566,11 @@ int launch_route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStr
 //   c[i] - sum c q = sum over j of (c[i] - c[j]) q[j] + c[i] rest
 // in 64 bits.  The others' exponentials and their sum are fp32, which no difference is formed of; 87 below the row's
 // largest logit they begin to lose digits.
-// 8192 x 256 fp32 with k 8, other logits from call to call: 6.9 us dense, 17 MB read and written (6.2 with the
-// difference formed from an fp32 sum, which left no right digit where the best logit was 16 above the next), 5.2 for
-// the others, which write 8 MB alone; 32 tokens 3.9 and 3.1.  A wave a row took 10.2 where 16 lanes took 5.4: most
-// lanes had no chosen value.
+// 8192 x 256 fp32 with k 8, other logits from call to call: softmax 6.9 us, 17 MB read and written (6.2 with the
+// difference formed from an fp32 sum, which left no right digit where the best logit was 16 above the next);
+// renormalised 7.0 (5.4 from the chosen logits alone, which do not say whether there is a NaN); sigmoid 5.2, which
+// writes 8 MB alone; 32 tokens 3.7 and 3.1.  A wave a row took 10.2 where 16 lanes took 5.4: most lanes had no chosen
+// value.
 
 // exp(x) for x <= 0, off by some 3 u of itself however far x is: what the product with log2 e loses in its
 // rounding (1.3 |x| u of the result) is multiplied back in.
@@ -617,7 +618,6 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
   if (t >= a.T) return;
   const size_t at = (size_t)t * a.E;
   const int E = a.E;
-  const bool dense = !a.sigmoid && !a.renormalize;
   auto most = [](double x, double y) { return x > y ? x : (y == y ? y : x); };
   int id[2] = {-1, -1};
   double c[2] = {}, l[2] = {-INFINITY, -INFINITY}, q[2] = {}, d[2];
@@ -631,9 +631,11 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
     c[h] = (double)a.scale * (double)dgates[t * a.k + j];
     l[h] = (double)logit_at<BF16>(a.logits, at + e);
   }
-  float v[PER];  // of a dense row the logits, their exponentials, then -p sum c p
-  float top32 = 0.f, z = 0.f;  // the largest logit; the sum of the exponentials that are not chosen
-  if (dense) {
+  // softmax: the row's logits, their exponentials, then -p sum c p (renormalised 0).  A NaN among them reaches z, and
+  // from there all values of the row, as it reaches all gates of the forward call.
+  float v[PER];
+  float base = 0.f, z = 0.f;  // the largest logit (of nothing but -Inf 0); the sum of the exponentials that are not chosen
+  if (!a.sigmoid) {
     uint32_t* const mine = chosen + (row * ROUTE_LANES + lane) * WORDS;
 #pragma unroll
     for (int w = 0; w < WORDS; ++w) mine[w] = 0;
@@ -658,9 +660,10 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
 #pragma unroll
       for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i + j]);
     }
-    top32 = route_value(row16_max(route_key(m)));
+    base = route_value(row16_max(route_key(m)));
+    if (base == -INFINITY) base = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = exp_far(v[i] - top32);
+    for (int i = 0; i < PER; ++i) v[i] = exp_far(v[i] - base);
     // where a lane's logits are chosen ones: its places' bits, from the lanes that have the ids
     row_written();
 #pragma unroll
@@ -674,7 +677,7 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
 #pragma unroll
     for (int w = 0; w < WORDS; ++w) taken[w] = mine[w];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) z += (taken[i / 32] >> (i & 31)) & 1 ? 0.f : v[i];
+    for (int i = 0; i < PER; ++i) z += (taken[i / 32] >> (i & 31)) & 1 ? 0.f * v[i] : v[i];
     z = row16_sum(z);
   }
   double rest = 0.0;
@@ -688,20 +691,23 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
       for (int h = 0; h < 2; ++h) q[h] = s == 0.0 ? 0.0 : q[h] / s;
     }
   } else {
-    const double top = dense ? (double)top32 : row16(most(l[0], l[1]), most);
-    const bool nothing = top == -INFINITY;  // but -Inf: every score is 0
+    double top = base;
+    if (a.renormalize) {
+      top = row16(most(l[0], l[1]), most);
+      if (top == -INFINITY) top = 0.0;
+      z *= 0.f;
+    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (id[h] >= 0 && !nothing) q[h] = exp(l[h] - top);
-    const double inv = nothing ? 1.0 : 1.0 / (row16_plus(q[0] + q[1]) + (double)z);
-    rest = nothing ? 0.0 : (double)z * inv;
+      if (id[h] >= 0) q[h] = exp(l[h] - top);
+    const double sum = row16_plus(q[0] + q[1]) + (double)z, inv = sum == 0.0 ? 1.0 : 1.0 / sum;
+    rest = (double)z * inv;
 #pragma unroll
     for (int h = 0; h < 2; ++h) q[h] *= inv;
-    if (dense) {
-      const float f = (float)(-row16_plus(c[0] * q[0] + c[1] * q[1]) * inv);
+    const double cp = row16_plus(c[0] * q[0] + c[1] * q[1]);
+    const float f = (float)(a.renormalize ? 0.0 * sum : -cp * inv);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = nothing ? 0.f : f * v[i];
-    }
+    for (int i = 0; i < PER; ++i) v[i] *= f;
   }
   if (a.sigmoid && !a.renormalize) {
     d[0] = c[0], d[1] = c[1];
@@ -720,7 +726,7 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
     const int e = 4 * (lane + ROUTE_LANES * (i / 4));
     float o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = dense ? v[i + j] : 0.f;
+    for (int j = 0; j < 4; ++j) o[j] = a.sigmoid ? 0.f : v[i + j];
     if (e + 4 <= E) {
       if constexpr (BF16)
         *reinterpret_cast<u32x2_any*>(static_cast<uint16_t*>(dlogits) + at + e) =

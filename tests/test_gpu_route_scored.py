@@ -575,3 +575,40 @@ def test_backward_of_vanishing_sigmoid_scores(mx):
     d = mx.moe_route_scored_backward(dg.to(DEV), l.to(DEV), ids, "sigmoid", True, 2.5)
     assert bool(d.isfinite().all())
     check_pairs(d, dg, l, ids.cpu(), "sigmoid", True, 2.5)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E,k", [(32, 4), (384, 8), (96, 32), (1024, 3)])
+def test_backward_of_nan_rows(mx, E, k, bf16):
+    """A softmax row with a NaN logit has gates NaN and a gradient of NaN, whatever else is in the row and whether
+    the NaN is chosen; a sigmoid row where the chosen logit (renormalised: any chosen one) is NaN.  Other rows are
+    as they are without it."""
+    g = gen(E)
+    T = 9
+    l = torch.randn(T, E, generator=g).to(torch.bfloat16 if bf16 else torch.float32)
+    clean = l.clone()
+    l[1] = math.nan
+    l[2] = -math.inf
+    l[2, E - 1] = math.nan   # not chosen: -Inf has the lower ids
+    l[3] = -math.inf
+    l[3, 0] = math.nan       # chosen
+    l[5, E // 2] = math.nan  # behind all others, not chosen
+    l[6, k:] = math.nan
+    l[7, 1] = -math.nan
+    bad = torch.tensor([False, True, True, True, False, True, True, True, False])
+    dg = torch.randn(T, k, generator=g)
+    for kind in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            say("nan rows", E, k, kind, renorm)
+            ids, gates = mx.moe_route_scored(l.to(DEV), k, kind, renormalize=renorm)
+            d = mx.moe_route_scored_backward(dg.to(DEV), l.to(DEV), ids, kind, renorm).cpu()
+            ids_clean = mx.moe_route_scored(clean.to(DEV), k, kind, renormalize=renorm)[0]
+            want = mx.moe_route_scored_backward(dg.to(DEV), clean.to(DEV), ids_clean, kind, renorm).cpu()
+            assert torch.equal(d[~bad], want[~bad])
+            if kind == "softmax":
+                assert gates.cpu()[bad].isnan().all()
+                assert d[bad].isnan().all(), f"rows {(~d.isnan().all(1) & bad).nonzero().flatten().tolist()}"
+            else:
+                chosen = torch.zeros(T, E, dtype=torch.bool).scatter(1, ids.cpu().long(), True)
+                hit = chosen & (l.isnan().logical_and(chosen).any(1, keepdim=True) if renorm else l.isnan())
+                assert d[hit].isnan().all() and not d[~hit].isnan().any()
