@@ -618,7 +618,6 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
   if (t >= a.T) return;
   const size_t at = (size_t)t * a.E;
   const int E = a.E;
-  auto most = [](double x, double y) { return x > y ? x : (y == y ? y : x); };
   int id[2] = {-1, -1};
   double c[2] = {}, l[2] = {-INFINITY, -INFINITY}, q[2] = {}, d[2];
 #pragma unroll
@@ -681,29 +680,27 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
     z = row16_sum(z);
   }
   double rest = 0.0;
+  auto renormalize = [&]() __attribute__((always_inline)) {  // scores whose sum is 0 in 64 bits have gates 0, as in the forward call
+    const double s = row16_plus(q[0] + q[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) q[h] = s == 0.0 ? 0.0 : q[h] / s;
+  };
   if (a.sigmoid) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
       if (id[h] >= 0) q[h] = 1.0 / (1.0 + exp(-l[h]));
-    if (a.renormalize) {
-      const double s = row16_plus(q[0] + q[1]);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) q[h] = s == 0.0 ? 0.0 : q[h] / s;
-    }
+    if (a.renormalize) renormalize();
   } else {
-    double top = base;
-    if (a.renormalize) {
-      top = row16(most(l[0], l[1]), most);
-      if (top == -INFINITY) top = 0.0;
-      z *= 0.f;
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (id[h] >= 0) q[h] = exp(l[h] - top);
+      if (id[h] >= 0) q[h] = exp(l[h] - (double)base);
     const double sum = row16_plus(q[0] + q[1]) + (double)z, inv = sum == 0.0 ? 1.0 : 1.0 / sum;
-    rest = (double)z * inv;
 #pragma unroll
     for (int h = 0; h < 2; ++h) q[h] *= inv;
+    if (a.renormalize)
+      renormalize();
+    else
+      rest = (double)z * inv;
     const double cp = row16_plus(c[0] * q[0] + c[1] * q[1]);
     const float f = (float)(a.renormalize ? 0.0 * sum : -cp * inv);
 #pragma unroll

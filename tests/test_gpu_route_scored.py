@@ -612,3 +612,24 @@ def test_backward_of_nan_rows(mx, E, k, bf16):
                 chosen = torch.zeros(T, E, dtype=torch.bool).scatter(1, ids.cpu().long(), True)
                 hit = chosen & (l.isnan().logical_and(chosen).any(1, keepdim=True) if renorm else l.isnan())
                 assert d[hit].isnan().all() and not d[~hit].isnan().any()
+
+
+def test_backward_where_gates_are_0(mx):
+    """A bias that chooses experts so far below the others that their scores are 0 in 64 bits: the gates are 0, and
+    so is the gradient; a little nearer both are there."""
+    E, k = 16, 4
+    g = gen(41)
+    l = torch.randn(3, E, generator=g)
+    l[0, 4:] -= 800
+    l[1, 4:] -= 300
+    l[2, 4:] = -math.inf
+    bias = torch.zeros(E)
+    bias[:4] = -10.0
+    dg = torch.randn(3, k, generator=g)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = l.to(dtype)
+        ids, gates = mx.moe_route_scored(x.to(DEV), k, "softmax", bias.to(DEV), renormalize=True)
+        assert (ids.cpu() >= 4).all() and (gates[0] == 0).all() and (gates[2] == 0).all() and (gates[1] > 0).all()
+        d = mx.moe_route_scored_backward(dg.to(DEV), x.to(DEV), ids, "softmax", True)
+        assert (d[2] == 0).all() and (d[0] == 0).all(), d[0].tolist()
+        check_pairs(d[1:2], dg[1:2], x[1:2], ids[1:2].cpu(), "softmax", True, 1.0)
