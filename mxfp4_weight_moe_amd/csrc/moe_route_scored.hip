@@ -13,15 +13,16 @@
 // paid once for four).  Its keys are made in fp32 (without a bias they are the logits, exact), cut to
 // 22 to 26 bits above the expert's number, and the k + 2 largest found one by one; those few are then put in order
 // by their 64-bit keys.  That is the answer unless the key of a chosen expert lies within the fp32 error
-// of those that were not looked at, or two candidates' softmax scores within that of each other; then
-// (and where equal keys fill the border) the row's choice is made again, in 64 bits and one by one.  The same
-// for the groups.  Such rows cost a launch 10 to 30 us, few or many of them (softmax with a bias, 16384 bf16
-// tokens of 256 experts: 13 us without, up to 44 with).
+// of those that were not looked at; then (and where equal keys fill the border) the row's choice is made again, in
+// 64 bits and one by one.  The same for the groups.
+// Softmax's sum is taken in 64 bits (not where a gate does not need it: renormalised, without bias and groups), so
+// that a gate is rounded once, whatever the experts are chosen by.  16384 x 384 16.2 us, with an fp32 sum of fp32
+// exponentials 13.5, whose gates were off by up to 3 half steps; with a bias, where the candidates' order needs the sum
+// in 64 bits too, 16384 x 256 13.1, 43 with fp32 exponentials and the rows that they left open made again.
 //
-// Bound by instructions, not memory: 16384 x 384 fp32 logits, 25 MB, take 12.9 us where reading them alone
-// takes 5 (one choice after the other in 64 bits took 117, passes over all of a lane's keys for each candidate
-// 18.5); 16384 x 256 sigmoid scores with a bias 13.5, with groups 18.  A decode step is one chain of dependent
-// steps: 6.7 us for 1 token, 9.7 for 32 with a bias and groups.
+// Bound by instructions, not memory: 16384 x 384 fp32 logits are 25 MB, 5 us to read (one choice after the other in 64
+// bits took 117, passes over all of a lane's keys for each candidate 18.5); 16384 x 256 sigmoid scores with a bias 14.2,
+// with groups 19.6.  A decode step is one chain of dependent steps: 4.2 us for 1 token, 8.3 for 32 with a bias and groups.
 #include "mx_internal.hpp"
 #include "moe_route.hpp"
 #include "mx_tile.hpp"
@@ -69,13 +70,32 @@ __device__ __forceinline__ uint32_t rotate16(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x120 + N, 0xF, 0xF, false);  // row_ror
 }
 template <int N>
-__device__ __forceinline__ float rotate16(float v) {
-  return __uint_as_float(rotate16<N>(__float_as_uint(v)));
-}
-template <int N>
 __device__ __forceinline__ double rotate16(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
   return __builtin_bit_cast(double, (uint64_t)rotate16<N>((uint32_t)(b >> 32)) << 32 | rotate16<N>((uint32_t)b));
+}
+
+// The same sum in each lane of a row: at every step two lanes add the same two values.
+__device__ __forceinline__ double row16_plus(double v) {
+  v += rotate16<8>(v);
+  v += rotate16<4>(v);
+  v += rotate16<2>(v);
+  return v + rotate16<1>(v);
+}
+
+// exp(x) for x <= 0, of itself off by 2^-49, exactly 1 at 0; below e^-800, and of NaN, 0 or next to it.  2^n times a
+// polynomial in x log2 e - n, |.| <= 1/2: 1 + y g(y), g interpolating (2^y - 1) / y at the 10 Chebyshev nodes (error 2^-50.6).
+// What a sum over a row takes in 64 bits, at 17 instructions a term where the library's exp has its ends to look after.
+__device__ __forceinline__ double exp_term(double x) {
+  constexpr double LOG2E = 0x1.71547652b82fep+0, ROUND = 0x1.8p52;  // whose last place is 1
+  x = __builtin_fmax(x, -800.0);
+  const double n = __builtin_fma(x, LOG2E, ROUND), y = __builtin_fma(x, LOG2E, -(n - ROUND));
+  double p = 0x1.e5e9f548e5725p-28;
+  for (double c : {0x1.b6571de2f2351p-24, 0x1.62bfe46117445p-20, 0x1.ffcb76789860fp-17, 0x1.4309130378460p-13,
+                   0x1.5d87fe908f88ap-10, 0x1.3b2ab6fba385fp-7, 0x1.c6b08d7044119p-5, 0x1.ebfbdff82c590p-3,
+                   0x1.62e42fefa39f7p-1, 0x1.0000000000000p+0})
+    p = __builtin_fma(p, y, c);
+  return __builtin_ldexp(p, (int)(uint32_t)__builtin_bit_cast(uint64_t, n));
 }
 
 // The middle one.
@@ -128,17 +148,10 @@ __device__ __forceinline__ void row16_best(double& k, int& id) {
 // 16 / groups lanes to a group (a power of two, one at least).
 __device__ __forceinline__ int group_lanes(int groups) { return groups <= 2 ? 8 : groups <= 4 ? 4 : groups <= 8 ? 2 : 1; }
 
-// A row's keys in 64 bits, to its place in the LDS; softmax: s.sum becomes exact.
+// A row's keys in 64 bits, to its place in the LDS.
 template <bool BF16>
-__device__ __forceinline__ void exact_keys(Scores<BF16>& s, int E, int lane, double* keys) {
+__device__ __forceinline__ void exact_keys(const Scores<BF16>& s, int E, int lane, double* keys) {
   row_written();  // what was there has been read
-  if (!s.sigmoid) {
-    double sum = 0.0;
-#pragma unroll 4
-    for (int e = lane; e < E; e += ROUTE_LANES) sum += exp(s.logit(e) - s.top);
-    s.sum = row16(sum, [](double x, double y) { return x + y; });
-    if (s.sum == 0.0) s.sum = 1.0;  // nothing but -Inf: every score is 0
-  }
 #pragma unroll 4
   for (int e = lane; e < E; e += ROUTE_LANES) keys[e] = s.key(e);
   row_written();
@@ -179,10 +192,9 @@ __device__ __forceinline__ uint64_t exact_groups(const RouteScored& a, int lane,
 constexpr int ROUTE_MORE = 2;
 // Bounds of an fp32 score's distance from its 64-bit one, u = 2^-24.  Sigmoid: the exponential is off by
 // (1.3 |l| + 2) u of itself, which p (1 - p) <= 1/4 and |l| p (1 - p) < 0.23 leave 0.8 u of, the sum and its
-// reciprocal by 1.5 u: 3 u.  Softmax: a sum of E <= 1024 terms, 64 a lane and 4 steps, the terms
-// off by (1.3 |x| + 2) u with a weighted mean |x| below 4.5, and the score's own exponential: 88 u of the
-// largest score.  Adding the bias
-// rounds by u |key|.
+// reciprocal by 2 u: 3 u.  Softmax: x = l - top by |x| u, so the exponential by (2.3 |x| + 2) u e^x < 3 u, and half a step
+// each for the reciprocal of the 64-bit sum and the product: 6 u of the largest score.  Adding the bias rounds by
+// u |key|.
 constexpr float ROUTE_U = 0x1p-24f;
 
 // PER: logits of a lane, chunks of 4 consecutive ones, E <= 16 PER; C: candidates of a lane, k + 2 <= 16 C
@@ -217,9 +229,9 @@ __global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_score
   auto number = [&](int i) { return 4 * (lane + ROUTE_LANES * (i / 4)) + i % 4; };
   constexpr uint32_t LAST = PER <= 4 ? 63 : PER <= 8 ? 127 : PER <= 16 ? 255 : PER <= 32 ? 511 : 1023;  // number
 
-  // softmax: the largest logit and the sum
-  float top = 0.f, sum = 1.f;
-  double total = 0.0;  // the sum, for the candidates
+  // softmax: the largest logit, and the sum in 64 bits, which the candidates' keys and the gates are made with
+  float top = 0.f;
+  double sum = 1.0;
   if (!a.sigmoid) {
     float m = -INFINITY;
 #pragma unroll
@@ -230,34 +242,30 @@ __global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_score
       float z = 0.f;
 #pragma unroll
       for (int i = 0; i < PER; ++i) z += l[i] != l[i] ? l[i] : 0.f;
-      sum = row16_sum(z) + 1.f;
+      sum = (double)(row16_sum(z) + 1.f);
     } else if (!a.renormalize || a.bias || a.groups > 1) {
-      float z = 0.f;
+      sum = 0.0;
+      bool bad = top == INFINITY;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) z += __expf(l[i] - top);
-      sum = row16_sum(z);
-      total = (double)sum;
-      if (a.bias) {  // fewer candidates come too near to one another
-        total = 0.0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) total += (double)__expf(l[i] - top);
-        total = row16(total, [](double x, double y) { return x + y; });
+      for (int i = 0; i < PER; ++i) {
+        sum += exp_term((double)l[i] - (double)top);
+        bad = bad || l[i] != l[i];
       }
+      sum = row16_plus(bad ? (double)NAN : sum);
     } else {
       float z = 0.f;  // a NaN reaches every gate of its row
 #pragma unroll
       for (int i = 0; i < PER; ++i) z += l[i] != l[i] || l[i] == INFINITY ? l[i] - top : 0.f;
-      sum = row16_sum(z) + 1.f;
+      sum = (double)(row16_sum(z) + 1.f);
     }
   }
-  if (total == 0.0) total = (double)sum;
-  Scores<BF16> s{a.logits, a.bias, at, a.sigmoid, (double)top, total};
-  const float inv = 1.f / sum;
+  const Scores<BF16> s{a.logits, a.bias, at, a.sigmoid, (double)top, sum};
+  const float inv = (float)(1.0 / sum);
   auto score32 = [&](float v) { return a.sigmoid ? __builtin_amdgcn_rcpf(1.f + __expf(-v)) : __expf(v - top) * inv; };
   auto ordered32 = [](float v) { return v == v ? v : -INFINITY; };
 
   bool exact = false;          // 64-bit keys are in the LDS
-  double off = 0.0, near = 0;  // bounds of the error of an fp32 key, of a candidate's softmax score
+  double off = 0.0;            // bound of the error of an fp32 key
   double* const row_lds = shared + row * (E + a.groups);
   uint32_t comp[PER];
   const bool groups = a.groups > 1;
@@ -278,9 +286,7 @@ __global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_score
       size_of = fmaxf(size_of, key[i] == -INFINITY ? 0.f : fabsf(key[i]));
     }
     size_of = row16(size_of, [](float x, float y) { return fmaxf(x, y); });
-    off = (double)(ROUTE_U * ((a.sigmoid ? 3.f : 88.f * inv) + size_of));
-    // exponentials off by (1.3 |x| + 2) u, summed in 64 bits: of E <= 1024 the mean |x|, weighted, is below 4.5
-    near = (double)(ROUTE_U * 12.f * inv);
+    off = (double)(ROUTE_U * ((a.sigmoid ? 3.f : 6.f * inv) + size_of));
     if (groups) {
       __syncthreads();
       const int share = group_lanes(a.groups);
@@ -394,38 +400,29 @@ __global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_score
 
   // the candidates' 64-bit keys, their order, and whether it is certain
   int id[C], rank[C];
-  float cl[C], cb[C];
+  float cl[C];
   double key[C], p[C];
-  const bool rough = a.bias && !a.sigmoid && !exact;  // the sum is of fp32 exponentials
   bool again = false;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     id[c] = cand[c] ? (int)(LAST - (cand[c] & LAST)) : 1 << 20;
     cl[c] = cand[c] ? logit_at<BF16>(a.logits, at + id[c]) : -INFINITY;
-    cb[c] = a.bias && cand[c] ? a.bias[id[c]] : 0.f;
     p[c] = s.score_of((double)cl[c]);
-    key[c] = a.bias ? ordered(p[c] + (double)cb[c]) : ordered((double)cl[c]);
+    key[c] = ordered(a.bias && cand[c] ? p[c] + (double)a.bias[id[c]] : (double)cl[c]);
     if (!cand[c]) key[c] = -INFINITY;  // its number puts it behind all others
     rank[c] = 0;
   }
   if (a.bias) {
-    auto compare = [&](double ok, int oid, float ol, float ob, int d) {
-      rank[d] += before(ok, oid, key[d], id[d]);
-      if (rough && oid != id[d] && !(fabs(ok - key[d]) > 2.0 * near) && !(ol == cl[d] && ob == cb[d]))
-        again = again || (cand[d] != 0 && oid < 1 << 20);
-    };
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int d = 0; d < C; ++d)
-        if (c != d) compare(key[c], id[c], cl[c], cb[c], d);
+        if (c != d) rank[d] += before(key[c], id[c], key[d], id[d]);
       unrolled<ROUTE_LANES - 1>([&](auto N) __attribute__((always_inline)) {
         const double ok = rotate16<N + 1>(key[c]);
         const int oid = (int)rotate16<N + 1>((uint32_t)id[c]);
-        float ol = 0.f, ob = 0.f;
-        if (rough) ol = rotate16<N + 1>(cl[c]), ob = rotate16<N + 1>(cb[c]);
 #pragma unroll
-        for (int d = 0; d < C; ++d) compare(ok, oid, ol, ob, d);
+        for (int d = 0; d < C; ++d) rank[d] += before(ok, oid, key[d], id[d]);
       });
     }
   } else {
@@ -507,7 +504,7 @@ __global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_score
     double all = 0.0;
 #pragma unroll
     for (int c = 0; c < C; ++c) all += p[c];
-    all = row16(all, [](double x, double y) { return x + y; });
+    all = row16_plus(all);
 #pragma unroll
     for (int c = 0; c < C; ++c) p[c] = all == 0.0 ? 0.0 : p[c] / all;
   }
@@ -581,13 +578,6 @@ __device__ __forceinline__ float exp_far(float x) {
   return x > -126.f ? __builtin_fmaf(e, left * 0.693147181f, e) : e;  // not for -Inf, whose left is NaN
 }
 
-// The same sum in each lane of a row: at every step two lanes add the same two values.
-__device__ __forceinline__ double row16_plus(double v) {
-  v += rotate16<8>(v);
-  v += rotate16<4>(v);
-  v += rotate16<2>(v);
-  return v + rotate16<1>(v);
-}
 // Of lane J of the row.
 template <int J>
 __device__ __forceinline__ double broadcast16(double v) {

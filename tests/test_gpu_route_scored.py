@@ -633,3 +633,32 @@ def test_backward_where_gates_are_0(mx):
         d = mx.moe_route_scored_backward(dg.to(DEV), x.to(DEV), ids, "softmax", True)
         assert (d[2] == 0).all() and (d[0] == 0).all(), d[0].tolist()
         check_pairs(d[1:2], dg[1:2], x[1:2], ids[1:2].cpu(), "softmax", True, 1.0)
+
+
+# ------------------------------------------------------------------ gates
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("E,k", [(1, 1), (17, 5), (64, 8), (128, 8), (256, 8), (384, 8), (512, 12), (1000, 16), (1024, 32), (96, 32)])
+def test_gates_are_rounded_once(mx, E, k, bf16):
+    """Half a step of fp32 from the 64-bit value, for softmax over all experts as for the others, and the same bits
+    whatever chooses the experts: without a bias, with one of zeros, with groups that are all there and with
+    candidates that are decided again."""
+    for spread in (0.01, 1.5, 6.0):
+        g = gen(E + int(10 * spread))
+        l = (torch.randn(130, E, generator=g) * spread).to(torch.bfloat16 if bf16 else torch.float32)
+        for renorm in (False, True):
+            ids, gates = mx.moe_route_scored(l.to(DEV), k, "softmax", renormalize=renorm)
+            want = ref(l, k, "softmax", None, 1, 1, "max", renorm, 1.0)[1]
+            off = ((gates.double().cpu() - want).abs() / (U * (1 + 2.0 ** -16) * want + 2.0 ** -150)).max()
+            assert off <= 1, f"{spread} {renorm}: {float(off):.3g} half steps"
+            zeros = torch.zeros(E, device=DEV)
+            again = mx.moe_route_scored(l.to(DEV), k, "softmax", zeros, renormalize=renorm)
+            assert torch.equal(again[0], ids) and torch.equal(again[1], gates), f"{spread} {renorm}"
+            if E % 8 == 0:
+                # the same experts again, by groups that keep them all in place: seven of eight, the last one shut out by a bias
+                shut = zeros.clone()
+                shut[E // 8 * 7:] = -100.0
+                if k <= E // 8 * 7:
+                    a = mx.moe_route_scored(l.to(DEV), k, "softmax", shut, renormalize=renorm)
+                    b = mx.moe_route_scored(l.to(DEV), k, "softmax", shut, 8, 7, "max", renormalize=renorm)
+                    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
