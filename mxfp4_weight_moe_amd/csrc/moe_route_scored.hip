@@ -200,8 +200,11 @@ constexpr float ROUTE_U = 0x1p-24f;
 // PER: logits of a lane, chunks of 4 consecutive ones, E <= 16 PER; C: candidates of a lane, k + 2 <= 16 C
 // (k at most 32 with C = 3).
 // WHOLE of a lane's places hold an expert whatever E.
+// Waves a SIMD: four up to 384 experts, which at 24 places spill 3 registers (16384 x 384 softmax 16.1 us, with three
+// waves and no spill 16.6; with groups or a bias 3 to 5% the other way); three up to 512, where four would spill 50 (8192 x
+// 512 softmax 13.5 for 12.3, with a bias 16.3 for 13.5); beyond, and for more than 14 chosen, what the registers allow.
 template <bool BF16, int PER, int C, int WHOLE>
-__global__ void __launch_bounds__(64, (C == 1 && PER <= 32 ? 4 : 1)) route_scored_kernel(RouteScored a, int32_t* __restrict__ ids, float* __restrict__ gates) {
+__global__ void __launch_bounds__(64, (C != 1 || PER > 32 ? 1 : PER > 24 ? 3 : 4)) route_scored_kernel(RouteScored a, int32_t* __restrict__ ids, float* __restrict__ gates) {
   extern __shared__ double shared[];  // with a bias or groups: per row E + groups values
   const int lane = threadIdx.x % ROUTE_LANES, row = threadIdx.x / ROUTE_LANES;
   const int64_t t0 = (int64_t)blockIdx.x * ROUTE_ROWS + row, t = t0 < a.T ? t0 : a.T - 1;  // rows past the last: it again
