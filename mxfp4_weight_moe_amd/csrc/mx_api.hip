@@ -324,6 +324,53 @@ static int moe_forward_args(const uint16_t* x, const float* router_logits, int64
   return MX_OK;
 }
 
+// How the expert GEMMs run behind a routing.
+enum ExpertPlan {
+  BOTH_SORTING,     // one launch for both, which sorts the slots in every workgroup; h filled with 0xFFFF before it
+  GATE_UP_SORTING,  // up to 32 tokens: gate_up sorts the slots in every workgroup, then down
+  BOTH,             // shared experts, or more than 256 slots: a sort launch and one for both; h filled with 0xFFFF
+  SEPARATE          // a sort launch, gate_up, down
+};
+static ExpertPlan expert_plan(int t, int h, int i, int e, int k, int n) {
+  if (n == 0 && experts_sorted_fits(t, e, k, h, i) && experts_sorted_pays(t, e, k, i)) return BOTH_SORTING;
+  if (n == 0 && gate_up_sorted_fits(t, e, k, h, i)) return GATE_UP_SORTING;
+  if (t > 16 && t <= EXPERTS_MAX_T && experts_fits(h, i) && experts_sorted_pays(t, e + n, k + n, i)) return BOTH;
+  return SEPARATE;
+}
+
+static SortView sort_view(const MoeWorkspace& ws) {
+  return {ws.counts, ws.offsets, ws.sorted_slots, ws.active, ws.num_active};
+}
+
+// Down and the combine of the slots that gate_up left in ws.h, sorted in ws; e and k with the shared experts.
+static int down_and_combine(const MoeWorkspace& ws, const float* gates, const uint8_t* w_down, const uint8_t* s_down,
+                            uint16_t* y, int t, int h, int i, int e, int k, bool act8, hipStream_t s) {
+  bool combined = false;
+  const int st = launch_down(ws.h, gates, w_down, s_down, sort_view(ws), ws.dpart, y, &combined, ws.ctl, t, h, i, e, k,
+                             act8, s);
+  return st != MX_OK || combined ? st : launch_combine(ws.dpart, gates, y, t, h, k, s);
+}
+
+// The launches behind the routing; BOTH and SEPARATE from the sort in ws.
+static int launch_expert_plan(ExpertPlan plan, const uint16_t* x, const int32_t* ids, const float* gates,
+                              const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,
+                              const uint8_t* s_down, uint16_t* y, const MoeWorkspace& ws, int t, int h, int i, int e, int k,
+                              bool act8, hipStream_t s) {
+  int st;
+  if (plan == BOTH_SORTING || plan == BOTH) {
+    st = plan == BOTH ? launch_experts(x, sort_view(ws), w_gate_up, s_gate_up, w_down, s_down, ws.h, ws.dpart, ws.ctl, h, i,
+                                       k, act8, s)
+                      : launch_experts_sorted(x, ids, w_gate_up, s_gate_up, w_down, s_down, ws.h, ws.dpart, ws.ctl, t, h, i,
+                                              e, k, act8, s);
+    return st != MX_OK ? st : launch_combine(ws.dpart, gates, y, t, h, k, s);
+  }
+  st = plan == GATE_UP_SORTING
+           ? launch_gate_up_sorted(x, ids, w_gate_up, s_gate_up, ws.h, ws.counts, ws.offsets, ws.sorted_slots, ws.active,
+                                   ws.num_active, ws.ctl, t, h, i, e, k, act8, s)
+           : launch_gate_up(x, w_gate_up, s_gate_up, sort_view(ws), ws.h, ws.ctl, t, h, i, e, k, act8, s);
+  return st != MX_OK ? st : down_and_combine(ws, gates, w_down, s_down, y, t, h, i, e, k, act8, s);
+}
+
 static int moe_forward_impl(const uint16_t* x, const float* router_logits, int64_t top_k, int64_t ns,
                             const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,
                             const uint8_t* s_down, uint16_t* y, int64_t T, int64_t H, int64_t I, int64_t E,
@@ -336,50 +383,26 @@ static int moe_forward_impl(const uint16_t* x, const float* router_logits, int64
   if (workspace_bytes < ws.bytes) return MX_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int t = (int)T, h = (int)H, i = (int)I, e = (int)E, k = (int)top_k, n = (int)ns;
-  const SortView sv{ws.counts, ws.offsets, ws.sorted_slots, ws.active, ws.num_active};
-  if (n == 0 && experts_sorted_fits(t, e, k, h, i) && experts_sorted_pays(t, e, k, i)) {
-    // the routing launch (which also fills h with 0xFFFF), one launch for both expert
-    // GEMMs, then the combine
-    if ((st = launch_route(router_logits, t, e, k, 0, ws.ids, ws.gates, s, ws.h, (size_t)t * k * i * 2)) != MX_OK)
-      return st;
-    if ((st = launch_experts_sorted(x, ws.ids, w_gate_up, s_gate_up, w_down, s_down, ws.h, ws.dpart, ws.ctl, t, h, i, e,
-                                    k, act8, s)) != MX_OK)
-      return st;
-    return launch_combine(ws.dpart, ws.gates, y, t, h, k, s);
-  } else if (n == 0 && gate_up_routed_fits(t, e, k, h, i)) {
+  const ExpertPlan plan = expert_plan(t, h, i, e, k, n);
+  if (plan != BOTH_SORTING && n == 0 && gate_up_routed_fits(t, e, k, h, i)) {
     // small T: gate_up routes and sorts in every workgroup and writes the sort for down
     if ((st = launch_gate_up_routed(x, router_logits, w_gate_up, s_gate_up, ws.h, ws.counts, ws.offsets,
                                     ws.sorted_slots, ws.active, ws.num_active, ws.gates, t, h, i, e, k, act8, s)) !=
         MX_OK)
       return st;
-  } else if (n == 0 && gate_up_sorted_fits(t, e, k, h, i)) {
-    // up to 32 tokens: the routing launch, then gate_up sorts the slots in every workgroup
-    if ((st = launch_route(router_logits, t, e, k, 0, ws.ids, ws.gates, s)) != MX_OK) return st;
-    if ((st = launch_gate_up_sorted(x, ws.ids, w_gate_up, s_gate_up, ws.h, ws.counts, ws.offsets, ws.sorted_slots,
-                                    ws.active, ws.num_active, ws.ctl, t, h, i, e, k, act8, s)) != MX_OK)
-      return st;
-  } else if (t > 16 && t <= EXPERTS_MAX_T && experts_fits(h, i) && experts_sorted_pays(t, e + n, k + n, i)) {
-    // shared experts, or more than 256 slots: the route and sort launches (the route launch
-    // also fills h with 0xFFFF), one launch for both expert GEMMs, then the combine
-    if ((st = launch_route_sort(router_logits, t, e, k, n, ws.ids, ws.gates, ws.counts, ws.offsets, ws.sorted_slots,
-                                ws.active, ws.num_active, s, ws.h, (size_t)t * (k + n) * i * 2)) != MX_OK)
-      return st;
-    if ((st = launch_experts(x, sv, w_gate_up, s_gate_up, w_down, s_down, ws.h, ws.dpart, ws.ctl, h, i, k + n, act8,
-                             s)) != MX_OK)
-      return st;
-    return launch_combine(ws.dpart, ws.gates, y, t, h, k + n, s);
-  } else {
-    if ((st = launch_route_sort(router_logits, t, e, k, n, ws.ids, ws.gates, ws.counts, ws.offsets, ws.sorted_slots,
-                                ws.active, ws.num_active, s)) != MX_OK)
-      return st;
-    if ((st = launch_gate_up(x, w_gate_up, s_gate_up, sv, ws.h, ws.ctl, t, h, i, e + n, k + n, act8, s)) != MX_OK)
-      return st;
+    return down_and_combine(ws, ws.gates, w_down, s_down, y, t, h, i, e, k, act8, s);
   }
-  bool combined = false;
-  if ((st = launch_down(ws.h, ws.gates, w_down, s_down, sv, ws.dpart, y, &combined, ws.ctl, t, h, i, e + n, k + n,
-                        act8, s)) != MX_OK)
-    return st;
-  return combined ? MX_OK : launch_combine(ws.dpart, ws.gates, y, t, h, k + n, s);
+  // the routing launch (with the sort where no launch behind it sorts) also fills h with 0xFFFF for the plans that want it
+  const bool fill = plan == BOTH_SORTING || plan == BOTH;
+  void* const filled = fill ? ws.h : nullptr;
+  const size_t bytes = fill ? (size_t)t * (k + n) * i * 2 : 0;
+  st = plan == BOTH_SORTING || plan == GATE_UP_SORTING
+           ? launch_route(router_logits, t, e, k, 0, ws.ids, ws.gates, s, filled, bytes)
+           : launch_route_sort(router_logits, t, e, k, n, ws.ids, ws.gates, ws.counts, ws.offsets, ws.sorted_slots,
+                               ws.active, ws.num_active, s, filled, bytes);
+  if (st != MX_OK) return st;
+  return launch_expert_plan(plan, x, ws.ids, ws.gates, w_gate_up, s_gate_up, w_down, s_down, y, ws, t, h, i, e + n, k + n,
+                            act8, s);
 }
 
 int moe_mxfp4_forward(const uint16_t* x, const float* router_logits, int64_t top_k, const uint8_t* w_gate_up,
@@ -432,28 +455,13 @@ int moe_mxfp4_forward_routed(const uint16_t* x, const int32_t* ids, const float*
   if (workspace_bytes < ws.bytes) return MX_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int t = (int)T, h = (int)H, i = (int)I, e = (int)E, k = (int)top_k;
-  const bool a8 = act8 != 0;
-  const SortView sv{ws.counts, ws.offsets, ws.sorted_slots, ws.active, ws.num_active};
-  // the launches of moe_mxfp4_forward behind its routing
-  if (experts_sorted_fits(t, e, k, h, i) && experts_sorted_pays(t, e, k, i)) {
-    if ((st = launch_fill_ones(ws.h, (size_t)t * k * i * 2, s)) != MX_OK) return st;
-    if ((st = launch_experts_sorted(x, ids, w_gate_up, s_gate_up, w_down, s_down, ws.h, ws.dpart, ws.ctl, t, h, i, e, k,
-                                    a8, s)) != MX_OK)
-      return st;
-    return launch_combine(ws.dpart, gates, y, t, h, k, s);
-  }
-  if (gate_up_sorted_fits(t, e, k, h, i)) {
-    st = launch_gate_up_sorted(x, ids, w_gate_up, s_gate_up, ws.h, ws.counts, ws.offsets, ws.sorted_slots, ws.active,
-                               ws.num_active, ws.ctl, t, h, i, e, k, a8, s);
-  } else {
-    st = launch_sort(ids, t, k, e, ws.counts, ws.offsets, ws.sorted_slots, ws.active, ws.num_active, s);
-    if (st == MX_OK) st = launch_gate_up(x, w_gate_up, s_gate_up, sv, ws.h, ws.ctl, t, h, i, e, k, a8, s);
-  }
-  if (st != MX_OK) return st;
-  bool combined = false;
-  if ((st = launch_down(ws.h, gates, w_down, s_down, sv, ws.dpart, y, &combined, ws.ctl, t, h, i, e, k, a8, s)) != MX_OK)
+  // as moe_mxfp4_forward behind its routing; what that launch does on the way, filling and sorting, by launches of their own
+  const ExpertPlan plan = expert_plan(t, h, i, e, k, 0);
+  if ((plan == BOTH_SORTING || plan == BOTH) && (st = launch_fill_ones(ws.h, (size_t)t * k * i * 2, s)) != MX_OK) return st;
+  if ((plan == BOTH || plan == SEPARATE) && (st = launch_sort(ids, t, k, e, ws.counts, ws.offsets, ws.sorted_slots,
+                                                              ws.active, ws.num_active, s)) != MX_OK)
     return st;
-  return combined ? MX_OK : launch_combine(ws.dpart, gates, y, t, h, k, s);
+  return launch_expert_plan(plan, x, ids, gates, w_gate_up, s_gate_up, w_down, s_down, y, ws, t, h, i, e, k, act8 != 0, s);
 }
 
 int moe_mxfp4_forward_persistent(const uint16_t* x, const float* router_logits, int64_t top_k,

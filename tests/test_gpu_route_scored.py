@@ -662,3 +662,21 @@ def test_gates_are_rounded_once(mx, E, k, bf16):
                     a = mx.moe_route_scored(l.to(DEV), k, "softmax", shut, renormalize=renorm)
                     b = mx.moe_route_scored(l.to(DEV), k, "softmax", shut, 8, 7, "max", renormalize=renorm)
                     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("act8", [False, True])
+@pytest.mark.parametrize("T,E,k,I,H", [(32, 256, 16, 512, 1024), (17, 192, 16, 512, 2048), (32, 256, 9, 512, 1024), (33, 256, 16, 512, 1024),
+                                       (16, 256, 16, 512, 1024), (12, 128, 4, 1024, 1024), (25, 200, 8, 768, 1024)])
+def test_forward_routed_takes_every_plan(mx, T, E, k, I, H, act8):
+    """Up to and beyond 256 slots and 32 tokens, where the layer's plans change: bit for bit moe_mxfp4_forward,
+    again and again from the workspace that the call before left."""
+    g = gen(T + E + k)
+    W = expert_weights(E, H, I, g)
+    x = torch.randn(T, H, generator=g).bfloat16().to(DEV)
+    l = torch.randn(T, E, generator=g).to(DEV)
+    say("plans", T, E, k, I, act8)
+    ids, gates = mx.moe_route_topk(l, k)
+    want = mx.moe_mxfp4_forward(x, l, k, *W, act8=act8)
+    ws = mx.workspace(T, H, I, E, k, x.device)
+    for _ in range(3):
+        assert torch.equal(mx.moe_mxfp4_forward_routed(x, ids, gates, *W, act8=act8, ws=ws), want)
