@@ -639,6 +639,7 @@ MX_API int mx_gate_up_quantized(const uint8_t* a_codes, const uint8_t* a_scales,
  *   [T, top_k] (written)
  *   E <= MX_MAX_EXPERTS, top_k <= MX_MAX_TOPK, n_group <= MX_MAX_GROUPS and divides E,
  *   1 <= topk_group <= n_group, top_k <= topk_group * E / n_group; scale finite.
+ *   Outputs must not overlap inputs or one another.
  */
 enum mx_score {
   MX_SCORE_SOFTMAX = 0,

@@ -946,6 +946,9 @@ def mx_norm_residual_quantize(x: torch.Tensor, b: torch.Tensor | None = None, w_
             _tensor(y, "out", _BF16, (T, H), dev)
             _apart(y, x, "x", itself=True)
             _apart(y, b, "b", itself=True)
+            _clear_of(y, (w_post, "w_post"), (w_pre, "w_pre"))
+            if gate is not None:
+                _apart(y, gate, "gate", itself=mode == _GATE_FULL)
     codes = x.new_empty((T, H // 2 if code else H), dtype=_U8)
     scales = x.new_empty((T, H // 32), dtype=_U8)
     xn = torch.empty_like(x) if save_xn else None
@@ -974,6 +977,8 @@ def _clear_of(out, *ts):
     """Refuses an output over a tensor that other workgroups still read while it is written."""
     o, n = out.data_ptr(), out.numel() * out.element_size()
     for t, name in ts:
+        if t is None:
+            continue
         i = t.data_ptr()
         if o < i + t.numel() * t.element_size() and i < o + n:
             raise ValueError(f"out must not overlap {name}")
@@ -1005,7 +1010,7 @@ def mx_linear_quantized(codes: torch.Tensor, scales: torch.Tensor, w_codes: torc
         out = codes.new_empty((T, N), dtype=_BF16)
     else:
         _tensor(out, "out", _BF16, (T, N), dev)
-        _clear_of(out, (codes, "codes"), (scales, "scales"))
+        _clear_of(out, (codes, "codes"), (scales, "scales"), (w_codes, "weight codes"), (w_scales, "weight scales"), (bias, "bias"))
         if residual is not None:
             _apart(out, residual, "residual", itself=True)
     z = codes.new_empty((T, N), dtype=_BF16) if save_z else None
@@ -1095,12 +1100,12 @@ def moe_route_scored(logits: torch.Tensor, top_k: int, score: str = "softmax", b
         ids = logits.new_empty((T, top_k), dtype=_I32)
     else:
         _tensor(ids, "ids", _I32, (T, top_k), dev)
+        _clear_of(ids, (logits, "router_logits"), (bias, "bias"))
     if gates is None:
         gates = logits.new_empty((T, top_k), dtype=_F32)
     else:
         _tensor(gates, "gates", _F32, (T, top_k), dev)
-        _clear_of(gates, (logits, "router_logits"), (ids, "ids"))
-    _clear_of(ids, (logits, "router_logits"))
+        _clear_of(gates, (logits, "router_logits"), (bias, "bias"), (ids, "ids"))
     _call(_lib.moe_route_scored, dev, logits.data_ptr(), kind, _opt(bias), sc, n_group, topk_group, gs,
           1 if renormalize else 0, scale, ids.data_ptr(), gates.data_ptr(), T, E, top_k)
     return ids, gates
@@ -1144,14 +1149,17 @@ def moe_mxfp4_forward_routed(x: torch.Tensor, ids: torch.Tensor, gates: torch.Te
     if (W_gate_up.shape != (E, 2 * I, H // 2) or S_gate_up.shape != (E, 2 * I, H // 32)
             or W_down.shape != (E, H, I // 2) or S_down.shape != (E, H, I // 32)):
         raise ValueError("expert weight shapes do not match [E, 2I, H/2], [E, 2I, H/32], [E, H, I/2], [E, H, I/32]")
-    if out is None:
+    given = out is not None
+    if not given:
         out = torch.empty((T, H), dtype=_BF16, device=dev)
     else:
         _tensor(out, "out", _BF16, (T, H), dev)
-        _apart(out, x, "x")
     if ws is None:
         ws = workspace(T, H, I, E, k, dev)
     _check(ws, "workspace", _U8, 1, dev)
+    if given:
+        _clear_of(out, (x, "x"), (ids, "ids"), (gates, "gates"), (W_gate_up, "W_gate_up"), (S_gate_up, "S_gate_up"),
+                  (W_down, "W_down"), (S_down, "S_down"), (ws, "workspace"))
     _call(_lib.moe_mxfp4_forward_routed, dev, x.data_ptr(), ids.data_ptr(), gates.data_ptr(), k, W_gate_up.data_ptr(),
           S_gate_up.data_ptr(), W_down.data_ptr(), S_down.data_ptr(), 1 if act8 else 0, out.data_ptr(), T, H, I, E,
           ws.data_ptr(), ws.numel())

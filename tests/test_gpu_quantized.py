@@ -641,3 +641,38 @@ def test_straight_through_gradients(mx):
     edz = torch.cat((d.abs() * zc[:, I:].abs() * e, d.abs() * e), 1) + 4 * U * dz.abs()
     err = edz @ Wgu.abs() + (2 * I + 8) * U * size + B * size
     within(dx, want, (1 + B) * err + B * want.abs(), "dx")
+
+
+def test_outputs_over_weights_and_vectors(mx):
+    """Weights, bias, gate and norm weights are read by other workgroups while outputs are written."""
+    T, K, N = 64, 512, 64
+    g = gen(61)
+    a, sa = activations(T, K, "mxfp8", g)
+    w, s = weights(N, K, g)
+    a, sa, w, s = cuda(a, sa, w, s)
+    out = w.view(-1)[: T * N * 2].view(torch.bfloat16).view(T, N)
+    with pytest.raises(ValueError, match="weight codes"):
+        mx.mx_linear_quantized(a, sa, w, s, out=out)
+    room = torch.zeros(T * N * 2 + 4096, dtype=torch.uint8, device=DEV)
+    out = room[: T * N * 2].view(torch.bfloat16).view(T, N)
+    with pytest.raises(ValueError, match="weight scales"):
+        mx.mx_linear_quantized(a, sa, w, room[64:64 + N * K // 32].view(N, K // 32), out=out)
+    with pytest.raises(ValueError, match="bias"):
+        mx.mx_linear_quantized(a, sa, w, s, room[128:128 + 2 * N].view(torch.bfloat16), out=out)
+    H = 256
+    x, b = cuda(bf(T, H, g=g), bf(T, H, g=g))
+    room = torch.ones(2 * T * H, dtype=torch.bfloat16, device=DEV)
+    out, ones = room[: T * H].view(T, H), torch.ones(H, dtype=torch.bfloat16, device=DEV)
+    over = room[T * H - 8: T * H - 8 + H]
+    for name, kw in (("w_post", dict(w_post=over, w_pre=ones)), ("w_pre", dict(w_pre=over)), ("gate", dict(w_pre=ones, gate=over)),
+                     ("gate", dict(w_pre=ones, gate=room[T * H - 8:][: T].view(T, 1))),
+                     ("gate", dict(w_pre=ones, gate=room[8: 8 + T * H].view(T, H)))):
+        with pytest.raises(ValueError, match=name):
+            mx.mx_norm_residual_quantize(x, b, out=out, **kw)
+    want = mx.mx_norm_residual_quantize(x, b, gate=room[T * H:].view(T, H).clone(), w_pre=ones)
+    got = mx.mx_norm_residual_quantize(x, b, gate=room[T * H:].view(T, H), w_pre=ones, out=out)
+    assert all(torch.equal(p, q) for p, q in zip(want[:3], got[:3]))
+    full = bf(T, H, g=g).to(DEV)
+    want = mx.mx_norm_residual_quantize(x, b, gate=full, w_pre=ones)
+    got = mx.mx_norm_residual_quantize(x, b, gate=full, w_pre=ones, out=full)  # each element read before it is written
+    assert all(torch.equal(p, q) for p, q in zip(want[:3], got[:3]))

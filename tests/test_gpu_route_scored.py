@@ -680,3 +680,36 @@ def test_forward_routed_takes_every_plan(mx, T, E, k, I, H, act8):
     ws = mx.workspace(T, H, I, E, k, x.device)
     for _ in range(3):
         assert torch.equal(mx.moe_mxfp4_forward_routed(x, ids, gates, *W, act8=act8, ws=ws), want)
+
+
+def test_outputs_over_what_is_read(mx):
+    """An output over an input that other workgroups still read is refused: the bias as well as the logits; the
+    layer's ids, gates, weights and workspace as well as x."""
+    T, E, k = 64, 64, 4
+    l = torch.randn(T, E, generator=gen(51)).to(DEV)
+    room = torch.zeros(T * k + E, device=DEV)
+    bias = room[T * k - 8: T * k - 8 + E]
+    with pytest.raises(ValueError, match="bias"):
+        mx.moe_route_scored(l, k, bias=bias, gates=room[:T * k].view(T, k))
+    with pytest.raises(ValueError, match="bias"):
+        mx.moe_route_scored(l, k, bias=bias, ids=room[:T * k].view(torch.int32).view(T, k))
+    want = mx.moe_route_scored(l, k, bias=room[T * k:].clone())
+    got = mx.moe_route_scored(l, k, bias=room[T * k:], gates=room[:T * k].view(T, k))  # side by side
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+    H, I, E = 1024, 256, 16
+    W = expert_weights(E, H, I, gen(52))
+    x = torch.randn(T, H, generator=gen(53)).bfloat16().to(DEV)
+    ids, gates = mx.moe_route_topk(torch.randn(T, E, generator=gen(54)).to(DEV), k)
+    room = torch.zeros(T * H * 2, dtype=torch.uint8, device=DEV)
+    out = room.view(torch.bfloat16).view(T, H)
+    over = room[: T * k * 4]
+    for name, args in (("gates", (x, ids, over.view(torch.float32).view(T, k), *W)),
+                       ("ids", (x, over.view(torch.int32).view(T, k), gates, *W))):
+        with pytest.raises(ValueError, match=name):
+            mx.moe_mxfp4_forward_routed(*args, out=out)
+    ws = mx.workspace(T, H, I, E, k, x.device)
+    with pytest.raises(ValueError, match="workspace"):
+        mx.moe_mxfp4_forward_routed(x, ids, gates, *W, out=ws[: T * H * 2].view(torch.bfloat16).view(T, H), ws=ws)
+    with pytest.raises(ValueError, match="W_down"):
+        mx.moe_mxfp4_forward_routed(x, ids, gates, *W, out=W[2].view(-1)[: T * H * 2].view(torch.bfloat16).view(T, H))
