@@ -565,18 +565,19 @@ int launch_route_scored(const RouteScored& a, int32_t* ids, float* gates, hipStr
 // and `rest` what the others have (0 renormalised),
 //   c[i] - sum c q = sum over j of (c[i] - c[j]) q[j] + c[i] rest
 // in 64 bits.  The others' exponentials and their sum are fp32, which no difference is formed of; 87 below the row's
-// largest logit they begin to lose digits.
-// 8192 x 256 fp32 with k 8, other logits from call to call: softmax 6.9 us, 17 MB read and written (6.2 with the
+// largest logit they are 0 (in 64 bits, too, a launch took 1 us more).
+// 8192 x 256 fp32 with k 8, other logits from call to call: softmax 7.1 us, 17 MB read and written (6.2 with the
 // difference formed from an fp32 sum, which left no right digit where the best logit was 16 above the next);
-// renormalised 7.0 (5.4 from the chosen logits alone, which do not say whether there is a NaN); sigmoid 5.2, which
-// writes 8 MB alone; 32 tokens 3.7 and 3.1.  A wave a row took 10.2 where 16 lanes took 5.4: most lanes had no chosen
+// renormalised 7.1 (5.4 from the chosen logits alone, which do not say whether there is a NaN); sigmoid 5.1, which
+// writes 8 MB alone; 32 tokens 4.0 and 3.0.  A wave a row took 10.2 where 16 lanes took 5.4: most lanes had no chosen
 // value.
 
-// exp(x) for x <= 0, off by some 3 u of itself however far x is: what the product with log2 e loses in its
-// rounding (1.3 |x| u of the result) is multiplied back in.
-__device__ __forceinline__ float exp_far(float x) {
-  const float t = x * 1.44269504f;
-  const float left = __builtin_fmaf(x, 1.44269504f, -t) + x * 1.92596299e-8f;  // log2 e = 1.44269504f + that
+// exp(l - top) for l <= top, off by some 3 u of itself however far they are apart: what the difference and its product
+// with log2 e lose in their roundings (1 and 1.3 |x| u of the result) is multiplied back in.  0 from 87 on.
+__device__ __forceinline__ float exp_far(float l, float top) {
+  const float x = l - top, b = x - l, lost = (l - (x - b)) - (top + b);
+  const float t = x * 1.44269504f;  // log2 e = 1.44269504f + 1.92596299e-8f
+  const float left = __builtin_fmaf(lost, 1.44269504f, __builtin_fmaf(x, 1.92596299e-8f, __builtin_fmaf(x, 1.44269504f, -t)));
   const float e = __builtin_amdgcn_exp2f(t);
   return x > -126.f ? __builtin_fmaf(e, left * 0.693147181f, e) : e;  // not for -Inf, whose left is NaN
 }
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
     base = route_value(row16_max(route_key(m)));
     if (base == -INFINITY) base = 0.f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = exp_far(v[i] - base);
+    for (int i = 0; i < PER; ++i) v[i] = exp_far(v[i], base);
     // where a lane's logits are chosen ones: its places' bits, from the lanes that have the ids
     row_written();
 #pragma unroll
