@@ -467,6 +467,7 @@ def workspace_size(T: int, H: int, I: int, E: int, top_k: int) -> int:
     return int(_lib.moe_mxfp4_workspace_size(T, H, I, E, top_k))
 
 
+MX_WORKSPACE_CTL_BYTES = 57344
 _ws_cache: dict = {}
 
 

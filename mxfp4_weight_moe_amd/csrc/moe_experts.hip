@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(WG_WAVES * 64) moe_gate_up_kernel(const uint16
   p.nquad = I / (P::TILE * WG_WAVES);
   p.na = p.m.num_active();
   p.n_items = ((p.m.max_rows() + 15) >> 4) * p.na * p.nquad;  // row-group levels that exist
-  ClaimedUnits seq{claim, (lds_i32*)cq, p.na * p.nquad, 0, false};
+  ClaimedUnits seq{claim, (lds_i32*)cq, p.na * p.nquad, (int)blockIdx.x, 0, false};
   p.xact = x;
   p.wgu = wgu;
   p.sgu = sgu;
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(WG_WAVES * 64) moe_down_kernel(const uint16_t*
   p.nquad = H / (P::TILE * WG_WAVES);
   p.na = p.m.num_active();
   p.n_items = ((p.m.max_rows() + 15) >> 4) * p.na * p.nquad;  // row-group levels that exist
-  ClaimedUnits seq{ctl + CTL_CLAIM_DN, (lds_i32*)cq, p.na * p.nquad, 0, false};
+  ClaimedUnits seq{ctl + CTL_CLAIM_DN, (lds_i32*)cq, p.na * p.nquad, (int)blockIdx.x, 0, false};
   p.xact = h;
   p.wd = wd;
   p.sd = sd;

@@ -487,17 +487,20 @@ __device__ __forceinline__ V wg_exclusive_scan(V v, WS ws, V& total, int lane, i
 }
 
 // The workgroup's sort of the T * k routed slots (ids: [T, k], T <= 32, E <= 1024) into
-// *ws, with `tmp` as 8 KB of scratch (token masks and expert offsets).  Each thread takes
+// *ws, with `tmp` as 8 KB of scratch (token masks and expert offsets); behind_load is called once the ids are
+// on their way.  Each thread takes
 // 4 consecutive experts.  Must be called by all threads.
+template <class F>
 __device__ __forceinline__ void wg_sort_slots(const int32_t* __restrict__ ids, int T, int E, int k, lds_wgsort* ws,
-                                              uint8_t* __restrict__ tmp) {
+                                              uint8_t* __restrict__ tmp, F behind_load) {
   uint32_t* bits = reinterpret_cast<uint32_t*>(tmp);       // [E] token masks
   int32_t* eoff = reinterpret_cast<int32_t*>(tmp + 4096);  // [E] first sorted position
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int F = T * k;
+  const int slots = T * k;
   for (int i = tid; i < E; i += WG_WAVES * 64) bits[i] = 0u;
   __syncthreads();
-  const int my_e = (tid < F) ? ids[tid] : -1;  // F <= 256 = one slot per thread
+  const int my_e = (tid < slots) ? ids[tid] : -1;  // slots <= 256 = one per thread
+  behind_load();
   if (my_e >= 0 && my_e < E) atomicOr(&bits[my_e], 1u << (tid / k));
   __syncthreads();
   int c[4];
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(WG_WAVES * 64) moe_gate_up_sorted_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   if (tid < 2) xctr[tid] = 0u;
   lds_wgsort* ws = (lds_wgsort*)&wsort;
-  wg_sort_slots(ids, T, E, k, ws, xbufs);
+  wg_sort_slots(ids, T, E, k, ws, xbufs, [] {});
   const LdsSortW meta{ws};
   const int na = meta.num_active();
   if (blockIdx.x == 0) {
@@ -608,7 +611,7 @@ __global__ void __launch_bounds__(WG_WAVES * 64) moe_gate_up_sorted_kernel(
   p.kinv = ((1u << 24) + (uint32_t)k - 1u) / (uint32_t)k;
   p.e_codes = (size_t)2 * I * (H / 2);
   p.e_scales = (size_t)2 * I * (H / 32);
-  ClaimedUnits seq{claim, (lds_i32*)cq, na * p.nquad, 0, false};
+  ClaimedUnits seq{claim, (lds_i32*)cq, na * p.nquad, (int)blockIdx.x, 0, false};
   stream_items<PG, SPS>(p, seq, xbufs, xctr, slabs[wave], sslabs[wave], wave, lane);
   seq.finish();
 }
@@ -672,13 +675,21 @@ int launch_gate_up_sorted(const uint16_t* x, const int32_t* ids, const uint8_t* 
 // by gate_up was measured instead and cost 3-40 us at 32 tokens (stores and atomics from
 // many workgroups into a few cache lines queue behind one another).
 //
-// Workgroups wait for one another only in that rare case, and only for workgroups of the
-// launch to finish their gate_up items, which need nothing from anyone: the grid is sized to
-// what the device holds at once at this kernel's occupancy, so every workgroup runs.  A wait
-// that outlasts SPIN_LIMIT polls sets the error word and goes on.  The last workgroup to
+// Workgroups wait for one another only in that rare case, and only for gate_up items, which need
+// nothing from anyone, to be finished by workgroups that run.  The grid is sized to what the
+// device holds at once at this kernel's occupancy, but other launches may hold a part of it (two
+// layers on two streams: each would wait for its own workgroups, which cannot start).  So the
+// items that are dealt to a workgroup beforehand, its share, belong to whoever marks it first: itself when it
+// starts, or one that is through with its own and finds unmarked ones.  Nobody goes on to down
+// while a share is unmarked, so GU_DONE, the shares finished, reaches the grid's size without another
+// workgroup having to start; one whose share is gone when it starts only helps with down.  In a launch that has
+// the device to itself the marks' latency hides: a mark is set beside the loads of the sort, and all are read, a
+// word a lane, beside the wait for the h stores (6, 16 and 32 tokens of 256 experts, top 8: 176.4, 292.5 and 422.1 us per layer
+// before, 176.6, 291.9 and 422.8 with them).
+// A wait that outlasts SPIN_LIMIT polls sets the error word and goes on.  The last workgroup to
 // exit resets the counters, so the control words are zero again after the launch.
 // The down phase runs at gate_up's occupancy (2 workgroups per CU, not down's 3), so its
-// waves keep two steps of 2 segments in flight instead of one; the registers are there (205).
+// waves keep two steps of 2 segments in flight instead of one; the registers are there (214).
 // Measured: T = 32 Zipf 380.4 -> 379.7 us per layer, uniform T = 32 587.6 -> 585.6.
 constexpr int DN_SPS_DEEP = 4;
 static_assert(SRUN % DN_SPS_DEEP == 0, "scale runs end on steps");
@@ -711,6 +722,31 @@ struct ExpertsLds {
   int32_t* last;     // 1
 };
 
+// Marks share w of gate_up; returns whether somebody had it.
+__device__ __forceinline__ bool mark_share(int32_t* ctl, int w) {
+  int32_t* const word = ctl + CTL_SHARE0 + w % CTL_SHARE_WORDS * CTL_SHARE_STRIDE;
+  const int bit = w / CTL_SHARE_WORDS;
+  return (__hip_atomic_fetch_or(word, 1 << bit, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >> bit) & 1;
+}
+// The word of share marks that lane `lane` looks after.
+__device__ __forceinline__ uint32_t share_word(const int32_t* ctl, int lane) {
+  return (uint32_t)__hip_atomic_load(ctl + CTL_SHARE0 + lane * CTL_SHARE_STRIDE, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// A share that nobody had, now this workgroup's (one wave calls, with the words); -1: all have somebody.
+__device__ __forceinline__ int take_share(int32_t* ctl, uint32_t word, int lane) {
+  const int n = gridDim.x;
+  for (;;) {
+    const int w = lane + CTL_SHARE_WORDS * (int)__builtin_ctz(~word);
+    const uint64_t open = __ballot(~word != 0 && w < n);
+    if (open == 0) return -1;
+    const int who = (int)__builtin_ctzll(open);
+    bool had = false;
+    if (lane == who) had = mark_share(ctl, w);
+    if (__ballot(had) == 0) return __builtin_amdgcn_readlane(w, who);
+    word = share_word(ctl, lane);
+  }
+}
+
 // Both phases and the exit, for the sort in `meta` (the workgroup's own in LDS, or the sort
 // launches' in global memory); A8: MXFP8 activations (x and h quantized as they are staged).
 template <bool A8, class Meta>
@@ -718,7 +754,7 @@ __device__ __forceinline__ void experts_phases(const Meta& meta, const ExpertsLd
                                                const uint8_t* __restrict__ wgu, const uint8_t* __restrict__ sgu,
                                                const uint8_t* __restrict__ wd, const uint8_t* __restrict__ sd,
                                                uint16_t* h, float* __restrict__ dpart, int32_t* ctl, int H, int I,
-                                               int k) {
+                                               int k, bool taken) {
   constexpr int SSLAB = ScaleRun4::slab_bytes<2>();
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
@@ -746,20 +782,34 @@ __device__ __forceinline__ void experts_phases(const Meta& meta, const ExpertsLd
     p.kinv = ((1u << 24) + (uint32_t)k - 1u) / (uint32_t)k;
     p.e_codes = (size_t)2 * I * (H / 2);
     p.e_scales = (size_t)2 * I * (H / 32);
-    ClaimedUnits seq{ctl + CTL_CLAIM_GU, (lds_i32*)L.cq, na * p.nquad, 0, false};
-    stream_items<PG, GU_SPS>(p, seq, L.xbufs, L.xctr, L.slabs + wave * SLAB_BYTES, L.sslabs + wave * SSLAB, wave,
-                             lane);
-    seq.finish();
+    if (tid == 0) *L.last = taken ? -1 : (int)blockIdx.x;
+    __syncthreads();
+    for (;;) {
+      const int w = __builtin_amdgcn_readfirstlane(*L.last);
+      if (w >= 0) {
+        ClaimedUnits seq{ctl + CTL_CLAIM_GU, (lds_i32*)L.cq, na * p.nquad, w, 0, false};
+        stream_items<PG, GU_SPS>(p, seq, L.xbufs, L.xctr, L.slabs + wave * SLAB_BYTES, L.sslabs + wave * SSLAB, wave,
+                                 lane);
+        seq.finish();
+      }
+      // the share's h stores are complete; count it, start a fresh chunk hand-off, and look for a share to take over
+      uint32_t marks = 0;
+      if (wave == 0) marks = share_word(ctl, lane);
+      wait_own_stores();
+      __syncthreads();
+      if (wave == 0) {
+        if (tid == 0) {
+          if (w >= 0) __hip_atomic_fetch_add(&ctl[CTL_GU_DONE], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          L.xctr[0] = 0u;
+          L.xctr[1] = 0u;
+        }
+        const int next = take_share(ctl, marks, lane);
+        if (tid == 0) *L.last = next;
+      }
+      __syncthreads();
+      if (__builtin_amdgcn_readfirstlane(*L.last) < 0) break;
+    }
   }
-  // this workgroup's h stores are complete; count it, and start a fresh chunk hand-off
-  wait_own_stores();
-  __syncthreads();
-  if (tid == 0) {
-    __hip_atomic_fetch_add(&ctl[CTL_GU_DONE], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    L.xctr[0] = 0u;
-    L.xctr[1] = 0u;
-  }
-  __syncthreads();
 
   // ---------------------------------------------------------------- down
   {
@@ -786,7 +836,7 @@ __device__ __forceinline__ void experts_phases(const Meta& meta, const ExpertsLd
     p.err = ctl + CTL_ERR;
     p.flag = nullptr;
     p.wave = wave;
-    ClaimedUnits seq{ctl + CTL_CLAIM_DN, (lds_i32*)L.cq, na * p.nquad, 0, false};
+    ClaimedUnits seq{ctl + CTL_CLAIM_DN, (lds_i32*)L.cq, na * p.nquad, (int)blockIdx.x, 0, false};
     stream_items<PD, SPS>(p, seq, L.xbufs, L.xctr, L.slabs + wave * SLAB_BYTES, L.sslabs + wave * SSLAB, wave,
                                   lane);
     seq.finish();
@@ -798,9 +848,13 @@ __device__ __forceinline__ void experts_phases(const Meta& meta, const ExpertsLd
     *L.last = __hip_atomic_fetch_add(&ctl[CTL_EXIT], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
               (int)gridDim.x - 1;
   __syncthreads();
-  if (*L.last && tid == 0) {
-    __hip_atomic_store(&ctl[CTL_GU_DONE], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __hip_atomic_store(&ctl[CTL_EXIT], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (*L.last) {
+    if (tid < CTL_SHARE_WORDS)
+      __hip_atomic_store(&ctl[CTL_SHARE0 + tid * CTL_SHARE_STRIDE], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (tid == 0) {
+      __hip_atomic_store(&ctl[CTL_GU_DONE], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&ctl[CTL_EXIT], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
   }
 }
 
@@ -814,28 +868,32 @@ __device__ __forceinline__ void experts_phases(const Meta& meta, const ExpertsLd
   const ExpertsLds lds{xbufs, slabs, sslabs, xctr, cq, &last};                            \
   if (threadIdx.x < 2) xctr[threadIdx.x] = 0u
 
-// T <= 32: every workgroup sorts the routed ids itself.
+// T <= 32: every workgroup sorts the routed ids itself.  Two waves a SIMD: MXFP8 would take 268 registers.
 template <bool A8>
-__global__ void __launch_bounds__(WG_WAVES * 64) moe_experts_sorted_kernel(
+__global__ void __launch_bounds__(WG_WAVES * 64, 2) moe_experts_sorted_kernel(
     const uint16_t* __restrict__ x, const int32_t* __restrict__ ids, const uint8_t* __restrict__ wgu,
     const uint8_t* __restrict__ sgu, const uint8_t* __restrict__ wd, const uint8_t* __restrict__ sd, uint16_t* h,
     float* __restrict__ dpart, int32_t* ctl, int T, int H, int I, int E, int k) {
   MX_EXPERTS_LDS;
   __shared__ WgSort wsort;
   lds_wgsort* ws = (lds_wgsort*)&wsort;
-  wg_sort_slots(ids, T, E, k, ws, xbufs);  // ends with a barrier: xbufs is free again
-  experts_phases<A8>(LdsSortW{ws}, lds, x, wgu, sgu, wd, sd, h, dpart, ctl, H, I, k);
+  bool taken = false;
+  wg_sort_slots(ids, T, E, k, ws, xbufs, [&] {  // ends with a barrier: xbufs is free again
+    if (threadIdx.x == 0) taken = mark_share(ctl, (int)blockIdx.x);
+  });
+  experts_phases<A8>(LdsSortW{ws}, lds, x, wgu, sgu, wd, sd, h, dpart, ctl, H, I, k, taken);
 }
 
 // Any T: the sort launches' result in global memory.
 template <bool A8>
-__global__ void __launch_bounds__(WG_WAVES * 64) moe_experts_kernel(
+__global__ void __launch_bounds__(WG_WAVES * 64, 2) moe_experts_kernel(
     const uint16_t* __restrict__ x, SortView sv, const uint8_t* __restrict__ wgu, const uint8_t* __restrict__ sgu,
     const uint8_t* __restrict__ wd, const uint8_t* __restrict__ sd, uint16_t* h, float* __restrict__ dpart,
     int32_t* ctl, int H, int I, int k) {
   MX_EXPERTS_LDS;
+  const bool taken = threadIdx.x == 0 && mark_share(ctl, (int)blockIdx.x);
   __syncthreads();
-  experts_phases<A8>(GlobalSort{sv}, lds, x, wgu, sgu, wd, sd, h, dpart, ctl, H, I, k);
+  experts_phases<A8>(GlobalSort{sv}, lds, x, wgu, sgu, wd, sd, h, dpart, ctl, H, I, k, taken);
 }
 #undef MX_EXPERTS_LDS
 
@@ -864,7 +922,7 @@ static int launch_experts_sorted_run(const uint16_t* x, const int32_t* ids, cons
                                      const uint8_t* wd, const uint8_t* sd, uint16_t* h, float* dpart, int32_t* ctl,
                                      int T, int H, int I, int E, int k, hipStream_t stream) {
   static const int occ = routed_occupancy(moe_experts_sorted_kernel<A8>);
-  const dim3 grid((unsigned)(device_cu_count() * occ)), block(WG_WAVES * 64);
+  const dim3 grid((unsigned)std::min(device_cu_count() * occ, CTL_MAX_SHARES)), block(WG_WAVES * 64);
   hipLaunchKernelGGL(moe_experts_sorted_kernel<A8>, grid, block, 0, stream, x, ids, wgu, sgu, wd, sd, h, dpart, ctl, T,
                      H, I, E, k);
   return hip_status(hipGetLastError());
@@ -888,7 +946,7 @@ static int launch_experts_run(const uint16_t* x, const SortView& sv, const uint8
                               const uint8_t* wd, const uint8_t* sd, uint16_t* h, float* dpart, int32_t* ctl, int H,
                               int I, int k, hipStream_t stream) {
   static const int occ = routed_occupancy(moe_experts_kernel<A8>);
-  const dim3 grid((unsigned)(device_cu_count() * occ)), block(WG_WAVES * 64);
+  const dim3 grid((unsigned)std::min(device_cu_count() * occ, CTL_MAX_SHARES)), block(WG_WAVES * 64);
   hipLaunchKernelGGL(moe_experts_kernel<A8>, grid, block, 0, stream, x, sv, wgu, sgu, wd, sd, h, dpart, ctl, H, I, k);
   return hip_status(hipGetLastError());
 }

@@ -14,7 +14,7 @@ namespace mx {
 // expert GEMMs' claim counters and the single-launch layer's counters and flags.  Words
 // that many workgroups update sit on lines of their own, 512 bytes apart, so that their
 // traffic spreads over memory channels instead of queueing on one.
-constexpr int CTL_GU_DONE = 0;      // single launch: gate_up items whose h rows are written
+constexpr int CTL_GU_DONE = 0;      // single launch: gate_up items (of both expert GEMMs: shares) whose h rows are written
 constexpr int CTL_EXIT = 1;         // single launch: workgroups that have finished
 constexpr int CTL_ERR = 2;          // single launch: set to 1 by a wait that gave up (sticky)
 constexpr int CTL_CLAIM_GU = 256;   // gate_up claim classes (16 x 128 words)
@@ -25,6 +25,13 @@ constexpr int CTL_MAX_QUADS = 1024;
 constexpr int CTL_READY0 = 6144;
 constexpr int CTL_READY_REPLICAS = 64;
 constexpr int CTL_READY_STRIDE = 128;
+// Single launch of both expert GEMMs, in the same words: per share of gate_up, whether somebody has it (share w is bit w / 64 of
+// word w % 64: few workgroups to a word).
+constexpr int CTL_SHARE0 = CTL_READY0;
+constexpr int CTL_SHARE_WORDS = CTL_READY_REPLICAS;
+constexpr int CTL_SHARE_STRIDE = CTL_READY_STRIDE;
+constexpr int CTL_MAX_SHARES = 32 * CTL_SHARE_WORDS;
+static_assert(CTL_SHARE_WORDS == 64, "a word a lane");
 static_assert(CTL_CLAIM_DN - CTL_CLAIM_GU >= 16 * 128 && CTL_QUAD0 - CTL_CLAIM_DN >= 16 * 128, "claim classes");
 static_assert(CTL_QUAD0 + CTL_MAX_QUADS <= CTL_READY0, "control block layout");
 static_assert((CTL_READY0 + CTL_READY_REPLICAS * CTL_READY_STRIDE) * 4 == MX_WORKSPACE_CTL_BYTES, "control block size");

@@ -429,6 +429,7 @@ __device__ __forceinline__ void segment_compute_a8(u32x4 (&w)[NS][2], const uint
 // reaches every item first, enters the n-th.
 constexpr int STATIC_UNITS = 3;
 struct StaticUnits {
+  __device__ __forceinline__ int share() const { return (int)blockIdx.x; }
   __device__ __forceinline__ int unit(int n) const { return (int)blockIdx.x + n * (int)gridDim.x; }
   __device__ __forceinline__ void enter(int) {}
 };
@@ -456,13 +457,15 @@ struct ClaimedUnits {
   int32_t* ctr;
   lds_i32* q;      // 4 LDS words: claim results for ordinals n & 3
   int n_first;     // first-group items of the launch
+  int w;           // whose items: this workgroup's, or those of one that has not started
   int pending;     // thread 0: the last claim issued
   bool claimed;    // thread 0: a claim was issued
   // Claiming pays once workgroups average more than DYNAMIC_MIN items; below that the
   // claims, issued in near lockstep, cost more than the balance gains.
   __device__ __forceinline__ bool dynamic() const { return n_first > DYNAMIC_MIN * (int)gridDim.x; }
   __device__ __forceinline__ int classes() const { return min(CLAIM_CLASSES, (int)gridDim.x); }
-  __device__ __forceinline__ int cls() const { return (int)blockIdx.x % classes(); }
+  __device__ __forceinline__ int share() const { return w; }
+  __device__ __forceinline__ int cls() const { return w % classes(); }
   __device__ __forceinline__ int32_t* class_ctr() const { return ctr + cls() * CLAIM_STRIDE; }
   // An increment-with-wrap (at 2^32 - 1: never reached) rather than an add: the compiler's
   // atomic optimizer turns a lone thread's add into a wave reduction that consumes the
@@ -474,7 +477,7 @@ struct ClaimedUnits {
   }
   __device__ __forceinline__ int unit(int n) const {
     // static launches deal every item round-robin: the 4th is past the end
-    if (n < STATIC_UNITS || !dynamic()) return (int)blockIdx.x + n * (int)gridDim.x;
+    if (n < STATIC_UNITS || !dynamic()) return w + n * (int)gridDim.x;
     return STATIC_UNITS * (int)gridDim.x + cls() + classes() * __builtin_amdgcn_readfirstlane(q[n & 3]);
   }
   // the chunk loader enters ordinal m (m >= 1): publish the claim for ordinal m + 1 (issued
@@ -541,7 +544,7 @@ __device__ __forceinline__ void stream_items(P& p, Seq& seq, uint8_t* __restrict
   const uint32_t sshift = 8u * (uint32_t)(lane >> 4);
 
   const int n_first = p.first_groups();
-  const int wg = blockIdx.x, n_wg = gridDim.x;
+  const int wg = seq.share(), n_wg = gridDim.x;
   // phase A: the next valid extra-group item at or after `it` in this workgroup's stride.
   // Most candidates are invalid (only experts with more than 16 rows have extra groups),
   // and each check reads the active list and then the expert's count, so the candidates

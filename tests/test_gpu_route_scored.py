@@ -712,3 +712,41 @@ def test_outputs_over_what_is_read(mx):
         mx.moe_mxfp4_forward_routed(x, ids, gates, *W, out=ws[: T * H * 2].view(torch.bfloat16).view(T, H), ws=ws)
     with pytest.raises(ValueError, match="W_down"):
         mx.moe_mxfp4_forward_routed(x, ids, gates, *W, out=W[2].view(-1)[: T * H * 2].view(torch.bfloat16).view(T, H))
+
+
+def test_layers_on_streams_at_once(mx):
+    """The layer, behind a routing and as a whole, on four streams at once, each with a workspace of its own: no
+    launch has the device to itself, and none waits for workgroups of its own that cannot start."""
+    H, I, E, k = 1024, 1024, 96, 8
+    W = expert_weights(E, H, I, gen(81))
+    runs = []
+    for T, act8, shared in ((24, False, 0), (32, True, 0), (32, False, 0), (20, False, 1)):
+        g = gen(T + act8 + shared)
+        x = torch.randn(T, H, generator=g).bfloat16().to(DEV)
+        l = torch.randn(T, E - shared, generator=g).to(DEV)
+
+        def run(x=x, l=l, act8=act8, shared=shared):
+            whole = mx.moe_mxfp4_forward(x, l, k, *W, act8=act8, n_shared=shared)
+            if shared:
+                return [whole]
+            return [mx.moe_mxfp4_forward_routed(x, *mx.moe_route_topk(l, k), *W, act8=act8), whole]
+
+        runs.append(run)
+    wants = [[t.clone() for t in r()] for r in runs]
+    streams = [torch.cuda.Stream() for _ in runs]
+    spaces = [mx.workspace(32, H, I, E, k + 1, DEV, stream=s) for s in streams]
+    torch.cuda.synchronize()
+    for i in range(5):
+        say("streams", i)
+        got = [[] for _ in runs]
+        for _ in range(4):
+            for s, r, o in zip(streams, runs, got):
+                with torch.cuda.stream(s):
+                    o.append(r())
+        torch.cuda.synchronize()
+        for o, w in zip(got, wants):
+            for ys in o:
+                for y, want in zip(ys, w):
+                    assert torch.equal(y, want), i
+        for ws in spaces:
+            assert not ws[:mx.MX_WORKSPACE_CTL_BYTES].any()  # no wait gave up, nothing is left marked
