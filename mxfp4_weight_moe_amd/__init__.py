@@ -476,11 +476,17 @@ def workspace(T: int, H: int, I: int, E: int, top_k: int, device, stream=None) -
     stream) -- by default the device's current stream.  Calls that share a workspace must
     not overlap in time: calls on one stream run one after another, and calls on two
     streams get two workspaces.  Allocated zero-filled: its leading control words must start
-    at zero, and every call leaves them so."""
+    at zero, and every call leaves them so.  Under graph capture a fresh one from the graph's
+    memory, whose control words the graph clears: other graphs, and eager calls, may run
+    beside its replays."""
     need = workspace_size(T, H, I, E, top_k)
     dev = torch.device(device)
     if dev.index is None:
         dev = torch.device(dev.type, torch.cuda.current_device())
+    if torch.cuda.is_current_stream_capturing():
+        buf = torch.empty(need, dtype=torch.uint8, device=dev)
+        buf[:MX_WORKSPACE_CTL_BYTES].zero_()
+        return buf
     if stream is None:
         stream = torch.cuda.current_stream(dev)
     key = (dev, int(stream.cuda_stream))

@@ -750,3 +750,47 @@ def test_layers_on_streams_at_once(mx):
                     assert torch.equal(y, want), i
         for ws in spaces:
             assert not ws[:mx.MX_WORKSPACE_CTL_BYTES].any()  # no wait gave up, nothing is left marked
+
+
+def test_captured_layers_have_workspaces_of_their_own(mx):
+    """The layer behind a routing, and the layer itself, captured without a workspace: two graphs replayed at once on
+    two streams, eager calls beside them, and a graph whose sibling is gone give the eager results."""
+    H, I, E, k = 1024, 1024, 96, 8
+    W = expert_weights(E, H, I, gen(71))
+    runs = []
+    for T, act8 in ((24, False), (32, True), (4, False)):
+        g = gen(T)
+        x = torch.randn(T, H, generator=g).bfloat16().to(DEV)
+        l = torch.randn(T, E, generator=g).to(DEV)
+
+        def run(x=x, l=l, act8=act8):
+            ids, gates = mx.moe_route_scored(l, k, "sigmoid", renormalize=True)
+            return mx.moe_mxfp4_forward_routed(x, ids, gates, *W, act8=act8), mx.moe_mxfp4_forward(x, l, k, *W, act8=act8)
+
+        runs.append(run)
+    wants = [[t.clone() for t in r()] for r in runs]
+    torch.cuda.synchronize()
+    held = len(mx._ws_cache)
+    graphs, outs = [], []
+    for r in runs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs.append(r())
+        graphs.append(graph)
+    assert len(mx._ws_cache) == held  # nothing of a graph's memory outlives it
+    streams = [torch.cuda.Stream() for _ in graphs]
+    say("three graphs")
+    for i in range(4):
+        if i == 3:
+            graphs[0].reset()
+        for s, graph, o in list(zip(streams, graphs, outs))[int(i == 3):]:
+            for t in o:
+                t.fill_(math.nan)
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                graph.replay()
+        eager = runs[i % 3]()
+        torch.cuda.synchronize()
+        for o, w in list(zip(outs, wants))[int(i == 3):] + [(eager, wants[i % 3])]:
+            for a, b in zip(o, w):
+                assert torch.equal(a, b), i
