@@ -597,7 +597,9 @@ MX_API int mx_norm_residual_quantize(const uint16_t* x, const uint16_t* b, const
  *   a_codes, a_scales  the activations in `format`, [T, K];  other arguments as for mx_linear_fused
  * The products are exact; the scaled matrix instructions sum them in fp32 but drop, within groups of 8,
  * bits more than about 14 binades below the group's largest product, so |z - exact| stays below about
- * 2^-10 of sum_k |a w| (2^-8 |z| more where it is stored in bf16).
+ * 2^-10 of sum_k |a w| (2^-8 |z| more where it is stored in bf16).  MXFP8 activations of N(0, 1) values:
+ * 3e-6 to 6e-6 of z, root mean square; MXFP4's products all lie within 8 binades.  For fp32 sums over
+ * the same values pass mx_quantize's `values` to mx_linear_fused or mx_gate_up.
  */
 MX_API size_t mx_linear_quantized_workspace_size(int64_t T, int64_t K, int64_t N);
 MX_API int mx_linear_quantized(const uint8_t* a_codes, const uint8_t* a_scales, int format, const uint8_t* w_codes,
@@ -663,6 +665,8 @@ MX_API int moe_route_scored(const void* logits, int logits_type, const float* bi
  *   row distinct; ids outside [0, E) are skipped);  dlogits  logits_type [T, E] (written)
  * Rows of the forward's gates 0 have gradient 0.  A softmax row with a NaN logit, chosen or not, has gradient
  * NaN, as it has gates NaN; a sigmoid row has it where a chosen logit is NaN (renormalised: at all that are chosen).
+ * No difference of nearly equal values is formed, so one expert that has nearly all of a row keeps its gradient's
+ * digits.  Scores of experts that are not chosen are fp32, 0 below 2^-126.
  */
 MX_API int moe_route_scored_backward(const float* dgates, const void* logits, int logits_type, const int32_t* ids,
                                      int score, int renormalize, float scale, void* dlogits, int64_t T, int64_t E,
@@ -673,7 +677,8 @@ MX_API int moe_route_scored_backward(const float* dgates, const void* logits, in
  * first stage.
  *   ids int32 [T, top_k], each row top_k distinct ids in [0, E);  gates fp32 [T, top_k]
  *   act8  nonzero: MXFP8 activations, as moe_mxfp4_forward_a8
- * Other arguments, workspace and limits as for moe_mxfp4_forward (T <= MX_MAX_TOKENS).
+ * Other arguments, workspace and limits as for moe_mxfp4_forward (T <= MX_MAX_TOKENS).  No shared
+ * experts: one beside the layer is mx_gate_up_quantized and mx_linear_quantized with y as the residual.
  */
 MX_API int moe_mxfp4_forward_routed(const uint16_t* x, const int32_t* ids, const float* gates, int64_t top_k,
                                     const uint8_t* w_gate_up, const uint8_t* s_gate_up, const uint8_t* w_down,

@@ -54,6 +54,7 @@ __device__ __forceinline__ f32x4 mfma_stream_q(const u32x4& w, const QFragment<F
 // those ahead: two 16-byte pieces of a weight row, four (two) of a token, 8 scale bytes of each.
 // Bound by latency: 7168 -> 4096, 15.6 MB, takes 6.5 us in MXFP8 and 6.1 in MXFP4 for 1 token (2.5 TB/s), 9.0 and 7.6
 // for 16, of which a launch and a first load are about 3.  16 waves a workgroup or 2 units ahead are equal.
+// 17 to 32 tokens in MXFP8 with 8 waves spill 10 or 11 registers (the four units of two token groups).
 constexpr int Q_UNIT = 256;
 template <int FMT, int W, int MT, bool GATED, class Epilogue>
 __global__ void __launch_bounds__(W * 64) stream_q_kernel(QOperands o, Epilogue epi, float* __restrict__ parts, int T,
@@ -560,7 +561,8 @@ TilePlan quantized_plan(int64_t T, int64_t K, int64_t rows, bool gated, bool qua
     auto tiles = [&](int64_t nt) { return (all + 64 * nt - 1) / (64 * nt) * p.mtiles; };
     if (p.mt < 4 && tiles(2) <= GPU_CUS) {
       // Fewer tiles than CUs: 128 or 64 weight rows a tile, K whole or in parts, by what a workgroup reads
-      // (a CU's read path gives some 50 kB a microsecond) and what parts cost (written at 3 and read at
+      // (a CU's read path gives some 50 kB a microsecond of half lines, which all tiles are counted at, MXFP4's of
+      // whole lines too; tiles of 64 tokens beyond 64 are not weighed) and what parts cost (written at 3 and read at
       // 4 MB a microsecond, 2.5 for the second launch).  7168 -> 4096 in MXFP8: 128 tokens 14.3 us with 64 rows in 4
       // parts, 19.3 with 128 rows in 8; 2048 -> 7168, 128 tokens: 10.7 with 64 rows whole, 19.4 with 128 in 4 (14.1 and
       // 9.6 since, with fewer stages ahead).
