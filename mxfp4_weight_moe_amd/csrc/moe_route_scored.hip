@@ -83,9 +83,10 @@ __device__ __forceinline__ double row16_plus(double v) {
   return v + rotate16<1>(v);
 }
 
-// exp(x) for x <= 0, of itself off by 2^-49, exactly 1 at 0; below e^-800, and of NaN, 0 or next to it.  2^n times a
-// polynomial in x log2 e - n, |.| <= 1/2: 1 + y g(y), g interpolating (2^y - 1) / y at the 10 Chebyshev nodes (error 2^-50.6).
-// What a sum over a row takes in 64 bits, at 17 instructions a term where the library's exp has its ends to look after.
+// exp(x) for x <= 0, exactly 1 at 0, of itself off by 2^-49 (beyond x = -32 by |x| 2^-54, which a sum that has a 1 in it
+// does not see); below e^-800, and of NaN, 0.  2^n times a polynomial in y = x log2 e - n, |y| <= 1/2: 1 + y g(y),
+// g interpolating (2^y - 1) / y at the 10 Chebyshev nodes (error 2^-50.6).  What a sum over a row takes in 64 bits, at
+// some 18 instructions a term where the library's exp has its ends to look after.
 __device__ __forceinline__ double exp_term(double x) {
   constexpr double LOG2E = 0x1.71547652b82fep+0, ROUND = 0x1.8p52;  // whose last place is 1
   x = __builtin_fmax(x, -800.0);
@@ -204,7 +205,8 @@ constexpr float ROUTE_U = 0x1p-24f;
 // waves and no spill 16.6; with groups or a bias 3 to 5% the other way); three up to 512, where four would spill 50 (8192 x
 // 512 softmax 13.5 for 12.3, with a bias 16.3 for 13.5); beyond, and for more than 14 chosen, what the registers allow.
 template <bool BF16, int PER, int C, int WHOLE>
-__global__ void __launch_bounds__(64, (C != 1 || PER > 32 ? 1 : PER > 24 ? 3 : 4)) route_scored_kernel(RouteScored a, int32_t* __restrict__ ids, float* __restrict__ gates) {
+__global__ void __launch_bounds__(64, (C != 1 || PER > 32 ? 1 : PER > 24 ? 3 : 4))
+    route_scored_kernel(RouteScored a, int32_t* __restrict__ ids, float* __restrict__ gates) {
   extern __shared__ double shared[];  // with a bias or groups: per row E + groups values
   const int lane = threadIdx.x % ROUTE_LANES, row = threadIdx.x / ROUTE_LANES;
   const int64_t t0 = (int64_t)blockIdx.x * ROUTE_ROWS + row, t = t0 < a.T ? t0 : a.T - 1;  // rows past the last: it again
@@ -674,7 +676,8 @@ __global__ void __launch_bounds__(64) route_scored_backward_kernel(RouteScored a
     z = row16_sum(z);
   }
   double rest = 0.0;
-  auto renormalize = [&]() __attribute__((always_inline)) {  // scores whose sum is 0 in 64 bits have gates 0, as in the forward call
+  // scores whose sum is 0 in 64 bits have gates 0, as in the forward call
+  auto renormalize = [&]() __attribute__((always_inline)) {
     const double s = row16_plus(q[0] + q[1]);
 #pragma unroll
     for (int h = 0; h < 2; ++h) q[h] = s == 0.0 ? 0.0 : q[h] / s;
